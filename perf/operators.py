@@ -167,8 +167,8 @@ def run(state):
                               out=state["out"], **teacher)
             return {"loss": got["loss"], "grad": got["grad"]}
         got = dca.distill(state["logits"], state["ids"], state["values"], out={"loss": state["out"]["loss"]}, **teacher)
-        grad = dca.distill_backward(state["logits"], state["ids"], state["values"], got["stats"], state["grad_loss"],
-                                    out=state["out"]["grad"], **teacher)
+        grad = dca.distill_backward(state["logits"], state["ids"], got["stats"], state["grad_loss"],
+                                    temperature=case["tau"], n_rows=state["n_rows"], out=state["out"]["grad"])
         return {"loss": got["loss"], "grad": grad}
     if case["op"] == "top":
         return _plain_top(state["logits"], case["k"], case["tau"], state["n_rows"])
