@@ -8,4 +8,8 @@ from .binding import (  # noqa: F401
     LIB_PATH, SYMBOLS, DominoError, DominoHead, accept_len, load_library, verify, verify_noalloc,
     verify_workspace_size,
 )
+from .rows import (  # noqa: F401
+    beam_step, beam_step_workspace_size, distill, distill_backward, distill_workspace_size, top_logits,
+    top_logits_workspace_size,
+)
 from .tensors import device_tensor, head_weights_to_device  # noqa: F401

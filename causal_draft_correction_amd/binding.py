@@ -34,7 +34,10 @@ FLAG_SYNC_TIMEOUT = 2
 ERRORS = {-1: "EINVAL", -2: "EUNSUPPORTED", -3: "EWORKSPACE", -4: "EHIP", -5: "EDEVICE"}
 
 SYMBOLS = ("domino_head_workspace_size", "domino_head_create", "domino_head_draft", "domino_accept_len",
-           "domino_verify_workspace_size", "domino_verify", "domino_verify_noalloc", "domino_head_check_error", "domino_head_exec_info",
+           "domino_verify_workspace_size", "domino_verify", "domino_verify_noalloc",
+           "domino_top_logits_workspace_size", "domino_top_logits", "domino_beam_step_workspace_size",
+           "domino_beam_step", "domino_distill_workspace_size", "domino_distill", "domino_distill_backward",
+           "domino_head_check_error", "domino_head_exec_info",
            "domino_head_set_spin_limit", "domino_head_param_count", "domino_head_destroy", "domino_last_error")
 
 

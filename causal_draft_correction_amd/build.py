@@ -11,7 +11,8 @@ from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 SRC_DIR = os.path.join(HERE, "csrc")
-UNITS = ["domino_head.hip", "domino_head_res.hip", "domino_head_bat.hip", "domino_head_rb.hip", "domino_verify.hip"]
+UNITS = ["domino_head.hip", "domino_head_res.hip", "domino_head_bat.hip", "domino_head_rb.hip", "domino_verify.hip",
+         "domino_top.hip", "domino_distill.hip"]
 LIB = os.path.join(HERE, "libdomino_head.so")
 # the instrumented library: these units replace domino_head_res.hip and domino_head_rb.hip
 TRACE_UNITS = ["trace/trace_res.hip", "trace/trace_rb.hip"]

@@ -1,0 +1,30 @@
+// Distillation from a teacher's top logits: launches of the device code in domino_distill.hip.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/domino_head.h"
+
+namespace dhdistill {
+
+constexpr int MAX_K = 128;  // teacher logits of a row
+constexpr int STAT_HEAD = 4;  // floats of a row's statistics before those of its k ids
+
+size_t workspace_bytes(const domino_logits &lg);
+
+struct Teacher {
+    int k;
+    const int32_t *ids;    // [B, R, k]
+    const float *values;   // [B, R, k]
+    const float *lse;      // [B, R] or NULL
+};
+
+// Arguments were checked by the caller.
+hipError_t forward(const domino_logits &lg, const Teacher &t, float tau, const int32_t *n_rows, void *ws, float *loss,
+                   float *stats, hipStream_t st);
+hipError_t backward(const domino_logits &lg, int k, const int32_t *ids, const float *stats, const float *grad_loss,
+                    float tau, const int32_t *n_rows, const domino_logits &grad, hipStream_t st);
+
+}  // namespace dhdistill

@@ -1,0 +1,447 @@
+// Distillation of the head from a teacher's top logits: the loss of a student's rows, and its gradient.
+//
+// With y = z / tau, q = softmax(y), the teacher's entries j (id in [0, V)), t_j = value_j / tau - L with L the
+// teacher's log-sum-exp (given, or that of the entries alone), p_j = exp t_j, P = sum p_j,
+//     rest = max(0, 1 - P) where L is given, else 0;   Mm = P + rest;   Qr = sum of q over ids no entry names
+//     loss = tau^2 [ sum_j p_j (t_j - log q_j) + rest log(rest / Qr) ]
+//     dloss/dz_v = tau [ Mm q_v - sum_{j: id_j = v} p_j ]     where an entry names v
+//                = tau (q_v / Qr) [ Mm Qr - rest ]             elsewhere
+// The sum over the ids that no entry names is taken by itself (named elements count as -inf), never as a
+// difference, and has a maximum of its own: it keeps its precision where the student is nearly certain.
+//
+// The forward pass reads a row once (k_distill_part, one block per chunk, values in registers) and joins the
+// chunks and the k entries in 64 bits (k_distill_final).  The backward pass reads it once and writes it once
+// (k_distill_grad).  All are bound by HBM bandwidth for many rows, by latency for few.
+#define DH_NT 256
+#define DH_NS dhd
+#include "dh_rows.h"
+#include "dh_distill.h"
+
+namespace DH_NS {
+
+constexpr int MAX_IDS = dhdistill::MAX_K, HEAD = dhdistill::STAT_HEAD;
+static_assert(MAX_IDS <= NT, "one thread per id");
+
+struct Teach {
+    int k;
+    const int32_t *ids;
+    const float *values, *lse;
+};
+
+__device__ inline bool in_row(int id, int V) { return id >= 0 && id < V; }
+
+// The chunk's maximum and sum of exponentials; with TAIL over the elements that no entry names.
+template <typename T, int NV, bool TAIL>
+__global__ __launch_bounds__(NT) void k_distill_part(Rows rows, Teach te, int nch, int cvec, Scale sc, Part *parts)
+{
+    typedef Vec<T> VT;
+    constexpr int BITS = NV * VT::N, WORDS = (BITS + 31) / 32;
+    __shared__ uint32_t mask[WORDS][NT];
+    __shared__ float red_m[NWAVE], red_s[NWAVE];
+    const int row = blockIdx.x / nch, c = blockIdx.x % nch, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    if (!rows.counts(row / rows.R, row % rows.R))
+        return;
+    int id = -1;
+    if (static_cast<int>(threadIdx.x) < te.k)
+        id = te.ids[static_cast<int64_t>(row) * te.k + threadIdx.x];
+    if constexpr (TAIL) {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i)
+            mask[i][threadIdx.x] = 0;
+    }
+    if (!__syncthreads_or(in_row(id, rows.V)))
+        return;
+    typename VT::raw x[NV];
+    load_chunk<T, NV>(x, row_at<T>(rows, row / rows.R, row % rows.R), rows.V, c, cvec);
+    if constexpr (TAIL) {
+        const int v0 = chunk_begin<T>(c, cvec, rows.V), v1 = chunk_begin<T>(c + 1, cvec, rows.V);
+        if (id >= v0 && id < v1) {
+            const int o = id - v0, i = o / VT::N, bit = i / NT * VT::N + o % VT::N;
+            atomicOr(&mask[bit >> 5][i % NT], 1u << (bit & 31));
+        }
+        __syncthreads();
+        uint32_t mine[WORDS], any = 0;
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i)
+            any |= mine[i] = mask[i][threadIdx.x];
+        if (any) {
+#pragma unroll
+            for (int u = 0; u < NV; ++u)
+#pragma unroll
+                for (int e = 0; e < VT::N; ++e)
+                    if ((mine[(u * VT::N + e) >> 5] >> ((u * VT::N + e) & 31)) & 1u)
+                        VT::set(x[u], e, NEG_INF);
+        }
+    }
+    float m = NEG_INF;
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+#pragma unroll
+        for (int e = 0; e < VT::N; ++e)
+            m = fmaxf(m, VT::get(x[u], e));
+    m = wave_max(m);
+    if (lane == 0)
+        red_m[wave] = m;
+    __syncthreads();
+    m = red_m[0];
+#pragma unroll
+    for (int w = 1; w < NWAVE; ++w)
+        m = fmaxf(m, red_m[w]);
+    const float ref = m > NEG_INF ? m : 0.f;
+    float s = 0.f;
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+#pragma unroll
+        for (int e = 0; e < VT::N; ++e)
+            s += exp_scaled(VT::get(x[u], e) - ref, sc);
+    s = wave_sum(s);
+    if (lane == 0)
+        red_s[wave] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double total = 0.0;
+#pragma unroll
+        for (int w = 0; w < NWAVE; ++w)
+            total += static_cast<double>(red_s[w]);
+        // a NaN or +inf in the chunk makes the sum NaN: so the row's
+        parts[static_cast<int64_t>(row) * nch + c] = Part{total != total ? __builtin_nanf("") : m, static_cast<float>(total)};
+    }
+}
+
+__device__ inline double block_sum_f64(double v, double *red)
+{
+    v = wave_sum_f64(v);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0)
+        red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    double s = red[0];
+#pragma unroll
+    for (int w = 1; w < NWAVE; ++w)
+        s += red[w];
+    return s;
+}
+// (NaN operands are passed over)
+__device__ inline double block_max_f64(double v, double *red)
+{
+#pragma unroll
+    for (int o = 32; o; o >>= 1)
+        v = fmax(v, __shfl_xor(v, o));
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0)
+        red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    double s = red[0];
+#pragma unroll
+    for (int w = 1; w < NWAVE; ++w)
+        s = fmax(s, red[w]);
+    return s;
+}
+
+// One row: its loss, and what the backward pass needs of it:
+//     stats = { m, A, 1 (0: a row that is left out), log-sum-exp, h_0 .. h_{k-1} }
+// so that dloss/dz_v = tau A exp((z_v - m) / tau), and tau h_j for v = id_j.
+template <typename T>
+__global__ __launch_bounds__(NT) void k_distill_final(Rows rows, Teach te, int nch, double tau, const Part *parts,
+                                                      float *loss, float *stats)
+{
+    __shared__ double red[NWAVE];
+    __shared__ double s_rest;
+    __shared__ float m_rest;
+    __shared__ int s_id[MAX_IDS];
+    __shared__ double s_p[MAX_IDS];
+    const double NINF = -__builtin_huge_val();
+    const int row = blockIdx.x, j = threadIdx.x;
+    const double inv_tau = 1.0 / tau;
+    float *st = stats ? stats + static_cast<int64_t>(row) * (HEAD + te.k) : nullptr;
+    const bool counts = rows.counts(row / rows.R, row % rows.R);
+    int id = -1;
+    if (counts && j < te.k)
+        id = te.ids[static_cast<int64_t>(row) * te.k + j];
+    const bool valid = in_row(id, rows.V);
+    bool live = __syncthreads_or(valid);
+    // differences are taken from the maxima, before their logarithms: rows at the type's lowest value keep them
+    double t = NINF, z = NINF;
+    if (valid) {
+        t = static_cast<double>(te.values[static_cast<int64_t>(row) * te.k + j]) * inv_tau;
+        z = Vec<T>::one(row_at<T>(rows, row / rows.R, row % rows.R) + id);
+    }
+    if (live) {
+        if (te.lse) {
+            t -= static_cast<double>(te.lse[row]);
+        } else {
+            const double top = block_max_f64(t, red);
+            if (top > NINF)
+                t = (t - top) - log(block_sum_f64(valid ? exp(t - top) : 0.0, red));
+            else  // nothing but -inf (no mass: left out) or NaN
+                live = __syncthreads_or(valid && t != t), t = __builtin_nan("");
+        }
+    }
+    if (!live) {
+        if (j == 0)
+            loss[row] = 0.f;
+        if (st)
+            for (int i = j; i < HEAD + te.k; i += NT)
+                st[i] = 0.f;
+        return;
+    }
+    const double p = valid ? exp(t) : 0.0;
+    if (j < te.k)
+        s_id[j] = valid ? id : -1, s_p[j] = p;
+    if (j < 64) {
+        float m;
+        double s;
+        join_parts(parts + static_cast<int64_t>(row) * nch, nch, inv_tau, m, s);
+        if (j == 0)
+            m_rest = m, s_rest = s;
+    }
+    __syncthreads();
+    bool first = valid;     // of the entries that name this id
+    double named = 0.0;     // their mass
+    if (valid)
+        for (int i = 0; i < te.k; ++i)
+            if (s_id[i] == id) {
+                named += s_p[i];
+                first &= i >= j;
+            }
+    const double mass = block_sum_f64(p, red);
+    double rest = 0.0, m = m_rest, s = s_rest;
+    if (te.lse) {
+        rest = 1.0 - mass;
+        rest = rest < 0.0 ? 0.0 : rest;
+        const double top = block_max_f64(z, red);
+        m = m > top || m != m ? m : top;
+        s = block_sum_f64(first ? (z == m ? 1.0 : exp((z - m) * inv_tau)) : 0.0, red);
+        if (m_rest > NEG_INF || m_rest != m_rest)
+            s += s_rest * (m_rest == m ? 1.0 : exp((m_rest - m) * inv_tau));
+        if (m == NINF)
+            s = 0.0;
+    }
+    const double total = mass + rest;
+    const double log_s = log(s), lse = m == NINF ? NINF : m * inv_tau + log_s;
+    const double logq = z == NINF ? NINF : (z - m) * inv_tau - log_s;
+    double sum = block_sum_f64(p == 0.0 ? 0.0 : p * (t - logq), red);
+    double A = s > 0.0 || s != s ? total / s : 0.0;
+    double ref = m;
+    if (te.lse) {
+        const double log_rest = m_rest == NEG_INF ? NINF : (m_rest - m) * inv_tau + log(s_rest) - log_s;
+        if (rest > 0.0)
+            sum += rest * (log(rest) - log_rest);
+        A = m_rest == NEG_INF ? 0.0 : (total * exp(log_rest) - rest) / s_rest;
+        ref = m_rest;
+    }
+    const bool none = !(lse < -NINF);  // a NaN or +inf among the logits: no distribution
+    if (none)
+        sum = A = __builtin_nan("");
+    if (j == 0)
+        loss[row] = static_cast<float>(tau * tau * sum);
+    if (st) {
+        if (j == 0) {
+            st[0] = ref > NINF || ref != ref ? static_cast<float>(ref) : 0.f;
+            st[1] = static_cast<float>(A);
+            st[2] = 1.f;
+            st[3] = static_cast<float>(lse);
+        }
+        if (j < te.k)
+            st[HEAD + j] = none ? __builtin_nanf("") : static_cast<float>(total * exp(logq) - named);
+    }
+}
+
+// dloss/dz of one chunk.  The elements that entries name are written again once the block's other stores are done.
+template <typename T, int NV>
+__global__ __launch_bounds__(NT) void k_distill_grad(Rows rows, int k, int nch, int cvec, const int32_t *ids,
+                                                     const float *stats, const float *grad_loss, float tau, Scale sc,
+                                                     Rows grad)
+{
+    typedef Vec<T> VT;
+    const int row = blockIdx.x / nch, c = blockIdx.x % nch, b = row / rows.R, r = row % rows.R;
+    T *out = const_cast<T *>(row_at<T>(grad, b, r));
+    const float *st = stats + static_cast<int64_t>(row) * (HEAD + k);
+    const bool live = rows.counts(b, r) && st[2] != 0.f;
+    const int v0 = chunk_begin<T>(c, cvec, rows.V), v1 = chunk_begin<T>(c + 1, cvec, rows.V);
+    typename VT::raw x[NV];
+    if (live) {
+        load_chunk<T, NV>(x, row_at<T>(rows, b, r), rows.V, c, cvec);
+        const float g = grad_loss[row] * tau, m = st[0], A = st[1] * g;
+#pragma unroll
+        for (int u = 0; u < NV; ++u)
+#pragma unroll
+            for (int e = 0; e < VT::N; ++e)
+                VT::set(x[u], e, A * exp_scaled(VT::get(x[u], e) - m, sc));
+    } else {
+#pragma unroll
+        for (int u = 0; u < NV; ++u)
+            x[u] = typename VT::raw{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        const int v = v0 + (u * NT + static_cast<int>(threadIdx.x)) * VT::N;
+        if (v + VT::N <= v1) {
+            __builtin_nontemporal_store(x[u], reinterpret_cast<typename VT::mem *>(out + v));
+        } else if (v < v1) {
+#pragma unroll
+            for (int e = 0; e < VT::N; ++e)
+                if (v + e < v1)
+                    VT::put(out + v + e, VT::get(x[u], e));
+        }
+    }
+    if (!live)
+        return;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the block's stores are done
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) < k) {
+        const int id = ids[static_cast<int64_t>(row) * k + threadIdx.x];
+        if (id >= v0 && id < v1)
+            VT::put(out + id, st[HEAD + threadIdx.x] * (grad_loss[row] * tau));
+    }
+}
+
+}  // namespace DH_NS
+
+namespace dhdistill {
+
+using namespace dhd;
+
+namespace {
+
+constexpr int TARGET_BLOCKS = 1024;
+
+Split split_of(const domino_logits &lg)
+{
+    const int64_t rows = static_cast<int64_t>(lg.B) * lg.R;
+    const int per = lg.dtype == DOMINO_F32 ? 4 : 8;
+    const int nvec = static_cast<int>((static_cast<int64_t>(lg.V) + per - 1) / per);
+    const int least = static_cast<int>((static_cast<int64_t>(nvec) + NT * 16 - 1) / (NT * 16));
+    int64_t n = rows ? (TARGET_BLOCKS + rows - 1) / rows : 1;
+    n = n < nvec / NT ? n : nvec / NT;
+    n = n > least ? n : least;
+    Split sp;
+    sp.cvec = static_cast<int>((nvec + n - 1) / n);
+    sp.nch = (nvec + sp.cvec - 1) / sp.cvec;
+    sp.nv = 1;
+    while (sp.nv * NT < sp.cvec)
+        sp.nv *= 2;
+    return sp;
+}
+
+Rows rows_of(const domino_logits &lg, const int32_t *n_rows)
+{
+    Rows r;
+    r.data = lg.data;
+    r.bs = lg.batch_stride;
+    r.rs = lg.row_stride;
+    r.R = lg.R;
+    r.V = lg.V;
+    r.n_rows = n_rows;
+    return r;
+}
+
+struct PartCall {
+    Rows rows;
+    Teach te;
+    Split sp;
+    Scale sc;
+    Part *parts;
+    unsigned grid;
+    hipStream_t st;
+    template <typename T, int NV>
+    void run() const
+    {
+        if (te.lse)
+            hipLaunchKernelGGL((k_distill_part<T, NV, true>), dim3(grid), dim3(NT), 0, st, rows, te, sp.nch, sp.cvec,
+                               sc, parts);
+        else
+            hipLaunchKernelGGL((k_distill_part<T, NV, false>), dim3(grid), dim3(NT), 0, st, rows, te, sp.nch, sp.cvec,
+                               sc, parts);
+    }
+};
+
+struct GradCall {
+    Rows rows, grad;
+    int k;
+    const int32_t *ids;
+    const float *stats, *grad_loss;
+    float tau;
+    Split sp;
+    Scale sc;
+    unsigned grid;
+    hipStream_t st;
+    template <typename T, int NV>
+    void run() const
+    {
+        hipLaunchKernelGGL((k_distill_grad<T, NV>), dim3(grid), dim3(NT), 0, st, rows, k, sp.nch, sp.cvec, ids, stats,
+                           grad_loss, tau, sc, grad);
+    }
+};
+
+template <typename T, typename C>
+void pick(const C &call)
+{
+    if (call.sp.nv <= 2)
+        call.template run<T, 2>();
+    else if (call.sp.nv <= 4)
+        call.template run<T, 4>();
+    else if (call.sp.nv <= 8)
+        call.template run<T, 8>();
+    else
+        call.template run<T, 16>();
+}
+
+}  // namespace
+
+size_t workspace_bytes(const domino_logits &lg)
+{
+    return static_cast<size_t>(lg.B) * lg.R * split_of(lg).nch * sizeof(Part);
+}
+
+hipError_t forward(const domino_logits &lg, const Teacher &t, float tau, const int32_t *n_rows, void *ws, float *loss,
+                   float *stats, hipStream_t st)
+{
+    PartCall c;
+    c.rows = rows_of(lg, n_rows);
+    c.te = Teach{t.k, t.ids, t.values, t.lse};
+    c.sp = split_of(lg);
+    c.sc = scale_of(tau);
+    c.parts = static_cast<Part *>(ws);
+    const unsigned n = static_cast<unsigned>(lg.B) * static_cast<unsigned>(lg.R);
+    c.grid = n * c.sp.nch;
+    c.st = st;
+    if (lg.dtype == DOMINO_F32)
+        pick<float>(c);
+    else
+        pick<bf16s>(c);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return e;
+    if (lg.dtype == DOMINO_F32)
+        hipLaunchKernelGGL((k_distill_final<float>), dim3(n), dim3(NT), 0, st, c.rows, c.te, c.sp.nch,
+                           static_cast<double>(tau), c.parts, loss, stats);
+    else
+        hipLaunchKernelGGL((k_distill_final<bf16s>), dim3(n), dim3(NT), 0, st, c.rows, c.te, c.sp.nch,
+                           static_cast<double>(tau), c.parts, loss, stats);
+    return hipGetLastError();
+}
+
+hipError_t backward(const domino_logits &lg, int k, const int32_t *ids, const float *stats, const float *grad_loss,
+                    float tau, const int32_t *n_rows, const domino_logits &grad, hipStream_t st)
+{
+    GradCall c;
+    c.rows = rows_of(lg, n_rows);
+    c.grad = rows_of(grad, nullptr);
+    c.k = k;
+    c.ids = ids;
+    c.stats = stats;
+    c.grad_loss = grad_loss;
+    c.tau = tau;
+    c.sp = split_of(lg);
+    c.sc = scale_of(tau);
+    c.grid = static_cast<unsigned>(lg.B) * static_cast<unsigned>(lg.R) * c.sp.nch;
+    c.st = st;
+    if (lg.dtype == DOMINO_F32)
+        pick<float>(c);
+    else
+        pick<bf16s>(c);
+    return hipGetLastError();
+}
+
+}  // namespace dhdistill

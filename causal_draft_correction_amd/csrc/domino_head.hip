@@ -30,6 +30,8 @@
 #include "dh_resident.h"
 #include "dh_batched.h"
 #include "dh_verify.h"
+#include "dh_top.h"
+#include "dh_distill.h"
 #include "dh_rbatch.h"
 
 using namespace dh;
@@ -1156,6 +1158,256 @@ int domino_verify_noalloc(int32_t B, int32_t K, int32_t V, const float *logits, 
     HIP_TRY(dhverify::launch(B, K, V, logits, draft, static_cast<uint64_t *>(ws), target, accept, next,
                              static_cast<hipStream_t>(stream)),
             "launch verify");
+    return DOMINO_OK;
+}
+
+// Shape and type of a [B, R, V] operand.
+static int logits_args(const domino_logits *lg, const char *what)
+{
+    if (!lg)
+        return fail(DOMINO_EINVAL, "%s is NULL", what);
+    if (lg->dtype != DOMINO_F32 && lg->dtype != DOMINO_BF16)
+        return fail(DOMINO_EUNSUPPORTED, "%s: dtype %d is neither DOMINO_F32 nor DOMINO_BF16", what, lg->dtype);
+    if (lg->B < 0 || lg->R < 1 || lg->V < 1)
+        return fail(DOMINO_EINVAL, "%s: B=%d, R=%d, V=%d (B >= 0, R >= 1, V >= 1)", what, lg->B, lg->R, lg->V);
+    if (lg->batch_stride < 0 || lg->row_stride < 0)
+        return fail(DOMINO_EINVAL, "%s: strides %lld, %lld are negative", what,
+                    static_cast<long long>(lg->batch_stride), static_cast<long long>(lg->row_stride));
+    const __int128 reach = static_cast<__int128>(lg->B) * lg->batch_stride + static_cast<__int128>(lg->R) * lg->row_stride;
+    if (reach > (static_cast<__int128>(1) << 48))
+        return fail(DOMINO_EINVAL, "%s: strides %lld, %lld reach past any memory", what,
+                    static_cast<long long>(lg->batch_stride), static_cast<long long>(lg->row_stride));
+    // one block per chunk of a row, of 1024 elements at least
+    const long long rows = static_cast<long long>(lg->B) * lg->R;
+    if (rows > 0x7FFFFFFFll || rows * (lg->V / 1024 + 1ll) > 0x7FFFFFFFll)
+        return fail(DOMINO_EUNSUPPORTED, "%s: %lld rows of %d are too many for one launch", what, rows, lg->V);
+    return DOMINO_OK;
+}
+
+static int logits_data(const domino_logits *lg, const char *what)
+{
+    if (!lg->data)
+        return fail(DOMINO_EINVAL, "%s: NULL pointer", what);
+    if (reinterpret_cast<uintptr_t>(lg->data) % (lg->dtype == DOMINO_F32 ? 4 : 2))
+        return fail(DOMINO_EINVAL, "%s: data is not aligned to its elements", what);
+    return DOMINO_OK;
+}
+
+static int temperature_arg(float t)
+{
+    if (!(t >= 1e-4f && t <= 1e4f))
+        return fail(DOMINO_EINVAL, "temperature %g outside [1e-4, 1e4]", static_cast<double>(t));
+    return DOMINO_OK;
+}
+
+static int top_args(const domino_logits *lg, int32_t k)
+{
+    const int rc = logits_args(lg, "logits");
+    if (rc)
+        return rc;
+    if (k < 1 || k > dhtop::MAX_K || k > lg->V)
+        return fail(DOMINO_EINVAL, "k=%d outside [1, min(%d, V=%d)]", k, dhtop::MAX_K, lg->V);
+    if (lg->V > dhtop::MAX_V)
+        return fail(DOMINO_EUNSUPPORTED, "V=%d > %d", lg->V, dhtop::MAX_V);
+    return DOMINO_OK;
+}
+
+static int beam_args(const domino_logits *lg, int32_t n_out)
+{
+    const int rc = logits_args(lg, "logits");
+    if (rc)
+        return rc;
+    if (lg->V > dhtop::MAX_V || lg->R > dhtop::MAX_W)
+        return fail(DOMINO_EUNSUPPORTED, "W=%d beams over V=%d: at most %d over %d", lg->R, lg->V, dhtop::MAX_W,
+                    dhtop::MAX_V);
+    if (n_out < 1 || n_out > dhtop::MAX_K || n_out > static_cast<long long>(lg->R) * lg->V)
+        return fail(DOMINO_EINVAL, "n_out=%d outside [1, min(%d, W V)]", n_out, dhtop::MAX_K);
+    return DOMINO_OK;
+}
+
+static int workspace_arg(const void *ws, size_t have, size_t need)
+{
+    if (!ws)
+        return fail(DOMINO_EINVAL, "workspace is NULL");
+    if (!aligned16(ws))
+        return fail(DOMINO_EINVAL, "pointers must be 16-byte aligned");
+    if (have < need)
+        return fail(DOMINO_EWORKSPACE, "workspace of %zu bytes, need %zu", have, need);
+    return DOMINO_OK;
+}
+
+int domino_top_logits_workspace_size(const domino_logits *lg, int32_t k, size_t *bytes)
+{
+    const int rc = top_args(lg, k);
+    if (rc)
+        return rc;
+    if (!bytes)
+        return fail(DOMINO_EINVAL, "bytes is NULL");
+    *bytes = lg->B ? dhtop::workspace_bytes(*lg, k) : 0;
+    return DOMINO_OK;
+}
+
+int domino_top_logits(const domino_logits *lg, int32_t k, float temperature, const int32_t *n_rows, void *workspace,
+                      size_t workspace_bytes, int32_t *ids, float *values, float *lse, void *stream)
+{
+    int rc = top_args(lg, k);
+    if (!rc)
+        rc = temperature_arg(temperature);
+    if (rc || lg->B == 0)
+        return rc;
+    if ((rc = logits_data(lg, "logits")))
+        return rc;
+    if (!ids || !values || !lse)
+        return fail(DOMINO_EINVAL, "NULL pointer");
+    if (!aligned16(ids) || !aligned16(values) || !aligned16(lse) || !aligned16(n_rows))
+        return fail(DOMINO_EINVAL, "pointers must be 16-byte aligned");
+    if ((rc = workspace_arg(workspace, workspace_bytes, dhtop::workspace_bytes(*lg, k))))
+        return rc;
+    HIP_TRY(dhtop::top(*lg, k, temperature, n_rows, workspace, ids, values, lse, static_cast<hipStream_t>(stream)),
+            "launch top_logits");
+    return DOMINO_OK;
+}
+
+int domino_beam_step_workspace_size(const domino_logits *lg, int32_t n_out, size_t *bytes)
+{
+    const int rc = beam_args(lg, n_out);
+    if (rc)
+        return rc;
+    if (!bytes)
+        return fail(DOMINO_EINVAL, "bytes is NULL");
+    *bytes = lg->B ? dhtop::workspace_bytes(*lg, std::min(n_out, lg->V)) : 0;
+    return DOMINO_OK;
+}
+
+int domino_beam_step(const domino_logits *lg, const domino_beam *bm, void *workspace, size_t workspace_bytes,
+                     void *stream)
+{
+    if (!bm)
+        return fail(DOMINO_EINVAL, "beam is NULL");
+    int rc = beam_args(lg, bm->n_out);
+    if (rc)
+        return rc;
+    if (bm->eos < -1 || bm->eos >= lg->V || (bm->finished && bm->eos < 0))
+        return fail(DOMINO_EINVAL, "eos=%d outside [0, V=%d) (-1 for none, without finished)", bm->eos, lg->V);
+    if (bm->history && (bm->T < 1 || bm->step < 0 || bm->step >= bm->T))
+        return fail(DOMINO_EINVAL, "step=%d outside [0, T=%d)", bm->step, bm->T);
+    if (bm->state && (bm->state_bytes < 4 || bm->state_bytes % 4 || bm->state_bytes > (1ll << 40)))
+        return fail(DOMINO_EINVAL, "state_bytes=%lld is not a positive multiple of 4", static_cast<long long>(bm->state_bytes));
+    if (lg->B == 0)
+        return DOMINO_OK;
+    if ((rc = logits_data(lg, "logits")))
+        return rc;
+    if (!bm->scores || !bm->out_scores || !bm->out_parent || !bm->out_token || (bm->state && !bm->out_state) ||
+        (bm->history && !bm->out_history))
+        return fail(DOMINO_EINVAL, "NULL pointer");
+    for (const void *p : {static_cast<const void *>(bm->scores), static_cast<const void *>(bm->finished), bm->state,
+                          static_cast<const void *>(bm->history), static_cast<const void *>(bm->out_scores),
+                          static_cast<const void *>(bm->out_parent), static_cast<const void *>(bm->out_token),
+                          static_cast<const void *>(bm->out_finished), static_cast<const void *>(bm->out_state),
+                          static_cast<const void *>(bm->out_history)})
+        if (!aligned16(p))
+            return fail(DOMINO_EINVAL, "pointers must be 16-byte aligned");
+    if ((rc = workspace_arg(workspace, workspace_bytes, dhtop::workspace_bytes(*lg, std::min(bm->n_out, lg->V)))))
+        return rc;
+    HIP_TRY(dhtop::beam(*lg, *bm, workspace, static_cast<hipStream_t>(stream)), "launch beam_step");
+    return DOMINO_OK;
+}
+
+static int distill_args(const domino_logits *lg, int32_t k, float temperature)
+{
+    const int rc = logits_args(lg, "logits");
+    if (rc)
+        return rc;
+    if (k < 1 || k > dhdistill::MAX_K)
+        return fail(DOMINO_EINVAL, "k=%d outside [1, %d]", k, dhdistill::MAX_K);
+    return temperature_arg(temperature);
+}
+
+// grad: the logits' own rows, or memory apart from them.
+static int grad_args(const domino_logits *lg, const domino_logits *grad)
+{
+    int rc = logits_args(grad, "grad");
+    if (rc)
+        return rc;
+    if (grad->dtype != lg->dtype || grad->B != lg->B || grad->R != lg->R || grad->V != lg->V)
+        return fail(DOMINO_EINVAL, "grad differs from the logits in type or shape");
+    // either the rows of a batch entry lie within its stride, or the batch entries of a row within the row's
+    const int64_t rows_span = (grad->R - 1) * grad->row_stride + grad->V;
+    const int64_t batch_span = (grad->B - 1) * grad->batch_stride + grad->V;
+    if ((grad->R > 1 && grad->row_stride < grad->V) || (grad->B > 1 && grad->batch_stride < grad->V) ||
+        (grad->R > 1 && grad->B > 1 && grad->batch_stride < rows_span && grad->row_stride < batch_span))
+        return fail(DOMINO_EINVAL, "grad's rows overlap");
+    if (lg->B == 0)
+        return DOMINO_OK;
+    if ((rc = logits_data(grad, "grad")))
+        return rc;
+    if (grad->data == lg->data && (grad->batch_stride != lg->batch_stride || grad->row_stride != lg->row_stride))
+        return fail(DOMINO_EINVAL, "grad in the logits' place has other strides");
+    return DOMINO_OK;
+}
+
+int domino_distill_workspace_size(const domino_logits *lg, size_t *bytes)
+{
+    const int rc = logits_args(lg, "logits");
+    if (rc)
+        return rc;
+    if (!bytes)
+        return fail(DOMINO_EINVAL, "bytes is NULL");
+    *bytes = lg->B ? dhdistill::workspace_bytes(*lg) : 0;
+    return DOMINO_OK;
+}
+
+int domino_distill(const domino_logits *lg, int32_t k, const int32_t *ids, const float *values,
+                   const float *teacher_lse, float temperature, const int32_t *n_rows, void *workspace,
+                   size_t workspace_bytes, float *loss, float *stats, const float *grad_loss,
+                   const domino_logits *grad, void *stream)
+{
+    int rc = distill_args(lg, k, temperature);
+    if (rc)
+        return rc;
+    if (!grad_loss != !grad || (grad && !stats && lg->B))
+        return fail(DOMINO_EINVAL, "grad_loss, grad and stats go together");
+    if (grad && (rc = grad_args(lg, grad)))
+        return rc;
+    if (lg->B == 0)
+        return DOMINO_OK;
+    if ((rc = logits_data(lg, "logits")))
+        return rc;
+    if (!ids || !values || !loss)
+        return fail(DOMINO_EINVAL, "NULL pointer");
+    for (const void *p : {static_cast<const void *>(ids), static_cast<const void *>(values),
+                          static_cast<const void *>(teacher_lse), static_cast<const void *>(n_rows),
+                          static_cast<const void *>(loss), static_cast<const void *>(stats),
+                          static_cast<const void *>(grad_loss)})
+        if (!aligned16(p))
+            return fail(DOMINO_EINVAL, "pointers must be 16-byte aligned");
+    if ((rc = workspace_arg(workspace, workspace_bytes, dhdistill::workspace_bytes(*lg))))
+        return rc;
+    const dhdistill::Teacher t = {k, ids, values, teacher_lse};
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    HIP_TRY(dhdistill::forward(*lg, t, temperature, n_rows, workspace, loss, stats, st), "launch distill");
+    if (grad)
+        HIP_TRY(dhdistill::backward(*lg, k, ids, stats, grad_loss, temperature, n_rows, *grad, st),
+                "launch distill_backward");
+    return DOMINO_OK;
+}
+
+int domino_distill_backward(const domino_logits *lg, int32_t k, const int32_t *ids, const float *stats,
+                            const float *grad_loss, float temperature, const int32_t *n_rows,
+                            const domino_logits *grad, void *stream)
+{
+    int rc = distill_args(lg, k, temperature);
+    if (rc || (rc = grad_args(lg, grad)) || lg->B == 0)
+        return rc;
+    if ((rc = logits_data(lg, "logits")))
+        return rc;
+    if (!ids || !stats || !grad_loss)
+        return fail(DOMINO_EINVAL, "NULL pointer");
+    if (!aligned16(ids) || !aligned16(stats) || !aligned16(grad_loss) || !aligned16(n_rows))
+        return fail(DOMINO_EINVAL, "pointers must be 16-byte aligned");
+    HIP_TRY(dhdistill::backward(*lg, k, ids, stats, grad_loss, temperature, n_rows, *grad,
+                                static_cast<hipStream_t>(stream)),
+            "launch distill_backward");
     return DOMINO_OK;
 }
 

@@ -235,6 +235,119 @@ int domino_verify_noalloc(int32_t B, int32_t K, int32_t V, const float *logits, 
                           int32_t *target, int32_t *accept, int32_t *next, void *stream);
 
 /*
+ * ---- operators over vocabulary rows: top logits, beam selection, distillation ----
+ *
+ * Rows of logits [B, R, V] (R: the K+1 rows of a verified block, the K rows of a draft, the beams of a
+ * search).  `data` is a device pointer of `dtype` (DOMINO_F32, or DOMINO_BF16 as raw 16-bit patterns) with
+ * any element alignment; strides count elements, so that a slice of a larger tensor or a padded vocabulary
+ * is passed as it is.  0 <= batch_stride, 0 <= row_stride; an output's rows may not overlap.
+ */
+typedef struct domino_logits {
+    const void *data;
+    int64_t batch_stride, row_stride;
+    int32_t B, R, V, dtype;
+} domino_logits;
+
+/*
+ * The k largest logits of every row, and the row's log-sum-exp: what a teacher leaves behind for
+ * domino_distill, and what sampling from the head of the distribution needs.
+ *   n_rows  [B] int32           NULL = all R; else rows r >= n_rows[b] are left out (not read)
+ *   workspace                   >= domino_top_logits_workspace_size bytes; scratch of this call
+ * Outputs (device):
+ *   ids     [B, R, k] int32     the k largest, largest first; ties go to the lowest id, a NaN counts as
+ *                               larger than any number, -0 equals +0; -1 in rows left out
+ *   values  [B, R, k] float32   their logits (-inf in rows left out)
+ *   lse     [B, R]    float32   log sum_v exp(z_v / temperature): -inf where every logit is -inf and in rows
+ *                               left out, +inf where one is +inf, NaN where one is NaN
+ * 0 <= B, 1 <= R, 1 <= k <= 128, k <= V <= 524288, 1e-4 <= temperature <= 1e4; B = 0 is a no-op.  The result
+ * does not depend on how a row is split over the device.  At most two launches, asynchronous on `stream`; no
+ * allocation, no synchronization.  Pointers other than logits->data 16-byte aligned; outputs may not alias
+ * inputs or the workspace.
+ */
+int domino_top_logits_workspace_size(const domino_logits *logits, int32_t k, size_t *bytes);
+int domino_top_logits(const domino_logits *logits, int32_t k, float temperature, const int32_t *n_rows,
+                      void *workspace, size_t workspace_bytes, int32_t *ids, float *values, float *lse, void *stream);
+
+/*
+ * One step of beam search.  Row w of batch entry b holds the logits of beam w (W = logits->R beams).  The
+ * candidates are all (w, v), with
+ *     score(w, v) = scores[b][w] + z_wv - log sum_u exp(z_wu),
+ * and the n_out best of them become the beams of the next step: higher scores first, equal ones by lowest
+ * w, then lowest v (a beam's own candidates are ordered by their logits).  Scores are compared in 64 bits.
+ *   - A beam whose score is -inf is dead: its candidates score -inf.  So do tokens whose logit is -inf, in a
+ *     row of nothing but -inf too.
+ *   - An ended beam (finished[b][w] != 0) has one candidate, (w, eos), with the score it has; the others
+ *     score -inf.
+ *   - A score of NaN or +inf, or a row with a NaN or +inf logit, makes a beam's candidates NaN, which counts
+ *     as larger than any number: it shows in the result, from token 0 on.
+ *   Rows of dead and ended beams are not read.  Candidates of -inf are taken, by their places, only when
+ *   nothing else is left; parent and token are valid indices then, too.
+ * Inputs (device): scores [B, W] float32; finished [B, W] bytes or NULL; state [B, W, state_bytes] or NULL
+ * (any beam state, state_bytes a positive multiple of 4); history [B, W, T] int32 or NULL.
+ * Outputs (device): out_scores [B, n_out] float32; out_parent, out_token [B, n_out] int32; out_finished
+ * [B, n_out] bytes, NULL = not stored (the parent had ended, or the token is eos); out_state [B, n_out,
+ * state_bytes]: the parent's state; out_history [B, n_out, T]: the parent's history with token at `step`.
+ * eos: the end token, or -1 for none (then finished must be NULL).
+ * Limits: 1 <= W <= 32, 1 <= n_out <= 128, n_out <= W V, V <= 524288, 0 <= step < T.  B = 0 is a no-op.  At
+ * most three launches, asynchronous on `stream`; no allocation, no synchronization.  Pointers other than
+ * logits->data 16-byte aligned; outputs may not alias inputs or the workspace.
+ */
+typedef struct domino_beam {
+    int32_t n_out, eos, T, step;
+    int64_t state_bytes;
+    const float *scores;
+    const uint8_t *finished;
+    const void *state;
+    const int32_t *history;
+    float *out_scores;
+    int32_t *out_parent, *out_token;
+    uint8_t *out_finished;
+    void *out_state;
+    int32_t *out_history;
+} domino_beam;
+
+int domino_beam_step_workspace_size(const domino_logits *logits, int32_t n_out, size_t *bytes);
+int domino_beam_step(const domino_logits *logits, const domino_beam *beam, void *workspace, size_t workspace_bytes,
+                     void *stream);
+
+/*
+ * Distillation of a student's rows from a teacher's top logits.  With y = z / temperature, q = softmax(y),
+ * the entries j of a row whose id lies in [0, V), t_j = values_j / temperature - L, p_j = exp(t_j):
+ *     L = teacher_lse where given (domino_top_logits' lse at this temperature), else log sum_j exp(values_j /
+ *         temperature): the teacher's distribution over its entries alone
+ *     rest = max(0, 1 - sum_j p_j) where teacher_lse is given (the mass of all other ids, taken as one
+ *         event), else 0;  Qr = the sum of q over the ids that no entry names
+ *     loss = temperature^2 ( sum_j p_j (t_j - log q_j) + rest log(rest / Qr) )
+ * An id outside [0, V) (-1 pads a row) is passed over; an id named twice has both masses.  A row without a
+ * valid id, one whose entries' values are all -inf (without teacher_lse), and rows r >= n_rows[b] are left
+ * out: loss 0, gradient 0; without a valid id and past n_rows they are not read.  A row of nothing but -inf has
+ * q = 0; a NaN or +inf among a row's logits makes its loss and gradient NaN.
+ *   ids        [B, R, k] int32, values [B, R, k] float32, teacher_lse [B, R] float32 or NULL
+ *   n_rows     [B] int32 or NULL (all R)
+ *   workspace  >= domino_distill_workspace_size bytes; scratch of this call
+ *   loss       [B, R] float32
+ *   stats      [B, R, 4 + k] float32: what the backward pass needs of the forward pass; NULL = not stored
+ *   grad_loss  [B, R] float32 or NULL.  Given, the call also writes the gradient grad_loss[b][r] *
+ *              dloss/dz to `grad` (then not NULL, and stats must be given)
+ *   grad       same dtype, B, R and V as the logits; its rows may be the logits' own (same data and strides:
+ *              the gradient takes their place) or lie apart from them
+ * domino_distill_backward writes the gradient from the forward pass' stats, with the same logits, ids,
+ * temperature and n_rows.  0 <= B, 1 <= R, 1 <= V, 1 <= k <= 128, 1e-4 <= temperature <= 1e4; B = 0 is a
+ * no-op.  Sums and statistics are float32 within a chunk of a row and 64 bits across; results do not change
+ * from call to call.  At most two launches for the loss and one for the gradient, asynchronous on `stream`; no
+ * allocation, no synchronization.  Pointers other than the logits' and the gradient's data 16-byte aligned;
+ * apart from what is said of grad, outputs may not alias inputs or the workspace.
+ */
+int domino_distill_workspace_size(const domino_logits *logits, size_t *bytes);
+int domino_distill(const domino_logits *logits, int32_t k, const int32_t *ids, const float *values,
+                   const float *teacher_lse, float temperature, const int32_t *n_rows, void *workspace,
+                   size_t workspace_bytes, float *loss, float *stats, const float *grad_loss,
+                   const domino_logits *grad, void *stream);
+int domino_distill_backward(const domino_logits *logits, int32_t k, const int32_t *ids, const float *stats,
+                            const float *grad_loss, float temperature, const int32_t *n_rows,
+                            const domino_logits *grad, void *stream);
+
+/*
  * Synchronizes the device (every stream, so drafts replayed from a captured
  * HIP graph on any stream are included), reads and clears the device flags
  * (DOMINO_FLAG_*) into *device_flags (may be NULL) and resets the handle's
