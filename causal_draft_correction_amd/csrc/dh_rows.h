@@ -38,8 +38,19 @@ struct Vec<float> {
     typedef float raw __attribute__((ext_vector_type(4)));
     typedef float mem __attribute__((ext_vector_type(4), aligned(4)));
     __device__ static raw fill() { return raw{NEG_INF, NEG_INF, NEG_INF, NEG_INF}; }
+    __device__ static raw from(const uint4 &q)
+    {
+        return raw{__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z), __uint_as_float(q.w)};
+    }
     __device__ static float get(const raw &x, int e) { return x[e]; }
     __device__ static void set(raw &x, int e, float f) { x[e] = f; }
+    template <typename F>
+    __device__ static void map(raw &x, F f)
+    {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            x[e] = f(x[e]);
+    }
     __device__ static float one(const float *p) { return *p; }
     __device__ static void put(float *p, float f) { *p = f; }
 };
@@ -49,6 +60,7 @@ struct Vec<bf16s> {
     typedef uint32_t raw __attribute__((ext_vector_type(4)));
     typedef uint32_t mem __attribute__((ext_vector_type(4), aligned(2)));
     __device__ static raw fill() { return raw{0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u}; }
+    __device__ static raw from(const uint4 &q) { return raw{q.x, q.y, q.z, q.w}; }
     __device__ static float get(const raw &x, int e)
     {
         return __uint_as_float((e & 1) ? (x[e >> 1] & 0xFFFF0000u) : (x[e >> 1] << 16));
@@ -61,6 +73,16 @@ struct Vec<bf16s> {
     __device__ static void set(raw &x, int e, float f)
     {
         x[e >> 1] = (e & 1) ? ((x[e >> 1] & 0xFFFFu) | (bits(f) << 16)) : ((x[e >> 1] & 0xFFFF0000u) | bits(f));
+    }
+    template <typename F>
+    __device__ static void map(raw &x, F f)
+    {
+        typedef __bf16 pair __attribute__((ext_vector_type(2)));
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const pair p = {static_cast<__bf16>(f(get(x, 2 * i))), static_cast<__bf16>(f(get(x, 2 * i + 1)))};
+            x[i] = __builtin_bit_cast(uint32_t, p);
+        }
     }
     __device__ static float one(const bf16s *p) { return __uint_as_float(static_cast<uint32_t>(p->bits) << 16); }
     __device__ static void put(bf16s *p, float f) { p->bits = static_cast<uint16_t>(bits(f)); }
@@ -104,6 +126,16 @@ __device__ inline void load_chunk(typename Vec<T>::raw (&x)[NV], const T *row, i
     }
 }
 
+// Makes the vectors' values opaque, so that bfloat16 elements are widened again where they are next used, and not
+// kept in registers as floats.
+template <typename V, int NV>
+__device__ inline void forget(V (&x)[NV])
+{
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+        asm volatile("" : "+v"(x[u]));
+}
+
 // First element of chunk c and the element after its last.
 template <typename T>
 __device__ inline int chunk_begin(int c, int cvec, int V)
@@ -112,25 +144,58 @@ __device__ inline int chunk_begin(int c, int cvec, int V)
     return v < V ? static_cast<int>(v) : V;
 }
 
-// exp(d / tau) as 2^(d log2(e) / tau), d <= 0; the factor in two parts, since its own rounding would be an error
-// common to all terms of a sum.  Both parts are above 0, so that d = -inf gives 0.  (v_exp_f32 flushes results
-// below 2^-126.)
+// exp((z - ref) / tau) as a power of 2, with s = log2(e) / tau.
+//
+// Where |ref s| < 1024 (SMALL) it is 2^(z near + c): near is s rounded to float32, c = -ref near rounded, so that an
+// element takes one fused multiply-add.  The rounding of c is the same factor in every term of a sum, and taken
+// out of it (fix); that of near weighs |log2 q| 2^-25 in a term q, below 4e-7 of a sum over any distribution.
+// Elsewhere it is 2^(d hi + d lo) with d = z - ref, hi + lo = s and both above 0, so that d = -inf gives 0.
+// (v_exp_f32 flushes results below 2^-126.)
 struct Scale {
-    float hi, lo;
+    float near, hi, lo;
 };
 inline Scale scale_of(float tau)
 {
     const double s = 1.4426950408889634074 / static_cast<double>(tau);
     Scale sc;
-    sc.hi = static_cast<float>(s);
+    sc.near = sc.hi = static_cast<float>(s);
     if (static_cast<double>(sc.hi) >= s)
         sc.hi = std::nextafterf(sc.hi, 0.f);
     sc.lo = static_cast<float>(s - static_cast<double>(sc.hi));
     return sc;
 }
-__device__ inline float exp_scaled(float d, const Scale &s)
+struct Expo {
+    float ref, c;
+    bool small;
+    __device__ Expo(float r, const Scale &s) : ref(r), c(-r * s.near), small(fabsf(r * s.near) < 1024.f) {}
+    template <bool SMALL>
+    __device__ float at(float z, const Scale &s) const
+    {
+        if constexpr (SMALL)
+            return __builtin_amdgcn_exp2f(fmaf(z, s.near, c));
+        const float d = z - ref;
+        return __builtin_amdgcn_exp2f(fmaf(d, s.hi, d * s.lo));
+    }
+    // what a sum of at() has to be multiplied by
+    __device__ double fix(const Scale &s) const
+    {
+        const double y = 0.69314718055994531 * (static_cast<double>(c) + static_cast<double>(ref) * s.near);
+        return small ? 1.0 - y + 0.5 * y * y : 1.0;
+    }
+};
+
+// Sum of the thread's exponentials.
+template <typename T, bool SMALL, int NV>
+__device__ inline float sum_exps(typename Vec<T>::raw (&x)[NV], const Expo &ex, const Scale &sc)
 {
-    return __builtin_amdgcn_exp2f(fmaf(d, s.hi, d * s.lo));
+    forget(x);
+    float s = 0.f;
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+#pragma unroll
+        for (int e = 0; e < Vec<T>::N; ++e)
+            s += ex.at<SMALL>(Vec<T>::get(x[u], e), sc);
+    return s;
 }
 
 __device__ inline float wave_max(float v)
@@ -146,12 +211,55 @@ __device__ inline float wave_max(float v)
     return fmaxf(__uint_as_float(a), __uint_as_float(b));
 }
 
+template <int CTRL>
+__device__ inline double dpp_f64(double v)
+{
+    return __builtin_bit_cast(double, dpp_u64<CTRL>(__builtin_bit_cast(uint64_t, v)));
+}
+// The values of the even and odd row of a row pair, and of the lower and upper half of the wave.
+__device__ inline void row_pair_values(double v, double &even, double &odd)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    uint32_t el, ol, eh, oh;
+    row_pair_values(static_cast<uint32_t>(u), el, ol);
+    row_pair_values(static_cast<uint32_t>(u >> 32), eh, oh);
+    even = __builtin_bit_cast(double, (static_cast<uint64_t>(eh) << 32) | el);
+    odd = __builtin_bit_cast(double, (static_cast<uint64_t>(oh) << 32) | ol);
+}
+__device__ inline void half_values(double v, double &lo, double &hi)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    uint32_t ll, hl, lh, hh;
+    half_values(static_cast<uint32_t>(u), ll, hl);
+    half_values(static_cast<uint32_t>(u >> 32), lh, hh);
+    lo = __builtin_bit_cast(double, (static_cast<uint64_t>(lh) << 32) | ll);
+    hi = __builtin_bit_cast(double, (static_cast<uint64_t>(hh) << 32) | hl);
+}
+
+// Sum over the wave, the same bits in every lane.
 __device__ inline double wave_sum_f64(double v)
 {
-#pragma unroll
-    for (int o = 32; o; o >>= 1)
-        v += __shfl_xor(v, o);
-    return v;
+    v += dpp_f64<DPP_QUAD_XOR1>(v);
+    v += dpp_f64<DPP_QUAD_XOR2>(v);
+    v += dpp_f64<DPP_HALF_MIRROR>(v);
+    v += dpp_f64<DPP_ROW_MIRROR>(v);
+    double a, b;
+    row_pair_values(v, a, b);
+    half_values(a + b, a, b);
+    return a + b;
+}
+
+// Maximum over the wave; NaN operands are passed over.
+__device__ inline double wave_max_f64(double v)
+{
+    v = fmax(v, dpp_f64<DPP_QUAD_XOR1>(v));
+    v = fmax(v, dpp_f64<DPP_QUAD_XOR2>(v));
+    v = fmax(v, dpp_f64<DPP_HALF_MIRROR>(v));
+    v = fmax(v, dpp_f64<DPP_ROW_MIRROR>(v));
+    double a, b;
+    row_pair_values(v, a, b);
+    half_values(fmax(a, b), a, b);
+    return fmax(a, b);
 }
 
 // What the chunks of a row leave of its log-sum-exp: the maximum m (NaN: the chunk holds a NaN) and
@@ -160,14 +268,21 @@ struct Part {
     float m, s;
 };
 
-// A row's maximum and its sum of exponentials from its chunks' parts, in 64 bits; every lane of the wave gets
-// them.  A NaN part makes both NaN.
-__device__ inline void join_parts(const Part *parts, int nch, double inv_tau, float &m, double &s)
+// The first part a lane has to join (loaded early, ahead of what else the caller waits for).
+__device__ inline Part first_part(const Part *parts, int nch)
 {
     const int lane = threadIdx.x & 63;
-    float mx = NEG_INF;
-    bool bad = false;
-    for (int c = lane; c < nch; c += 64) {
+    return lane < nch ? parts[lane] : Part{NEG_INF, 0.f};
+}
+
+// A row's maximum and its sum of exponentials from its chunks' parts, in 64 bits; every lane of the wave gets
+// them.  A NaN part makes both NaN.
+__device__ inline void join_parts(const Part &first, const Part *parts, int nch, double inv_tau, float &m, double &s)
+{
+    const int lane = threadIdx.x & 63;
+    float mx = fmaxf(NEG_INF, first.m);
+    bool bad = first.m != first.m;
+    for (int c = lane + 64; c < nch; c += 64) {
         const float v = parts[c].m;
         bad |= v != v;
         mx = fmaxf(mx, v);
@@ -175,7 +290,9 @@ __device__ inline void join_parts(const Part *parts, int nch, double inv_tau, fl
     m = wave_max(mx);
     bad = __ballot(bad) != 0;
     double t = 0.0;
-    for (int c = lane; c < nch; c += 64) {
+    if (first.m > NEG_INF)
+        t = static_cast<double>(first.s) * (first.m == m ? 1.0 : exp((static_cast<double>(first.m) - m) * inv_tau));
+    for (int c = lane + 64; c < nch; c += 64) {
         const Part p = parts[c];
         if (p.m > NEG_INF)
             t += static_cast<double>(p.s) * (p.m == m ? 1.0 : exp((static_cast<double>(p.m) - m) * inv_tau));

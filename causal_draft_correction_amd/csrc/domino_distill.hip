@@ -12,6 +12,12 @@
 // The forward pass reads a row once (k_distill_part, one block per chunk, values in registers) and joins the
 // chunks and the k entries in 64 bits (k_distill_final).  The backward pass reads it once and writes it once
 // (k_distill_grad).  All are bound by HBM bandwidth for many rows, by latency for few.
+#ifndef TUNE_NV
+#define TUNE_NV 8
+#endif
+#ifndef TUNE_TARGET
+#define TUNE_TARGET 1024
+#endif
 #define DH_NT 256
 #define DH_NS dhd
 #include "dh_rows.h"
@@ -20,7 +26,7 @@
 namespace DH_NS {
 
 constexpr int MAX_IDS = dhdistill::MAX_K, HEAD = dhdistill::STAT_HEAD;
-static_assert(MAX_IDS <= NT, "one thread per id");
+static_assert(MAX_IDS == 128, "one thread, or half a lane, per id");
 
 struct Teach {
     int k;
@@ -87,13 +93,8 @@ __global__ __launch_bounds__(NT) void k_distill_part(Rows rows, Teach te, int nc
 #pragma unroll
     for (int w = 1; w < NWAVE; ++w)
         m = fmaxf(m, red_m[w]);
-    const float ref = m > NEG_INF ? m : 0.f;
-    float s = 0.f;
-#pragma unroll
-    for (int u = 0; u < NV; ++u)
-#pragma unroll
-        for (int e = 0; e < VT::N; ++e)
-            s += exp_scaled(VT::get(x[u], e) - ref, sc);
+    const Expo ex(m > NEG_INF ? m : 0.f, sc);
+    float s = ex.small ? sum_exps<T, true>(x, ex, sc) : sum_exps<T, false>(x, ex, sc);
     s = wave_sum(s);
     if (lane == 0)
         red_s[wave] = s;
@@ -103,115 +104,119 @@ __global__ __launch_bounds__(NT) void k_distill_part(Rows rows, Teach te, int nc
 #pragma unroll
         for (int w = 0; w < NWAVE; ++w)
             total += static_cast<double>(red_s[w]);
+        total *= ex.fix(sc);
         // a NaN or +inf in the chunk makes the sum NaN: so the row's
         parts[static_cast<int64_t>(row) * nch + c] = Part{total != total ? __builtin_nanf("") : m, static_cast<float>(total)};
     }
 }
 
-__device__ inline double block_sum_f64(double v, double *red)
-{
-    v = wave_sum_f64(v);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0)
-        red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    double s = red[0];
-#pragma unroll
-    for (int w = 1; w < NWAVE; ++w)
-        s += red[w];
-    return s;
-}
-// (NaN operands are passed over)
-__device__ inline double block_max_f64(double v, double *red)
-{
-#pragma unroll
-    for (int o = 32; o; o >>= 1)
-        v = fmax(v, __shfl_xor(v, o));
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0)
-        red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    double s = red[0];
-#pragma unroll
-    for (int w = 1; w < NWAVE; ++w)
-        s = fmax(s, red[w]);
-    return s;
-}
-
-// One row: its loss, and what the backward pass needs of it:
+// One row, by one wave: its loss, and what the backward pass needs of it:
 //     stats = { m, A, 1 (0: a row that is left out), log-sum-exp, h_0 .. h_{k-1} }
-// so that dloss/dz_v = tau A exp((z_v - m) / tau), and tau h_j for v = id_j.
+// so that dloss/dz_v = tau A exp((z_v - m) / tau), and tau h_j for v = id_j.  A lane takes the entries lane and
+// lane + 64.  Everything is in 64 bits; differences are taken from the maxima, before their logarithms: rows at the
+// type's lowest value keep them.
 template <typename T>
-__global__ __launch_bounds__(NT) void k_distill_final(Rows rows, Teach te, int nch, double tau, const Part *parts,
-                                                      float *loss, float *stats)
+__device__ inline void finish_row(const Rows &rows, const Teach &te, int row, int nch, double tau, const Part *parts,
+                                  float *loss, float *stats, int *s_id, double *s_p)
 {
-    __shared__ double red[NWAVE];
-    __shared__ double s_rest;
-    __shared__ float m_rest;
-    __shared__ int s_id[MAX_IDS];
-    __shared__ double s_p[MAX_IDS];
     const double NINF = -__builtin_huge_val();
-    const int row = blockIdx.x, j = threadIdx.x;
+    const int lane = threadIdx.x & 63;
     const double inv_tau = 1.0 / tau;
     float *st = stats ? stats + static_cast<int64_t>(row) * (HEAD + te.k) : nullptr;
-    const bool counts = rows.counts(row / rows.R, row % rows.R);
-    int id = -1;
-    if (counts && j < te.k)
-        id = te.ids[static_cast<int64_t>(row) * te.k + j];
-    const bool valid = in_row(id, rows.V);
-    bool live = __syncthreads_or(valid);
-    // differences are taken from the maxima, before their logarithms: rows at the type's lowest value keep them
-    double t = NINF, z = NINF;
-    if (valid) {
-        t = static_cast<double>(te.values[static_cast<int64_t>(row) * te.k + j]) * inv_tau;
-        z = Vec<T>::one(row_at<T>(rows, row / rows.R, row % rows.R) + id);
+    const int64_t at = static_cast<int64_t>(row) * te.k;
+    const T *zr = row_at<T>(rows, row / rows.R, row % rows.R);
+    const Part part = first_part(parts + static_cast<int64_t>(row) * nch, nch);
+    int id[2] = {-1, -1};
+    float value[2] = {NEG_INF, NEG_INF};
+    const double L = te.lse ? te.lse[row] : 0.0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (lane + 64 * i < te.k) {
+            id[i] = te.ids[at + lane + 64 * i];
+            value[i] = te.values[at + lane + 64 * i];
+        }
+    if (!rows.counts(row / rows.R, row % rows.R))
+        id[0] = id[1] = -1;
+    double t[2] = {NINF, NINF}, z[2] = {NINF, NINF};
+    bool valid[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        valid[i] = in_row(id[i], rows.V);
+        if (valid[i]) {
+            t[i] = static_cast<double>(value[i]) * inv_tau;
+            z[i] = Vec<T>::one(zr + id[i]);
+        }
     }
+    bool live = __ballot(valid[0] || valid[1]) != 0;
     if (live) {
         if (te.lse) {
-            t -= static_cast<double>(te.lse[row]);
+            t[0] -= L, t[1] -= L;
         } else {
-            const double top = block_max_f64(t, red);
-            if (top > NINF)
-                t = (t - top) - log(block_sum_f64(valid ? exp(t - top) : 0.0, red));
-            else  // nothing but -inf (no mass: left out) or NaN
-                live = __syncthreads_or(valid && t != t), t = __builtin_nan("");
+            const double top = wave_max_f64(fmax(t[0], t[1]));
+            if (top > NINF) {
+                const double l = log(wave_sum_f64((valid[0] ? exp(t[0] - top) : 0.0) + (valid[1] ? exp(t[1] - top) : 0.0)));
+                t[0] = (t[0] - top) - l, t[1] = (t[1] - top) - l;
+            } else {  // nothing but -inf (no mass: left out) or NaN
+                live = __ballot((valid[0] && t[0] != t[0]) || (valid[1] && t[1] != t[1])) != 0;
+                t[0] = t[1] = __builtin_nan("");
+            }
         }
     }
     if (!live) {
-        if (j == 0)
+        if (lane == 0)
             loss[row] = 0.f;
         if (st)
-            for (int i = j; i < HEAD + te.k; i += NT)
+            for (int i = lane; i < HEAD + te.k; i += 64)
                 st[i] = 0.f;
         return;
     }
-    const double p = valid ? exp(t) : 0.0;
-    if (j < te.k)
-        s_id[j] = valid ? id : -1, s_p[j] = p;
-    if (j < 64) {
-        float m;
-        double s;
-        join_parts(parts + static_cast<int64_t>(row) * nch, nch, inv_tau, m, s);
-        if (j == 0)
-            m_rest = m, s_rest = s;
+    float m_rest;
+    double s_rest;
+    join_parts(part, parts + static_cast<int64_t>(row) * nch, nch, inv_tau, m_rest, s_rest);
+    // entries that name an id again: the first of them stands for it, with the mass of all
+    double p[2], named[2];
+    bool first[2] = {valid[0], valid[1]}, again = false;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        named[i] = p[i] = valid[i] ? exp(t[i]) : 0.0;
+        s_id[lane + 64 * i] = valid[i] ? id[i] : -1;
+        s_p[lane + 64 * i] = p[i];
     }
-    __syncthreads();
-    bool first = valid;     // of the entries that name this id
-    double named = 0.0;     // their mass
-    if (valid)
-        for (int i = 0; i < te.k; ++i)
-            if (s_id[i] == id) {
-                named += s_p[i];
-                first &= i >= j;
-            }
-    const double mass = block_sum_f64(p, red);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    for (int j = 0; j < te.k; j += 4) {
+        const int4 four = *reinterpret_cast<const int4 *>(s_id + j);
+        const int o[4] = {four.x, four.y, four.z, four.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                again |= valid[i] && o[e] == id[i] && j + e != lane + 64 * i;
+    }
+    if (__ballot(again)) {
+        named[0] = named[1] = 0.0;
+        for (int j = 0; j < te.k; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (valid[i] && s_id[j] == id[i]) {
+                    named[i] += s_p[j];
+                    first[i] = first[i] && j >= lane + 64 * i;
+                }
+    }
+    const double mass = wave_sum_f64(p[0] + p[1]);
     double rest = 0.0, m = m_rest, s = s_rest;
     if (te.lse) {
         rest = 1.0 - mass;
         rest = rest < 0.0 ? 0.0 : rest;
-        const double top = block_max_f64(z, red);
+        const double top = wave_max_f64(fmax(z[0], z[1]));
         m = m > top || m != m ? m : top;
-        s = block_sum_f64(first ? (z == m ? 1.0 : exp((z - m) * inv_tau)) : 0.0, red);
+        double e = 0.0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (first[i])
+                e += z[i] == m ? 1.0 : exp((z[i] - m) * inv_tau);
+        s = wave_sum_f64(e);
         if (m_rest > NEG_INF || m_rest != m_rest)
             s += s_rest * (m_rest == m ? 1.0 : exp((m_rest - m) * inv_tau));
         if (m == NINF)
@@ -219,8 +224,13 @@ __global__ __launch_bounds__(NT) void k_distill_final(Rows rows, Teach te, int n
     }
     const double total = mass + rest;
     const double log_s = log(s), lse = m == NINF ? NINF : m * inv_tau + log_s;
-    const double logq = z == NINF ? NINF : (z - m) * inv_tau - log_s;
-    double sum = block_sum_f64(p == 0.0 ? 0.0 : p * (t - logq), red);
+    double logq[2], terms = 0.0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        logq[i] = z[i] == NINF ? NINF : (z[i] - m) * inv_tau - log_s;
+        terms += p[i] == 0.0 ? 0.0 : p[i] * (t[i] - logq[i]);
+    }
+    double sum = wave_sum_f64(terms);
     double A = s > 0.0 || s != s ? total / s : 0.0;
     double ref = m;
     if (te.lse) {
@@ -233,18 +243,40 @@ __global__ __launch_bounds__(NT) void k_distill_final(Rows rows, Teach te, int n
     const bool none = !(lse < -NINF);  // a NaN or +inf among the logits: no distribution
     if (none)
         sum = A = __builtin_nan("");
-    if (j == 0)
+    if (lane == 0)
         loss[row] = static_cast<float>(tau * tau * sum);
     if (st) {
-        if (j == 0) {
+        if (lane == 0) {
             st[0] = ref > NINF || ref != ref ? static_cast<float>(ref) : 0.f;
             st[1] = static_cast<float>(A);
             st[2] = 1.f;
             st[3] = static_cast<float>(lse);
         }
-        if (j < te.k)
-            st[HEAD + j] = none ? __builtin_nanf("") : static_cast<float>(total * exp(logq) - named);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (lane + 64 * i < te.k)
+                st[HEAD + lane + 64 * i] = none ? __builtin_nanf("") : static_cast<float>(total * exp(logq[i]) - named[i]);
     }
+}
+
+template <typename T>
+__global__ __launch_bounds__(NT) void k_distill_final(Rows rows, Teach te, int n_all, int nch, double tau,
+                                                      const Part *parts, float *loss, float *stats)
+{
+    __shared__ __align__(16) int s_id[NWAVE][MAX_IDS];
+    __shared__ double s_p[NWAVE][MAX_IDS];
+    const int wave = threadIdx.x >> 6, row = blockIdx.x * NWAVE + wave;
+    if (row < n_all)
+        finish_row<T>(rows, te, row, nch, tau, parts, loss, stats, s_id[wave], s_p[wave]);
+}
+
+// Each element becomes A times its exponential.
+template <typename T, bool SMALL, int NV>
+__device__ inline void scale_exps(typename Vec<T>::raw (&x)[NV], const Expo &ex, const Scale &sc, float A)
+{
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+        Vec<T>::map(x[u], [&](float z) { return A * ex.at<SMALL>(z, sc); });
 }
 
 // dloss/dz of one chunk.  The elements that entries name are written again once the block's other stores are done.
@@ -262,12 +294,12 @@ __global__ __launch_bounds__(NT) void k_distill_grad(Rows rows, int k, int nch, 
     typename VT::raw x[NV];
     if (live) {
         load_chunk<T, NV>(x, row_at<T>(rows, b, r), rows.V, c, cvec);
-        const float g = grad_loss[row] * tau, m = st[0], A = st[1] * g;
-#pragma unroll
-        for (int u = 0; u < NV; ++u)
-#pragma unroll
-            for (int e = 0; e < VT::N; ++e)
-                VT::set(x[u], e, A * exp_scaled(VT::get(x[u], e) - m, sc));
+        const Expo ex(st[0], sc);
+        const float A = st[1] * (grad_loss[row] * tau) * static_cast<float>(ex.fix(sc));
+        if (ex.small)
+            scale_exps<T, true>(x, ex, sc, A);
+        else
+            scale_exps<T, false>(x, ex, sc, A);
     } else {
 #pragma unroll
         for (int u = 0; u < NV; ++u)
@@ -304,14 +336,15 @@ using namespace dhd;
 
 namespace {
 
-constexpr int TARGET_BLOCKS = 1024;
+constexpr int TARGET_BLOCKS = TUNE_TARGET;
+constexpr int MAX_NV = TUNE_NV;
 
 Split split_of(const domino_logits &lg)
 {
     const int64_t rows = static_cast<int64_t>(lg.B) * lg.R;
     const int per = lg.dtype == DOMINO_F32 ? 4 : 8;
     const int nvec = static_cast<int>((static_cast<int64_t>(lg.V) + per - 1) / per);
-    const int least = static_cast<int>((static_cast<int64_t>(nvec) + NT * 16 - 1) / (NT * 16));
+    const int least = static_cast<int>((static_cast<int64_t>(nvec) + NT * MAX_NV - 1) / (NT * MAX_NV));
     int64_t n = rows ? (TARGET_BLOCKS + rows - 1) / rows : 1;
     n = n < nvec / NT ? n : nvec / NT;
     n = n > least ? n : least;
@@ -381,10 +414,8 @@ void pick(const C &call)
         call.template run<T, 2>();
     else if (call.sp.nv <= 4)
         call.template run<T, 4>();
-    else if (call.sp.nv <= 8)
-        call.template run<T, 8>();
     else
-        call.template run<T, 16>();
+        call.template run<T, 8>();
 }
 
 }  // namespace
@@ -414,10 +445,12 @@ hipError_t forward(const domino_logits &lg, const Teacher &t, float tau, const i
     if (e != hipSuccess)
         return e;
     if (lg.dtype == DOMINO_F32)
-        hipLaunchKernelGGL((k_distill_final<float>), dim3(n), dim3(NT), 0, st, c.rows, c.te, c.sp.nch,
+        hipLaunchKernelGGL((k_distill_final<float>), dim3((n + NWAVE - 1) / NWAVE), dim3(NT), 0, st, c.rows, c.te,
+                           static_cast<int>(n), c.sp.nch,
                            static_cast<double>(tau), c.parts, loss, stats);
     else
-        hipLaunchKernelGGL((k_distill_final<bf16s>), dim3(n), dim3(NT), 0, st, c.rows, c.te, c.sp.nch,
+        hipLaunchKernelGGL((k_distill_final<bf16s>), dim3((n + NWAVE - 1) / NWAVE), dim3(NT), 0, st, c.rows, c.te,
+                           static_cast<int>(n), c.sp.nch,
                            static_cast<double>(tau), c.parts, loss, stats);
     return hipGetLastError();
 }

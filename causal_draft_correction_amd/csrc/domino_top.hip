@@ -4,16 +4,21 @@
 // number, -0 == +0) and lse = log sum_v exp(z_v / tau).  Both follow from one reading of the row, so the work
 // is bound by HBM bandwidth for many rows and by latency for few.
 //
-// k_top_chunk: one block takes one chunk of a row into registers.  Each thread's maximum is a candidate; the
-// ceil(k/4)-th largest of a wave's 64 maxima, the lowest of the four waves', is a bound that at least k elements
-// of the chunk reach and (on rows in no particular order) about 1.5 k to 3 k do.  It is found by 32 ballots and no
-// exchange.  The elements that reach it go to a list in LDS, and the place of each among the largest is the
-// number of greater ones.
-// k_top_merge joins the chunks' lists of a row the same way.
+// k_top_chunk: one block takes one chunk of a row into registers.  The k-th largest of its 256 threads' maxima is a
+// bound that at least k elements of the chunk reach and (on rows in no particular order) hardly more do.  It is
+// found by ballots, 16 bits deep.  The vectors that reach it go to LDS, their elements that do to a list, and the
+// place of each among the largest is the number of greater ones.
+// k_top_merge joins the chunks' lists of a row the same way; its bound is the k-th largest of the lists' heads.
 //
-// beam: W beams' candidates score s_w + z_wv - lse_w.  Within a beam they are ordered by their logits, so the
-// M best of all are among the M largest of each row; k_beam_merge ranks these by binary searches in the other
-// beams' lists and writes state and history in the new order.
+// beam: W beams' candidates score s_w + log softmax(z_w)_v.  Within a beam they are ordered by their logits, so the
+// M best of all are among the M largest of each chunk.  k_beam_merge scores these and ranks them as k_top_merge
+// does, and writes state and history in the new order.
+#ifndef TUNE_NV
+#define TUNE_NV 8
+#endif
+#ifndef TUNE_TARGET
+#define TUNE_TARGET 1024
+#endif
 #define DH_NT 256
 #define DH_NS dht
 #include "dh_rows.h"
@@ -21,12 +26,16 @@
 
 namespace DH_NS {
 
-constexpr int LIST = 2048;         // candidates of a chunk that the LDS list holds
+constexpr int VECS = 512;          // vectors of a chunk that the LDS list holds
+constexpr int LIST = 1024;         // elements of a chunk that the LDS list holds
 constexpr int MERGE_LIST = 4096;   // candidates of a row's chunks
-constexpr int MAX_TIES = 128;      // of them kept for elements equal to the bound (at least MAX_K)
+constexpr int HEADS = 4;           // heads of the chunks' lists a lane takes
+constexpr int BEAM_LIST = 512;     // candidates of a beam step that are ranked by counting
+constexpr int MAX_TIES = 128;      // places of the list kept for elements equal to the bound (at least MAX_K)
 constexpr int COUNT_MAX = 256;     // up to here places are counted, above the list is sorted
 constexpr int MAX_BEAMS = dhtop::MAX_W, MAX_OUT = dhtop::MAX_K;
 static_assert(MAX_TIES >= dhtop::MAX_K, "the ties alone may be the result");
+static_assert(LIST >= dhtop::MAX_K * 8, "a chunk of fewer vectors than k is taken whole");
 
 // Rows that are not read: past n_rows; beams that are dead (score -inf), ended, or without a usable score.
 struct Live {
@@ -53,26 +62,27 @@ __device__ inline float unord_f32(uint32_t o)
 {
     return __uint_as_float((o & 0x80000000u) ? (o ^ 0x80000000u) : ~o);
 }
+constexpr uint32_t ORD_NEG_INF = 0x007FFFFFu;  // ord_f32(-inf)
+__device__ inline uint32_t word(float f) { return __float_as_uint(f); }
+__device__ inline uint32_t word(uint32_t u) { return u; }
 __device__ inline float key_value(uint64_t key) { return unord_f32(static_cast<uint32_t>(key >> 32)); }
 
-// Largest t that at least n lanes reach (0 if fewer than n lanes hold more than 0).
-__device__ inline uint32_t wave_nth(uint32_t v, int n)
+// A bound that at least n of the wave's 64 N values reach: the n-th largest with its bits below `last` cleared
+// (0 if there are fewer than n values above 0).  All lanes get it.
+template <int N>
+__device__ inline uint32_t wave_bound(const uint32_t (&v)[N], int n, int last)
 {
     uint32_t t = 0;
-    for (int bit = 31; bit >= 0; --bit) {
+    for (int bit = 31; bit >= last; --bit) {
         const uint32_t c = t | (1u << bit);
-        if (__popcll(__ballot(v >= c)) >= n)
+        int have = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            have += __popcll(__ballot(v[i] >= c));
+        if (have >= n)
             t = c;
     }
     return t;
-}
-__device__ inline uint64_t wave_nth(uint64_t v, int n)
-{
-    const uint32_t hi = wave_nth(static_cast<uint32_t>(v >> 32), n);
-    const bool tie = static_cast<uint32_t>(v >> 32) == hi;
-    const int above = __popcll(__ballot(static_cast<uint32_t>(v >> 32) > hi));
-    const uint32_t lo = wave_nth(tie ? static_cast<uint32_t>(v) : 0u, n - above);
-    return (static_cast<uint64_t>(hi) << 32) | lo;
 }
 
 // Sorts list[0, n) in descending order (n <= LEN; list holds the next power of two).
@@ -122,25 +132,14 @@ __device__ inline void emit_largest(uint64_t *list, int n, int k, F emit)
 
 struct ChunkShared {
     uint64_t list[LIST];
+    uint4 vec[VECS];
+    int at[VECS];            // first element of each
+    uint32_t top[NT];        // the threads' maxima
     uint64_t best[NWAVE];
     float m[NWAVE], s[NWAVE];
-    uint32_t t[NWAVE];
-    int n, ties;
+    uint32_t count[NWAVE];
+    int nvec, n;
 };
-
-__device__ inline float block_max(float v, float *red)
-{
-    const int wave = threadIdx.x >> 6;
-    v = wave_max(v);
-    if ((threadIdx.x & 63) == 0)
-        red[wave] = v;
-    __syncthreads();
-    float m = red[0];
-#pragma unroll
-    for (int w = 1; w < NWAVE; ++w)
-        m = fmaxf(m, red[w]);
-    return m;
-}
 
 // The k largest of row[v0, v1) by k passes, each for the largest key below the last: any values, NaN and
 // infinities among them.  For rows with such values and for orders that overflow the list.
@@ -199,13 +198,13 @@ __device__ inline bool list_with_ties(const T *row, int v0, int v1, float t, int
         const bool tie = v < v1 && Vec<T>::one(row + v) == t;
         const uint64_t mask = __ballot(tie);
         if (lane == 0)
-            sh.t[wave] = __popcll(mask);
+            sh.count[wave] = __popcll(mask);
         __syncthreads();
         int before = have, all = have;
 #pragma unroll
         for (int w = 0; w < NWAVE; ++w) {
-            before += w < wave ? static_cast<int>(sh.t[w]) : 0;
-            all += static_cast<int>(sh.t[w]);
+            before += w < wave ? static_cast<int>(sh.count[w]) : 0;
+            all += static_cast<int>(sh.count[w]);
         }
         const int at = greater + before + __popcll(mask & ((1ull << lane) - 1));
         if (tie && at < k)
@@ -257,43 +256,48 @@ __global__ __launch_bounds__(NT) void k_top_chunk(Rows rows, Live live, int k, i
     typename VT::raw x[NV];
     load_chunk<T, NV>(x, z, rows.V, c, cvec);
     if (threadIdx.x == 0)
-        sh.n = 0;
+        sh.nvec = sh.n = 0;
 
-    float tm = NEG_INF;
+    float vm[NV], tm = NEG_INF;
 #pragma unroll
-    for (int u = 0; u < NV; ++u)
+    for (int u = 0; u < NV; ++u) {
+        vm[u] = VT::get(x[u], 0);
 #pragma unroll
-        for (int e = 0; e < VT::N; ++e)
-            tm = fmaxf(tm, VT::get(x[u], e));
-    // the bound: a lane without an element counts as below everything
+        for (int e = 1; e < VT::N; ++e)
+            vm[u] = fmaxf(vm[u], VT::get(x[u], e));
+        tm = fmaxf(tm, vm[u]);
+    }
+    // the bound: a thread without an element counts as below everything
     const bool any = v0 + static_cast<int>(threadIdx.x) * VT::N < v1;
-    const uint32_t t_wave = wave_nth(any ? ord_f32(tm) : 0u, (k + NWAVE - 1) / NWAVE);
+    sh.top[threadIdx.x] = any ? ord_f32(tm) : 0u;
+    const float wm = wave_max(tm);
     if (lane == 0)
-        sh.t[wave] = t_wave;
-    const float m = block_max(tm, sh.m);
-    uint32_t t_ord = sh.t[0];
+        sh.m[wave] = wm;
+    __syncthreads();
+    float m = sh.m[0];
 #pragma unroll
     for (int w = 1; w < NWAVE; ++w)
-        t_ord = t_ord < sh.t[w] ? t_ord : sh.t[w];
-    const float t = t_ord ? unord_f32(t_ord) : NEG_INF;
-
-    const float ref = m > NEG_INF ? m : 0.f;
-    float s = 0.f;
+        m = fmaxf(m, sh.m[w]);
+    uint32_t tops[NWAVE];
+#pragma unroll
+    for (int w = 0; w < NWAVE; ++w)
+        tops[w] = sh.top[w * 64 + lane];
+    const uint32_t t_ord = wave_bound(tops, k, 16);
+    const float t = t_ord > ORD_NEG_INF ? unord_f32(t_ord) : NEG_INF;
 #pragma unroll
     for (int u = 0; u < NV; ++u)
-#pragma unroll
-        for (int e = 0; e < VT::N; ++e) {
-            const float f = VT::get(x[u], e);
-            s += exp_scaled(f - ref, sc);
-            if (f >= t) {
-                const int v = v0 + (u * NT + static_cast<int>(threadIdx.x)) * VT::N + e;
-                if (v < v1) {
-                    const int at = atomicAdd(&sh.n, 1);
-                    if (at < LIST)
-                        sh.list[at] = argmax_key(f, static_cast<uint32_t>(v));
+        if (vm[u] >= t) {
+            const int v = v0 + (u * NT + static_cast<int>(threadIdx.x)) * VT::N;
+            if (v < v1) {
+                const int at = atomicAdd(&sh.nvec, 1);
+                if (at < VECS) {
+                    sh.vec[at] = make_uint4(word(x[u][0]), word(x[u][1]), word(x[u][2]), word(x[u][3]));
+                    sh.at[at] = v;
                 }
             }
         }
+    const Expo ex(m > NEG_INF ? m : 0.f, sc);
+    float s = ex.small ? sum_exps<T, true>(x, ex, sc) : sum_exps<T, false>(x, ex, sc);
     s = wave_sum(s);
     if (lane == 0)
         sh.s[wave] = s;
@@ -302,6 +306,7 @@ __global__ __launch_bounds__(NT) void k_top_chunk(Rows rows, Live live, int k, i
 #pragma unroll
     for (int w = 0; w < NWAVE; ++w)
         total += static_cast<double>(sh.s[w]);
+    total *= ex.fix(sc);
     const int64_t slot = static_cast<int64_t>(row) * nch + c;
     auto emit = [&](int place, uint64_t key) {
         if (direct)
@@ -310,8 +315,27 @@ __global__ __launch_bounds__(NT) void k_top_chunk(Rows rows, Live live, int k, i
             out.keys[slot * k + place] = key;
     };
 
+    const int nvec = sh.nvec;
+    for (int i = threadIdx.x; i < nvec && nvec <= VECS; i += NT) {
+        const uint4 q = sh.vec[i];
+        const typename VT::raw y = VT::from(q);
+        const int v = sh.at[i];
+#pragma unroll
+        for (int e = 0; e < VT::N; ++e) {
+            const float f = VT::get(y, e);
+            if (f >= t && v + e < v1) {
+                const int at = atomicAdd(&sh.n, 1);
+                if (at < LIST)
+                    sh.list[at] = argmax_key(f, static_cast<uint32_t>(v + e));
+            }
+        }
+    }
+    __syncthreads();
     Part part = {m, static_cast<float>(total)};
     const int n = sh.n;
+    // more reach the bound than the lists hold: the exact one, since most of them may be equal to it
+    const bool over = nvec > VECS || n > LIST;
+    const uint32_t t_exact = over ? wave_bound(tops, k, 0) : 0;
     if (total != total) {
         // NaN or +inf among the elements (+inf alone makes the maximum +inf)
         bool nan = false;
@@ -323,9 +347,9 @@ __global__ __launch_bounds__(NT) void k_top_chunk(Rows rows, Live live, int k, i
         part = nan ? Part{__builtin_nanf(""), 1.f} : Part{-NEG_INF, 1.f};
         total = 1.0;
         largest_by_rounds(z, v0, v1, k, sh, emit);
-    } else if (n <= LIST) {
+    } else if (!over) {
         emit_largest(sh.list, n, k, emit);
-    } else if (list_with_ties(z, v0, v1, t, k, sh)) {
+    } else if (list_with_ties(z, v0, v1, t_exact ? unord_f32(t_exact) : NEG_INF, k, sh)) {
         emit_largest(sh.list, sh.n, k, emit);
     } else {
         largest_by_rounds(z, v0, v1, k, sh, emit);
@@ -338,66 +362,65 @@ __global__ __launch_bounds__(NT) void k_top_chunk(Rows rows, Live live, int k, i
     }
 }
 
-// The k largest of a row from its chunks' lists, and its log-sum-exp.
 struct MergeShared {
     uint64_t list[MERGE_LIST];
-    uint64_t t[NWAVE];
     int n;
 };
 
-__device__ inline int merge_list(const uint64_t *keys, int n, int k, MergeShared &sh)
+// The candidates of nch sorted lists of k keys that reach the k-th largest of the lists' heads go to sh.list;
+// returns how many.  q heads of each list, nch q <= 64 HEADS unless q is 1 and the lists are more.
+__device__ inline int merge_list(const uint64_t *keys, int nch, int k, MergeShared &sh)
 {
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    uint64_t best = 0;
-    for (int i = threadIdx.x; i < n; i += NT)
-        best = max_u64(best, keys[i]);
-    const uint64_t t_wave = wave_nth(best, (k + NWAVE - 1) / NWAVE);
-    if (lane == 0)
-        sh.t[wave] = t_wave;
+    constexpr int PER = MERGE_LIST / NT;
+    const int lane = threadIdx.x & 63, n = nch * k;
+    uint64_t mine[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int at = i * NT + static_cast<int>(threadIdx.x);
+        mine[i] = at < n ? keys[at] : 0;
+    }
+    int q = 64 * HEADS / nch;
+    q = q < 1 ? 1 : q < k ? q : k;
+    uint32_t head[HEADS];
+#pragma unroll
+    for (int i = 0; i < HEADS; ++i) {
+        const int h = i * 64 + lane, c = h / q;
+        head[i] = c < nch ? static_cast<uint32_t>(keys[static_cast<int64_t>(c) * k + (h - c * q)] >> 32) : 0;
+    }
     if (threadIdx.x == 0)
         sh.n = 0;
     __syncthreads();
-    uint64_t t = sh.t[0];
+    const uint32_t t = wave_bound(head, k, 0);
 #pragma unroll
-    for (int w = 1; w < NWAVE; ++w)
-        t = t < sh.t[w] ? t : sh.t[w];
-    for (int i = threadIdx.x; i < n; i += NT) {
-        const uint64_t key = keys[i];
-        if (key >= t && key)
-            sh.list[atomicAdd(&sh.n, 1)] = key;
-    }
+    for (int i = 0; i < PER; ++i)
+        if (static_cast<uint32_t>(mine[i] >> 32) >= t && mine[i])
+            sh.list[atomicAdd(&sh.n, 1)] = mine[i];
     __syncthreads();
     return sh.n;
 }
 
-__global__ __launch_bounds__(NT) void k_top_merge(Rows rows, Live live, int k, int nch, double inv_tau, TopOut out,
-                                                  uint64_t *merged)
+// The k largest of a row from its chunks' lists, and its log-sum-exp.
+__global__ __launch_bounds__(NT) void k_top_merge(Rows rows, Live live, int k, int nch, double inv_tau, TopOut out)
 {
     __shared__ MergeShared sh;
     const int row = blockIdx.x;
     if (!row_live(rows, live, row)) {
-        if (out.ids) {
-            for (int i = threadIdx.x; i < k; i += NT) {
-                out.ids[static_cast<int64_t>(row) * k + i] = -1;
-                out.values[static_cast<int64_t>(row) * k + i] = NEG_INF;
-            }
-            if (threadIdx.x == 0)
-                out.lse[row] = NEG_INF;
+        for (int i = threadIdx.x; i < k; i += NT) {
+            out.ids[static_cast<int64_t>(row) * k + i] = -1;
+            out.values[static_cast<int64_t>(row) * k + i] = NEG_INF;
         }
+        if (threadIdx.x == 0)
+            out.lse[row] = NEG_INF;
         return;
     }
     const int64_t slot = static_cast<int64_t>(row) * nch;
-    const int n = merge_list(out.keys + slot * k, nch * k, k, sh);
-    emit_largest(sh.list, n, k, [&](int place, uint64_t key) {
-        if (out.ids)
-            put_result(out, row, k, place, key);
-        else
-            merged[static_cast<int64_t>(row) * k + place] = key;
-    });
-    if (out.ids && threadIdx.x < 64) {
+    const Part part = first_part(out.parts + slot, nch);
+    const int n = merge_list(out.keys + slot * k, nch, k, sh);
+    emit_largest(sh.list, n, k, [&](int place, uint64_t key) { put_result(out, row, k, place, key); });
+    if (threadIdx.x < 64) {
         float m;
         double s;
-        join_parts(out.parts + slot, nch, inv_tau, m, s);
+        join_parts(part, out.parts + slot, nch, inv_tau, m, s);
         if (threadIdx.x == 0)
             out.lse[row] = m == NEG_INF ? NEG_INF : static_cast<float>(m * inv_tau + log(s));
     }
@@ -415,7 +438,7 @@ __device__ inline uint64_t ord_f64(double d)
 struct BeamArgs {
     int W, M, V, kc, nch, eos, T, step;
     int64_t state_bytes;
-    const uint64_t *lists;   // [B * W, kc]: each live beam's largest logits, largest first
+    const uint64_t *keys;    // [B * W, nch, kc]: the largest logits of each chunk, largest first
     const Part *parts;       // [B * W, nch]
     const float *scores;
     const uint8_t *finished;
@@ -433,114 +456,239 @@ __device__ inline void copy_rows(const char *src, char *dst, int64_t bytes, int 
                                  int nparts)
 {
     const int64_t per = bytes / static_cast<int64_t>(sizeof(V)), all = per * M;
-    for (int64_t i = static_cast<int64_t>(part) * NT + threadIdx.x; i < all; i += static_cast<int64_t>(nparts) * NT) {
-        const int64_t j = i / per, e = i - j * per;
+    const int64_t stride = static_cast<int64_t>(nparts) * blockDim.x;
+    for (int64_t i = static_cast<int64_t>(part) * blockDim.x + threadIdx.x; i < all; i += stride) {
+        const int64_t j = all <= 0x7FFFFFFF ? static_cast<int>(i) / static_cast<int>(per) : i / per, e = i - j * per;
         reinterpret_cast<V *>(dst)[i] = reinterpret_cast<const V *>(src)[parent[j] * per + e];
     }
 }
 
-// One batch entry.  Its blocks (blockIdx.y) all rank the candidates and share the copying of the state; block 0
-// writes the rest.  LDS: scores' words [W kc], tokens [W kc].
-__global__ __launch_bounds__(NT) void k_beam_merge(BeamArgs a)
+// A candidate: its score's word, its beam, and its place among that beam's candidates (larger: earlier; a live
+// beam's key, or the complement of the place).
+struct Cand {
+    uint64_t score, place;
+    int w;
+};
+__device__ inline bool before(const Cand &a, const Cand &b)
 {
-    extern __shared__ uint64_t dyn[];
-    __shared__ double log_s[MAX_BEAMS];
-    __shared__ float top[MAX_BEAMS];
-    __shared__ double s_score[MAX_OUT];
-    __shared__ int s_parent[MAX_OUT], s_token[MAX_OUT];
+    return a.score > b.score || (a.score == b.score && (a.w < b.w || (a.w == b.w && a.place > b.place)));
+}
+enum { LIVE, DEAD, ENDED, BAD };
+constexpr uint64_t ORD64_NEG_INF = 0x000FFFFFFFFFFFFFull;  // ord_f64(-inf)
+
+struct BeamShared {
+    Cand list[BEAM_LIST];
+    uint32_t top[1024];
+    Cand best[16];
+    double score[MAX_BEAMS], log_s[MAX_BEAMS];
+    float max[MAX_BEAMS];
+    int kind[MAX_BEAMS];
+    double o_score[MAX_OUT];
+    int o_parent[MAX_OUT], o_token[MAX_OUT];
+    int n;
+};
+
+__device__ inline double cand_score(const BeamShared &sh, int w, uint64_t key)
+{
+    const double z = key_value(key);
+    // (z - max first: a row at the type's lowest value keeps its differences)
+    return z == static_cast<double>(NEG_INF) ? z
+                                             : sh.score[w] + ((z - static_cast<double>(sh.max[w])) - sh.log_s[w]);
+}
+
+__device__ inline void put_beam(BeamShared &sh, const BeamArgs &a, int i, const Cand &c)
+{
+    const uint64_t u = (c.score >> 63) ? (c.score ^ (1ull << 63)) : ~c.score;
+    sh.o_score[i] = c.score == ~0ull ? __builtin_nan("") : __builtin_bit_cast(double, u);
+    sh.o_parent[i] = c.w;
+    int tok = static_cast<int>(key_index(c.place));
+    if (sh.kind[c.w] == ENDED)  // the end token, then the others
+        tok = tok == 0 ? a.eos : (tok - 1 < a.eos ? tok - 1 : tok);
+    sh.o_token[i] = tok;
+}
+
+// The M best one by one: any mixture of dead, ended and live beams, NaN and -inf.
+__device__ inline void best_by_rounds(const BeamArgs &a, const uint64_t *keys, BeamShared &sh)
+{
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, nwave = blockDim.x >> 6;
+    const int per = a.nch * a.kc;  // keys of a beam
+    Cand last = {~0ull, ~0ull, -1};
+    for (int i = 0; i < a.M; ++i) {
+        Cand best = {0, 0, a.W};
+        for (int w = 0; w < a.W; ++w) {
+            const int kind = sh.kind[w], n = kind == LIVE ? per : a.kc;
+            for (int j = threadIdx.x; j < n; j += blockDim.x) {
+                Cand c;
+                c.w = w;
+                if (kind == LIVE) {
+                    c.place = keys[static_cast<int64_t>(w) * per + j];
+                    if (!c.place)
+                        continue;
+                    c.score = ord_f64(cand_score(sh, w, c.place));
+                } else {
+                    c.place = 0xFFFFFFFFu - static_cast<uint32_t>(j);
+                    c.score = kind == BAD ? ~0ull : kind == ENDED && j == 0 ? ord_f64(sh.score[w]) : ORD64_NEG_INF;
+                }
+                if (before(last, c) && before(c, best))
+                    best = c;
+            }
+        }
+#pragma unroll
+        for (int o = 32; o; o >>= 1) {
+            Cand c;
+            c.score = __shfl_xor(best.score, o);
+            c.place = __shfl_xor(best.place, o);
+            c.w = __shfl_xor(best.w, o);
+            if (before(c, best))
+                best = c;
+        }
+        if (lane == 0)
+            sh.best[wave] = best;
+        __syncthreads();
+        best = sh.best[0];
+        for (int v = 1; v < nwave; ++v)
+            if (before(sh.best[v], best))
+                best = sh.best[v];
+        __syncthreads();
+        if (threadIdx.x == 0)
+            put_beam(sh, a, i, best);
+        last = best;
+    }
+    __syncthreads();
+}
+
+// One batch entry.  Its blocks (blockIdx.y) all rank the candidates and share the copying of the state; block 0
+// writes the rest.  The bound is the M-th largest of the threads' maxima, the candidates given out by their place
+// in the chunks' lists: the threads hold the heads of the lists.  PER > 0: a thread holds its (at most PER) keys in
+// registers, loaded before anything else is known; 0: any number, read twice.
+template <int NTB, int PER>
+__global__ __launch_bounds__(NTB) void k_beam_merge(BeamArgs a)
+{
+    __shared__ BeamShared sh;
     const int b = blockIdx.x, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int n = a.W * a.kc;
-    uint64_t *score = dyn;
-    int *token = reinterpret_cast<int *>(dyn + n);
-    for (int w = wave; w < a.W; w += NWAVE) {
+    const int lists = a.W * a.nch, n_cand = lists * a.kc;
+    const uint64_t *keys = a.keys + static_cast<int64_t>(b) * n_cand;
+    // candidate i: place i / lists of list i % lists
+    auto key_at = [&](int i, int &w) {
+        const int r = i / lists, l = i - r * lists;
+        w = l / a.nch;
+        return keys[static_cast<int64_t>(l) * a.kc + r];
+    };
+    uint64_t mine[PER ? PER : 1];
+    int from[PER ? PER : 1];
+    if constexpr (PER > 0) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int i = j * NTB + static_cast<int>(threadIdx.x);
+            from[j] = 0;
+            mine[j] = i < n_cand ? key_at(i, from[j]) : 0;
+        }
+    }
+    for (int w = wave; w < a.W; w += NTB / 64) {
         const int row = b * a.W + w;
+        const Part *parts = a.parts + static_cast<int64_t>(row) * a.nch;
+        const Part part = first_part(parts, a.nch);
         const float s = a.scores[row];
-        if (s > NEG_INF && s < -NEG_INF && !(a.finished && a.finished[row])) {
+        int kind = s == NEG_INF ? DEAD : a.finished && a.finished[row] ? ENDED : s < -NEG_INF ? LIVE : BAD;
+        if (kind == LIVE) {
             float m;
             double t;
-            join_parts(a.parts + static_cast<int64_t>(row) * a.nch, a.nch, 1.0, m, t);
+            join_parts(part, parts, a.nch, 1.0, m, t);
+            if (!(m < -NEG_INF))
+                kind = BAD;
             if (lane == 0)
-                top[w] = m, log_s[w] = log(t);
+                sh.max[w] = m, sh.log_s[w] = log(t);
+        }
+        if (lane == 0)
+            sh.kind[w] = kind, sh.score[w] = s;
+    }
+    if (threadIdx.x == 0)
+        sh.n = 0;
+    __syncthreads();
+    const bool own = threadIdx.x < a.W;
+    const int kind = own ? sh.kind[threadIdx.x] : DEAD;
+    const double own_score = own ? sh.score[threadIdx.x] : 0.0;
+    const uint64_t ended = kind == ENDED ? ord_f64(own_score) : 0;
+    auto word_of = [&](uint64_t key, int w) {
+        return key && sh.kind[w] == LIVE ? ord_f64(cand_score(sh, w, key)) : 0;
+    };
+    uint64_t top = ended;
+    if constexpr (PER > 0) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            top = max_u64(top, word_of(mine[j], from[j]));
+    } else {
+        for (int i = threadIdx.x; i < n_cand; i += NTB) {
+            int w;
+            const uint64_t key = key_at(i, w);
+            top = max_u64(top, word_of(key, w));
         }
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += NT) {
-        const int w = i / a.kc, j = i - w * a.kc, row = b * a.W + w;
-        const double s = a.scores[row];
-        double val;
-        int tok = j;
-        if (s == static_cast<double>(NEG_INF)) {           // dead
-            val = static_cast<double>(NEG_INF);
-        } else if (a.finished && a.finished[row]) {        // ended: the end token, then the others
-            tok = j == 0 ? a.eos : (j - 1 < a.eos ? j - 1 : j);
-            val = j == 0 ? s : static_cast<double>(NEG_INF);
-        } else if (!(s < -static_cast<double>(NEG_INF)) || !(top[w] < -NEG_INF)) {
-            val = __builtin_nan("");                       // no distribution
-        } else {
-            const uint64_t key = a.lists[static_cast<int64_t>(row) * a.kc + j];
-            const double z = key_value(key);
-            tok = static_cast<int>(key_index(key));
-            // (z - max first: a row at the type's lowest value keeps its differences)
-            val = z == static_cast<double>(NEG_INF) ? z : s + ((z - static_cast<double>(top[w])) - log_s[w]);
+    sh.top[threadIdx.x] = static_cast<uint32_t>(top >> 32);
+    const bool odd = __syncthreads_or(kind == BAD || (kind == ENDED && own_score != own_score));
+    uint32_t tops[NTB / 64];
+#pragma unroll
+    for (int i = 0; i < NTB / 64; ++i)
+        tops[i] = sh.top[i * 64 + lane];
+    const uint32_t t = wave_bound(tops, a.M, 8);
+    auto take = [&](uint64_t score, uint64_t place, int w) {
+        if (static_cast<uint32_t>(score >> 32) >= t && score > ORD64_NEG_INF) {
+            const int at = atomicAdd(&sh.n, 1);
+            if (at < BEAM_LIST)
+                sh.list[at] = Cand{score, place, w};
         }
-        score[i] = ord_f64(val);
-        token[i] = tok;
-    }
-    __syncthreads();
-    // place of candidate (w, j): j, and the candidates of other beams that go before it (equal scores: the
-    // earlier beam's)
-    for (int i = threadIdx.x; i < n; i += NT) {
-        const int w = i / a.kc, j = i - w * a.kc;
-        if (j >= a.M)
-            continue;
-        const uint64_t key = score[i];
-        int place = j;
-        for (int o = 0; o < a.W && place < a.M; ++o) {
-            if (o == w)
-                continue;
-            int lo = 0, hi = a.kc;  // first of o's list that does not go before
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                const uint64_t other = score[o * a.kc + mid];
-                if (other > key || (other == key && o < w))
-                    lo = mid + 1;
-                else
-                    hi = mid;
-            }
-            place += lo;
-        }
-        if (place < a.M) {
-            const uint64_t u = (key >> 63) ? (key ^ (1ull << 63)) : ~key;
-            s_score[place] = key == ~0ull ? __builtin_nan("") : __builtin_bit_cast(double, u);
-            s_parent[place] = w;
-            s_token[place] = token[i];
+    };
+    if constexpr (PER > 0) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            take(word_of(mine[j], from[j]), mine[j], from[j]);
+    } else {
+        for (int i = threadIdx.x; i < n_cand; i += NTB) {
+            int w;
+            const uint64_t key = key_at(i, w);
+            take(word_of(key, w), key, w);
         }
     }
+    take(ended, 0xFFFFFFFFull, static_cast<int>(threadIdx.x));
     __syncthreads();
+    const int n = sh.n;
+    if (odd || n < a.M || n > BEAM_LIST) {
+        best_by_rounds(a, keys, sh);
+    } else {
+        for (int i = threadIdx.x; i < n; i += NTB) {
+            const Cand c = sh.list[i];
+            int place = 0;
+            for (int j = 0; j < n; ++j)
+                place += before(sh.list[j], c);
+            if (place < a.M)
+                put_beam(sh, a, place, c);
+        }
+        __syncthreads();
+    }
     if (blockIdx.y == 0) {
-        for (int j = threadIdx.x; j < a.M; j += NT) {
+        for (int j = threadIdx.x; j < a.M; j += NTB) {
             const int64_t o = static_cast<int64_t>(b) * a.M + j;
-            a.o_scores[o] = static_cast<float>(s_score[j]);
-            a.o_parent[o] = s_parent[j];
-            a.o_token[o] = s_token[j];
+            a.o_scores[o] = static_cast<float>(sh.o_score[j]);
+            a.o_parent[o] = sh.o_parent[j];
+            a.o_token[o] = sh.o_token[j];
             if (a.o_finished)
-                a.o_finished[o] = (a.finished && a.finished[b * a.W + s_parent[j]]) || s_token[j] == a.eos;
+                a.o_finished[o] = (a.finished && a.finished[b * a.W + sh.o_parent[j]]) || sh.o_token[j] == a.eos;
         }
         if (a.o_history)
-            for (int i = threadIdx.x; i < a.M * a.T; i += NT) {
-                const int j = i / a.T, t = i - j * a.T;
+            for (int64_t i = threadIdx.x; i < static_cast<int64_t>(a.M) * a.T; i += NTB) {
+                const int j = static_cast<int>(i / a.T), at = static_cast<int>(i - static_cast<int64_t>(j) * a.T);
                 a.o_history[static_cast<int64_t>(b) * a.M * a.T + i] =
-                    t == a.step ? s_token[j]
-                                : a.history[(static_cast<int64_t>(b) * a.W + s_parent[j]) * a.T + t];
+                    at == a.step ? sh.o_token[j]
+                                 : a.history[(static_cast<int64_t>(b) * a.W + sh.o_parent[j]) * a.T + at];
             }
     }
     if (a.o_state) {
-        const char *src = a.state + b * a.W * a.state_bytes;
-        char *dst = a.o_state + b * a.M * a.state_bytes;
+        const char *src = a.state + static_cast<int64_t>(b) * a.W * a.state_bytes;
+        char *dst = a.o_state + static_cast<int64_t>(b) * a.M * a.state_bytes;
         if (a.state_bytes % 16 == 0)
-            copy_rows<uint4>(src, dst, a.state_bytes, a.M, s_parent, blockIdx.y, gridDim.y);
+            copy_rows<uint4>(src, dst, a.state_bytes, a.M, sh.o_parent, blockIdx.y, gridDim.y);
         else
-            copy_rows<uint32_t>(src, dst, a.state_bytes, a.M, s_parent, blockIdx.y, gridDim.y);
+            copy_rows<uint32_t>(src, dst, a.state_bytes, a.M, sh.o_parent, blockIdx.y, gridDim.y);
     }
 }
 
@@ -552,7 +700,8 @@ using namespace dht;
 
 namespace {
 
-constexpr int TARGET_BLOCKS = 1024;
+constexpr int TARGET_BLOCKS = TUNE_TARGET;
+constexpr int MAX_NV = TUNE_NV, LAST_NV = 16;
 
 int vec_len(int dtype) { return dtype == DOMINO_F32 ? 4 : 8; }
 
@@ -560,7 +709,9 @@ Split split_of(const domino_logits &lg, int k)
 {
     const int64_t rows = static_cast<int64_t>(lg.B) * lg.R;
     const int nvec = (lg.V + vec_len(lg.dtype) - 1) / vec_len(lg.dtype);
-    const int least = (nvec + NT * 16 - 1) / (NT * 16);
+    int least = (nvec + NT * MAX_NV - 1) / (NT * MAX_NV);
+    if (least * k > MERGE_LIST)  // long rows and many logits of each: larger chunks
+        least = (nvec + NT * LAST_NV - 1) / (NT * LAST_NV);
     int64_t n = rows ? (TARGET_BLOCKS + rows - 1) / rows : 1;
     n = n < nvec / NT ? n : nvec / NT;
     n = n < MERGE_LIST / k ? n : MERGE_LIST / k;
@@ -599,7 +750,7 @@ void pick_chunk(const Rows &rows, const Live &live, int k, const Split &sp, floa
 }
 
 struct Scratch {
-    uint64_t *keys, *merged;
+    uint64_t *keys;
     Part *parts;
     size_t bytes;
 };
@@ -610,9 +761,7 @@ Scratch scratch_of(const domino_logits &lg, int k, const Split &sp, void *ws)
     char *p = static_cast<char *>(ws);
     Scratch s;
     s.keys = reinterpret_cast<uint64_t *>(p);
-    size_t at = round16(slots * k * sizeof(uint64_t));
-    s.merged = reinterpret_cast<uint64_t *>(p + at);
-    at += sp.nch > 1 ? round16(rows * k * sizeof(uint64_t)) : 0;
+    const size_t at = round16(slots * k * sizeof(uint64_t));
     s.parts = reinterpret_cast<Part *>(p + at);
     s.bytes = at + round16(slots * sizeof(Part));
     return s;
@@ -630,21 +779,18 @@ Rows rows_of(const domino_logits &lg, const int32_t *n_rows)
     return r;
 }
 
-hipError_t select(const domino_logits &lg, const Rows &rows, const Live &live, int k, float tau, const Split &sp,
-                  const TopOut &out, uint64_t *merged, hipStream_t st)
+void chunks(const domino_logits &lg, const Rows &rows, const Live &live, int k, float tau, const Split &sp,
+            const TopOut &out, hipStream_t st)
 {
     const unsigned n = static_cast<unsigned>(lg.B) * static_cast<unsigned>(lg.R);
     if (lg.dtype == DOMINO_F32)
         pick_chunk<float>(rows, live, k, sp, tau, out, n * sp.nch, st);
     else
         pick_chunk<bf16s>(rows, live, k, sp, tau, out, n * sp.nch, st);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || sp.nch == 1)
-        return e;
-    hipLaunchKernelGGL(k_top_merge, dim3(n), dim3(NT), 0, st, rows, live, k, sp.nch, 1.0 / static_cast<double>(tau),
-                       out, merged);
-    return hipGetLastError();
 }
+
+static_assert((dhtop::MAX_V / 4 + NT * LAST_NV - 1) / (NT * LAST_NV) * dhtop::MAX_K <= MERGE_LIST,
+              "the candidates of the longest row fit one block's list");
 
 }  // namespace
 
@@ -659,7 +805,15 @@ hipError_t top(const domino_logits &lg, int k, float tau, const int32_t *n_rows,
     const Split sp = split_of(lg, k);
     const Scratch s = scratch_of(lg, k, sp, ws);
     const TopOut out = {s.keys, s.parts, ids, values, lse};
-    return select(lg, rows_of(lg, n_rows), Live{nullptr, nullptr}, k, tau, sp, out, nullptr, st);
+    const Rows rows = rows_of(lg, n_rows);
+    const Live live = {nullptr, nullptr};
+    chunks(lg, rows, live, k, tau, sp, out, st);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || sp.nch == 1)
+        return e;
+    hipLaunchKernelGGL(k_top_merge, dim3(static_cast<unsigned>(lg.B) * static_cast<unsigned>(lg.R)), dim3(NT), 0, st,
+                       rows, live, k, sp.nch, 1.0 / static_cast<double>(tau), out);
+    return hipGetLastError();
 }
 
 hipError_t beam(const domino_logits &lg, const domino_beam &bm, void *ws, hipStream_t st)
@@ -668,14 +822,14 @@ hipError_t beam(const domino_logits &lg, const domino_beam &bm, void *ws, hipStr
     const Split sp = split_of(lg, kc);
     const Scratch s = scratch_of(lg, kc, sp, ws);
     const TopOut out = {s.keys, s.parts, nullptr, nullptr, nullptr};
-    const hipError_t e =
-        select(lg, rows_of(lg, nullptr), Live{bm.scores, bm.finished}, kc, 1.f, sp, out, s.merged, st);
+    chunks(lg, rows_of(lg, nullptr), Live{bm.scores, bm.finished}, kc, 1.f, sp, out, st);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
     BeamArgs a;
     a.W = lg.R, a.M = bm.n_out, a.V = lg.V, a.kc = kc, a.nch = sp.nch, a.eos = bm.eos, a.T = bm.T, a.step = bm.step;
     a.state_bytes = bm.state ? bm.state_bytes : 0;
-    a.lists = sp.nch > 1 ? s.merged : s.keys;
+    a.keys = s.keys;
     a.parts = s.parts;
     a.scores = bm.scores;
     a.finished = bm.finished;
@@ -690,8 +844,14 @@ hipError_t beam(const domino_logits &lg, const domino_beam &bm, void *ws, hipStr
     // a block of its own for every 16 KiB of state, at most 64 a batch entry
     int64_t parts = a.o_state ? (a.M * a.state_bytes + 16383) / 16384 : 1;
     parts = parts < 1 ? 1 : parts > 64 ? 64 : parts;
-    const size_t lds = static_cast<size_t>(lg.R) * kc * (sizeof(uint64_t) + sizeof(int));
-    hipLaunchKernelGGL(k_beam_merge, dim3(lg.B, static_cast<unsigned>(parts)), dim3(NT), lds, st, a);
+    const dim3 grid(lg.B, static_cast<unsigned>(parts));
+    const int64_t n_cand = static_cast<int64_t>(a.W) * sp.nch * kc;
+    if (n_cand <= 256 * 4)
+        hipLaunchKernelGGL((k_beam_merge<256, 4>), grid, dim3(256), 0, st, a);
+    else if (n_cand <= 256 * 16)
+        hipLaunchKernelGGL((k_beam_merge<256, 16>), grid, dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL((k_beam_merge<1024, 0>), grid, dim3(1024), 0, st, a);
     return hipGetLastError();
 }
 

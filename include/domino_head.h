@@ -289,7 +289,7 @@ int domino_top_logits(const domino_logits *logits, int32_t k, float temperature,
  * state_bytes]: the parent's state; out_history [B, n_out, T]: the parent's history with token at `step`.
  * eos: the end token, or -1 for none (then finished must be NULL).
  * Limits: 1 <= W <= 32, 1 <= n_out <= 128, n_out <= W V, V <= 524288, 0 <= step < T.  B = 0 is a no-op.  At
- * most three launches, asynchronous on `stream`; no allocation, no synchronization.  Pointers other than
+ * most two launches, asynchronous on `stream`; no allocation, no synchronization.  Pointers other than
  * logits->data 16-byte aligned; outputs may not alias inputs or the workspace.
  */
 typedef struct domino_beam {
