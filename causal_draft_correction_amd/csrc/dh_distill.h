@@ -12,7 +12,8 @@ namespace dhdistill {
 constexpr int MAX_K = 128;  // teacher logits of a row
 constexpr int STAT_HEAD = 4;  // floats of a row's statistics before those of its k ids
 
-size_t workspace_bytes(const domino_logits &lg);
+// Bytes of scratch: the chunks' parts, and the rows' statistics where the caller does not keep them.
+size_t workspace_bytes(const domino_logits &lg, int k);
 
 struct Teacher {
     int k;
@@ -24,6 +25,8 @@ struct Teacher {
 // Arguments were checked by the caller.
 hipError_t forward(const domino_logits &lg, const Teacher &t, float tau, const int32_t *n_rows, void *ws, float *loss,
                    float *stats, hipStream_t st);
+hipError_t both(const domino_logits &lg, const Teacher &t, float tau, const int32_t *n_rows, void *ws, float *loss,
+                const float *grad_loss, const domino_logits &grad, hipStream_t st);
 hipError_t backward(const domino_logits &lg, int k, const int32_t *ids, const float *stats, const float *grad_loss,
                     float tau, const int32_t *n_rows, const domino_logits &grad, hipStream_t st);
 

@@ -94,34 +94,59 @@ __device__ inline const T *row_at(const Rows &rows, int b, int r)
     return static_cast<const T *>(rows.data) + b * rows.bs + r * rows.rs;
 }
 
-// The thread's vectors of chunk c; places past the chunk or the row hold -inf.
-template <typename T, int NV>
+// The thread's vectors of chunk c (vectors c * cvec on) for blocks of NTB threads; places past the chunk or the
+// row hold -inf.  KEEP: the row is read again soon, so it may stay in the caches.
+template <typename T, int NV, int NTB = NT, bool KEEP = false>
 __device__ inline void load_chunk(typename Vec<T>::raw (&x)[NV], const T *row, int V, int c, int cvec)
 {
     typedef Vec<T> VT;
     const int first = c * cvec;                                // the chunk's first vector
     const int full = V / VT::N;                                // whole vectors of the row
     const int n = full - first < cvec ? full - first : cvec;   // whole vectors of this chunk
+    const T *start = row + static_cast<int64_t>(first) * VT::N;
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
-        const int i = u * NT + static_cast<int>(threadIdx.x);
+        const int i = u * NTB + static_cast<int>(threadIdx.x);
         x[u] = VT::fill();
-        if (i < n)
-            x[u] = __builtin_nontemporal_load(
-                reinterpret_cast<const typename VT::mem *>(row + static_cast<int64_t>(first + i) * VT::N));
+        if (i < n) {
+            // (the chunk's start is the same in every thread, the rest 32 bits)
+            const auto *p = reinterpret_cast<const typename VT::mem *>(start + static_cast<uint32_t>(i) * VT::N);
+            x[u] = KEEP ? *p : __builtin_nontemporal_load(p);
+        }
     }
     const int tail = V - full * VT::N;
     if (tail && n >= 0 && n < cvec) {  // the row's last elements, element by element
         typename VT::raw t = VT::fill();
-        if (n % NT == static_cast<int>(threadIdx.x)) {
+        if (n % NTB == static_cast<int>(threadIdx.x)) {
 #pragma unroll
             for (int e = 0; e < VT::N; ++e)
                 if (e < tail)
                     VT::set(t, e, VT::one(row + static_cast<int64_t>(full) * VT::N + e));
 #pragma unroll
             for (int u = 0; u < NV; ++u)
-                if (u * NT + static_cast<int>(threadIdx.x) == n)
+                if (u * NTB + static_cast<int>(threadIdx.x) == n)
                     x[u] = t;
+        }
+    }
+}
+
+// Stores the thread's vectors of chunk c = elements [v0, v1).
+template <typename T, int NV, int NTB = NT>
+__device__ inline void store_chunk(const typename Vec<T>::raw (&x)[NV], T *row, int v0, int v1)
+{
+    typedef Vec<T> VT;
+    T *start = row + v0;
+    const int n = v1 - v0;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        const int i = (u * NTB + static_cast<int>(threadIdx.x)) * VT::N;
+        if (i + VT::N <= n) {
+            __builtin_nontemporal_store(x[u], reinterpret_cast<typename VT::mem *>(start + static_cast<uint32_t>(i)));
+        } else if (i < n) {
+#pragma unroll
+            for (int e = 0; e < VT::N; ++e)
+                if (i + e < n)
+                    VT::put(start + i + e, VT::get(x[u], e));
         }
     }
 }
@@ -184,17 +209,18 @@ struct Expo {
     }
 };
 
-// Sum of the thread's exponentials.
+// Sum of the thread's exponentials over its first `used` vectors (the same number in every thread).
 template <typename T, bool SMALL, int NV>
-__device__ inline float sum_exps(typename Vec<T>::raw (&x)[NV], const Expo &ex, const Scale &sc)
+__device__ inline float sum_exps(typename Vec<T>::raw (&x)[NV], const Expo &ex, const Scale &sc, int used = NV)
 {
     forget(x);
     float s = 0.f;
 #pragma unroll
     for (int u = 0; u < NV; ++u)
+        if (u < used)
 #pragma unroll
-        for (int e = 0; e < Vec<T>::N; ++e)
-            s += ex.at<SMALL>(Vec<T>::get(x[u], e), sc);
+            for (int e = 0; e < Vec<T>::N; ++e)
+                s += ex.at<SMALL>(Vec<T>::get(x[u], e), sc);
     return s;
 }
 

@@ -18,6 +18,9 @@
 #ifndef TUNE_TARGET
 #define TUNE_TARGET 1024
 #endif
+#ifndef TUNE_GRADNV
+#define TUNE_GRADNV 4
+#endif
 #define DH_NT 256
 #define DH_NS dhd
 #include "dh_rows.h"
@@ -26,7 +29,7 @@
 namespace DH_NS {
 
 constexpr int MAX_IDS = dhdistill::MAX_K, HEAD = dhdistill::STAT_HEAD;
-static_assert(MAX_IDS == 128, "one thread, or half a lane, per id");
+static_assert(MAX_IDS == 128 && MAX_IDS <= NT, "one thread, or half a lane, per id");
 
 struct Teach {
     int k;
@@ -36,55 +39,54 @@ struct Teach {
 
 __device__ inline bool in_row(int id, int V) { return id >= 0 && id < V; }
 
-// The chunk's maximum and sum of exponentials; with TAIL over the elements that no entry names.
-template <typename T, int NV, bool TAIL>
-__global__ __launch_bounds__(NT) void k_distill_part(Rows rows, Teach te, int nch, int cvec, Scale sc, Part *parts)
+// One bit for each element of a chunk that an entry names, in the words of the thread that holds it.
+template <typename T, int NV>
+constexpr int MASK_WORDS = (NV * Vec<T>::N + 31) / 32;
+
+template <int WORDS>
+__device__ inline void clear_mask(uint32_t (&mask)[WORDS][NT])
+{
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i)
+        mask[i][threadIdx.x] = 0;
+}
+
+// Named elements of the chunk [v0, v1) become -inf.  `id`: the thread's entry, or -1.  The mask was cleared before
+// the block's last barrier.
+template <typename T, int NV, int WORDS>
+__device__ inline void drop_named(typename Vec<T>::raw (&x)[NV], uint32_t (&mask)[WORDS][NT], int id, int v0, int v1)
 {
     typedef Vec<T> VT;
-    constexpr int BITS = NV * VT::N, WORDS = (BITS + 31) / 32;
-    __shared__ uint32_t mask[WORDS][NT];
-    __shared__ float red_m[NWAVE], red_s[NWAVE];
-    const int row = blockIdx.x / nch, c = blockIdx.x % nch, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    if (!rows.counts(row / rows.R, row % rows.R))
-        return;
-    int id = -1;
-    if (static_cast<int>(threadIdx.x) < te.k)
-        id = te.ids[static_cast<int64_t>(row) * te.k + threadIdx.x];
-    if constexpr (TAIL) {
-#pragma unroll
-        for (int i = 0; i < WORDS; ++i)
-            mask[i][threadIdx.x] = 0;
+    if (id >= v0 && id < v1) {
+        const int o = id - v0, i = o / VT::N, bit = i / NT * VT::N + o % VT::N;
+        atomicOr(&mask[bit >> 5][i % NT], 1u << (bit & 31));
     }
-    if (!__syncthreads_or(in_row(id, rows.V)))
-        return;
-    typename VT::raw x[NV];
-    load_chunk<T, NV>(x, row_at<T>(rows, row / rows.R, row % rows.R), rows.V, c, cvec);
-    if constexpr (TAIL) {
-        const int v0 = chunk_begin<T>(c, cvec, rows.V), v1 = chunk_begin<T>(c + 1, cvec, rows.V);
-        if (id >= v0 && id < v1) {
-            const int o = id - v0, i = o / VT::N, bit = i / NT * VT::N + o % VT::N;
-            atomicOr(&mask[bit >> 5][i % NT], 1u << (bit & 31));
-        }
-        __syncthreads();
-        uint32_t mine[WORDS], any = 0;
+    __syncthreads();
+    uint32_t mine[WORDS], any = 0;
 #pragma unroll
-        for (int i = 0; i < WORDS; ++i)
-            any |= mine[i] = mask[i][threadIdx.x];
-        if (any) {
+    for (int i = 0; i < WORDS; ++i)
+        any |= mine[i] = mask[i][threadIdx.x];
+    if (any) {
 #pragma unroll
-            for (int u = 0; u < NV; ++u)
+        for (int u = 0; u < NV; ++u)
 #pragma unroll
-                for (int e = 0; e < VT::N; ++e)
-                    if ((mine[(u * VT::N + e) >> 5] >> ((u * VT::N + e) & 31)) & 1u)
-                        VT::set(x[u], e, NEG_INF);
-        }
+            for (int e = 0; e < VT::N; ++e)
+                if ((mine[(u * VT::N + e) >> 5] >> ((u * VT::N + e) & 31)) & 1u)
+                    VT::set(x[u], e, NEG_INF);
     }
+}
+
+// The block's maximum and sum of exponentials (a NaN or +inf makes both NaN: so the row's), in every thread.
+template <typename T, int NV>
+__device__ inline Part chunk_part(typename Vec<T>::raw (&x)[NV], const Scale &sc, float *red_m, float *red_s)
+{
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     float m = NEG_INF;
 #pragma unroll
     for (int u = 0; u < NV; ++u)
 #pragma unroll
-        for (int e = 0; e < VT::N; ++e)
-            m = fmaxf(m, VT::get(x[u], e));
+        for (int e = 0; e < Vec<T>::N; ++e)
+            m = fmaxf(m, Vec<T>::get(x[u], e));
     m = wave_max(m);
     if (lane == 0)
         red_m[wave] = m;
@@ -99,33 +101,54 @@ __global__ __launch_bounds__(NT) void k_distill_part(Rows rows, Teach te, int nc
     if (lane == 0)
         red_s[wave] = s;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        double total = 0.0;
+    double total = 0.0;
 #pragma unroll
-        for (int w = 0; w < NWAVE; ++w)
-            total += static_cast<double>(red_s[w]);
-        total *= ex.fix(sc);
-        // a NaN or +inf in the chunk makes the sum NaN: so the row's
-        parts[static_cast<int64_t>(row) * nch + c] = Part{total != total ? __builtin_nanf("") : m, static_cast<float>(total)};
-    }
+    for (int w = 0; w < NWAVE; ++w)
+        total += static_cast<double>(red_s[w]);
+    total *= ex.fix(sc);
+    return Part{total != total ? __builtin_nanf("") : m, static_cast<float>(total)};
 }
 
-// One row, by one wave: its loss, and what the backward pass needs of it:
+// The chunk's part; with TAIL over the elements that no entry names.
+template <typename T, int NV, bool TAIL>
+__global__ __launch_bounds__(NT) void k_distill_part(Rows rows, Teach te, int nch, int cvec, Scale sc, Part *parts)
+{
+    __shared__ uint32_t mask[TAIL ? MASK_WORDS<T, NV> : 1][NT];
+    __shared__ float red_m[NWAVE], red_s[NWAVE];
+    const int row = blockIdx.x / nch, c = blockIdx.x % nch;
+    if (!rows.counts(row / rows.R, row % rows.R))
+        return;
+    int id = -1;
+    if (static_cast<int>(threadIdx.x) < te.k)
+        id = te.ids[static_cast<int64_t>(row) * te.k + threadIdx.x];
+    if constexpr (TAIL)
+        clear_mask(mask);
+    if (!__syncthreads_or(in_row(id, rows.V)))
+        return;
+    typename Vec<T>::raw x[NV];
+    load_chunk<T, NV>(x, row_at<T>(rows, row / rows.R, row % rows.R), rows.V, c, cvec);
+    if constexpr (TAIL)
+        drop_named<T, NV>(x, mask, id, chunk_begin<T>(c, cvec, rows.V), chunk_begin<T>(c + 1, cvec, rows.V));
+    const Part part = chunk_part<T, NV>(x, sc, red_m, red_s);
+    if (threadIdx.x == 0)
+        parts[static_cast<int64_t>(row) * nch + c] = part;
+}
+
+// One row, by one wave, from the parts of its nch chunks: its loss, and what the backward pass needs of it:
 //     stats = { m, A, 1 (0: a row that is left out), log-sum-exp, h_0 .. h_{k-1} }
 // so that dloss/dz_v = tau A exp((z_v - m) / tau), and tau h_j for v = id_j.  A lane takes the entries lane and
 // lane + 64.  Everything is in 64 bits; differences are taken from the maxima, before their logarithms: rows at the
 // type's lowest value keep them.
 template <typename T>
 __device__ inline void finish_row(const Rows &rows, const Teach &te, int row, int nch, double tau, const Part *parts,
-                                  float *loss, float *stats, int *s_id, double *s_p)
+                                  float *loss, float *st, int *s_id, double *s_p)
 {
     const double NINF = -__builtin_huge_val();
     const int lane = threadIdx.x & 63;
     const double inv_tau = 1.0 / tau;
-    float *st = stats ? stats + static_cast<int64_t>(row) * (HEAD + te.k) : nullptr;
     const int64_t at = static_cast<int64_t>(row) * te.k;
     const T *zr = row_at<T>(rows, row / rows.R, row % rows.R);
-    const Part part = first_part(parts + static_cast<int64_t>(row) * nch, nch);
+    const Part part = first_part(parts, nch);
     int id[2] = {-1, -1};
     float value[2] = {NEG_INF, NEG_INF};
     const double L = te.lse ? te.lse[row] : 0.0;
@@ -146,20 +169,17 @@ __device__ inline void finish_row(const Rows &rows, const Teach &te, int row, in
             t[i] = static_cast<double>(value[i]) * inv_tau;
             z[i] = Vec<T>::one(zr + id[i]);
         }
+        s_id[lane + 64 * i] = valid[i] ? id[i] : -1;
     }
+    // the entries' masses are p / p_sum; t becomes log of p where their sum is not needed for it
     bool live = __ballot(valid[0] || valid[1]) != 0;
-    if (live) {
-        if (te.lse) {
-            t[0] -= L, t[1] -= L;
-        } else {
-            const double top = wave_max_f64(fmax(t[0], t[1]));
-            if (top > NINF) {
-                const double l = log(wave_sum_f64((valid[0] ? exp(t[0] - top) : 0.0) + (valid[1] ? exp(t[1] - top) : 0.0)));
-                t[0] = (t[0] - top) - l, t[1] = (t[1] - top) - l;
-            } else {  // nothing but -inf (no mass: left out) or NaN
-                live = __ballot((valid[0] && t[0] != t[0]) || (valid[1] && t[1] != t[1])) != 0;
-                t[0] = t[1] = __builtin_nan("");
-            }
+    double p[2] = {0.0, 0.0};
+    double t_top = L;
+    if (live && !te.lse) {
+        t_top = wave_max_f64(fmax(t[0], t[1]));
+        if (!(t_top > NINF)) {  // nothing but -inf (no mass: left out) or NaN
+            live = __ballot((valid[0] && t[0] != t[0]) || (valid[1] && t[1] != t[1])) != 0;
+            t_top = __builtin_nan("");
         }
     }
     if (!live) {
@@ -170,21 +190,29 @@ __device__ inline void finish_row(const Rows &rows, const Teach &te, int row, in
                 st[i] = 0.f;
         return;
     }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (valid[i]) {
+            t[i] -= t_top;
+            p[i] = exp(t[i]);
+        }
+    const double p_sum = wave_sum_f64(p[0] + p[1]);
     float m_rest;
     double s_rest;
-    join_parts(part, parts + static_cast<int64_t>(row) * nch, nch, inv_tau, m_rest, s_rest);
-    // entries that name an id again: the first of them stands for it, with the mass of all
-    double p[2], named[2];
-    bool first[2] = {valid[0], valid[1]}, again = false;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        named[i] = p[i] = valid[i] ? exp(t[i]) : 0.0;
-        s_id[lane + 64 * i] = valid[i] ? id[i] : -1;
-        s_p[lane + 64 * i] = p[i];
+    join_parts(part, parts, nch, inv_tau, m_rest, s_rest);
+    double mass = p_sum, log_p = 0.0;
+    if (!te.lse) {
+        p[0] /= p_sum, p[1] /= p_sum;
+        mass = wave_sum_f64(p[0] + p[1]);
     }
+    // entries that name an id again: the first of them stands for it, with the mass of all
+    double named[2] = {p[0], p[1]};
+    bool first[2] = {valid[0], valid[1]}, again = false;
+    s_p[lane] = p[0], s_p[lane + 64] = p[1];
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll 4
     for (int j = 0; j < te.k; j += 4) {
         const int4 four = *reinterpret_cast<const int4 *>(s_id + j);
         const int o[4] = {four.x, four.y, four.z, four.w};
@@ -204,40 +232,41 @@ __device__ inline void finish_row(const Rows &rows, const Teach &te, int row, in
                     first[i] = first[i] && j >= lane + 64 * i;
                 }
     }
-    const double mass = wave_sum_f64(p[0] + p[1]);
-    double rest = 0.0, m = m_rest, s = s_rest;
+    double rest = 0.0, m = m_rest, s = s_rest, of_rest = s_rest;
     if (te.lse) {
         rest = 1.0 - mass;
         rest = rest < 0.0 ? 0.0 : rest;
         const double top = wave_max_f64(fmax(z[0], z[1]));
         m = m > top || m != m ? m : top;
-        double e = 0.0;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (first[i])
-                e += z[i] == m ? 1.0 : exp((z[i] - m) * inv_tau);
-        s = wave_sum_f64(e);
-        if (m_rest > NEG_INF || m_rest != m_rest)
-            s += s_rest * (m_rest == m ? 1.0 : exp((m_rest - m) * inv_tau));
-        if (m == NINF)
-            s = 0.0;
+        of_rest = m_rest == NEG_INF ? 0.0 : m_rest == m ? s_rest : s_rest * exp((m_rest - m) * inv_tau);
     }
+    double q[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        q[i] = !valid[i] || m == NINF ? 0.0 : z[i] == m ? 1.0 : exp((z[i] - m) * inv_tau);
+    if (te.lse)
+        s = wave_sum_f64((first[0] ? q[0] : 0.0) + (first[1] ? q[1] : 0.0)) + of_rest;
+    // four logarithms, one in each of the first lanes
+    const double logs = log(lane == 0 ? s : lane == 1 ? s_rest : lane == 2 ? rest : p_sum);
+    const double log_s = __shfl(logs, 0), log_s_rest = __shfl(logs, 1), log_r = __shfl(logs, 2);
+    if (!te.lse)
+        log_p = __shfl(logs, 3);
     const double total = mass + rest;
-    const double log_s = log(s), lse = m == NINF ? NINF : m * inv_tau + log_s;
-    double logq[2], terms = 0.0;
+    const double lse = m == NINF ? NINF : m * inv_tau + log_s;
+    double terms = 0.0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        logq[i] = z[i] == NINF ? NINF : (z[i] - m) * inv_tau - log_s;
-        terms += p[i] == 0.0 ? 0.0 : p[i] * (t[i] - logq[i]);
+        const double logq = z[i] == NINF ? NINF : (z[i] - m) * inv_tau - log_s;
+        terms += p[i] == 0.0 ? 0.0 : p[i] * ((t[i] - log_p) - logq);
     }
     double sum = wave_sum_f64(terms);
-    double A = s > 0.0 || s != s ? total / s : 0.0;
+    const double inv_s = s > 0.0 || s != s ? 1.0 / s : 0.0;
+    double A = total * inv_s;
     double ref = m;
     if (te.lse) {
-        const double log_rest = m_rest == NEG_INF ? NINF : (m_rest - m) * inv_tau + log(s_rest) - log_s;
         if (rest > 0.0)
-            sum += rest * (log(rest) - log_rest);
-        A = m_rest == NEG_INF ? 0.0 : (total * exp(log_rest) - rest) / s_rest;
+            sum += rest * (log_r - (m_rest == NEG_INF ? NINF : (m_rest - m) * inv_tau + log_s_rest - log_s));
+        A = m_rest == NEG_INF ? 0.0 : (total * of_rest * inv_s - rest) / s_rest;
         ref = m_rest;
     }
     const bool none = !(lse < -NINF);  // a NaN or +inf among the logits: no distribution
@@ -255,7 +284,7 @@ __device__ inline void finish_row(const Rows &rows, const Teach &te, int row, in
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             if (lane + 64 * i < te.k)
-                st[HEAD + lane + 64 * i] = none ? __builtin_nanf("") : static_cast<float>(total * exp(logq[i]) - named[i]);
+                st[HEAD + lane + 64 * i] = none ? __builtin_nanf("") : static_cast<float>(total * q[i] * inv_s - named[i]);
     }
 }
 
@@ -267,16 +296,31 @@ __global__ __launch_bounds__(NT) void k_distill_final(Rows rows, Teach te, int n
     __shared__ double s_p[NWAVE][MAX_IDS];
     const int wave = threadIdx.x >> 6, row = blockIdx.x * NWAVE + wave;
     if (row < n_all)
-        finish_row<T>(rows, te, row, nch, tau, parts, loss, stats, s_id[wave], s_p[wave]);
+        finish_row<T>(rows, te, row, nch, tau, parts + static_cast<int64_t>(row) * nch, loss,
+                      stats ? stats + static_cast<int64_t>(row) * (HEAD + te.k) : nullptr, s_id[wave], s_p[wave]);
 }
 
-// Each element becomes A times its exponential.
-template <typename T, bool SMALL, int NV>
-__device__ inline void scale_exps(typename Vec<T>::raw (&x)[NV], const Expo &ex, const Scale &sc, float A)
+// The chunk's elements become A exp((z - m) / tau), or 0 in rows left out.
+template <typename T, int NV>
+__device__ inline void chunk_grad(typename Vec<T>::raw (&x)[NV], bool live, float m, float A, const Scale &sc)
 {
+    if (!live) {
 #pragma unroll
-    for (int u = 0; u < NV; ++u)
-        Vec<T>::map(x[u], [&](float z) { return A * ex.at<SMALL>(z, sc); });
+        for (int u = 0; u < NV; ++u)
+            x[u] = typename Vec<T>::raw{0, 0, 0, 0};
+        return;
+    }
+    const Expo ex(m, sc);
+    const float a = A * static_cast<float>(ex.fix(sc));
+    if (ex.small) {
+#pragma unroll
+        for (int u = 0; u < NV; ++u)
+            Vec<T>::map(x[u], [&](float z) { return a * ex.at<true>(z, sc); });
+    } else {
+#pragma unroll
+        for (int u = 0; u < NV; ++u)
+            Vec<T>::map(x[u], [&](float z) { return a * ex.at<false>(z, sc); });
+    }
 }
 
 // dloss/dz of one chunk.  The elements that entries name are written again once the block's other stores are done.
@@ -285,38 +329,18 @@ __global__ __launch_bounds__(NT) void k_distill_grad(Rows rows, int k, int nch, 
                                                      const float *stats, const float *grad_loss, float tau, Scale sc,
                                                      Rows grad)
 {
-    typedef Vec<T> VT;
     const int row = blockIdx.x / nch, c = blockIdx.x % nch, b = row / rows.R, r = row % rows.R;
     T *out = const_cast<T *>(row_at<T>(grad, b, r));
     const float *st = stats + static_cast<int64_t>(row) * (HEAD + k);
-    const bool live = rows.counts(b, r) && st[2] != 0.f;
+    const bool counts = rows.counts(b, r);
     const int v0 = chunk_begin<T>(c, cvec, rows.V), v1 = chunk_begin<T>(c + 1, cvec, rows.V);
-    typename VT::raw x[NV];
-    if (live) {
+    typename Vec<T>::raw x[NV];
+    if (counts)
         load_chunk<T, NV>(x, row_at<T>(rows, b, r), rows.V, c, cvec);
-        const Expo ex(st[0], sc);
-        const float A = st[1] * (grad_loss[row] * tau) * static_cast<float>(ex.fix(sc));
-        if (ex.small)
-            scale_exps<T, true>(x, ex, sc, A);
-        else
-            scale_exps<T, false>(x, ex, sc, A);
-    } else {
-#pragma unroll
-        for (int u = 0; u < NV; ++u)
-            x[u] = typename VT::raw{0, 0, 0, 0};
-    }
-#pragma unroll
-    for (int u = 0; u < NV; ++u) {
-        const int v = v0 + (u * NT + static_cast<int>(threadIdx.x)) * VT::N;
-        if (v + VT::N <= v1) {
-            __builtin_nontemporal_store(x[u], reinterpret_cast<typename VT::mem *>(out + v));
-        } else if (v < v1) {
-#pragma unroll
-            for (int e = 0; e < VT::N; ++e)
-                if (v + e < v1)
-                    VT::put(out + v + e, VT::get(x[u], e));
-        }
-    }
+    const bool live = counts && st[2] != 0.f;
+    const float g = grad_loss[row] * tau;
+    chunk_grad<T, NV>(x, live, st[0], st[1] * g, sc);
+    store_chunk<T, NV>(x, out, v0, v1);
     if (!live)
         return;
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the block's stores are done
@@ -324,7 +348,66 @@ __global__ __launch_bounds__(NT) void k_distill_grad(Rows rows, int k, int nch, 
     if (static_cast<int>(threadIdx.x) < k) {
         const int id = ids[static_cast<int64_t>(row) * k + threadIdx.x];
         if (id >= v0 && id < v1)
-            VT::put(out + id, st[HEAD + threadIdx.x] * (grad_loss[row] * tau));
+            Vec<T>::put(out + id, st[HEAD + threadIdx.x] * g);
+    }
+}
+
+// A row of at most NV vectors a thread, by one block: loss, and with GRAD its gradient (else the statistics for a
+// later backward pass).  The row stays in registers from its maximum to its gradient.
+template <typename T, int NV, bool TAIL, bool GRAD>
+__global__ __launch_bounds__(NT) void k_distill_row(Rows rows, Teach te, double tau, Scale sc, float *loss,
+                                                    float *stats, const float *grad_loss, Rows grad)
+{
+    typedef Vec<T> VT;
+    __shared__ float red_m[NWAVE], red_s[NWAVE];
+    __shared__ Part part;
+    __shared__ uint32_t mask[TAIL ? MASK_WORDS<T, NV> : 1][NT];
+    __shared__ __align__(16) int s_id[MAX_IDS];
+    __shared__ double s_p[MAX_IDS];
+    __shared__ float s_stat[HEAD + MAX_IDS];
+    const int row = blockIdx.x, b = row / rows.R, r = row % rows.R, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    int id = -1;
+    if (static_cast<int>(threadIdx.x) < te.k && rows.counts(b, r))
+        id = te.ids[static_cast<int64_t>(row) * te.k + threadIdx.x];
+    if constexpr (TAIL)
+        clear_mask(mask);
+    typename VT::raw x[NV];
+    const bool any = __syncthreads_or(in_row(id, rows.V));
+    if (any) {
+        load_chunk<T, NV>(x, row_at<T>(rows, b, r), rows.V, 0, NV * NT);
+        if constexpr (TAIL)
+            drop_named<T, NV>(x, mask, id, 0, rows.V);  // (their gradients are written last)
+        const Part got = chunk_part<T, NV>(x, sc, red_m, red_s);
+        if (threadIdx.x == 0)
+            part = got;
+    }
+    __syncthreads();
+    if (wave == 0) {
+        if (any) {
+            finish_row<T>(rows, te, row, 1, tau, &part, loss, s_stat, s_id, s_p);
+        } else {
+            for (int i = lane; i < HEAD + te.k; i += 64)
+                s_stat[i] = 0.f;
+            if (lane == 0)
+                loss[row] = 0.f;
+        }
+    }
+    __syncthreads();
+    if constexpr (GRAD) {
+        T *out = const_cast<T *>(row_at<T>(grad, b, r));
+        const float g = grad_loss[row] * static_cast<float>(tau);
+        const bool live = s_stat[2] != 0.f;
+        chunk_grad<T, NV>(x, live, s_stat[0], s_stat[1] * g, sc);
+        store_chunk<T, NV>(x, out, 0, rows.V);
+        if (live) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the block's stores are done
+            __syncthreads();
+            if (in_row(id, rows.V))
+                VT::put(out + id, s_stat[HEAD + threadIdx.x] * g);
+        }
+    } else if (stats) {
+        for (int i = threadIdx.x; i < HEAD + te.k; i += NT)
+            stats[static_cast<int64_t>(row) * (HEAD + te.k) + i] = s_stat[i];
     }
 }
 
@@ -337,23 +420,27 @@ using namespace dhd;
 namespace {
 
 constexpr int TARGET_BLOCKS = TUNE_TARGET;
-constexpr int MAX_NV = TUNE_NV;
+constexpr int PART_NV = TUNE_NV;        // vectors a thread takes at most: forward
+constexpr int GRAD_NV = TUNE_GRADNV;    // backward
 
-Split split_of(const domino_logits &lg)
+int vectors(const domino_logits &lg)
+{
+    const int per = lg.dtype == DOMINO_F32 ? 4 : 8;
+    return static_cast<int>((static_cast<int64_t>(lg.V) + per - 1) / per);
+}
+
+Split split_of(const domino_logits &lg, int max_nv)
 {
     const int64_t rows = static_cast<int64_t>(lg.B) * lg.R;
-    const int per = lg.dtype == DOMINO_F32 ? 4 : 8;
-    const int nvec = static_cast<int>((static_cast<int64_t>(lg.V) + per - 1) / per);
-    const int least = static_cast<int>((static_cast<int64_t>(nvec) + NT * MAX_NV - 1) / (NT * MAX_NV));
+    const int nvec = vectors(lg);
+    const int least = static_cast<int>((static_cast<int64_t>(nvec) + NT * max_nv - 1) / (NT * max_nv));
     int64_t n = rows ? (TARGET_BLOCKS + rows - 1) / rows : 1;
     n = n < nvec / NT ? n : nvec / NT;
     n = n > least ? n : least;
     Split sp;
     sp.cvec = static_cast<int>((nvec + n - 1) / n);
     sp.nch = (nvec + sp.cvec - 1) / sp.cvec;
-    sp.nv = 1;
-    while (sp.nv * NT < sp.cvec)
-        sp.nv *= 2;
+    sp.nv = (sp.cvec + NT - 1) / NT;
     return sp;
 }
 
@@ -402,8 +489,39 @@ struct GradCall {
     template <typename T, int NV>
     void run() const
     {
+        if constexpr (NV <= GRAD_NV)
         hipLaunchKernelGGL((k_distill_grad<T, NV>), dim3(grid), dim3(NT), 0, st, rows, k, sp.nch, sp.cvec, ids, stats,
                            grad_loss, tau, sc, grad);
+    }
+};
+
+struct RowCall {
+    Rows rows, grad;
+    Teach te;
+    Split sp;
+    float tau;
+    Scale sc;
+    float *loss, *stats;
+    const float *grad_loss;
+    unsigned n;
+    hipStream_t st;
+    template <typename T, int NV, bool TAIL>
+    void launch() const
+    {
+        if (grad_loss)
+            hipLaunchKernelGGL((k_distill_row<T, NV, TAIL, true>), dim3(n), dim3(NT), 0, st, rows, te,
+                               static_cast<double>(tau), sc, loss, stats, grad_loss, grad);
+        else
+            hipLaunchKernelGGL((k_distill_row<T, NV, TAIL, false>), dim3(n), dim3(NT), 0, st, rows, te,
+                               static_cast<double>(tau), sc, loss, stats, grad_loss, grad);
+    }
+    template <typename T, int NV>
+    void run() const
+    {
+        if (te.lse)
+            launch<T, NV, true>();
+        else
+            launch<T, NV, false>();
     }
 };
 
@@ -420,18 +538,58 @@ void pick(const C &call)
 
 }  // namespace
 
-size_t workspace_bytes(const domino_logits &lg)
+namespace {
+
+size_t parts_bytes(const domino_logits &lg)
 {
-    return static_cast<size_t>(lg.B) * lg.R * split_of(lg).nch * sizeof(Part);
+    return (static_cast<size_t>(lg.B) * lg.R * split_of(lg, PART_NV).nch * sizeof(Part) + 15) & ~static_cast<size_t>(15);
 }
+
+}  // namespace
+
+size_t workspace_bytes(const domino_logits &lg, int k)
+{
+    return parts_bytes(lg) + static_cast<size_t>(lg.B) * lg.R * (HEAD + k) * sizeof(float);
+}
+
+namespace {
+
+// Loss, and gradient or statistics, in one launch.  False: the rows are too long for it.
+bool by_rows(const domino_logits &lg, const Teacher &t, float tau, const int32_t *n_rows, float *loss, float *stats,
+             const float *grad_loss, const domino_logits *grad, hipStream_t st)
+{
+    RowCall c;
+    c.sp = Split{1, vectors(lg), (vectors(lg) + NT - 1) / NT};
+    if (c.sp.nv > PART_NV)
+        return false;
+    c.rows = rows_of(lg, n_rows);
+    c.grad = grad ? rows_of(*grad, nullptr) : Rows{};
+    c.te = Teach{t.k, t.ids, t.values, t.lse};
+    c.tau = tau;
+    c.sc = scale_of(tau);
+    c.loss = loss;
+    c.stats = stats;
+    c.grad_loss = grad_loss;
+    c.n = static_cast<unsigned>(lg.B) * static_cast<unsigned>(lg.R);
+    c.st = st;
+    if (lg.dtype == DOMINO_F32)
+        pick<float>(c);
+    else
+        pick<bf16s>(c);
+    return true;
+}
+
+}  // namespace
 
 hipError_t forward(const domino_logits &lg, const Teacher &t, float tau, const int32_t *n_rows, void *ws, float *loss,
                    float *stats, hipStream_t st)
 {
+    if (by_rows(lg, t, tau, n_rows, loss, stats, nullptr, nullptr, st))
+        return hipGetLastError();
     PartCall c;
     c.rows = rows_of(lg, n_rows);
     c.te = Teach{t.k, t.ids, t.values, t.lse};
-    c.sp = split_of(lg);
+    c.sp = split_of(lg, PART_NV);
     c.sc = scale_of(tau);
     c.parts = static_cast<Part *>(ws);
     const unsigned n = static_cast<unsigned>(lg.B) * static_cast<unsigned>(lg.R);
@@ -466,7 +624,7 @@ hipError_t backward(const domino_logits &lg, int k, const int32_t *ids, const fl
     c.stats = stats;
     c.grad_loss = grad_loss;
     c.tau = tau;
-    c.sp = split_of(lg);
+    c.sp = split_of(lg, GRAD_NV);
     c.sc = scale_of(tau);
     c.grid = static_cast<unsigned>(lg.B) * static_cast<unsigned>(lg.R) * c.sp.nch;
     c.st = st;
@@ -475,6 +633,16 @@ hipError_t backward(const domino_logits &lg, int k, const int32_t *ids, const fl
     else
         pick<bf16s>(c);
     return hipGetLastError();
+}
+
+hipError_t both(const domino_logits &lg, const Teacher &t, float tau, const int32_t *n_rows, void *ws, float *loss,
+                const float *grad_loss, const domino_logits &grad, hipStream_t st)
+{
+    if (by_rows(lg, t, tau, n_rows, loss, nullptr, grad_loss, &grad, st))
+        return hipGetLastError();
+    float *stats = reinterpret_cast<float *>(static_cast<char *>(ws) + parts_bytes(lg));
+    const hipError_t e = forward(lg, t, tau, n_rows, ws, loss, stats, st);
+    return e == hipSuccess ? backward(lg, t.k, t.ids, stats, grad_loss, tau, n_rows, grad, st) : e;
 }
 
 }  // namespace dhdistill

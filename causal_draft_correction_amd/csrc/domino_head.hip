@@ -1346,14 +1346,14 @@ static int grad_args(const domino_logits *lg, const domino_logits *grad)
     return DOMINO_OK;
 }
 
-int domino_distill_workspace_size(const domino_logits *lg, size_t *bytes)
+int domino_distill_workspace_size(const domino_logits *lg, int32_t k, size_t *bytes)
 {
-    const int rc = logits_args(lg, "logits");
+    const int rc = distill_args(lg, k, 1.f);
     if (rc)
         return rc;
     if (!bytes)
         return fail(DOMINO_EINVAL, "bytes is NULL");
-    *bytes = lg->B ? dhdistill::workspace_bytes(*lg) : 0;
+    *bytes = lg->B ? dhdistill::workspace_bytes(*lg, k) : 0;
     return DOMINO_OK;
 }
 
@@ -1365,8 +1365,8 @@ int domino_distill(const domino_logits *lg, int32_t k, const int32_t *ids, const
     int rc = distill_args(lg, k, temperature);
     if (rc)
         return rc;
-    if (!grad_loss != !grad || (grad && !stats && lg->B))
-        return fail(DOMINO_EINVAL, "grad_loss, grad and stats go together");
+    if (!grad_loss != !grad || (grad && stats))
+        return fail(DOMINO_EINVAL, "grad_loss and grad go together, without stats");
     if (grad && (rc = grad_args(lg, grad)))
         return rc;
     if (lg->B == 0)
@@ -1381,14 +1381,14 @@ int domino_distill(const domino_logits *lg, int32_t k, const int32_t *ids, const
                           static_cast<const void *>(grad_loss)})
         if (!aligned16(p))
             return fail(DOMINO_EINVAL, "pointers must be 16-byte aligned");
-    if ((rc = workspace_arg(workspace, workspace_bytes, dhdistill::workspace_bytes(*lg))))
+    if ((rc = workspace_arg(workspace, workspace_bytes, dhdistill::workspace_bytes(*lg, k))))
         return rc;
     const dhdistill::Teacher t = {k, ids, values, teacher_lse};
     hipStream_t st = static_cast<hipStream_t>(stream);
-    HIP_TRY(dhdistill::forward(*lg, t, temperature, n_rows, workspace, loss, stats, st), "launch distill");
     if (grad)
-        HIP_TRY(dhdistill::backward(*lg, k, ids, stats, grad_loss, temperature, n_rows, *grad, st),
-                "launch distill_backward");
+        HIP_TRY(dhdistill::both(*lg, t, temperature, n_rows, workspace, loss, grad_loss, *grad, st), "launch distill");
+    else
+        HIP_TRY(dhdistill::forward(*lg, t, temperature, n_rows, workspace, loss, stats, st), "launch distill");
     return DOMINO_OK;
 }
 

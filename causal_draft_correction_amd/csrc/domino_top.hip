@@ -120,7 +120,7 @@ __device__ inline void emit_largest(uint64_t *list, int n, int k, F emit)
     if (t < n) {
         const uint64_t key = list[t];
         int place = 0;
-#pragma unroll 4
+#pragma unroll 8
         for (int j = 0; j < n; ++j)
             place += list[j] > key;
         if (place < k)
@@ -390,7 +390,7 @@ __device__ inline int merge_list(const uint64_t *keys, int nch, int k, MergeShar
     if (threadIdx.x == 0)
         sh.n = 0;
     __syncthreads();
-    const uint32_t t = wave_bound(head, k, 0);
+    const uint32_t t = wave_bound(head, k, 12);
 #pragma unroll
     for (int i = 0; i < PER; ++i)
         if (static_cast<uint32_t>(mine[i] >> 32) >= t && mine[i])
@@ -416,14 +416,14 @@ __global__ __launch_bounds__(NT) void k_top_merge(Rows rows, Live live, int k, i
     const int64_t slot = static_cast<int64_t>(row) * nch;
     const Part part = first_part(out.parts + slot, nch);
     const int n = merge_list(out.keys + slot * k, nch, k, sh);
-    emit_largest(sh.list, n, k, [&](int place, uint64_t key) { put_result(out, row, k, place, key); });
-    if (threadIdx.x < 64) {
+    if (threadIdx.x >= NT - 64) {  // the wave with the least to rank
         float m;
         double s;
         join_parts(part, out.parts + slot, nch, inv_tau, m, s);
-        if (threadIdx.x == 0)
+        if (threadIdx.x == NT - 1)
             out.lse[row] = m == NEG_INF ? NEG_INF : static_cast<float>(m * inv_tau + log(s));
     }
+    emit_largest(sh.list, n, k, [&](int place, uint64_t key) { put_result(out, row, k, place, key); });
 }
 
 // Unsigned words in the order of doubles: NaN above +inf, -0 as +0.
@@ -451,15 +451,28 @@ struct BeamArgs {
     int32_t *o_history;
 };
 
+// Part `part` of nparts of the M rows of `bytes` bytes each, row j from src's row parent[j]; four loads in flight.
 template <typename V>
 __device__ inline void copy_rows(const char *src, char *dst, int64_t bytes, int M, const int *parent, int part,
                                  int nparts)
 {
     const int64_t per = bytes / static_cast<int64_t>(sizeof(V)), all = per * M;
     const int64_t stride = static_cast<int64_t>(nparts) * blockDim.x;
-    for (int64_t i = static_cast<int64_t>(part) * blockDim.x + threadIdx.x; i < all; i += stride) {
-        const int64_t j = all <= 0x7FFFFFFF ? static_cast<int>(i) / static_cast<int>(per) : i / per, e = i - j * per;
-        reinterpret_cast<V *>(dst)[i] = reinterpret_cast<const V *>(src)[parent[j] * per + e];
+    const bool narrow = all + 4 * stride <= 0x7FFFFFFF;
+    for (int64_t i0 = static_cast<int64_t>(part) * blockDim.x + threadIdx.x; i0 < all; i0 += 4 * stride) {
+        V v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t i = i0 + u * stride;
+            if (i < all) {
+                const int64_t j = narrow ? static_cast<uint32_t>(i) / static_cast<uint32_t>(per) : i / per;
+                v[u] = reinterpret_cast<const V *>(src)[parent[j] * per + (i - j * per)];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (i0 + u * stride < all)
+                reinterpret_cast<V *>(dst)[i0 + u * stride] = v[u];
     }
 }
 
@@ -589,7 +602,8 @@ __global__ __launch_bounds__(NTB) void k_beam_merge(BeamArgs a)
         const Part *parts = a.parts + static_cast<int64_t>(row) * a.nch;
         const Part part = first_part(parts, a.nch);
         const float s = a.scores[row];
-        int kind = s == NEG_INF ? DEAD : a.finished && a.finished[row] ? ENDED : s < -NEG_INF ? LIVE : BAD;
+        const bool ended = a.finished && a.finished[row];
+        int kind = s == NEG_INF ? DEAD : ended ? ENDED : s < -NEG_INF ? LIVE : BAD;
         if (kind == LIVE) {
             float m;
             double t;
@@ -616,7 +630,8 @@ __global__ __launch_bounds__(NTB) void k_beam_merge(BeamArgs a)
     if constexpr (PER > 0) {
 #pragma unroll
         for (int j = 0; j < PER; ++j)
-            top = max_u64(top, word_of(mine[j], from[j]));
+            if (j * NTB < n_cand)
+                top = max_u64(top, word_of(mine[j], from[j]));
     } else {
         for (int i = threadIdx.x; i < n_cand; i += NTB) {
             int w;
@@ -641,7 +656,8 @@ __global__ __launch_bounds__(NTB) void k_beam_merge(BeamArgs a)
     if constexpr (PER > 0) {
 #pragma unroll
         for (int j = 0; j < PER; ++j)
-            take(word_of(mine[j], from[j]), mine[j], from[j]);
+            if (j * NTB < n_cand)
+                take(word_of(mine[j], from[j]), mine[j], from[j]);
     } else {
         for (int i = threadIdx.x; i < n_cand; i += NTB) {
             int w;
@@ -846,10 +862,10 @@ hipError_t beam(const domino_logits &lg, const domino_beam &bm, void *ws, hipStr
     parts = parts < 1 ? 1 : parts > 64 ? 64 : parts;
     const dim3 grid(lg.B, static_cast<unsigned>(parts));
     const int64_t n_cand = static_cast<int64_t>(a.W) * sp.nch * kc;
-    if (n_cand <= 256 * 4)
-        hipLaunchKernelGGL((k_beam_merge<256, 4>), grid, dim3(256), 0, st, a);
-    else if (n_cand <= 256 * 16)
-        hipLaunchKernelGGL((k_beam_merge<256, 16>), grid, dim3(256), 0, st, a);
+    if (n_cand <= 512 * 2)
+        hipLaunchKernelGGL((k_beam_merge<512, 2>), grid, dim3(512), 0, st, a);
+    else if (n_cand <= 512 * 8)
+        hipLaunchKernelGGL((k_beam_merge<512, 8>), grid, dim3(512), 0, st, a);
     else
         hipLaunchKernelGGL((k_beam_merge<1024, 0>), grid, dim3(1024), 0, st, a);
     return hipGetLastError();

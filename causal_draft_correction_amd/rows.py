@@ -8,11 +8,12 @@ special cases are those of include/domino_head.h.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 import torch
 
-from .binding import DOMINO_BF16, DOMINO_F32, _check, _ptr, _stream_handle, load_library
+from .binding import DOMINO_BF16, DOMINO_F32, _check, load_library
 
 STAT_HEAD = 4  # floats of a row's statistics before those of its ids
 _DTYPES = {torch.float32: DOMINO_F32, torch.bfloat16: DOMINO_BF16}
@@ -44,7 +45,7 @@ def _lib():
         lib.domino_top_logits.argtypes = [LG, I32, F32, P, P, SZ, P, P, P, P]
         lib.domino_beam_step_workspace_size.argtypes = [LG, I32, ctypes.POINTER(SZ)]
         lib.domino_beam_step.argtypes = [LG, ctypes.POINTER(Beam), P, SZ, P]
-        lib.domino_distill_workspace_size.argtypes = [LG, ctypes.POINTER(SZ)]
+        lib.domino_distill_workspace_size.argtypes = [LG, I32, ctypes.POINTER(SZ)]
         lib.domino_distill.argtypes = [LG, I32, P, P, P, F32, P, P, SZ, P, P, P, LG, P]
         lib.domino_distill_backward.argtypes = [LG, I32, P, P, P, F32, P, LG, P]
         _declared = lib
@@ -52,52 +53,64 @@ def _lib():
 
 
 def _logits(name: str, t) -> Logits:
-    if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES or t.dim() not in (2, 3) or not t.is_cuda or \
-            (t.stride(-1) != 1 and t.shape[-1] != 1):
+    dtype = _DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    shape = t.shape if dtype is not None else ()
+    if len(shape) not in (2, 3) or not t.is_cuda or (t.stride(-1) != 1 and shape[-1] != 1):
         raise ValueError("%s: expected a CUDA float32 or bfloat16 tensor [B, R, V] or [N, V] whose last dimension is "
                          "contiguous, got %s" % (name, _said(t)))
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch.cuda.current_device():
         raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, torch.cuda.current_device()))
-    if t.dim() == 2:
-        return Logits(t.data_ptr(), t.stride(0), t.shape[1], t.shape[0], 1, t.shape[1], _DTYPES[t.dtype])
-    return Logits(t.data_ptr(), t.stride(0), t.stride(1), t.shape[0], t.shape[1], t.shape[2], _DTYPES[t.dtype])
+    if len(shape) == 2:
+        return Logits(t.data_ptr(), t.stride(0), shape[1], shape[0], 1, shape[1], dtype)
+    return Logits(t.data_ptr(), t.stride(0), t.stride(1), shape[0], shape[1], shape[2], dtype)
 
 
 def _said(t) -> str:
     return "%s %s on %s" % (t.dtype, tuple(t.shape), t.device) if isinstance(t, torch.Tensor) else type(t).__name__
 
 
-def _need(name: str, t, shape, dtype, device):
+def _need(name: str, t, shape, dtype, device) -> int:
+    """The tensor's address, if it is a contiguous one of this shape and type."""
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or t.device != device or \
             not t.is_contiguous():
         raise ValueError("%s: expected a contiguous %s tensor on %s of shape %s, got %s" %
                          (name, dtype, device, tuple(shape), _said(t)))
+    return t.data_ptr()
 
 
-def _outputs(out: Optional[dict], wanted: dict, device) -> dict:
-    """The output tensors by name: those of `out`, checked, and new ones for the rest."""
+def _maybe(name: str, t, shape, dtype, device):
+    return None if t is None else _need(name, t, shape, dtype, device)
+
+
+def _output(out: dict, name: str, shape, dtype, device) -> int:
+    """The address of output `name`: the caller's tensor, checked, or a new one."""
+    t = out.get(name)
+    if t is None:
+        t = out[name] = torch.empty(shape, dtype=dtype, device=device)
+        return t.data_ptr()
+    return _need("out[%r]" % name, t, shape, dtype, device)
+
+
+def _known(out: Optional[dict], names) -> dict:
     out = {} if out is None else dict(out)
     for name in out:
-        if name not in wanted:
-            raise ValueError("out: unknown entry %r (expected %s)" % (name, ", ".join(wanted)))
-    for name, (shape, dtype) in wanted.items():
-        t = out.get(name)
-        if t is None:
-            out[name] = torch.empty(shape, dtype=dtype, device=device)
-        else:
-            _need("out[%r]" % name, t, shape, dtype, device)
+        if name not in names:
+            raise ValueError("out: unknown entry %r (expected %s)" % (name, ", ".join(names)))
     return out
 
 
-def _workspace(given: Optional[torch.Tensor], size_fn, *args) -> torch.Tensor:
-    n = ctypes.c_size_t()
-    _check(size_fn(*args, ctypes.byref(n)))
+def _scratch(given: Optional[torch.Tensor], need: int, device) -> torch.Tensor:
     if given is None:
-        return torch.empty(max(n.value, 16), dtype=torch.uint8, device="cuda")
-    if not isinstance(given, torch.Tensor) or given.dtype != torch.uint8 or not given.is_cuda or \
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if not isinstance(given, torch.Tensor) or given.dtype != torch.uint8 or given.device != device or \
             not given.is_contiguous():
-        raise ValueError("workspace: expected a contiguous CUDA uint8 tensor, got %s" % _said(given))
+        raise ValueError("workspace: expected a contiguous uint8 tensor on %s, got %s" % (device, _said(given)))
     return given
+
+
+def _stream(logits: torch.Tensor) -> int:
+    """The current stream's handle (torch.cuda.current_stream() builds a Stream object around it each time)."""
+    return torch._C._cuda_getCurrentRawStream(logits.get_device())
 
 
 def _size_of(fn, lg: Logits, *args) -> int:
@@ -112,19 +125,22 @@ def _shape_only(B: int, R: int, V: int, dtype: torch.dtype) -> Logits:
     return Logits(None, 0, 0, B, R, V, _DTYPES[dtype])
 
 
+@functools.lru_cache(maxsize=1024)
 def top_logits_workspace_size(B: int, R: int, V: int, k: int, dtype: torch.dtype = torch.float32) -> int:
     """Bytes of device workspace `top_logits` needs (host only)."""
     return _size_of(_lib().domino_top_logits_workspace_size, _shape_only(B, R, V, dtype), k)
 
 
+@functools.lru_cache(maxsize=1024)
 def beam_step_workspace_size(B: int, W: int, V: int, n_out: int, dtype: torch.dtype = torch.float32) -> int:
     """Bytes of device workspace `beam_step` needs (host only)."""
     return _size_of(_lib().domino_beam_step_workspace_size, _shape_only(B, W, V, dtype), n_out)
 
 
-def distill_workspace_size(B: int, R: int, V: int, dtype: torch.dtype = torch.float32) -> int:
+@functools.lru_cache(maxsize=1024)
+def distill_workspace_size(B: int, R: int, V: int, k: int, dtype: torch.dtype = torch.float32) -> int:
     """Bytes of device workspace `distill` needs (host only)."""
-    return _size_of(_lib().domino_distill_workspace_size, _shape_only(B, R, V, dtype))
+    return _size_of(_lib().domino_distill_workspace_size, _shape_only(B, R, V, dtype), k)
 
 
 def top_logits(logits: torch.Tensor, k: int, temperature: float = 1.0, n_rows: Optional[torch.Tensor] = None,
@@ -138,13 +154,15 @@ def top_logits(logits: torch.Tensor, k: int, temperature: float = 1.0, n_rows: O
     lib = _lib()
     lg = _logits("logits", logits)
     dev, lead = logits.device, logits.shape[:-1]
-    out = _outputs(out, {"ids": (lead + (k,), torch.int32), "values": (lead + (k,), torch.float32),
-                         "lse": (lead, torch.float32)}, dev)
-    if n_rows is not None:
-        _need("n_rows", n_rows, (lg.B,), torch.int32, dev)
-    ws = _workspace(workspace, lib.domino_top_logits_workspace_size, ctypes.byref(lg), k)
-    _check(lib.domino_top_logits(ctypes.byref(lg), k, temperature, _ptr(n_rows), _ptr(ws), ws.numel(),
-                                 _ptr(out["ids"]), _ptr(out["values"]), _ptr(out["lse"]), _stream_handle()))
+    need = top_logits_workspace_size(lg.B, lg.R, lg.V, k, logits.dtype)
+    out = _known(out, ("ids", "values", "lse"))
+    ids = _output(out, "ids", lead + (k,), torch.int32, dev)
+    values = _output(out, "values", lead + (k,), torch.float32, dev)
+    lse = _output(out, "lse", lead, torch.float32, dev)
+    rows = _maybe("n_rows", n_rows, (lg.B,), torch.int32, dev)
+    ws = _scratch(workspace, need, dev)
+    _check(lib.domino_top_logits(ctypes.byref(lg), k, temperature, rows, ws.data_ptr(), ws.numel(), ids, values, lse,
+                                 _stream(logits)))
     return out
 
 
@@ -169,38 +187,38 @@ def beam_step(logits: torch.Tensor, scores: torch.Tensor, n_out: Optional[int] =
         raise ValueError("logits must be [B, W, V]")
     dev, (B, W, V) = logits.device, logits.shape
     M = W if n_out is None else n_out
-    _need("scores", scores, (B, W), torch.float32, dev)
-    bm = Beam(n_out=M, eos=eos, scores=scores.data_ptr())
-    wanted = {"scores": ((B, M), torch.float32), "parent": ((B, M), torch.int32), "token": ((B, M), torch.int32)}
+    need = beam_step_workspace_size(B, W, V, M, logits.dtype)
+    out = _known(out, ("scores", "parent", "token") + (("finished",) if eos >= 0 else ()) +
+                 (("state",) if state is not None else ()) + (("history",) if history is not None else ()))
+    given = {"scores": _need("scores", scores, (B, W), torch.float32, dev),
+             "finished": _maybe("finished", finished, (B, W), torch.bool, dev), "state": None, "history": None}
+    state_bytes = T = 0
+    o_finished = o_state = o_history = None
+    o_scores = _output(out, "scores", (B, M), torch.float32, dev)
+    o_parent = _output(out, "parent", (B, M), torch.int32, dev)
+    o_token = _output(out, "token", (B, M), torch.int32, dev)
     if eos >= 0:
-        wanted["finished"] = ((B, M), torch.bool)
-    if finished is not None:
-        _need("finished", finished, (B, W), torch.bool, dev)
-        bm.finished = finished.data_ptr()
+        o_finished = _output(out, "finished", (B, M), torch.bool, dev)
     if state is not None:
         if not isinstance(state, torch.Tensor) or state.dim() < 2:
             raise ValueError("state must be [B, W, ...]")
-        _need("state", state, (B, W) + state.shape[2:], state.dtype, dev)
-        bm.state, bm.state_bytes = state.data_ptr(), state.shape[2:].numel() * state.element_size()
-        wanted["state"] = ((B, M) + state.shape[2:], state.dtype)
+        one = state.shape[2:]
+        given["state"] = _need("state", state, (B, W) + one, state.dtype, dev)
+        o_state = _output(out, "state", (B, M) + one, state.dtype, dev)
+        state_bytes = one.numel() * state.element_size()
     if history is not None:
         if not isinstance(history, torch.Tensor) or history.dim() != 3:
             raise ValueError("history must be [B, W, T]")
-        _need("history", history, (B, W, history.shape[2]), torch.int32, dev)
-        bm.history, bm.T, bm.step = history.data_ptr(), history.shape[2], step
-        wanted["history"] = ((B, M, history.shape[2]), torch.int32)
-    out = _outputs(out, wanted, dev)
-    for name, given in (("scores", scores), ("finished", finished), ("state", state), ("history", history)):
-        if given is not None and name in out:
-            if B and out[name].data_ptr() == given.data_ptr():
-                raise ValueError("out[%r] is the input" % name)
-    bm.out_scores, bm.out_parent, bm.out_token = (out["scores"].data_ptr(), out["parent"].data_ptr(),
-                                                  out["token"].data_ptr())
-    bm.out_finished = out["finished"].data_ptr() if eos >= 0 else None
-    bm.out_state = out["state"].data_ptr() if state is not None else None
-    bm.out_history = out["history"].data_ptr() if history is not None else None
-    ws = _workspace(workspace, lib.domino_beam_step_workspace_size, ctypes.byref(lg), M)
-    _check(lib.domino_beam_step(ctypes.byref(lg), ctypes.byref(bm), _ptr(ws), ws.numel(), _stream_handle()))
+        T = history.shape[2]
+        given["history"] = _need("history", history, (B, W, T), torch.int32, dev)
+        o_history = _output(out, "history", (B, M, T), torch.int32, dev)
+    if B and (o_scores == given["scores"] or (o_state and o_state == given["state"]) or
+              (o_history and o_history == given["history"]) or (o_finished and o_finished == given["finished"])):
+        raise ValueError("out: an output tensor is the input it is made from")
+    bm = Beam(M, eos, T, step, state_bytes, given["scores"], given["finished"], given["state"], given["history"],
+              o_scores, o_parent, o_token, o_finished, o_state, o_history)
+    ws = _scratch(workspace, need, dev)
+    _check(lib.domino_beam_step(ctypes.byref(lg), ctypes.byref(bm), ws.data_ptr(), ws.numel(), _stream(logits)))
     return out
 
 
@@ -214,35 +232,34 @@ def distill(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor, teach
     more event, without it the teacher is its entries alone.  n_rows [B] int32: rows r >= n_rows[b] are left
     out (loss and gradient 0).
 
-    Returns loss [B, R] float32 (temperature^2 times the divergence) and stats [B, R, 4 + k] float32 for
-    `distill_backward`; with grad_loss [B, R] float32 also grad = grad_loss * dloss/dlogits, of the logits'
-    shape and type.  ``out`` may supply these tensors (grad may be the logits themselves, or any tensor of
-    their shape and type with a contiguous last dimension), ``workspace`` (uint8) the scratch.
+    Returns loss [B, R] float32 (temperature^2 times the divergence).  Without grad_loss also stats
+    [B, R, 4 + k] float32 for `distill_backward`; with grad_loss [B, R] float32 instead grad = grad_loss *
+    dloss/dlogits, of the logits' shape and type.  ``out`` may supply these tensors (grad may be the logits
+    themselves, or any tensor of their shape and type with a contiguous last dimension), ``workspace`` (uint8)
+    the scratch.
     """
     lib = _lib()
     lg = _logits("logits", logits)
     dev, lead = logits.device, logits.shape[:-1]
     k = _teacher_ids(ids, lead, dev)
-    _need("values", values, ids.shape, torch.float32, dev)
-    if teacher_lse is not None:
-        _need("teacher_lse", teacher_lse, lead, torch.float32, dev)
-    if n_rows is not None:
-        _need("n_rows", n_rows, (lg.B,), torch.int32, dev)
-    out = {} if out is None else dict(out)
-    grad = None
-    if grad_loss is not None:
-        _need("grad_loss", grad_loss, lead, torch.float32, dev)
-        grad = out.pop("grad", None)
-        if grad is None:
-            grad = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
-    gd = None if grad is None else _grad("out['grad']", grad, logits)
-    out = _outputs(out, {"loss": (lead, torch.float32), "stats": (lead + (STAT_HEAD + k,), torch.float32)}, dev)
-    ws = _workspace(workspace, lib.domino_distill_workspace_size, ctypes.byref(lg))
-    _check(lib.domino_distill(ctypes.byref(lg), k, _ptr(ids), _ptr(values), _ptr(teacher_lse), temperature,
-                              _ptr(n_rows), _ptr(ws), ws.numel(), _ptr(out["loss"]), _ptr(out["stats"]),
-                              _ptr(grad_loss), None if gd is None else ctypes.byref(gd), _stream_handle()))
-    if grad is not None:
-        out["grad"] = grad
+    need = distill_workspace_size(lg.B, lg.R, lg.V, k, logits.dtype)
+    v_ptr = _need("values", values, ids.shape, torch.float32, dev)
+    lse = _maybe("teacher_lse", teacher_lse, lead, torch.float32, dev)
+    rows = _maybe("n_rows", n_rows, (lg.B,), torch.int32, dev)
+    g_ptr = _maybe("grad_loss", grad_loss, lead, torch.float32, dev)
+    stats = gd = None
+    if grad_loss is None:
+        out = _known(out, ("loss", "stats"))
+        stats = _output(out, "stats", lead + (STAT_HEAD + k,), torch.float32, dev)
+    else:
+        out = _known(out, ("loss", "grad"))
+        if out.get("grad") is None:
+            out["grad"] = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+        gd = ctypes.byref(_grad("out['grad']", out["grad"], logits))
+    loss = _output(out, "loss", lead, torch.float32, dev)
+    ws = _scratch(workspace, need, dev)
+    _check(lib.domino_distill(ctypes.byref(lg), k, ids.data_ptr(), v_ptr, lse, temperature, rows, ws.data_ptr(),
+                              ws.numel(), loss, stats, g_ptr, gd, _stream(logits)))
     return out
 
 
@@ -258,15 +275,14 @@ def distill_backward(logits: torch.Tensor, ids: torch.Tensor, stats: torch.Tenso
     lg = _logits("logits", logits)
     dev, lead = logits.device, logits.shape[:-1]
     k = _teacher_ids(ids, lead, dev)
-    _need("stats", stats, lead + (STAT_HEAD + k,), torch.float32, dev)
-    _need("grad_loss", grad_loss, lead, torch.float32, dev)
-    if n_rows is not None:
-        _need("n_rows", n_rows, (lg.B,), torch.int32, dev)
+    s_ptr = _need("stats", stats, lead + (STAT_HEAD + k,), torch.float32, dev)
+    g_ptr = _need("grad_loss", grad_loss, lead, torch.float32, dev)
+    rows = _maybe("n_rows", n_rows, (lg.B,), torch.int32, dev)
     if out is None:
         out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
     gd = _grad("out", out, logits)
-    _check(lib.domino_distill_backward(ctypes.byref(lg), k, _ptr(ids), _ptr(stats), _ptr(grad_loss), temperature,
-                                       _ptr(n_rows), ctypes.byref(gd), _stream_handle()))
+    _check(lib.domino_distill_backward(ctypes.byref(lg), k, ids.data_ptr(), s_ptr, g_ptr, temperature, rows,
+                                       ctypes.byref(gd), _stream(logits)))
     return out
 
 
@@ -279,7 +295,7 @@ def _teacher_ids(ids, lead, device) -> int:
 
 def _grad(name: str, grad, logits: torch.Tensor) -> Logits:
     gd = _logits(name, grad)
-    if grad.shape != logits.shape or grad.dtype != logits.dtype or grad.device != logits.device:
+    if grad.shape != logits.shape or grad.dtype != logits.dtype:
         raise ValueError("%s: expected a %s tensor on %s of shape %s, got %s" %
                          (name, logits.dtype, logits.device, tuple(logits.shape), _said(grad)))
     return gd

@@ -320,7 +320,7 @@ int domino_beam_step(const domino_logits *logits, const domino_beam *beam, void 
  *     loss = temperature^2 ( sum_j p_j (t_j - log q_j) + rest log(rest / Qr) )
  * An id outside [0, V) (-1 pads a row) is passed over; an id named twice has both masses.  A row without a
  * valid id, one whose entries' values are all -inf (without teacher_lse), and rows r >= n_rows[b] are left
- * out: loss 0, gradient 0; without a valid id and past n_rows they are not read.  A row of nothing but -inf has
+ * out: loss 0, gradient 0, whatever their logits hold.  A row of nothing but -inf has
  * q = 0; a NaN or +inf among a row's logits makes its loss and gradient NaN.
  *   ids        [B, R, k] int32, values [B, R, k] float32, teacher_lse [B, R] float32 or NULL
  *   n_rows     [B] int32 or NULL (all R)
@@ -328,7 +328,7 @@ int domino_beam_step(const domino_logits *logits, const domino_beam *beam, void 
  *   loss       [B, R] float32
  *   stats      [B, R, 4 + k] float32: what the backward pass needs of the forward pass; NULL = not stored
  *   grad_loss  [B, R] float32 or NULL.  Given, the call also writes the gradient grad_loss[b][r] *
- *              dloss/dz to `grad` (then not NULL, and stats must be given)
+ *              dloss/dz to `grad` (then not NULL), and stats must be NULL
  *   grad       same dtype, B, R and V as the logits; its rows may be the logits' own (same data and strides:
  *              the gradient takes their place) or lie apart from them
  * domino_distill_backward writes the gradient from the forward pass' stats, with the same logits, ids,
@@ -338,7 +338,7 @@ int domino_beam_step(const domino_logits *logits, const domino_beam *beam, void 
  * allocation, no synchronization.  Pointers other than the logits' and the gradient's data 16-byte aligned;
  * apart from what is said of grad, outputs may not alias inputs or the workspace.
  */
-int domino_distill_workspace_size(const domino_logits *logits, size_t *bytes);
+int domino_distill_workspace_size(const domino_logits *logits, int32_t k, size_t *bytes);
 int domino_distill(const domino_logits *logits, int32_t k, const int32_t *ids, const float *values,
                    const float *teacher_lse, float temperature, const int32_t *n_rows, void *workspace,
                    size_t workspace_bytes, float *loss, float *stats, const float *grad_loss,

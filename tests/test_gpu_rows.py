@@ -267,21 +267,19 @@ def check_distill(z, ids, values, lse, tau, n_rows=None, label=""):
     first = dca.distill(z, **teach)
     second = dca.distill_backward(z, dev(ids), first["stats"], dev(g), temperature=tau, n_rows=nr)
     torch.cuda.synchronize()
-    for name in ("loss", "stats"):
-        assert first[name].cpu().numpy().tobytes() == both[name].cpu().numpy().tobytes(), label
     with np.errstate(invalid="ignore"):
         loss, grad, size = plain.distill(host(z), ids.numpy(), values.numpy(), None if lse is None else lse.numpy(),
                                          tau, n_rows)
-        got = host(both["loss"]).astype(np.float64)
-        assert same_nan(got, loss), label
-        inf = np.isinf(loss)
-        assert np.array_equal(got[inf], loss[inf]), label
-        fine = np.isfinite(loss)
+        inf, fine = np.isinf(loss), np.isfinite(loss)
         # p weighs log q (SUM), rest weighs log Qr (two sums); masses sum to 1 (or to the sum of the p)
         t = values.numpy().astype(np.float64) / tau
         mass = np.ones((B, R)) if lse is None else np.maximum(1, np.exp(t - lse.numpy()[..., None]).sum(-1))
         most = 2 * tau * tau * SUM * mass + np.abs(loss) * H
-        assert (np.abs(got[fine] - loss[fine]) <= most[fine]).all(), label
+        for name, res in (("both", both["loss"]), ("first", first["loss"])):
+            got = host(res).astype(np.float64)
+            assert same_nan(got, loss), (label, name)
+            assert np.array_equal(got[inf], loss[inf]), (label, name)
+            assert (np.abs(got[fine] - loss[fine]) <= most[fine]).all(), (label, name)
         # an element: its sums (q: one, q / Qr and Qr: one each), its exponential (2 H, and the rounding of an
         # argument of at most 88 / log2(e) in size, both products), four products and A's rounding
         rel = 2 * SUM + 2 * H + 2 * 128 * H + 6 * H
@@ -305,7 +303,7 @@ def check_distill(z, ids, values, lse, tau, n_rows=None, label=""):
 @pytest.mark.parametrize("B,R,V,k,pad,shift,tau", [
     (1, 1, 1, 1, 0, 0, 1.0), (2, 2, 7, 7, 0, 1, 1.0), (1, 3, 130, 5, 3, 0, 0.5), (2, 2, 1024, 128, 0, 0, 1.0),
     (2, 1, 1025, 64, 0, 3, 2.0), (3, 2, 5003, 33, 1, 0, 1.0), (1, 1, 16384, 1, 0, 0, 1.0), (1, 2, 40001, 100, 7, 1, 3.0),
-    (1, 1, 151936, 64, 0, 0, 1.0), (33, 40, 2049, 8, 0, 0, 1.0),
+    (1, 1, 151936, 64, 0, 0, 1.0), (33, 40, 2049, 8, 0, 0, 1.0), (13, 16, 20011, 9, 0, 1, 1.0),
 ])
 def test_distill(B, R, V, k, pad, shift, tau, tail, dtype):
     z = rows(B, R, V, dtype, 3 * V + k, pad, shift)

@@ -26,7 +26,7 @@ def beam(x, ws=256, nbytes=BIG, **kw):
     return _lib().domino_beam_step(ctypes.byref(x), ctypes.byref(Beam(**base)), ws, nbytes, None)
 
 
-def distill(x, k=5, ids=16, values=32, lse=None, tau=1.0, n_rows=None, ws=256, nbytes=BIG, loss=48, stats=64,
+def distill(x, k=5, ids=16, values=32, lse=None, tau=1.0, n_rows=None, ws=256, nbytes=BIG, loss=48, stats=None,
             grad_loss=None, grad=None):
     return _lib().domino_distill(ctypes.byref(x), k, ids, values, lse, tau, n_rows, ws, nbytes, loss, stats, grad_loss,
                                  None if grad is None else ctypes.byref(grad), None)
@@ -98,7 +98,7 @@ def test_limits_of_beam_step():
 
 
 @pytest.mark.parametrize("kw", [
-    dict(grad_loss=80), dict(grad=lg(data=4096)), dict(grad_loss=80, grad=lg(data=4096), stats=None),
+    dict(grad_loss=80), dict(grad=lg(data=4096)), dict(grad_loss=80, grad=lg(data=4096), stats=64),
     dict(grad_loss=80, grad=lg(data=4096, V=99)), dict(grad_loss=80, grad=lg(data=4096, B=1)),
     dict(grad_loss=80, grad=lg(data=4096, R=2)), dict(grad_loss=80, grad=lg(data=4096, dtype=dca.DOMINO_BF16)),
     dict(grad_loss=80, grad=lg(data=None)), dict(grad_loss=80, grad=lg(data=4098)),
@@ -112,7 +112,7 @@ def test_arguments_of_distill(kw):
 
 
 def test_workspace_of_distill_and_arguments_of_backward():
-    need = dca.distill_workspace_size(2, 3, 100)
+    need = dca.distill_workspace_size(2, 3, 100, 5)
     assert need > 0 and distill(lg(), nbytes=need - 1) == EWORKSPACE
     for kw in (dict(stats=None), dict(grad_loss=None), dict(stats=24), dict(grad_loss=24),
                dict(grad=lg(data=4096, V=99)), dict(grad=lg(data=16, rs=200, bs=600))):
@@ -123,7 +123,7 @@ def test_workspace_of_distill_and_arguments_of_backward():
 def test_workspace_sizes():
     n = ctypes.c_size_t()
     for fn, args in ((_lib().domino_top_logits_workspace_size, (5,)), (_lib().domino_beam_step_workspace_size, (4,)),
-                     (_lib().domino_distill_workspace_size, ())):
+                     (_lib().domino_distill_workspace_size, (5,))):
         assert fn(ctypes.byref(lg()), *args, None) == EINVAL
         assert fn(None, *args, ctypes.byref(n)) == EINVAL
         assert fn(ctypes.byref(lg(B=0)), *args, ctypes.byref(n)) == 0 and n.value == 0
