@@ -38,10 +38,8 @@ struct Vec<float> {
     typedef float raw __attribute__((ext_vector_type(4)));
     typedef float mem __attribute__((ext_vector_type(4), aligned(4)));
     __device__ static raw fill() { return raw{NEG_INF, NEG_INF, NEG_INF, NEG_INF}; }
-    __device__ static raw from(const uint4 &q)
-    {
-        return raw{__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z), __uint_as_float(q.w)};
-    }
+    // element i of vectors stored as words
+    __device__ static float word_at(const uint32_t *words, int i) { return __uint_as_float(words[i]); }
     __device__ static float get(const raw &x, int e) { return x[e]; }
     __device__ static void set(raw &x, int e, float f) { x[e] = f; }
     template <typename F>
@@ -60,7 +58,10 @@ struct Vec<bf16s> {
     typedef uint32_t raw __attribute__((ext_vector_type(4)));
     typedef uint32_t mem __attribute__((ext_vector_type(4), aligned(2)));
     __device__ static raw fill() { return raw{0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u}; }
-    __device__ static raw from(const uint4 &q) { return raw{q.x, q.y, q.z, q.w}; }
+    __device__ static float word_at(const uint32_t *words, int i)
+    {
+        return __uint_as_float((i & 1) ? (words[i >> 1] & 0xFFFF0000u) : (words[i >> 1] << 16));
+    }
     __device__ static float get(const raw &x, int e)
     {
         return __uint_as_float((e & 1) ? (x[e >> 1] & 0xFFFF0000u) : (x[e >> 1] << 16));

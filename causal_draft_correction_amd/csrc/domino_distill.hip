@@ -162,6 +162,7 @@ __device__ inline void finish_row(const Rows &rows, const Teach &te, int row, in
         id[0] = id[1] = -1;
     double t[2] = {NINF, NINF}, z[2] = {NINF, NINF};
     bool valid[2];
+    int own[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         valid[i] = in_row(id[i], rows.V);
@@ -169,7 +170,8 @@ __device__ inline void finish_row(const Rows &rows, const Teach &te, int row, in
             t[i] = static_cast<double>(value[i]) * inv_tau;
             z[i] = Vec<T>::one(zr + id[i]);
         }
-        s_id[lane + 64 * i] = valid[i] ? id[i] : -1;
+        own[i] = valid[i] ? id[i] : -1 - (lane + 64 * i);  // (invalid ones differ from all others)
+        s_id[lane + 64 * i] = own[i];
     }
     // the entries' masses are p / p_sum; t becomes log of p where their sum is not needed for it
     bool live = __ballot(valid[0] || valid[1]) != 0;
@@ -207,22 +209,29 @@ __device__ inline void finish_row(const Rows &rows, const Teach &te, int row, in
     }
     // entries that name an id again: the first of them stands for it, with the mass of all
     double named[2] = {p[0], p[1]};
-    bool first[2] = {valid[0], valid[1]}, again = false;
+    bool first[2] = {valid[0], valid[1]};
     s_p[lane] = p[0], s_p[lane + 64] = p[1];
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-#pragma unroll 4
-    for (int j = 0; j < te.k; j += 4) {
-        const int4 four = *reinterpret_cast<const int4 *>(s_id + j);
-        const int o[4] = {four.x, four.y, four.z, four.w};
+    // entries with the lane's ids: one each, the entry itself, where no id is named twice
+    int same[2] = {0, 0};
+    const int4 *four = reinterpret_cast<const int4 *>(s_id);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                again |= valid[i] && o[e] == id[i] && j + e != lane + 64 * i;
+    for (int j = 0; j < 16; ++j) {
+        const int4 o = four[j];
+        same[0] += (o.x == own[0]) + (o.y == own[0]) + (o.z == own[0]) + (o.w == own[0]);
     }
-    if (__ballot(again)) {
+    if (te.k > 64) {
+#pragma unroll 4
+        for (int j = 0; j < 32; ++j) {
+            const int4 o = four[j];
+            same[1] += (o.x == own[1]) + (o.y == own[1]) + (o.z == own[1]) + (o.w == own[1]);
+            if (j >= 16)
+                same[0] += (o.x == own[0]) + (o.y == own[0]) + (o.z == own[0]) + (o.w == own[0]);
+        }
+    }
+    if (__ballot(same[0] > 1 || same[1] > 1)) {
         named[0] = named[1] = 0.0;
         for (int j = 0; j < te.k; ++j)
 #pragma unroll

@@ -29,7 +29,6 @@ namespace DH_NS {
 constexpr int VECS = 512;          // vectors of a chunk that the LDS list holds
 constexpr int LIST = 1024;         // elements of a chunk that the LDS list holds
 constexpr int MERGE_LIST = 4096;   // candidates of a row's chunks
-constexpr int HEADS = 4;           // heads of the chunks' lists a lane takes
 constexpr int BEAM_LIST = 512;     // candidates of a beam step that are ranked by counting
 constexpr int MAX_TIES = 128;      // places of the list kept for elements equal to the bound (at least MAX_K)
 constexpr int COUNT_MAX = 256;     // up to here places are counted, above the list is sorted
@@ -67,22 +66,80 @@ __device__ inline uint32_t word(float f) { return __float_as_uint(f); }
 __device__ inline uint32_t word(uint32_t u) { return u; }
 __device__ inline float key_value(uint64_t key) { return unord_f32(static_cast<uint32_t>(key >> 32)); }
 
-// A bound that at least n of the wave's 64 N values reach: the n-th largest with its bits below `last` cleared
-// (0 if there are fewer than n values above 0).  All lanes get it.
-template <int N>
-__device__ inline uint32_t wave_bound(const uint32_t (&v)[N], int n, int last)
+// The n-th largest of the wave's values with its bits below LAST cleared: at least n lanes reach it (0 if fewer
+// than n hold more than 0).  Two bits a step, from bit FROM on where the n-th largest shares the bits above with the
+// largest; all lanes get it.
+template <int LAST, int FROM>
+__device__ inline uint32_t wave_bound(uint32_t v, int n)
 {
+    static_assert(LAST % 2 == 0 && FROM % 2 == 0 && FROM <= 32, "two bits a step");
+    uint32_t top = v;
+    top = max(top, dpp_u32<DPP_QUAD_XOR1>(top));
+    top = max(top, dpp_u32<DPP_QUAD_XOR2>(top));
+    top = max(top, dpp_u32<DPP_HALF_MIRROR>(top));
+    top = max(top, dpp_u32<DPP_ROW_MIRROR>(top));
+    uint32_t a, b;
+    row_pair_values(top, a, b);
+    half_values(max(a, b), a, b);
+    top = __builtin_amdgcn_readfirstlane(max(a, b));
     uint32_t t = 0;
-    for (int bit = 31; bit >= last; --bit) {
-        const uint32_t c = t | (1u << bit);
-        int have = 0;
+    auto step = [&](int bit) {
+        const uint32_t c1 = t | (1u << bit), c2 = t | (2u << bit), c3 = t | (3u << bit);
+        const int n1 = __popcll(__ballot(v >= c1)), n2 = __popcll(__ballot(v >= c2)), n3 = __popcll(__ballot(v >= c3));
+        t = n3 >= n ? c3 : n2 >= n ? c2 : n1 >= n ? c1 : t;
+    };
+    const uint32_t high = top >> FROM << FROM;
+    if (__popcll(__ballot(v >= high)) >= n) {
+        t = high;
+    } else {
+#pragma unroll
+        for (int bit = 30; bit >= FROM; bit -= 2)
+            step(bit);
+    }
+#pragma unroll
+    for (int bit = FROM - 2; bit >= LAST; bit -= 2)
+        step(bit);
+    return t;
+}
+
+// A bound that at least n of the block's values reach: the lowest of the waves' bounds for their share of n.  `red`:
+// one word a wave.  Ends with a barrier's worth of order: all threads get the same.
+template <int LAST, int FROM, int NTB>
+__device__ inline uint32_t block_bound(uint32_t v, int n, uint32_t *red)
+{
+    constexpr int NW = NTB / 64;
+    const uint32_t w = wave_bound<LAST, FROM>(v, (n + NW - 1) / NW);
+    if ((threadIdx.x & 63) == 0)
+        red[threadIdx.x >> 6] = w;
+    __syncthreads();
+    uint32_t t = red[0];
+#pragma unroll
+    for (int i = 1; i < NW; ++i)
+        t = t < red[i] ? t : red[i];
+    return t;
+}
+
+// Places of the wave's hits in a list of the block, one atomic for all of them.
+template <int N>
+__device__ inline void wave_places(const bool (&hit)[N], int *count, int (&at)[N])
+{
+    int total = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint64_t mask = __ballot(hit[i]);
+        at[i] = total + static_cast<int>(__builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32),
+                                                                   __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0)));
+        total += __popcll(mask);
+    }
+    if (total) {
+        int base = 0;
+        if ((threadIdx.x & 63) == 0)
+            base = atomicAdd(count, total);
+        base = __builtin_amdgcn_readfirstlane(base);
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            have += __popcll(__ballot(v[i] >= c));
-        if (have >= n)
-            t = c;
+            at[i] += base;
     }
-    return t;
 }
 
 // Sorts list[0, n) in descending order (n <= LEN; list holds the next power of two).
@@ -108,7 +165,7 @@ __device__ inline void block_sort(uint64_t *list, int n)
 
 // Hands the k largest of list[0, n) to emit(place, key), largest first; places past n get key 0.
 template <typename F>
-__device__ inline void emit_largest(uint64_t *list, int n, int k, F emit)
+__device__ inline void emit_largest(uint64_t *list, int *place, int n, int k, F emit)
 {
     if (n > COUNT_MAX) {
         block_sort(list, n);
@@ -116,25 +173,39 @@ __device__ inline void emit_largest(uint64_t *list, int n, int k, F emit)
             emit(i, list[i]);
         return;
     }
-    const int t = threadIdx.x;
-    if (t < n) {
-        const uint64_t key = list[t];
-        int place = 0;
-#pragma unroll 8
-        for (int j = 0; j < n; ++j)
-            place += list[j] > key;
-        if (place < k)
-            emit(place, key);
+    // 2^shift threads take one key each, and 256 / 2^shift a slice of the others
+    const int t = threadIdx.x, shift = n <= 64 ? 6 : n <= 128 ? 7 : 8;
+    place[t] = 0;
+    if (t == 0 && (n & 1))
+        list[n] = 0;
+    __syncthreads();
+    const int i = t & ((1 << shift) - 1), slices = NT >> shift, pairs = (n + 1) / 2;
+    const int len = (pairs + slices - 1) / slices, j0 = (t >> shift) * len, j1 = j0 + len < pairs ? j0 + len : pairs;
+    if (i < n) {
+        const uint64_t key = list[i];
+        const ulonglong2 *two = reinterpret_cast<const ulonglong2 *>(list);
+        int above = 0;
+#pragma unroll 4
+        for (int j = j0; j < j1; ++j) {
+            const ulonglong2 o = two[j];
+            above += (o.x > key) + (o.y > key);
+        }
+        if (above)
+            atomicAdd(&place[i], above);
     }
-    for (int i = n + t; i < k; i += NT)
-        emit(i, 0ull);
+    __syncthreads();
+    if (t < n && place[t] < k)
+        emit(place[t], list[t]);
+    for (int at = n + t; at < k; at += NT)
+        emit(at, 0ull);
 }
 
 struct ChunkShared {
-    uint64_t list[LIST];
+    alignas(16) uint64_t list[LIST];
     uint4 vec[VECS];
     int at[VECS];            // first element of each
-    uint32_t top[NT];        // the threads' maxima
+    uint32_t bound[NWAVE];
+    int place[NT];
     uint64_t best[NWAVE];
     float m[NWAVE], s[NWAVE];
     uint32_t count[NWAVE];
@@ -269,32 +340,27 @@ __global__ __launch_bounds__(NT) void k_top_chunk(Rows rows, Live live, int k, i
     }
     // the bound: a thread without an element counts as below everything
     const bool any = v0 + static_cast<int>(threadIdx.x) * VT::N < v1;
-    sh.top[threadIdx.x] = any ? ord_f32(tm) : 0u;
+    const uint32_t top = any ? ord_f32(tm) : 0u;
     const float wm = wave_max(tm);
     if (lane == 0)
         sh.m[wave] = wm;
-    __syncthreads();
+    const uint32_t t_ord = block_bound<16, 26, NT>(top, k, sh.bound);
     float m = sh.m[0];
 #pragma unroll
     for (int w = 1; w < NWAVE; ++w)
         m = fmaxf(m, sh.m[w]);
-    uint32_t tops[NWAVE];
-#pragma unroll
-    for (int w = 0; w < NWAVE; ++w)
-        tops[w] = sh.top[w * 64 + lane];
-    const uint32_t t_ord = wave_bound(tops, k, 16);
     const float t = t_ord > ORD_NEG_INF ? unord_f32(t_ord) : NEG_INF;
+    bool hit[NV];
+    int at[NV];
 #pragma unroll
     for (int u = 0; u < NV; ++u)
-        if (vm[u] >= t) {
-            const int v = v0 + (u * NT + static_cast<int>(threadIdx.x)) * VT::N;
-            if (v < v1) {
-                const int at = atomicAdd(&sh.nvec, 1);
-                if (at < VECS) {
-                    sh.vec[at] = make_uint4(word(x[u][0]), word(x[u][1]), word(x[u][2]), word(x[u][3]));
-                    sh.at[at] = v;
-                }
-            }
+        hit[u] = vm[u] >= t && v0 + (u * NT + static_cast<int>(threadIdx.x)) * VT::N < v1;
+    wave_places(hit, &sh.nvec, at);
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+        if (hit[u] && at[u] < VECS) {
+            sh.vec[at[u]] = make_uint4(word(x[u][0]), word(x[u][1]), word(x[u][2]), word(x[u][3]));
+            sh.at[at[u]] = v0 + (u * NT + static_cast<int>(threadIdx.x)) * VT::N;
         }
     const Expo ex(m > NEG_INF ? m : 0.f, sc);
     float s = ex.small ? sum_exps<T, true>(x, ex, sc) : sum_exps<T, false>(x, ex, sc);
@@ -302,11 +368,23 @@ __global__ __launch_bounds__(NT) void k_top_chunk(Rows rows, Live live, int k, i
     if (lane == 0)
         sh.s[wave] = s;
     __syncthreads();
-    double total = 0.0;
+    const int nvec = sh.nvec;
+    bool nan = false;
 #pragma unroll
     for (int w = 0; w < NWAVE; ++w)
-        total += static_cast<double>(sh.s[w]);
-    total *= ex.fix(sc);
+        nan |= sh.s[w] != sh.s[w];
+    // one element a thread
+    if (nvec <= VECS)
+        for (int i = threadIdx.x; i < (nvec * VT::N + 63) / 64 * 64; i += NT) {
+            const int j = i / VT::N, e = i % VT::N, v = j < nvec ? sh.at[j] + e : v1;
+            const float f = VT::word_at(&sh.vec[0].x, i);
+            const bool one[1] = {v < v1 && f >= t};
+            int place[1];
+            wave_places(one, &sh.n, place);
+            if (one[0] && place[0] < LIST)
+                sh.list[place[0]] = argmax_key(f, static_cast<uint32_t>(v));
+        }
+    __syncthreads();
     const int64_t slot = static_cast<int64_t>(row) * nch + c;
     auto emit = [&](int place, uint64_t key) {
         if (direct)
@@ -314,64 +392,57 @@ __global__ __launch_bounds__(NT) void k_top_chunk(Rows rows, Live live, int k, i
         else
             out.keys[slot * k + place] = key;
     };
-
-    const int nvec = sh.nvec;
-    for (int i = threadIdx.x; i < nvec && nvec <= VECS; i += NT) {
-        const uint4 q = sh.vec[i];
-        const typename VT::raw y = VT::from(q);
-        const int v = sh.at[i];
-#pragma unroll
-        for (int e = 0; e < VT::N; ++e) {
-            const float f = VT::get(y, e);
-            if (f >= t && v + e < v1) {
-                const int at = atomicAdd(&sh.n, 1);
-                if (at < LIST)
-                    sh.list[at] = argmax_key(f, static_cast<uint32_t>(v + e));
-            }
-        }
-    }
-    __syncthreads();
-    Part part = {m, static_cast<float>(total)};
     const int n = sh.n;
-    // more reach the bound than the lists hold: the exact one, since most of them may be equal to it
-    const bool over = nvec > VECS || n > LIST;
-    const uint32_t t_exact = over ? wave_bound(tops, k, 0) : 0;
-    if (total != total) {
-        // NaN or +inf among the elements (+inf alone makes the maximum +inf)
-        bool nan = false;
+    bool infinite = false;
+    if (nan) {
+        // NaN or +inf among the elements
+        bool any_nan = false;
         for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += NT) {
             const float f = VT::one(z + v);
-            nan |= f != f;
+            any_nan |= f != f;
         }
-        nan = __syncthreads_or(nan);
-        part = nan ? Part{__builtin_nanf(""), 1.f} : Part{-NEG_INF, 1.f};
-        total = 1.0;
+        nan = __syncthreads_or(any_nan);
+        infinite = !nan;
         largest_by_rounds(z, v0, v1, k, sh, emit);
-    } else if (!over) {
-        emit_largest(sh.list, n, k, emit);
-    } else if (list_with_ties(z, v0, v1, t_exact ? unord_f32(t_exact) : NEG_INF, k, sh)) {
-        emit_largest(sh.list, sh.n, k, emit);
+    } else if (nvec <= VECS && n <= LIST) {
+        emit_largest(sh.list, sh.place, n, k, emit);
     } else {
-        largest_by_rounds(z, v0, v1, k, sh, emit);
+        // more reach the bound than the lists hold: the exact one, since most of them may be equal to it
+        const uint32_t exact = block_bound<0, 26, NT>(top, k, sh.bound);
+        if (list_with_ties(z, v0, v1, exact ? unord_f32(exact) : NEG_INF, k, sh))
+            emit_largest(sh.list, sh.place, sh.n, k, emit);
+        else
+            largest_by_rounds(z, v0, v1, k, sh, emit);
     }
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == NT - 1) {  // (of the wave with the least to rank)
+        double total = 0.0;
+#pragma unroll
+        for (int w = 0; w < NWAVE; ++w)
+            total += static_cast<double>(sh.s[w]);
+        total *= ex.fix(sc);
+        const Part part = nan ? Part{__builtin_nanf(""), 1.f} : infinite ? Part{-NEG_INF, 1.f}
+                                                                         : Part{m, static_cast<float>(total)};
         if (direct)
-            out.lse[row] = part.m == NEG_INF ? NEG_INF : static_cast<float>(part.m * inv_tau + log(total));
+            out.lse[row] = part.m == NEG_INF ? NEG_INF
+                           : nan || infinite ? part.m
+                                             : static_cast<float>(part.m * inv_tau + log(total));
         else
             out.parts[slot] = part;
     }
 }
 
 struct MergeShared {
-    uint64_t list[MERGE_LIST];
+    alignas(16) uint64_t list[MERGE_LIST];
+    uint32_t bound[NWAVE];
+    int place[NT];
     int n;
 };
 
 // The candidates of nch sorted lists of k keys that reach the k-th largest of the lists' heads go to sh.list;
-// returns how many.  q heads of each list, nch q <= 64 HEADS unless q is 1 and the lists are more.
+// returns how many.  A thread takes PER keys; q heads of each list, one a thread (of more than NT lists, the first NT heads).
+template <int PER>
 __device__ inline int merge_list(const uint64_t *keys, int nch, int k, MergeShared &sh)
 {
-    constexpr int PER = MERGE_LIST / NT;
     const int lane = threadIdx.x & 63, n = nch * k;
     uint64_t mine[PER];
 #pragma unroll
@@ -379,27 +450,30 @@ __device__ inline int merge_list(const uint64_t *keys, int nch, int k, MergeShar
         const int at = i * NT + static_cast<int>(threadIdx.x);
         mine[i] = at < n ? keys[at] : 0;
     }
-    int q = 64 * HEADS / nch;
+    int q = NT / nch;
     q = q < 1 ? 1 : q < k ? q : k;
-    uint32_t head[HEADS];
-#pragma unroll
-    for (int i = 0; i < HEADS; ++i) {
-        const int h = i * 64 + lane, c = h / q;
-        head[i] = c < nch ? static_cast<uint32_t>(keys[static_cast<int64_t>(c) * k + (h - c * q)] >> 32) : 0;
-    }
+    // head h: place h / nch of list h % nch, dealt out over the waves
+    const int h = lane * NWAVE + (static_cast<int>(threadIdx.x) >> 6), r = h / nch;
+    const uint32_t head = r < q ? static_cast<uint32_t>(keys[static_cast<int64_t>(h - r * nch) * k + r] >> 32) : 0;
     if (threadIdx.x == 0)
         sh.n = 0;
-    __syncthreads();
-    const uint32_t t = wave_bound(head, k, 12);
+    const uint32_t t = block_bound<12, 26, NT>(head, k, sh.bound);
+    bool hit[PER];
+    int at[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-        if (static_cast<uint32_t>(mine[i] >> 32) >= t && mine[i])
-            sh.list[atomicAdd(&sh.n, 1)] = mine[i];
+        hit[i] = static_cast<uint32_t>(mine[i] >> 32) >= t && mine[i];
+    wave_places(hit, &sh.n, at);
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (hit[i])
+            sh.list[at[i]] = mine[i];
     __syncthreads();
     return sh.n;
 }
 
 // The k largest of a row from its chunks' lists, and its log-sum-exp.
+template <int PER>
 __global__ __launch_bounds__(NT) void k_top_merge(Rows rows, Live live, int k, int nch, double inv_tau, TopOut out)
 {
     __shared__ MergeShared sh;
@@ -415,7 +489,8 @@ __global__ __launch_bounds__(NT) void k_top_merge(Rows rows, Live live, int k, i
     }
     const int64_t slot = static_cast<int64_t>(row) * nch;
     const Part part = first_part(out.parts + slot, nch);
-    const int n = merge_list(out.keys + slot * k, nch, k, sh);
+    const int n = merge_list<PER>(out.keys + slot * k, nch, k, sh);
+    emit_largest(sh.list, sh.place, n, k, [&](int place, uint64_t key) { put_result(out, row, k, place, key); });
     if (threadIdx.x >= NT - 64) {  // the wave with the least to rank
         float m;
         double s;
@@ -423,7 +498,6 @@ __global__ __launch_bounds__(NT) void k_top_merge(Rows rows, Live live, int k, i
         if (threadIdx.x == NT - 1)
             out.lse[row] = m == NEG_INF ? NEG_INF : static_cast<float>(m * inv_tau + log(s));
     }
-    emit_largest(sh.list, n, k, [&](int place, uint64_t key) { put_result(out, row, k, place, key); });
 }
 
 // Unsigned words in the order of doubles: NaN above +inf, -0 as +0.
@@ -463,11 +537,9 @@ __device__ inline void copy_rows(const char *src, char *dst, int64_t bytes, int 
         V v[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int64_t i = i0 + u * stride;
-            if (i < all) {
-                const int64_t j = narrow ? static_cast<uint32_t>(i) / static_cast<uint32_t>(per) : i / per;
-                v[u] = reinterpret_cast<const V *>(src)[parent[j] * per + (i - j * per)];
-            }
+            const int64_t i = i0 + u * stride < all ? i0 + u * stride : all - 1;
+            const int64_t j = narrow ? static_cast<uint32_t>(i) / static_cast<uint32_t>(per) : i / per;
+            v[u] = reinterpret_cast<const V *>(src)[parent[j] * per + (i - j * per)];
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u)
@@ -484,14 +556,23 @@ struct Cand {
 };
 __device__ inline bool before(const Cand &a, const Cand &b)
 {
-    return a.score > b.score || (a.score == b.score && (a.w < b.w || (a.w == b.w && a.place > b.place)));
+    // (no branches)
+    return (a.score > b.score) | ((a.score == b.score) & ((a.w < b.w) | ((a.w == b.w) & (a.place > b.place))));
+}
+__device__ inline void keep_first(Cand &best, const Cand &c, bool counts)
+{
+    const bool take = counts & before(c, best);
+    best.score = take ? c.score : best.score;
+    best.place = take ? c.place : best.place;
+    best.w = take ? c.w : best.w;
 }
 enum { LIVE, DEAD, ENDED, BAD };
 constexpr uint64_t ORD64_NEG_INF = 0x000FFFFFFFFFFFFFull;  // ord_f64(-inf)
 
 struct BeamShared {
     Cand list[BEAM_LIST];
-    uint32_t top[1024];
+    int place[BEAM_LIST];
+    uint32_t bound[16];
     Cand best[16];
     double score[MAX_BEAMS], log_s[MAX_BEAMS];
     float max[MAX_BEAMS];
@@ -542,8 +623,7 @@ __device__ inline void best_by_rounds(const BeamArgs &a, const uint64_t *keys, B
                     c.place = 0xFFFFFFFFu - static_cast<uint32_t>(j);
                     c.score = kind == BAD ? ~0ull : kind == ENDED && j == 0 ? ord_f64(sh.score[w]) : ORD64_NEG_INF;
                 }
-                if (before(last, c) && before(c, best))
-                    best = c;
+                keep_first(best, c, before(last, c));
             }
         }
 #pragma unroll
@@ -552,16 +632,14 @@ __device__ inline void best_by_rounds(const BeamArgs &a, const uint64_t *keys, B
             c.score = __shfl_xor(best.score, o);
             c.place = __shfl_xor(best.place, o);
             c.w = __shfl_xor(best.w, o);
-            if (before(c, best))
-                best = c;
+            keep_first(best, c, true);
         }
         if (lane == 0)
             sh.best[wave] = best;
         __syncthreads();
         best = sh.best[0];
         for (int v = 1; v < nwave; ++v)
-            if (before(sh.best[v], best))
-                best = sh.best[v];
+            keep_first(best, sh.best[v], true);
         __syncthreads();
         if (threadIdx.x == 0)
             put_beam(sh, a, i, best);
@@ -581,20 +659,21 @@ __global__ __launch_bounds__(NTB) void k_beam_merge(BeamArgs a)
     const int b = blockIdx.x, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int lists = a.W * a.nch, n_cand = lists * a.kc;
     const uint64_t *keys = a.keys + static_cast<int64_t>(b) * n_cand;
-    // candidate i: place i / lists of list i % lists
+    // threads are dealt out over the waves.  PER > 0: thread i takes places i / lists + j * deep, j < PER, of list
+    // i % lists.  PER = 0: candidate i is place i / lists of list i % lists.
+    const int at0 = lane * (NTB / 64) + wave;
+    const int deep = NTB / lists, r0 = at0 / lists, l0 = at0 - r0 * lists, w0 = l0 / a.nch;
     auto key_at = [&](int i, int &w) {
         const int r = i / lists, l = i - r * lists;
         w = l / a.nch;
         return keys[static_cast<int64_t>(l) * a.kc + r];
     };
-    uint64_t mine[PER ? PER : 1];
-    int from[PER ? PER : 1];
+    uint64_t mine[PER ? PER : 1], score[PER ? PER : 1];
     if constexpr (PER > 0) {
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            const int i = j * NTB + static_cast<int>(threadIdx.x);
-            from[j] = 0;
-            mine[j] = i < n_cand ? key_at(i, from[j]) : 0;
+            const int r = r0 + j * deep;
+            mine[j] = r0 < deep && r < a.kc ? keys[static_cast<int64_t>(l0) * a.kc + r] : 0;
         }
     }
     for (int w = wave; w < a.W; w += NTB / 64) {
@@ -629,23 +708,19 @@ __global__ __launch_bounds__(NTB) void k_beam_merge(BeamArgs a)
     uint64_t top = ended;
     if constexpr (PER > 0) {
 #pragma unroll
-        for (int j = 0; j < PER; ++j)
-            if (j * NTB < n_cand)
-                top = max_u64(top, word_of(mine[j], from[j]));
+        for (int j = 0; j < PER; ++j) {
+            score[j] = word_of(mine[j], w0);
+            top = max_u64(top, score[j]);
+        }
     } else {
-        for (int i = threadIdx.x; i < n_cand; i += NTB) {
+        for (int i = at0; i < n_cand; i += NTB) {
             int w;
             const uint64_t key = key_at(i, w);
             top = max_u64(top, word_of(key, w));
         }
     }
-    sh.top[threadIdx.x] = static_cast<uint32_t>(top >> 32);
     const bool odd = __syncthreads_or(kind == BAD || (kind == ENDED && own_score != own_score));
-    uint32_t tops[NTB / 64];
-#pragma unroll
-    for (int i = 0; i < NTB / 64; ++i)
-        tops[i] = sh.top[i * 64 + lane];
-    const uint32_t t = wave_bound(tops, a.M, 8);
+    const uint32_t t = block_bound<8, 22, NTB>(static_cast<uint32_t>(top >> 32), a.M, sh.bound);
     auto take = [&](uint64_t score, uint64_t place, int w) {
         if (static_cast<uint32_t>(score >> 32) >= t && score > ORD64_NEG_INF) {
             const int at = atomicAdd(&sh.n, 1);
@@ -654,12 +729,18 @@ __global__ __launch_bounds__(NTB) void k_beam_merge(BeamArgs a)
         }
     };
     if constexpr (PER > 0) {
+        bool hit[PER];
+        int at[PER];
 #pragma unroll
         for (int j = 0; j < PER; ++j)
-            if (j * NTB < n_cand)
-                take(word_of(mine[j], from[j]), mine[j], from[j]);
+            hit[j] = static_cast<uint32_t>(score[j] >> 32) >= t && score[j] > ORD64_NEG_INF;
+        wave_places(hit, &sh.n, at);
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            if (hit[j] && at[j] < BEAM_LIST)
+                sh.list[at[j]] = Cand{score[j], mine[j], w0};
     } else {
-        for (int i = threadIdx.x; i < n_cand; i += NTB) {
+        for (int i = at0; i < n_cand; i += NTB) {
             int w;
             const uint64_t key = key_at(i, w);
             take(word_of(key, w), key, w);
@@ -671,14 +752,25 @@ __global__ __launch_bounds__(NTB) void k_beam_merge(BeamArgs a)
     if (odd || n < a.M || n > BEAM_LIST) {
         best_by_rounds(a, keys, sh);
     } else {
-        for (int i = threadIdx.x; i < n; i += NTB) {
+        // 2^shift threads take one candidate each, and NTB / 2^shift a slice of the others
+        const int shift = n <= 32 ? 5 : n <= 64 ? 6 : n <= 128 ? 7 : n <= 256 ? 8 : 9;
+        const int i = threadIdx.x & ((1 << shift) - 1), slices = NTB >> shift, len = (n + slices - 1) / slices;
+        const int j0 = (threadIdx.x >> shift) * len, j1 = j0 + len < n ? j0 + len : n;
+        if (threadIdx.x < BEAM_LIST)
+            sh.place[threadIdx.x] = 0;
+        __syncthreads();
+        if (i < n) {
             const Cand c = sh.list[i];
             int place = 0;
-            for (int j = 0; j < n; ++j)
+#pragma unroll 2
+            for (int j = j0; j < j1; ++j)
                 place += before(sh.list[j], c);
-            if (place < a.M)
-                put_beam(sh, a, place, c);
+            if (place)
+                atomicAdd(&sh.place[i], place);
         }
+        __syncthreads();
+        if (threadIdx.x < n && sh.place[threadIdx.x] < a.M)
+            put_beam(sh, a, sh.place[threadIdx.x], sh.list[threadIdx.x]);
         __syncthreads();
     }
     if (blockIdx.y == 0) {
@@ -702,7 +794,7 @@ __global__ __launch_bounds__(NTB) void k_beam_merge(BeamArgs a)
         const char *src = a.state + static_cast<int64_t>(b) * a.W * a.state_bytes;
         char *dst = a.o_state + static_cast<int64_t>(b) * a.M * a.state_bytes;
         if (a.state_bytes % 16 == 0)
-            copy_rows<uint4>(src, dst, a.state_bytes, a.M, sh.o_parent, blockIdx.y, gridDim.y);
+            copy_rows<Vec<bf16s>::raw>(src, dst, a.state_bytes, a.M, sh.o_parent, blockIdx.y, gridDim.y);
         else
             copy_rows<uint32_t>(src, dst, a.state_bytes, a.M, sh.o_parent, blockIdx.y, gridDim.y);
     }
@@ -729,8 +821,9 @@ Split split_of(const domino_logits &lg, int k)
     if (least * k > MERGE_LIST)  // long rows and many logits of each: larger chunks
         least = (nvec + NT * LAST_NV - 1) / (NT * LAST_NV);
     int64_t n = rows ? (TARGET_BLOCKS + rows - 1) / rows : 1;
-    n = n < nvec / NT ? n : nvec / NT;
+    n = n < nvec / (2 * NT) ? n : nvec / (2 * NT);
     n = n < MERGE_LIST / k ? n : MERGE_LIST / k;
+    n = n < 64 ? n : 64;  // (a wave joins the parts of 64 at once)
     n = n > least ? n : least;
     Split sp;
     sp.cvec = static_cast<int>((nvec + n - 1) / n);
@@ -827,8 +920,12 @@ hipError_t top(const domino_logits &lg, int k, float tau, const int32_t *n_rows,
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || sp.nch == 1)
         return e;
-    hipLaunchKernelGGL(k_top_merge, dim3(static_cast<unsigned>(lg.B) * static_cast<unsigned>(lg.R)), dim3(NT), 0, st,
-                       rows, live, k, sp.nch, 1.0 / static_cast<double>(tau), out);
+    const dim3 grid(static_cast<unsigned>(lg.B) * static_cast<unsigned>(lg.R));
+    const double inv_tau = 1.0 / static_cast<double>(tau);
+    if (sp.nch * k <= NT * 4)
+        hipLaunchKernelGGL((k_top_merge<4>), grid, dim3(NT), 0, st, rows, live, k, sp.nch, inv_tau, out);
+    else
+        hipLaunchKernelGGL((k_top_merge<MERGE_LIST / NT>), grid, dim3(NT), 0, st, rows, live, k, sp.nch, inv_tau, out);
     return hipGetLastError();
 }
 
@@ -861,10 +958,11 @@ hipError_t beam(const domino_logits &lg, const domino_beam &bm, void *ws, hipStr
     int64_t parts = a.o_state ? (a.M * a.state_bytes + 16383) / 16384 : 1;
     parts = parts < 1 ? 1 : parts > 64 ? 64 : parts;
     const dim3 grid(lg.B, static_cast<unsigned>(parts));
-    const int64_t n_cand = static_cast<int64_t>(a.W) * sp.nch * kc;
-    if (n_cand <= 512 * 2)
+    // places a thread of a block of 512 takes of its list
+    const int lists = a.W * sp.nch, deep = lists <= 512 ? 512 / lists : 0, per = deep ? (kc + deep - 1) / deep : 1 << 30;
+    if (per <= 2)
         hipLaunchKernelGGL((k_beam_merge<512, 2>), grid, dim3(512), 0, st, a);
-    else if (n_cand <= 512 * 8)
+    else if (per <= 8)
         hipLaunchKernelGGL((k_beam_merge<512, 8>), grid, dim3(512), 0, st, a);
     else
         hipLaunchKernelGGL((k_beam_merge<1024, 0>), grid, dim3(1024), 0, st, a);
