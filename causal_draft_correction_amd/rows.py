@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import struct
 from typing import Optional
 
 import torch
@@ -16,7 +17,14 @@ import torch
 from .binding import DOMINO_BF16, DOMINO_F32, _check, load_library
 
 STAT_HEAD = 4  # floats of a row's statistics before those of its ids
+_TOP_OUT, _LOSS_OUT, _GRAD_OUT = {"ids", "values", "lse"}, {"loss", "stats"}, {"loss", "grad"}
+_BEAM_OUT = {"scores", "parent", "token", "finished", "state", "history"}
 _DTYPES = {torch.float32: DOMINO_F32, torch.bfloat16: DOMINO_BF16}
+
+
+# domino_logits and domino_beam as bytes, which take less time to make than their ctypes forms below
+_LOGITS = struct.Struct("=Qqqiiii").pack
+_BEAM = struct.Struct("=iiiiq10Q").pack
 
 
 class Logits(ctypes.Structure):
@@ -39,78 +47,78 @@ def _lib():
     global _declared
     lib = load_library()
     if _declared is not lib:
-        P, I32, F32, SZ, LG = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t,
-                               ctypes.POINTER(Logits))
-        lib.domino_top_logits_workspace_size.argtypes = [LG, I32, ctypes.POINTER(SZ)]
-        lib.domino_top_logits.argtypes = [LG, I32, F32, P, P, SZ, P, P, P, P]
-        lib.domino_beam_step_workspace_size.argtypes = [LG, I32, ctypes.POINTER(SZ)]
-        lib.domino_beam_step.argtypes = [LG, ctypes.POINTER(Beam), P, SZ, P]
-        lib.domino_distill_workspace_size.argtypes = [LG, I32, ctypes.POINTER(SZ)]
-        lib.domino_distill.argtypes = [LG, I32, P, P, P, F32, P, P, SZ, P, P, P, LG, P]
-        lib.domino_distill_backward.argtypes = [LG, I32, P, P, P, F32, P, LG, P]
+        P, I32, F32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
+        lib.domino_top_logits_workspace_size.argtypes = [P, I32, ctypes.POINTER(SZ)]
+        lib.domino_top_logits.argtypes = [P, I32, F32, P, P, SZ, P, P, P, P]
+        lib.domino_beam_step_workspace_size.argtypes = [P, I32, ctypes.POINTER(SZ)]
+        lib.domino_beam_step.argtypes = [P, P, P, SZ, P]
+        lib.domino_distill_workspace_size.argtypes = [P, I32, ctypes.POINTER(SZ)]
+        lib.domino_distill.argtypes = [P, I32, P, P, P, F32, P, P, SZ, P, P, P, P, P]
+        lib.domino_distill_backward.argtypes = [P, I32, P, P, P, F32, P, P, P]
         _declared = lib
     return lib
-
-
-def _logits(name: str, t) -> Logits:
-    dtype = _DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
-    shape = t.shape if dtype is not None else ()
-    if len(shape) not in (2, 3) or not t.is_cuda or (t.stride(-1) != 1 and shape[-1] != 1):
-        raise ValueError("%s: expected a CUDA float32 or bfloat16 tensor [B, R, V] or [N, V] whose last dimension is "
-                         "contiguous, got %s" % (name, _said(t)))
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError("%s is on %s, the current device is cuda:%d" % (name, t.device, torch.cuda.current_device()))
-    if len(shape) == 2:
-        return Logits(t.data_ptr(), t.stride(0), shape[1], shape[0], 1, shape[1], dtype)
-    return Logits(t.data_ptr(), t.stride(0), t.stride(1), shape[0], shape[1], shape[2], dtype)
 
 
 def _said(t) -> str:
     return "%s %s on %s" % (t.dtype, tuple(t.shape), t.device) if isinstance(t, torch.Tensor) else type(t).__name__
 
 
-def _need(name: str, t, shape, dtype, device) -> int:
-    """The tensor's address, if it is a contiguous one of this shape and type."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or t.device != device or \
+def _logits(name: str, t):
+    """(the packed domino_logits, B, R, V, device index) of a tensor of logits."""
+    dtype = _DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    shape = t.shape if dtype is not None else ()
+    n = len(shape)
+    if (n != 3 and n != 2) or not t.is_cuda:
+        raise ValueError("%s: expected a CUDA float32 or bfloat16 tensor [B, R, V] or [N, V], got %s" % (name, _said(t)))
+    stride, index = t.stride(), t.get_device()
+    if stride[-1] != 1 and shape[-1] != 1:
+        raise ValueError("%s: expected a contiguous last dimension, got strides %s" % (name, stride))
+    if index != torch.cuda.current_device():
+        raise ValueError("%s is on cuda:%d, the current device is cuda:%d" % (name, index, torch.cuda.current_device()))
+    if n == 3:
+        B, R, V = shape
+        return _LOGITS(t.data_ptr(), stride[0], stride[1], B, R, V, dtype), B, R, V, index
+    B, V = shape
+    return _LOGITS(t.data_ptr(), stride[0], V, B, 1, V, dtype), B, 1, V, index
+
+
+def _need(name: str, t, shape, dtype, index: int) -> int:
+    """The tensor's address, if it is a contiguous one of this shape and type on this GPU."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != index or \
             not t.is_contiguous():
-        raise ValueError("%s: expected a contiguous %s tensor on %s of shape %s, got %s" %
-                         (name, dtype, device, tuple(shape), _said(t)))
+        raise ValueError("%s: expected a contiguous %s tensor on cuda:%d of shape %s, got %s" %
+                         (name, dtype, index, tuple(shape), _said(t)))
     return t.data_ptr()
 
 
-def _maybe(name: str, t, shape, dtype, device):
-    return None if t is None else _need(name, t, shape, dtype, device)
-
-
-def _output(out: dict, name: str, shape, dtype, device) -> int:
+def _output(out: dict, name: str, shape, dtype, index: int) -> int:
     """The address of output `name`: the caller's tensor, checked, or a new one."""
     t = out.get(name)
     if t is None:
-        t = out[name] = torch.empty(shape, dtype=dtype, device=device)
+        t = out[name] = torch.empty(shape, dtype=dtype, device="cuda")
         return t.data_ptr()
-    return _need("out[%r]" % name, t, shape, dtype, device)
+    return _need(name, t, shape, dtype, index)
 
 
-def _known(out: Optional[dict], names) -> dict:
-    out = {} if out is None else dict(out)
-    for name in out:
-        if name not in names:
-            raise ValueError("out: unknown entry %r (expected %s)" % (name, ", ".join(names)))
-    return out
+def _known(out: Optional[dict], names: set) -> dict:
+    if out is None:
+        return {}
+    if not names.issuperset(out):
+        raise ValueError("out: unknown entries among %s (expected %s)" % (sorted(out), sorted(names)))
+    return dict(out)
 
 
-def _scratch(given: Optional[torch.Tensor], need: int, device) -> torch.Tensor:
+def _scratch(given: Optional[torch.Tensor], need: int, index: int) -> torch.Tensor:
     if given is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    if not isinstance(given, torch.Tensor) or given.dtype != torch.uint8 or given.device != device or \
+        return torch.empty(need, dtype=torch.uint8, device="cuda")
+    if not isinstance(given, torch.Tensor) or given.dtype is not torch.uint8 or given.get_device() != index or \
             not given.is_contiguous():
-        raise ValueError("workspace: expected a contiguous uint8 tensor on %s, got %s" % (device, _said(given)))
+        raise ValueError("workspace: expected a contiguous uint8 tensor on cuda:%d, got %s" % (index, _said(given)))
     return given
 
 
-def _stream(logits: torch.Tensor) -> int:
-    """The current stream's handle (torch.cuda.current_stream() builds a Stream object around it each time)."""
-    return torch._C._cuda_getCurrentRawStream(logits.get_device())
+# The current stream's handle of a GPU (torch.cuda.current_stream() builds a Stream object around it each time).
+_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _size_of(fn, lg: Logits, *args) -> int:
@@ -151,18 +159,17 @@ def top_logits(logits: torch.Tensor, k: int, temperature: float = 1.0, n_rows: O
     int32 and values [B, R, k] float32, largest first with ties to the lowest id, and lse [B, R] float32 (-1,
     -inf and -inf in rows left out).  ``out`` may supply these tensors, ``workspace`` (uint8) the scratch.
     """
-    lib = _lib()
-    lg = _logits("logits", logits)
-    dev, lead = logits.device, logits.shape[:-1]
-    need = top_logits_workspace_size(lg.B, lg.R, lg.V, k, logits.dtype)
-    out = _known(out, ("ids", "values", "lse"))
-    ids = _output(out, "ids", lead + (k,), torch.int32, dev)
-    values = _output(out, "values", lead + (k,), torch.float32, dev)
-    lse = _output(out, "lse", lead, torch.float32, dev)
-    rows = _maybe("n_rows", n_rows, (lg.B,), torch.int32, dev)
-    ws = _scratch(workspace, need, dev)
-    _check(lib.domino_top_logits(ctypes.byref(lg), k, temperature, rows, ws.data_ptr(), ws.numel(), ids, values, lse,
-                                 _stream(logits)))
+    lib = _declared or _lib()
+    lg, B, R, V, gpu = _logits("logits", logits)
+    need = top_logits_workspace_size(B, R, V, k, logits.dtype)
+    lead = logits.shape[:-1]
+    out = _known(out, _TOP_OUT)
+    ids = _output(out, "ids", lead + (k,), torch.int32, gpu)
+    values = _output(out, "values", lead + (k,), torch.float32, gpu)
+    lse = _output(out, "lse", lead, torch.float32, gpu)
+    rows = None if n_rows is None else _need("n_rows", n_rows, (B,), torch.int32, gpu)
+    ws = _scratch(workspace, need, gpu)
+    _check(lib.domino_top_logits(lg, k, temperature, rows, ws.data_ptr(), ws.numel(), ids, values, lse, _stream(gpu)))
     return out
 
 
@@ -181,44 +188,45 @@ def beam_step(logits: torch.Tensor, scores: torch.Tensor, n_out: Optional[int] =
     eos >= 0), state and history in the new order (where given).  ``out`` may supply these tensors,
     ``workspace`` (uint8) the scratch; outputs may not be the inputs.
     """
-    lib = _lib()
-    lg = _logits("logits", logits)
+    lib = _declared or _lib()
+    lg, B, W, V, gpu = _logits("logits", logits)
     if logits.dim() != 3:
         raise ValueError("logits must be [B, W, V]")
-    dev, (B, W, V) = logits.device, logits.shape
     M = W if n_out is None else n_out
     need = beam_step_workspace_size(B, W, V, M, logits.dtype)
-    out = _known(out, ("scores", "parent", "token") + (("finished",) if eos >= 0 else ()) +
-                 (("state",) if state is not None else ()) + (("history",) if history is not None else ()))
-    given = {"scores": _need("scores", scores, (B, W), torch.float32, dev),
-             "finished": _maybe("finished", finished, (B, W), torch.bool, dev), "state": None, "history": None}
-    state_bytes = T = 0
-    o_finished = o_state = o_history = None
-    o_scores = _output(out, "scores", (B, M), torch.float32, dev)
-    o_parent = _output(out, "parent", (B, M), torch.int32, dev)
-    o_token = _output(out, "token", (B, M), torch.int32, dev)
+    out = _known(out, _BEAM_OUT)
+    one = (B, M)
+    i_scores = _need("scores", scores, (B, W), torch.float32, gpu)
+    o_scores = _output(out, "scores", one, torch.float32, gpu)
+    o_parent = _output(out, "parent", one, torch.int32, gpu)
+    o_token = _output(out, "token", one, torch.int32, gpu)
+    i_finished = i_state = i_history = o_finished = o_state = o_history = state_bytes = T = 0
+    if finished is not None:
+        i_finished = _need("finished", finished, (B, W), torch.bool, gpu)
     if eos >= 0:
-        o_finished = _output(out, "finished", (B, M), torch.bool, dev)
+        o_finished = _output(out, "finished", one, torch.bool, gpu)
     if state is not None:
         if not isinstance(state, torch.Tensor) or state.dim() < 2:
             raise ValueError("state must be [B, W, ...]")
-        one = state.shape[2:]
-        given["state"] = _need("state", state, (B, W) + one, state.dtype, dev)
-        o_state = _output(out, "state", (B, M) + one, state.dtype, dev)
-        state_bytes = one.numel() * state.element_size()
+        rest = state.shape[2:]
+        i_state = _need("state", state, (B, W) + rest, state.dtype, gpu)
+        o_state = _output(out, "state", one + rest, state.dtype, gpu)
+        state_bytes = rest.numel() * state.element_size()
     if history is not None:
         if not isinstance(history, torch.Tensor) or history.dim() != 3:
             raise ValueError("history must be [B, W, T]")
         T = history.shape[2]
-        given["history"] = _need("history", history, (B, W, T), torch.int32, dev)
-        o_history = _output(out, "history", (B, M, T), torch.int32, dev)
-    if B and (o_scores == given["scores"] or (o_state and o_state == given["state"]) or
-              (o_history and o_history == given["history"]) or (o_finished and o_finished == given["finished"])):
+        i_history = _need("history", history, (B, W, T), torch.int32, gpu)
+        o_history = _output(out, "history", (B, M, T), torch.int32, gpu)
+    if len(out) != 3 + (eos >= 0) + (state is not None) + (history is not None):
+        raise ValueError("out: finished needs eos, state and history need their inputs (got %s)" % sorted(out))
+    if B and (o_scores == i_scores or (o_state and o_state == i_state) or (o_history and o_history == i_history) or
+              (o_finished and o_finished == i_finished)):
         raise ValueError("out: an output tensor is the input it is made from")
-    bm = Beam(M, eos, T, step, state_bytes, given["scores"], given["finished"], given["state"], given["history"],
-              o_scores, o_parent, o_token, o_finished, o_state, o_history)
-    ws = _scratch(workspace, need, dev)
-    _check(lib.domino_beam_step(ctypes.byref(lg), ctypes.byref(bm), ws.data_ptr(), ws.numel(), _stream(logits)))
+    bm = _BEAM(M, eos, T, step, state_bytes, i_scores, i_finished, i_state, i_history, o_scores, o_parent, o_token,
+               o_finished, o_state, o_history)
+    ws = _scratch(workspace, need, gpu)
+    _check(lib.domino_beam_step(lg, bm, ws.data_ptr(), ws.numel(), _stream(gpu)))
     return out
 
 
@@ -238,28 +246,28 @@ def distill(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor, teach
     themselves, or any tensor of their shape and type with a contiguous last dimension), ``workspace`` (uint8)
     the scratch.
     """
-    lib = _lib()
-    lg = _logits("logits", logits)
-    dev, lead = logits.device, logits.shape[:-1]
-    k = _teacher_ids(ids, lead, dev)
-    need = distill_workspace_size(lg.B, lg.R, lg.V, k, logits.dtype)
-    v_ptr = _need("values", values, ids.shape, torch.float32, dev)
-    lse = _maybe("teacher_lse", teacher_lse, lead, torch.float32, dev)
-    rows = _maybe("n_rows", n_rows, (lg.B,), torch.int32, dev)
-    g_ptr = _maybe("grad_loss", grad_loss, lead, torch.float32, dev)
-    stats = gd = None
+    lib = _declared or _lib()
+    lg, B, R, V, gpu = _logits("logits", logits)
+    lead = logits.shape[:-1]
+    k, i_ids = _teacher_ids(ids, lead, gpu)
+    need = distill_workspace_size(B, R, V, k, logits.dtype)
+    i_values = _need("values", values, lead + (k,), torch.float32, gpu)
+    i_lse = None if teacher_lse is None else _need("teacher_lse", teacher_lse, lead, torch.float32, gpu)
+    rows = None if n_rows is None else _need("n_rows", n_rows, (B,), torch.int32, gpu)
+    i_grad = stats = gd = None
     if grad_loss is None:
-        out = _known(out, ("loss", "stats"))
-        stats = _output(out, "stats", lead + (STAT_HEAD + k,), torch.float32, dev)
+        out = _known(out, _LOSS_OUT)
+        stats = _output(out, "stats", lead + (STAT_HEAD + k,), torch.float32, gpu)
     else:
-        out = _known(out, ("loss", "grad"))
+        i_grad = _need("grad_loss", grad_loss, lead, torch.float32, gpu)
+        out = _known(out, _GRAD_OUT)
         if out.get("grad") is None:
-            out["grad"] = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
-        gd = ctypes.byref(_grad("out['grad']", out["grad"], logits))
-    loss = _output(out, "loss", lead, torch.float32, dev)
-    ws = _scratch(workspace, need, dev)
-    _check(lib.domino_distill(ctypes.byref(lg), k, ids.data_ptr(), v_ptr, lse, temperature, rows, ws.data_ptr(),
-                              ws.numel(), loss, stats, g_ptr, gd, _stream(logits)))
+            out["grad"] = torch.empty(logits.shape, dtype=logits.dtype, device="cuda")
+        gd = _grad("out['grad']", out["grad"], logits)
+    loss = _output(out, "loss", lead, torch.float32, gpu)
+    ws = _scratch(workspace, need, gpu)
+    _check(lib.domino_distill(lg, k, i_ids, i_values, i_lse, temperature, rows, ws.data_ptr(), ws.numel(), loss, stats,
+                              i_grad, gd, _stream(gpu)))
     return out
 
 
@@ -271,31 +279,30 @@ def distill_backward(logits: torch.Tensor, ids: torch.Tensor, stats: torch.Tenso
     grad_loss [B, R] float32; temperature and n_rows as in that call.  ``out`` may be the logits themselves, or
     any tensor of their shape and type with a contiguous last dimension.
     """
-    lib = _lib()
-    lg = _logits("logits", logits)
-    dev, lead = logits.device, logits.shape[:-1]
-    k = _teacher_ids(ids, lead, dev)
-    s_ptr = _need("stats", stats, lead + (STAT_HEAD + k,), torch.float32, dev)
-    g_ptr = _need("grad_loss", grad_loss, lead, torch.float32, dev)
-    rows = _maybe("n_rows", n_rows, (lg.B,), torch.int32, dev)
+    lib = _declared or _lib()
+    lg, B, _, _, gpu = _logits("logits", logits)
+    lead = logits.shape[:-1]
+    k, i_ids = _teacher_ids(ids, lead, gpu)
+    i_stats = _need("stats", stats, lead + (STAT_HEAD + k,), torch.float32, gpu)
+    i_grad = _need("grad_loss", grad_loss, lead, torch.float32, gpu)
+    rows = None if n_rows is None else _need("n_rows", n_rows, (B,), torch.int32, gpu)
     if out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
-    gd = _grad("out", out, logits)
-    _check(lib.domino_distill_backward(ctypes.byref(lg), k, ids.data_ptr(), s_ptr, g_ptr, temperature, rows,
-                                       ctypes.byref(gd), _stream(logits)))
+        out = torch.empty(logits.shape, dtype=logits.dtype, device="cuda")
+    _check(lib.domino_distill_backward(lg, k, i_ids, i_stats, i_grad, temperature, rows, _grad("out", out, logits),
+                                       _stream(gpu)))
     return out
 
 
-def _teacher_ids(ids, lead, device) -> int:
+def _teacher_ids(ids, lead, gpu: int):
     if not isinstance(ids, torch.Tensor) or ids.dim() != len(lead) + 1:
         raise ValueError("ids: expected a tensor of shape %s, got %s" % (tuple(lead) + ("k",), _said(ids)))
-    _need("ids", ids, lead + ids.shape[-1:], torch.int32, device)
-    return ids.shape[-1]
+    k = ids.shape[-1]
+    return k, _need("ids", ids, lead + (k,), torch.int32, gpu)
 
 
-def _grad(name: str, grad, logits: torch.Tensor) -> Logits:
-    gd = _logits(name, grad)
-    if grad.shape != logits.shape or grad.dtype != logits.dtype:
+def _grad(name: str, grad, logits: torch.Tensor) -> bytes:
+    gd = _logits(name, grad)[0]
+    if grad.shape != logits.shape or grad.dtype is not logits.dtype:
         raise ValueError("%s: expected a %s tensor on %s of shape %s, got %s" %
                          (name, logits.dtype, logits.device, tuple(logits.shape), _said(grad)))
     return gd
