@@ -68,11 +68,15 @@ __device__ inline void drop_named(typename Vec<T>::raw (&x)[NV], uint32_t (&mask
         any |= mine[i] = mask[i][threadIdx.x];
     if (any) {
 #pragma unroll
-        for (int u = 0; u < NV; ++u)
+        for (int u = 0; u < NV; ++u) {
+            const uint32_t bits = (mine[u * VT::N >> 5] >> (u * VT::N & 31)) & ((1u << VT::N) - 1);
+            if (bits) {
 #pragma unroll
-            for (int e = 0; e < VT::N; ++e)
-                if ((mine[(u * VT::N + e) >> 5] >> ((u * VT::N + e) & 31)) & 1u)
-                    VT::set(x[u], e, NEG_INF);
+                for (int e = 0; e < VT::N; ++e)
+                    if ((bits >> e) & 1u)
+                        VT::set(x[u], e, NEG_INF);
+            }
+        }
     }
 }
 
@@ -111,7 +115,7 @@ __device__ inline Part chunk_part(typename Vec<T>::raw (&x)[NV], const Scale &sc
 
 // The chunk's part; with TAIL over the elements that no entry names.
 template <typename T, int NV, bool TAIL>
-__global__ __launch_bounds__(NT) void k_distill_part(Rows rows, Teach te, int nch, int cvec, Scale sc, Part *parts)
+__global__ __launch_bounds__(NT) void k_distill_part(Rows rows, Teach te, int nch, int cvec, bool keep, Scale sc, Part *parts)
 {
     __shared__ uint32_t mask[TAIL ? MASK_WORDS<T, NV> : 1][NT];
     __shared__ float red_m[NWAVE], red_s[NWAVE];
@@ -126,7 +130,11 @@ __global__ __launch_bounds__(NT) void k_distill_part(Rows rows, Teach te, int nc
     if (!__syncthreads_or(in_row(id, rows.V)))
         return;
     typename Vec<T>::raw x[NV];
-    load_chunk<T, NV>(x, row_at<T>(rows, row / rows.R, row % rows.R), rows.V, c, cvec);
+    const T *z = row_at<T>(rows, row / rows.R, row % rows.R);
+    if (keep)
+        load_chunk<T, NV, NT, true>(x, z, rows.V, c, cvec);
+    else
+        load_chunk<T, NV>(x, z, rows.V, c, cvec);
     if constexpr (TAIL)
         drop_named<T, NV>(x, mask, id, chunk_begin<T>(c, cvec, rows.V), chunk_begin<T>(c + 1, cvec, rows.V));
     const Part part = chunk_part<T, NV>(x, sc, red_m, red_s);
@@ -466,6 +474,7 @@ Rows rows_of(const domino_logits &lg, const int32_t *n_rows)
 }
 
 struct PartCall {
+    bool keep;
     Rows rows;
     Teach te;
     Split sp;
@@ -478,10 +487,10 @@ struct PartCall {
     {
         if (te.lse)
             hipLaunchKernelGGL((k_distill_part<T, NV, true>), dim3(grid), dim3(NT), 0, st, rows, te, sp.nch, sp.cvec,
-                               sc, parts);
+                               keep, sc, parts);
         else
             hipLaunchKernelGGL((k_distill_part<T, NV, false>), dim3(grid), dim3(NT), 0, st, rows, te, sp.nch, sp.cvec,
-                               sc, parts);
+                               keep, sc, parts);
     }
 };
 
@@ -601,6 +610,10 @@ hipError_t forward(const domino_logits &lg, const Teacher &t, float tau, const i
     c.sp = split_of(lg, PART_NV);
     c.sc = scale_of(tau);
     c.parts = static_cast<Part *>(ws);
+    // Logits that the 256 MB last-level cache holds beside the gradient are read to stay there for the backward
+    // pass.  512 bf16 rows of 151936 (156 MB): both passes 83.0 us without, 80.0 us with; 1024 f32 rows (622 MB):
+    // 294 us without, 297 us with.
+    c.keep = stats && static_cast<double>(lg.B) * lg.R * lg.V * (lg.dtype == DOMINO_F32 ? 4 : 2) <= 192e6;
     const unsigned n = static_cast<unsigned>(lg.B) * static_cast<unsigned>(lg.R);
     c.grid = n * c.sp.nch;
     c.st = st;
