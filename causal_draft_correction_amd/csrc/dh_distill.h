@@ -12,7 +12,8 @@ namespace dhdistill {
 constexpr int MAX_K = 128;  // teacher logits of a row
 constexpr int STAT_HEAD = 4;  // floats of a row's statistics before those of its k ids
 
-// Bytes of scratch: the chunks' parts, and the rows' statistics where the caller does not keep them.
+// Bytes of scratch: the chunks' parts, and the rows' statistics where the caller does not keep them; none for rows
+// that one block takes whole.
 size_t workspace_bytes(const domino_logits &lg, int k);
 
 struct Teacher {

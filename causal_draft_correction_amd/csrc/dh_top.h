@@ -13,8 +13,8 @@ constexpr int MAX_K = 128;         // logits kept of a row, continuations of a b
 constexpr int MAX_W = 32;          // beams
 constexpr int MAX_V = 1 << 19;     // longest row: its chunks' candidates have to fit one block's list
 
-// Bytes of scratch for the k largest of each row (k <= V).
-size_t workspace_bytes(const domino_logits &lg, int k);
+// Bytes of scratch for the k largest of each row (k <= V); top() needs none for rows that one block takes whole.
+size_t workspace_bytes(const domino_logits &lg, int k, bool for_beams);
 
 // Arguments were checked by the caller.
 hipError_t top(const domino_logits &lg, int k, float tau, const int32_t *n_rows, void *ws, int32_t *ids,

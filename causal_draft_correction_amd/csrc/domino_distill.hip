@@ -88,9 +88,7 @@ __device__ inline Part chunk_part(typename Vec<T>::raw (&x)[NV], const Scale &sc
     float m = NEG_INF;
 #pragma unroll
     for (int u = 0; u < NV; ++u)
-#pragma unroll
-        for (int e = 0; e < Vec<T>::N; ++e)
-            m = fmaxf(m, Vec<T>::get(x[u], e));
+        m = Vec<T>::max_with(x[u], m);
     m = wave_max(m);
     if (lane == 0)
         red_m[wave] = m;
@@ -115,11 +113,12 @@ __device__ inline Part chunk_part(typename Vec<T>::raw (&x)[NV], const Scale &sc
 
 // The chunk's part; with TAIL over the elements that no entry names.
 template <typename T, int NV, bool TAIL>
-__global__ __launch_bounds__(NT) void k_distill_part(Rows rows, Teach te, int nch, int cvec, bool keep, Scale sc, Part *parts)
+__global__ __launch_bounds__(NT) void k_distill_part(Rows rows, Teach te, int nch, int cvec, bool keep, Scale sc,
+                                                     Part *parts)
 {
     __shared__ uint32_t mask[TAIL ? MASK_WORDS<T, NV> : 1][NT];
     __shared__ float red_m[NWAVE], red_s[NWAVE];
-    const int row = blockIdx.x / nch, c = blockIdx.x % nch;
+    const int row = rows.at_place(blockIdx.x / nch), c = blockIdx.x % nch;
     if (!rows.counts(row / rows.R, row % rows.R))
         return;
     int id = -1;
@@ -301,7 +300,8 @@ __device__ inline void finish_row(const Rows &rows, const Teach &te, int row, in
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             if (lane + 64 * i < te.k)
-                st[HEAD + lane + 64 * i] = none ? __builtin_nanf("") : static_cast<float>(total * q[i] * inv_s - named[i]);
+                st[HEAD + lane + 64 * i] =
+                    none ? __builtin_nanf("") : static_cast<float>(total * q[i] * inv_s - named[i]);
     }
 }
 
@@ -346,7 +346,7 @@ __global__ __launch_bounds__(NT) void k_distill_grad(Rows rows, int k, int nch, 
                                                      const float *stats, const float *grad_loss, float tau, Scale sc,
                                                      Rows grad)
 {
-    const int row = blockIdx.x / nch, c = blockIdx.x % nch, b = row / rows.R, r = row % rows.R;
+    const int row = rows.at_place(blockIdx.x / nch), c = blockIdx.x % nch, b = row / rows.R, r = row % rows.R;
     T *out = const_cast<T *>(row_at<T>(grad, b, r));
     const float *st = stats + static_cast<int64_t>(row) * (HEAD + k);
     const bool counts = rows.counts(b, r);
@@ -382,7 +382,8 @@ __global__ __launch_bounds__(NT) void k_distill_row(Rows rows, Teach te, double 
     __shared__ __align__(16) int s_id[MAX_IDS];
     __shared__ double s_p[MAX_IDS];
     __shared__ float s_stat[HEAD + MAX_IDS];
-    const int row = blockIdx.x, b = row / rows.R, r = row % rows.R, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int row = rows.at_place(blockIdx.x), b = row / rows.R, r = row % rows.R;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     int id = -1;
     if (static_cast<int>(threadIdx.x) < te.k && rows.counts(b, r))
         id = te.ids[static_cast<int64_t>(row) * te.k + threadIdx.x];
@@ -467,6 +468,7 @@ Rows rows_of(const domino_logits &lg, const int32_t *n_rows)
     r.data = lg.data;
     r.bs = lg.batch_stride;
     r.rs = lg.row_stride;
+    r.B = lg.B;
     r.R = lg.R;
     r.V = lg.V;
     r.n_rows = n_rows;
@@ -560,13 +562,16 @@ namespace {
 
 size_t parts_bytes(const domino_logits &lg)
 {
-    return (static_cast<size_t>(lg.B) * lg.R * split_of(lg, PART_NV).nch * sizeof(Part) + 15) & ~static_cast<size_t>(15);
+    const size_t n = static_cast<size_t>(lg.B) * lg.R * split_of(lg, PART_NV).nch * sizeof(Part);
+    return (n + 15) & ~static_cast<size_t>(15);
 }
 
 }  // namespace
 
 size_t workspace_bytes(const domino_logits &lg, int k)
 {
+    if (vectors(lg) <= NT * PART_NV)
+        return 0;
     return parts_bytes(lg) + static_cast<size_t>(lg.B) * lg.R * (HEAD + k) * sizeof(float);
 }
 
@@ -577,9 +582,9 @@ bool by_rows(const domino_logits &lg, const Teacher &t, float tau, const int32_t
              const float *grad_loss, const domino_logits *grad, hipStream_t st)
 {
     RowCall c;
-    c.sp = Split{1, vectors(lg), (vectors(lg) + NT - 1) / NT};
-    if (c.sp.nv > PART_NV)
+    if (vectors(lg) > NT * PART_NV)
         return false;
+    c.sp = Split{1, vectors(lg), (vectors(lg) + NT - 1) / NT};
     c.rows = rows_of(lg, n_rows);
     c.grad = grad ? rows_of(*grad, nullptr) : Rows{};
     c.te = Teach{t.k, t.ids, t.values, t.lse};

@@ -1227,6 +1227,8 @@ static int beam_args(const domino_logits *lg, int32_t n_out)
 
 static int workspace_arg(const void *ws, size_t have, size_t need)
 {
+    if (!need)
+        return DOMINO_OK;
     if (!ws)
         return fail(DOMINO_EINVAL, "workspace is NULL");
     if (!aligned16(ws))
@@ -1243,7 +1245,7 @@ int domino_top_logits_workspace_size(const domino_logits *lg, int32_t k, size_t 
         return rc;
     if (!bytes)
         return fail(DOMINO_EINVAL, "bytes is NULL");
-    *bytes = lg->B ? dhtop::workspace_bytes(*lg, k) : 0;
+    *bytes = lg->B ? dhtop::workspace_bytes(*lg, k, false) : 0;
     return DOMINO_OK;
 }
 
@@ -1261,7 +1263,7 @@ int domino_top_logits(const domino_logits *lg, int32_t k, float temperature, con
         return fail(DOMINO_EINVAL, "NULL pointer");
     if (!aligned16(ids) || !aligned16(values) || !aligned16(lse) || !aligned16(n_rows))
         return fail(DOMINO_EINVAL, "pointers must be 16-byte aligned");
-    if ((rc = workspace_arg(workspace, workspace_bytes, dhtop::workspace_bytes(*lg, k))))
+    if ((rc = workspace_arg(workspace, workspace_bytes, dhtop::workspace_bytes(*lg, k, false))))
         return rc;
     HIP_TRY(dhtop::top(*lg, k, temperature, n_rows, workspace, ids, values, lse, static_cast<hipStream_t>(stream)),
             "launch top_logits");
@@ -1275,7 +1277,7 @@ int domino_beam_step_workspace_size(const domino_logits *lg, int32_t n_out, size
         return rc;
     if (!bytes)
         return fail(DOMINO_EINVAL, "bytes is NULL");
-    *bytes = lg->B ? dhtop::workspace_bytes(*lg, std::min(n_out, lg->V)) : 0;
+    *bytes = lg->B ? dhtop::workspace_bytes(*lg, std::min(n_out, lg->V), true) : 0;
     return DOMINO_OK;
 }
 
@@ -1307,7 +1309,7 @@ int domino_beam_step(const domino_logits *lg, const domino_beam *bm, void *works
                           static_cast<const void *>(bm->out_history)})
         if (!aligned16(p))
             return fail(DOMINO_EINVAL, "pointers must be 16-byte aligned");
-    if ((rc = workspace_arg(workspace, workspace_bytes, dhtop::workspace_bytes(*lg, std::min(bm->n_out, lg->V)))))
+    if ((rc = workspace_arg(workspace, workspace_bytes, dhtop::workspace_bytes(*lg, std::min(bm->n_out, lg->V), true))))
         return rc;
     HIP_TRY(dhtop::beam(*lg, *bm, workspace, static_cast<hipStream_t>(stream)), "launch beam_step");
     return DOMINO_OK;

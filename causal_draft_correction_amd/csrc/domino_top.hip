@@ -127,8 +127,8 @@ __device__ inline void wave_places(const bool (&hit)[N], int *count, int (&at)[N
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const uint64_t mask = __ballot(hit[i]);
-        at[i] = total + static_cast<int>(__builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32),
-                                                                   __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0)));
+        const uint32_t low = __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0);
+        at[i] = total + static_cast<int>(__builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32), low));
         total += __popcll(mask);
     }
     if (total) {
@@ -309,7 +309,8 @@ __global__ __launch_bounds__(NT) void k_top_chunk(Rows rows, Live live, int k, i
 {
     typedef Vec<T> VT;
     __shared__ ChunkShared sh;
-    const int row = blockIdx.x / nch, c = blockIdx.x % nch, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int row = rows.at_place(blockIdx.x / nch, live.scores != nullptr), c = blockIdx.x % nch;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const bool direct = nch == 1 && out.ids;
     if (!row_live(rows, live, row)) {
         if (direct) {
@@ -332,10 +333,7 @@ __global__ __launch_bounds__(NT) void k_top_chunk(Rows rows, Live live, int k, i
     float vm[NV], tm = NEG_INF;
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
-        vm[u] = VT::get(x[u], 0);
-#pragma unroll
-        for (int e = 1; e < VT::N; ++e)
-            vm[u] = fmaxf(vm[u], VT::get(x[u], e));
+        vm[u] = VT::max_with(x[u], NEG_INF);
         tm = fmaxf(tm, vm[u]);
     }
     // the bound: a thread without an element counts as below everything
@@ -354,7 +352,7 @@ __global__ __launch_bounds__(NT) void k_top_chunk(Rows rows, Live live, int k, i
     int at[NV];
 #pragma unroll
     for (int u = 0; u < NV; ++u)
-        hit[u] = vm[u] >= t && v0 + (u * NT + static_cast<int>(threadIdx.x)) * VT::N < v1;
+        hit[u] = vm[u] >= t;  // (places past the chunk are told by their index)
     wave_places(hit, &sh.nvec, at);
 #pragma unroll
     for (int u = 0; u < NV; ++u)
@@ -439,7 +437,8 @@ struct MergeShared {
 };
 
 // The candidates of nch sorted lists of k keys that reach the k-th largest of the lists' heads go to sh.list;
-// returns how many.  A thread takes PER keys; q heads of each list, one a thread (of more than NT lists, the first NT heads).
+// returns how many.  A thread takes PER keys; q heads of each list, one a thread (of more than NT lists, the first
+// NT heads).
 template <int PER>
 __device__ inline int merge_list(const uint64_t *keys, int nch, int k, MergeShared &sh)
 {
@@ -820,7 +819,9 @@ Split split_of(const domino_logits &lg, int k)
     int least = (nvec + NT * MAX_NV - 1) / (NT * MAX_NV);
     if (least * k > MERGE_LIST)  // long rows and many logits of each: larger chunks
         least = (nvec + NT * LAST_NV - 1) / (NT * LAST_NV);
-    int64_t n = rows ? (TARGET_BLOCKS + rows - 1) / rows : 1;
+    // few rows are split over more blocks; each block costs the join its k candidates
+    const int blocks = k > 32 ? TARGET_BLOCKS / 2 : TARGET_BLOCKS;
+    int64_t n = rows ? (blocks + rows - 1) / rows : 1;
     n = n < nvec / (2 * NT) ? n : nvec / (2 * NT);
     n = n < MERGE_LIST / k ? n : MERGE_LIST / k;
     n = n < 64 ? n : 64;  // (a wave joins the parts of 64 at once)
@@ -882,6 +883,7 @@ Rows rows_of(const domino_logits &lg, const int32_t *n_rows)
     r.data = lg.data;
     r.bs = lg.batch_stride;
     r.rs = lg.row_stride;
+    r.B = lg.B;
     r.R = lg.R;
     r.V = lg.V;
     r.n_rows = n_rows;
@@ -903,9 +905,10 @@ static_assert((dhtop::MAX_V / 4 + NT * LAST_NV - 1) / (NT * LAST_NV) * dhtop::MA
 
 }  // namespace
 
-size_t workspace_bytes(const domino_logits &lg, int k)
+size_t workspace_bytes(const domino_logits &lg, int k, bool for_beams)
 {
-    return scratch_of(lg, k, split_of(lg, k), nullptr).bytes;
+    const Split sp = split_of(lg, k);
+    return sp.nch == 1 && !for_beams ? 0 : scratch_of(lg, k, sp, nullptr).bytes;
 }
 
 hipError_t top(const domino_logits &lg, int k, float tau, const int32_t *n_rows, void *ws, int32_t *ids,
@@ -959,7 +962,8 @@ hipError_t beam(const domino_logits &lg, const domino_beam &bm, void *ws, hipStr
     parts = parts < 1 ? 1 : parts > 64 ? 64 : parts;
     const dim3 grid(lg.B, static_cast<unsigned>(parts));
     // places a thread of a block of 512 takes of its list
-    const int lists = a.W * sp.nch, deep = lists <= 512 ? 512 / lists : 0, per = deep ? (kc + deep - 1) / deep : 1 << 30;
+    const int lists = a.W * sp.nch, deep = lists <= 512 ? 512 / lists : 0;
+    const int per = deep ? (kc + deep - 1) / deep : 1 << 30;
     if (per <= 2)
         hipLaunchKernelGGL((k_beam_merge<512, 2>), grid, dim3(512), 0, st, a);
     else if (per <= 8)

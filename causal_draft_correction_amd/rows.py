@@ -69,7 +69,8 @@ def _logits(name: str, t):
     shape = t.shape if dtype is not None else ()
     n = len(shape)
     if (n != 3 and n != 2) or not t.is_cuda:
-        raise ValueError("%s: expected a CUDA float32 or bfloat16 tensor [B, R, V] or [N, V], got %s" % (name, _said(t)))
+        raise ValueError("%s: expected a CUDA float32 or bfloat16 tensor [B, R, V] or [N, V], got %s" %
+                         (name, _said(t)))
     stride, index = t.stride(), t.get_device()
     if stride[-1] != 1 and shape[-1] != 1:
         raise ValueError("%s: expected a contiguous last dimension, got strides %s" % (name, stride))
@@ -108,13 +109,17 @@ def _known(out: Optional[dict], names: set) -> dict:
     return dict(out)
 
 
-def _scratch(given: Optional[torch.Tensor], need: int, index: int) -> torch.Tensor:
+def _scratch(given: Optional[torch.Tensor], need: int, index: int):
+    """(a tensor that holds the scratch while the call is made, its address, its bytes)."""
     if given is None:
-        return torch.empty(need, dtype=torch.uint8, device="cuda")
+        if not need:
+            return None, None, 0
+        given = torch.empty(need, dtype=torch.uint8, device="cuda")
+        return given, given.data_ptr(), need
     if not isinstance(given, torch.Tensor) or given.dtype is not torch.uint8 or given.get_device() != index or \
             not given.is_contiguous():
         raise ValueError("workspace: expected a contiguous uint8 tensor on cuda:%d, got %s" % (index, _said(given)))
-    return given
+    return given, given.data_ptr(), given.numel()
 
 
 # The current stream's handle of a GPU (torch.cuda.current_stream() builds a Stream object around it each time).
@@ -168,8 +173,8 @@ def top_logits(logits: torch.Tensor, k: int, temperature: float = 1.0, n_rows: O
     values = _output(out, "values", lead + (k,), torch.float32, gpu)
     lse = _output(out, "lse", lead, torch.float32, gpu)
     rows = None if n_rows is None else _need("n_rows", n_rows, (B,), torch.int32, gpu)
-    ws = _scratch(workspace, need, gpu)
-    _check(lib.domino_top_logits(lg, k, temperature, rows, ws.data_ptr(), ws.numel(), ids, values, lse, _stream(gpu)))
+    _ws, ws, ws_bytes = _scratch(workspace, need, gpu)
+    _check(lib.domino_top_logits(lg, k, temperature, rows, ws, ws_bytes, ids, values, lse, _stream(gpu)))
     return out
 
 
@@ -225,8 +230,8 @@ def beam_step(logits: torch.Tensor, scores: torch.Tensor, n_out: Optional[int] =
         raise ValueError("out: an output tensor is the input it is made from")
     bm = _BEAM(M, eos, T, step, state_bytes, i_scores, i_finished, i_state, i_history, o_scores, o_parent, o_token,
                o_finished, o_state, o_history)
-    ws = _scratch(workspace, need, gpu)
-    _check(lib.domino_beam_step(lg, bm, ws.data_ptr(), ws.numel(), _stream(gpu)))
+    _ws, ws, ws_bytes = _scratch(workspace, need, gpu)
+    _check(lib.domino_beam_step(lg, bm, ws, ws_bytes, _stream(gpu)))
     return out
 
 
@@ -265,8 +270,8 @@ def distill(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor, teach
             out["grad"] = torch.empty(logits.shape, dtype=logits.dtype, device="cuda")
         gd = _grad("out['grad']", out["grad"], logits)
     loss = _output(out, "loss", lead, torch.float32, gpu)
-    ws = _scratch(workspace, need, gpu)
-    _check(lib.domino_distill(lg, k, i_ids, i_values, i_lse, temperature, rows, ws.data_ptr(), ws.numel(), loss, stats,
+    _ws, ws, ws_bytes = _scratch(workspace, need, gpu)
+    _check(lib.domino_distill(lg, k, i_ids, i_values, i_lse, temperature, rows, ws, ws_bytes, loss, stats,
                               i_grad, gd, _stream(gpu)))
     return out
 

@@ -252,7 +252,8 @@ typedef struct domino_logits {
  * The k largest logits of every row, and the row's log-sum-exp: what a teacher leaves behind for
  * domino_distill, and what sampling from the head of the distribution needs.
  *   n_rows  [B] int32           NULL = all R; else rows r >= n_rows[b] are left out (not read)
- *   workspace                   >= domino_top_logits_workspace_size bytes; scratch of this call
+ *   workspace                   >= domino_top_logits_workspace_size bytes; scratch of this call (where that is
+ *                               0, NULL will do)
  * Outputs (device):
  *   ids     [B, R, k] int32     the k largest, largest first; ties go to the lowest id, a NaN counts as
  *                               larger than any number, -0 equals +0; -1 in rows left out
@@ -324,7 +325,7 @@ int domino_beam_step(const domino_logits *logits, const domino_beam *beam, void 
  * q = 0; a NaN or +inf among a row's logits makes its loss and gradient NaN.
  *   ids        [B, R, k] int32, values [B, R, k] float32, teacher_lse [B, R] float32 or NULL
  *   n_rows     [B] int32 or NULL (all R)
- *   workspace  >= domino_distill_workspace_size bytes; scratch of this call
+ *   workspace  >= domino_distill_workspace_size bytes; scratch of this call (where that is 0, NULL will do)
  *   loss       [B, R] float32
  *   stats      [B, R, 4 + k] float32: what the backward pass needs of the forward pass; NULL = not stored
  *   grad_loss  [B, R] float32 or NULL.  Given, the call also writes the gradient grad_loss[b][r] *

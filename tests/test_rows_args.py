@@ -66,9 +66,10 @@ def test_arguments_of_top_logits():
     assert top(lg(V=2 ** 19 + 1)) == EUNSUPPORTED
     for name in ("values", "lse"):
         assert top(lg(), **{name: None}) == EINVAL and top(lg(), **{name: 8}) == EINVAL
-    assert top(lg(), ws=None) == EINVAL and top(lg(), ws=8) == EINVAL
-    need = dca.top_logits_workspace_size(2, 3, 100, 5)
-    assert need > 0 and top(lg(), nbytes=need - 1) == EWORKSPACE
+    wide = lg(V=40000, rs=40000, bs=120000)
+    assert top(wide, ws=None) == EINVAL and top(wide, ws=8) == EINVAL
+    need = dca.top_logits_workspace_size(2, 3, 40000, 5)
+    assert need > 0 and top(wide, nbytes=need - 1) == EWORKSPACE
     assert b"workspace" in _lib().domino_last_error()
     assert top(lg(B=0, data=None), ws=None, ids=None) == 0
 
@@ -105,15 +106,18 @@ def test_limits_of_beam_step():
     dict(grad_loss=80, grad=lg(data=4096, rs=99)), dict(grad_loss=80, grad=lg(data=4096, bs=299)),
     dict(grad_loss=80, grad=lg(data=4096, bs=0)), dict(grad_loss=80, grad=lg(data=4096, rs=0)),
     dict(grad_loss=80, grad=lg(data=16, rs=200, bs=600)), dict(grad_loss=72, grad=lg(data=4096)),
-    dict(values=None), dict(loss=None), dict(values=24), dict(loss=24), dict(lse=24), dict(stats=24), dict(ws=24),
-    dict(ws=None)])
+    dict(values=None), dict(loss=None), dict(values=24), dict(loss=24), dict(lse=24), dict(stats=24)])
 def test_arguments_of_distill(kw):
     assert distill(lg(), **kw) == EINVAL
 
 
 def test_workspace_of_distill_and_arguments_of_backward():
-    need = dca.distill_workspace_size(2, 3, 100, 5)
-    assert need > 0 and distill(lg(), nbytes=need - 1) == EWORKSPACE
+    wide = lg(V=40000, rs=40000, bs=120000)
+    need = dca.distill_workspace_size(2, 3, 40000, 5)
+    assert need > 0 and distill(wide, nbytes=need - 1) == EWORKSPACE
+    assert distill(wide, ws=None) == EINVAL and distill(wide, ws=24) == EINVAL
+    # rows that one block takes whole need none
+    assert dca.distill_workspace_size(2, 3, 100, 5) == dca.top_logits_workspace_size(2, 3, 100, 5) == 0
     for kw in (dict(stats=None), dict(grad_loss=None), dict(stats=24), dict(grad_loss=24),
                dict(grad=lg(data=4096, V=99)), dict(grad=lg(data=16, rs=200, bs=600))):
         assert backward(lg(), **kw) == EINVAL
