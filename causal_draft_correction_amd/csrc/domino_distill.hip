@@ -11,16 +11,18 @@
 //
 // The forward pass reads a row once (k_distill_part, one block per chunk, values in registers) and joins the
 // chunks and the k entries in 64 bits (k_distill_final).  The backward pass reads it once and writes it once
-// (k_distill_grad).  All are bound by HBM bandwidth for many rows, by latency for few.
-#ifndef TUNE_NV
-#define TUNE_NV 8
-#endif
-#ifndef TUNE_TARGET
-#define TUNE_TARGET 1024
-#endif
-#ifndef TUNE_GRADNV
-#define TUNE_GRADNV 4
-#endif
+// (k_distill_grad).  Rows of at most 8 vectors a thread go through one launch (k_distill_row): 32 f32 rows of 1024,
+// loss and gradient: 6.8 us, against 3.4 + 6.2 + 3.0 us and two more launches.
+//
+// What bounds them, on one MI355X.  1024 f32 rows of 151936 (622 MB), loss and gradient: 92 + 8.5 + 194 us, 6.8 TB/s
+// read, then 6.4 TB/s read and written; a large copy reaches 4.9 TB/s.  512 bf16 rows (156 MB): 28 + 5.4 + 47 us; in
+// bfloat16 the forward pass is bound by the vector units (525 instructions and 59 exponentials a wave, 23 us of
+// issue) as much as by the bytes (24 us).  The gradient needs the row's sum, so a row is read twice, from HBM where
+// the last-level cache does not hold it.  Keeping a row on chip between the two passes, one block of 256 to 1024
+// threads per row that reads its tiles again in the opposite order, was measured at 303 to 314 us for the f32 rows
+// and 164 to 189 us for 1024 bf16 ones (three launches: 294 and 159 us): a block's passes wait for each other.
+// k_distill_grad takes 4 vectors a thread: 194 us against 200 us with 8 and 198 us with 2; k_distill_part 8: in bf16
+// 26.6 us against 28.4 us with 4.
 #define DH_NT 256
 #define DH_NS dhd
 #include "dh_rows.h"
@@ -180,7 +182,7 @@ __device__ inline void finish_row(const Rows &rows, const Teach &te, int row, in
         own[i] = valid[i] ? id[i] : -1 - (lane + 64 * i);  // (invalid ones differ from all others)
         s_id[lane + 64 * i] = own[i];
     }
-    // the entries' masses are p / p_sum; t becomes log of p where their sum is not needed for it
+    // t becomes the logarithm of an entry's mass (without L: of its mass times p_sum)
     bool live = __ballot(valid[0] || valid[1]) != 0;
     double p[2] = {0.0, 0.0};
     double t_top = L;
@@ -437,9 +439,9 @@ using namespace dhd;
 
 namespace {
 
-constexpr int TARGET_BLOCKS = TUNE_TARGET;
-constexpr int PART_NV = TUNE_NV;        // vectors a thread takes at most: forward
-constexpr int GRAD_NV = TUNE_GRADNV;    // backward
+constexpr int TARGET_BLOCKS = 1024;
+constexpr int PART_NV = 8;        // vectors a thread takes at most: forward
+constexpr int GRAD_NV = 4;    // backward
 
 int vectors(const domino_logits &lg)
 {
@@ -509,9 +511,9 @@ struct GradCall {
     template <typename T, int NV>
     void run() const
     {
-        if constexpr (NV <= GRAD_NV)
-        hipLaunchKernelGGL((k_distill_grad<T, NV>), dim3(grid), dim3(NT), 0, st, rows, k, sp.nch, sp.cvec, ids, stats,
-                           grad_loss, tau, sc, grad);
+        if constexpr (NV <= GRAD_NV)  // (its split makes no larger chunks)
+            hipLaunchKernelGGL((k_distill_grad<T, NV>), dim3(grid), dim3(NT), 0, st, rows, k, sp.nch, sp.cvec, ids,
+                               stats, grad_loss, tau, sc, grad);
     }
 };
 

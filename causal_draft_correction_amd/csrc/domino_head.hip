@@ -1173,13 +1173,14 @@ static int logits_args(const domino_logits *lg, const char *what)
     if (lg->batch_stride < 0 || lg->row_stride < 0)
         return fail(DOMINO_EINVAL, "%s: strides %lld, %lld are negative", what,
                     static_cast<long long>(lg->batch_stride), static_cast<long long>(lg->row_stride));
-    const __int128 reach = static_cast<__int128>(lg->B) * lg->batch_stride + static_cast<__int128>(lg->R) * lg->row_stride;
+    const __int128 reach =
+        static_cast<__int128>(lg->B) * lg->batch_stride + static_cast<__int128>(lg->R) * lg->row_stride;
     if (reach > (static_cast<__int128>(1) << 48))
         return fail(DOMINO_EINVAL, "%s: strides %lld, %lld reach past any memory", what,
                     static_cast<long long>(lg->batch_stride), static_cast<long long>(lg->row_stride));
-    // one block per chunk of a row, of 1024 elements at least
+    // one block of 256 threads per chunk of a row, of 1024 elements at least; a launch has at most 2^32 - 1 threads
     const long long rows = static_cast<long long>(lg->B) * lg->R;
-    if (rows > 0x7FFFFFFFll || rows * (lg->V / 1024 + 1ll) > 0x7FFFFFFFll)
+    if (rows > 0xFFFFFFll || rows * (lg->V / 1024 + 1ll) > 0xFFFFFFll)
         return fail(DOMINO_EUNSUPPORTED, "%s: %lld rows of %d are too many for one launch", what, rows, lg->V);
     return DOMINO_OK;
 }
@@ -1217,6 +1218,8 @@ static int beam_args(const domino_logits *lg, int32_t n_out)
     const int rc = logits_args(lg, "logits");
     if (rc)
         return rc;
+    if (lg->B > 0x3FFFFF)  // blocks of up to 1024 threads
+        return fail(DOMINO_EUNSUPPORTED, "B=%d too large for one launch", lg->B);
     if (lg->V > dhtop::MAX_V || lg->R > dhtop::MAX_W)
         return fail(DOMINO_EUNSUPPORTED, "W=%d beams over V=%d: at most %d over %d", lg->R, lg->V, dhtop::MAX_W,
                     dhtop::MAX_V);
@@ -1294,7 +1297,8 @@ int domino_beam_step(const domino_logits *lg, const domino_beam *bm, void *works
     if (bm->history && (bm->T < 1 || bm->step < 0 || bm->step >= bm->T))
         return fail(DOMINO_EINVAL, "step=%d outside [0, T=%d)", bm->step, bm->T);
     if (bm->state && (bm->state_bytes < 4 || bm->state_bytes % 4 || bm->state_bytes > (1ll << 40)))
-        return fail(DOMINO_EINVAL, "state_bytes=%lld is not a positive multiple of 4", static_cast<long long>(bm->state_bytes));
+        return fail(DOMINO_EINVAL, "state_bytes=%lld is not a positive multiple of 4",
+                    static_cast<long long>(bm->state_bytes));
     if (lg->B == 0)
         return DOMINO_OK;
     if ((rc = logits_data(lg, "logits")))

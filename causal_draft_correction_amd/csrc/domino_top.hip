@@ -1,24 +1,29 @@
 // The largest logits of vocabulary rows, and one step of beam search over them.
 //
 // top: for each row z of [B, R, V] logits the k largest (largest first; ties to the lowest id, NaN above every
-// number, -0 == +0) and lse = log sum_v exp(z_v / tau).  Both follow from one reading of the row, so the work
-// is bound by HBM bandwidth for many rows and by latency for few.
+// number, -0 == +0) and lse = log sum_v exp(z_v / tau).
 //
-// k_top_chunk: one block takes one chunk of a row into registers.  The k-th largest of its 256 threads' maxima is a
-// bound that at least k elements of the chunk reach and (on rows in no particular order) hardly more do.  It is
-// found by ballots, 16 bits deep.  The vectors that reach it go to LDS, their elements that do to a list, and the
-// place of each among the largest is the number of greater ones.
-// k_top_merge joins the chunks' lists of a row the same way; its bound is the k-th largest of the lists' heads.
+// k_top_chunk reads a row once, one block per chunk (256 threads, at most 8 vectors each: 32 KiB), and leaves the
+// chunk's k largest and its part of the sum.  The k-th largest of the threads' maxima bounds the k-th largest of the
+// chunk from below; the waves' shares of it are found by ballots two bits at a time, 16 bits deep.  On rows in no
+// particular order 1.5 k to 3 k elements reach the bound: their vectors go to LDS, from there they go to a list, and
+// the place of each is the number of greater ones.  Nothing is sorted and no element is compared more than twice.
+// k_top_merge joins the chunks' lists of a row in the same way; its bound is taken from the lists' heads.
+//
+// What bounds it, on one MI355X: 512 bf16 rows of 151936, k = 20 (156 MB): 33.2 + 4.6 us, 4.7 TB/s in the chunks'
+// launch, which issues 760 vector instructions a wave, 4 cycles each, and 59 exponentials at 16: about 31 us of issue
+// at 2.4 GHz, so the vector units bound bfloat16, not the 24 us the bytes take.  float32 has half the elements a
+// byte: 1024 rows of 50021, k = 16 (205 MB): 38 us in all, 5.4 TB/s.  Few rows are bound by latency: 17 f32 rows,
+// k = 64: 9.4 + 5.1 us.
+//
+// Chunks of 8 vectors a thread against 16 (half the waves in flight): 33.2 against 35.8 us for the 512 rows.  More
+// chunks a row give few rows more blocks, and the join more candidates: 17 rows, k = 64, 31 chunks 9.4 + 5.1 us,
+// 61 chunks 10.4 + 5.4 us; so half as many blocks are aimed at for k > 32.
 //
 // beam: W beams' candidates score s_w + log softmax(z_w)_v.  Within a beam they are ordered by their logits, so the
-// M best of all are among the M largest of each chunk.  k_beam_merge scores these and ranks them as k_top_merge
-// does, and writes state and history in the new order.
-#ifndef TUNE_NV
-#define TUNE_NV 8
-#endif
-#ifndef TUNE_TARGET
-#define TUNE_TARGET 1024
-#endif
+// M best of all are among the M largest of each chunk, and k_top_chunk serves both.  k_beam_merge scores them in 64
+// bits, ranks them as k_top_merge does, and writes state and history in the new order: 32 x 8 bf16 beams of 151936,
+// 16 out of each, 4 KiB of state: 20.2 + 9.0 us (78 MB); four f32 beams of one request, 8 out: 5.4 + 8.0 us, latency.
 #define DH_NT 256
 #define DH_NS dht
 #include "dh_rows.h"
@@ -26,7 +31,7 @@
 
 namespace DH_NS {
 
-constexpr int VECS = 512;          // vectors of a chunk that the LDS list holds
+constexpr int VECS = 512;          // vectors of a chunk that LDS holds
 constexpr int LIST = 1024;         // elements of a chunk that the LDS list holds
 constexpr int MERGE_LIST = 4096;   // candidates of a row's chunks
 constexpr int BEAM_LIST = 512;     // candidates of a beam step that are ranked by counting
@@ -103,7 +108,7 @@ __device__ inline uint32_t wave_bound(uint32_t v, int n)
 }
 
 // A bound that at least n of the block's values reach: the lowest of the waves' bounds for their share of n.  `red`:
-// one word a wave.  Ends with a barrier's worth of order: all threads get the same.
+// one word a wave; one barrier.  All threads get the same.
 template <int LAST, int FROM, int NTB>
 __device__ inline uint32_t block_bound(uint32_t v, int n, uint32_t *red)
 {
@@ -142,7 +147,7 @@ __device__ inline void wave_places(const bool (&hit)[N], int *count, int (&at)[N
     }
 }
 
-// Sorts list[0, n) in descending order (n <= LEN; list holds the next power of two).
+// Sorts list[0, n) in descending order; the list has room up to the next power of two.
 __device__ inline void block_sort(uint64_t *list, int n)
 {
     int len = 2;
@@ -303,6 +308,7 @@ __device__ inline void put_result(const TopOut &o, int row, int k, int place, ui
     o.values[static_cast<int64_t>(row) * k + place] = key_value(key);
 }
 
+// One chunk of a row: its k largest and its part of the row's sum, or the row's results where it is one chunk.
 template <typename T, int NV>
 __global__ __launch_bounds__(NT) void k_top_chunk(Rows rows, Live live, int k, int nch, int cvec, Scale sc,
                                                   double inv_tau, TopOut out)
@@ -375,7 +381,7 @@ __global__ __launch_bounds__(NT) void k_top_chunk(Rows rows, Live live, int k, i
     if (nvec <= VECS)
         for (int i = threadIdx.x; i < (nvec * VT::N + 63) / 64 * 64; i += NT) {
             const int j = i / VT::N, e = i % VT::N, v = j < nvec ? sh.at[j] + e : v1;
-            const float f = VT::word_at(&sh.vec[0].x, i);
+            const float f = VT::word_at(reinterpret_cast<const uint32_t *>(sh.vec), i);
             const bool one[1] = {v < v1 && f >= t};
             int place[1];
             wave_places(one, &sh.n, place);
@@ -807,8 +813,8 @@ using namespace dht;
 
 namespace {
 
-constexpr int TARGET_BLOCKS = TUNE_TARGET;
-constexpr int MAX_NV = TUNE_NV, LAST_NV = 16;
+constexpr int TARGET_BLOCKS = 1024;           // aimed at where there are few rows
+constexpr int MAX_NV = 8, LAST_NV = 16;       // vectors a thread takes at most; where the join would overflow
 
 int vec_len(int dtype) { return dtype == DOMINO_F32 ? 4 : 8; }
 
@@ -957,7 +963,8 @@ hipError_t beam(const domino_logits &lg, const domino_beam &bm, void *ws, hipStr
     a.o_finished = bm.out_finished;
     a.o_state = bm.state ? static_cast<char *>(bm.out_state) : nullptr;
     a.o_history = bm.history ? bm.out_history : nullptr;
-    // a block of its own for every 16 KiB of state, at most 64 a batch entry
+    // a block of its own for every 16 KiB of state, at most 64 a batch entry: each ranks the candidates itself, which
+    // takes less time than a launch of its own for the copies (4 us)
     int64_t parts = a.o_state ? (a.M * a.state_bytes + 16383) / 16384 : 1;
     parts = parts < 1 ? 1 : parts > 64 ? 64 : parts;
     const dim3 grid(lg.B, static_cast<unsigned>(parts));

@@ -240,7 +240,8 @@ int domino_verify_noalloc(int32_t B, int32_t K, int32_t V, const float *logits, 
  * Rows of logits [B, R, V] (R: the K+1 rows of a verified block, the K rows of a draft, the beams of a
  * search).  `data` is a device pointer of `dtype` (DOMINO_F32, or DOMINO_BF16 as raw 16-bit patterns) with
  * any element alignment; strides count elements, so that a slice of a larger tensor or a padded vocabulary
- * is passed as it is.  0 <= batch_stride, 0 <= row_stride; an output's rows may not overlap.
+ * is passed as it is.  0 <= batch_stride, 0 <= row_stride; an output's rows may not overlap.  Every call takes
+ * B R (V / 1024 + 1) < 2^24 (DOMINO_EUNSUPPORTED above).
  */
 typedef struct domino_logits {
     const void *data;

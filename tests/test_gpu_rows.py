@@ -1,10 +1,12 @@
 """GPU results of the operators over vocabulary rows against their plain 64-bit forms (rows_plain.py).
 
 Bounds, in halves of a float32 step (H = 2^-24, torch.finfo(float32).eps / 2).  A thread adds at most 128
-exponentials one after the other (128 H), a wave joins 64 in 6 steps (6 H); an exponential has one step of its own
-(2 H), and the rounding of its argument, |d| log2(e) H for the product and |d| H for d = z - m: with terms exp(-|d|)
-these weigh at most max(d exp(-d)) (1 + log2 e) < 1 H.  Chunks are joined in 64 bits.  So a log-sum-exp is within
-SUM = 140 H, before it is rounded to float32 (|lse| H).
+exponentials, so at most 128 H whatever the order of its sum, and a wave joins 64 sums in 6 steps (6 H); chunks are
+joined in 64 bits.  An exponential has one step of its own (2 H) and the rounding of its argument, |d| log2(e) H for
+d = z - m, which with terms exp(-|d|) weighs less than 1 H in a sum.  The factor log2(e) / tau is rounded for
+arguments below 1024: |log2 q| ln 2 H / 2 in a term q, at most log2(V) ln 2 / 2 < 7 H in a sum.  A sum vector by
+vector has a depth of 22, not 128, so SUM = 140 H holds all of this for a log-sum-exp, before it is rounded to
+float32 (|lse| H).
 """
 import numpy as np
 import pytest

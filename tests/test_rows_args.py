@@ -40,7 +40,8 @@ def backward(x, k=5, ids=16, stats=32, grad_loss=48, tau=1.0, n_rows=None, grad=
 SHAPES = [(dict(B=-1), EINVAL), (dict(R=0), EINVAL), (dict(V=0), EINVAL), (dict(dtype=7), EUNSUPPORTED),
           (dict(bs=-1), EINVAL), (dict(rs=-1), EINVAL), (dict(bs=2 ** 62), EINVAL),
           (dict(rs=2 ** 62), EINVAL), (dict(B=2 ** 20, R=2 ** 20), EUNSUPPORTED),
-          (dict(B=2 ** 12, R=2 ** 11, V=500000), EUNSUPPORTED), (dict(data=None), EINVAL), (dict(data=18), EINVAL)]
+          (dict(B=2 ** 12, R=2 ** 11, V=500000), EUNSUPPORTED),
+          (dict(B=2 ** 22, R=4), EUNSUPPORTED), (dict(data=None), EINVAL), (dict(data=18), EINVAL)]
 
 
 @pytest.mark.parametrize("kw,code", SHAPES)
@@ -88,6 +89,7 @@ def test_arguments_of_beam_step(kw, code):
 
 
 def test_limits_of_beam_step():
+    assert beam(lg(B=2 ** 22, R=1, bs=100)) == EUNSUPPORTED
     assert beam(lg(R=33)) == EUNSUPPORTED and beam(lg(V=2 ** 19 + 1)) == EUNSUPPORTED
     assert beam(lg(R=1, V=3), n_out=4) == EINVAL
     need = dca.beam_step_workspace_size(2, 3, 100, 4)
