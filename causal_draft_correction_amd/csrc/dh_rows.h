@@ -11,28 +11,83 @@
 
 #include <cmath>
 
+#include "../../include/domino_head.h"
+
 namespace DH_NS {
 
 constexpr float NEG_INF = -__builtin_huge_valf();
+
+// Division of block numbers (below 2^31) by a divisor known on the host: with 2^shift the power of two not below
+// it and mul = floor(2^32 (2^shift - divisor) / divisor) + 1, n / divisor = (mulhi(n, mul) + n) >> shift.
+struct Divisor {
+    uint32_t d, mul, shift;
+    __device__ uint32_t quotient(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
+inline Divisor divisor(uint32_t d)
+{
+    Divisor v;
+    v.d = d;
+    v.shift = 0;
+    while ((uint64_t(1) << v.shift) < d)
+        ++v.shift;
+    v.mul = static_cast<uint32_t>((uint64_t(1) << 32) * ((uint64_t(1) << v.shift) - d) / d + 1);
+    return v;
+}
+
+// A row: row b R + r of the launch's.
+struct Place {
+    int b, r, row;
+};
 
 // [B, R, V] logits: element strides of a batch entry and of a row; n_rows: rows of each batch entry that
 // count (NULL = all R).
 struct Rows {
     const void *data;
     int64_t bs, rs;
-    int B, R, V;
+    int R, V;
     const int32_t *n_rows;
+    bool across;    // the order of a launch's rows: through the batch entries first
+    Divisor by;     // B, or R
     __device__ bool counts(int b, int r) const { return !n_rows || r < n_rows[b]; }
-    // The row (b R + r) of the i-th place in a launch.  Where some rows may be left out, places go through the batch
-    // entries first: those left out are the later ones of a batch entry, so the blocks with work come first and
-    // spread evenly over the device (24 x 16 bf16 rows of 50021, half of them left out: 17.3 us by rows, 14.4 us so).
-    __device__ int at_place(int i, bool some = false) const { return n_rows || some ? i % B * R + i / B : i; }
+    // The i-th row of a launch.  Where some rows may be left out, these are the later ones of a batch entry: with the
+    // batch entries first, the blocks with work come first and spread evenly over the device (24 x 16 bf16 rows of
+    // 50021, half of them left out: 17.3 us by batch entries, 14.4 us across them).
+    __device__ Place place(uint32_t i) const
+    {
+        const int q = static_cast<int>(by.quotient(i)), rem = static_cast<int>(i - q * by.d);
+        const int b = across ? rem : q, r = across ? q : rem;
+        return Place{b, r, b * R + r};
+    }
 };
+inline Rows rows_of(const domino_logits &lg, const int32_t *n_rows, bool across)
+{
+    Rows r;
+    r.data = lg.data;
+    r.bs = lg.batch_stride;
+    r.rs = lg.row_stride;
+    r.R = lg.R;
+    r.V = lg.V;
+    r.n_rows = n_rows;
+    r.across = across;
+    r.by = divisor(static_cast<uint32_t>(across ? lg.B : lg.R));
+    return r;
+}
 
-// How a row is split: nch chunks of cvec vectors (the last one may hold fewer).
+// How a row is split: nch chunks of cvec vectors (the last one may hold fewer), nv of them a thread; one block each,
+// the chunks of a row one after the other.
 struct Split {
     int nch, cvec, nv;
+    Divisor by;
 };
+inline Split split(int64_t nvec, int64_t n)
+{
+    Split sp;
+    sp.cvec = static_cast<int>((nvec + n - 1) / n);
+    sp.nch = static_cast<int>((nvec + sp.cvec - 1) / sp.cvec);
+    sp.nv = (sp.cvec + NT - 1) / NT;
+    sp.by = divisor(static_cast<uint32_t>(sp.nch));
+    return sp;
+}
 
 // A vector of 16 bytes at any element address: the compiler's unaligned global loads and stores.
 template <typename T>
@@ -108,9 +163,9 @@ struct Vec<bf16s> {
 };
 
 template <typename T>
-__device__ inline const T *row_at(const Rows &rows, int b, int r)
+__device__ inline const T *row_at(const Rows &rows, const Place &at)
 {
-    return static_cast<const T *>(rows.data) + b * rows.bs + r * rows.rs;
+    return static_cast<const T *>(rows.data) + at.b * rows.bs + at.r * rows.rs;
 }
 
 // The thread's vectors of chunk c (vectors c * cvec on) for blocks of NTB threads; places past the chunk or the
@@ -128,13 +183,9 @@ __device__ inline void load_chunk(typename Vec<T>::raw (&x)[NV], const T *row, i
         const int i = u * NTB + static_cast<int>(threadIdx.x);
         // (the chunk's start is the same in every thread, the rest 32 bits)
         const auto *p = reinterpret_cast<const typename VT::mem *>(start + static_cast<uint32_t>(i) * VT::N);
-        if ((u + 1) * NTB <= n) {  // the same for the whole block
+        x[u] = VT::fill();
+        if (i < n)
             x[u] = KEEP ? *p : __builtin_nontemporal_load(p);
-        } else {
-            x[u] = VT::fill();
-            if (i < n)
-                x[u] = KEEP ? *p : __builtin_nontemporal_load(p);
-        }
     }
     const int tail = V - full * VT::N;
     if (tail && n >= 0 && n < cvec) {  // the row's last elements, element by element

@@ -14,9 +14,9 @@
 // (k_distill_grad).  Rows of at most 8 vectors a thread go through one launch (k_distill_row): 32 f32 rows of 1024,
 // loss and gradient: 6.8 us, against 3.4 + 6.2 + 3.0 us and two more launches.
 //
-// What bounds them, on one MI355X.  1024 f32 rows of 151936 (622 MB), loss and gradient: 92 + 8.5 + 194 us, 6.8 TB/s
-// read, then 6.4 TB/s read and written; a large copy reaches 4.9 TB/s.  512 bf16 rows (156 MB): 28 + 5.4 + 47 us; in
-// bfloat16 the forward pass is bound by the vector units (525 instructions and 59 exponentials a wave, 23 us of
+// What bounds them, on one MI355X.  1024 f32 rows of 151936 (622 MB), loss and gradient: 92 + 8.6 + 194 us, 6.8 TB/s
+// read, then 6.4 TB/s read and written; a large copy reaches 4.9 TB/s.  512 bf16 rows (156 MB): 30 + 5.4 + 46 us; in
+// bfloat16 the forward pass is bound by the vector units (525 instructions a wave, 59 of them exponentials: 23 us of
 // issue) as much as by the bytes (24 us).  The gradient needs the row's sum, so a row is read twice, from HBM where
 // the last-level cache does not hold it.  Keeping a row on chip between the two passes, one block of 256 to 1024
 // threads per row that reads its tiles again in the opposite order, was measured at 303 to 314 us for the f32 rows
@@ -115,13 +115,14 @@ __device__ inline Part chunk_part(typename Vec<T>::raw (&x)[NV], const Scale &sc
 
 // The chunk's part; with TAIL over the elements that no entry names.
 template <typename T, int NV, bool TAIL>
-__global__ __launch_bounds__(NT) void k_distill_part(Rows rows, Teach te, int nch, int cvec, bool keep, Scale sc,
-                                                     Part *parts)
+__global__ __launch_bounds__(NT) void k_distill_part(Rows rows, Teach te, Split sp, bool keep, Scale sc, Part *parts)
 {
     __shared__ uint32_t mask[TAIL ? MASK_WORDS<T, NV> : 1][NT];
     __shared__ float red_m[NWAVE], red_s[NWAVE];
-    const int row = rows.at_place(blockIdx.x / nch), c = blockIdx.x % nch;
-    if (!rows.counts(row / rows.R, row % rows.R))
+    const int i_row = static_cast<int>(sp.by.quotient(blockIdx.x)), c = static_cast<int>(blockIdx.x) - i_row * sp.nch;
+    const Place place = rows.place(i_row);
+    const int row = place.row, cvec = sp.cvec;
+    if (!rows.counts(place.b, place.r))
         return;
     int id = -1;
     if (static_cast<int>(threadIdx.x) < te.k)
@@ -131,7 +132,7 @@ __global__ __launch_bounds__(NT) void k_distill_part(Rows rows, Teach te, int nc
     if (!__syncthreads_or(in_row(id, rows.V)))
         return;
     typename Vec<T>::raw x[NV];
-    const T *z = row_at<T>(rows, row / rows.R, row % rows.R);
+    const T *z = row_at<T>(rows, place);
     if (keep)
         load_chunk<T, NV, NT, true>(x, z, rows.V, c, cvec);
     else
@@ -140,7 +141,7 @@ __global__ __launch_bounds__(NT) void k_distill_part(Rows rows, Teach te, int nc
         drop_named<T, NV>(x, mask, id, chunk_begin<T>(c, cvec, rows.V), chunk_begin<T>(c + 1, cvec, rows.V));
     const Part part = chunk_part<T, NV>(x, sc, red_m, red_s);
     if (threadIdx.x == 0)
-        parts[static_cast<int64_t>(row) * nch + c] = part;
+        parts[static_cast<int64_t>(row) * sp.nch + c] = part;
 }
 
 // One row, by one wave, from the parts of its nch chunks: its loss, and what the backward pass needs of it:
@@ -149,14 +150,15 @@ __global__ __launch_bounds__(NT) void k_distill_part(Rows rows, Teach te, int nc
 // lane + 64.  Everything is in 64 bits; differences are taken from the maxima, before their logarithms: rows at the
 // type's lowest value keep them.
 template <typename T>
-__device__ inline void finish_row(const Rows &rows, const Teach &te, int row, int nch, double tau, const Part *parts,
-                                  float *loss, float *st, int *s_id, double *s_p)
+__device__ inline void finish_row(const Rows &rows, const Teach &te, const Place &place, int nch, double tau,
+                                  const Part *parts, float *loss, float *st, int *s_id, double *s_p)
 {
     const double NINF = -__builtin_huge_val();
     const int lane = threadIdx.x & 63;
     const double inv_tau = 1.0 / tau;
+    const int row = place.row;
     const int64_t at = static_cast<int64_t>(row) * te.k;
-    const T *zr = row_at<T>(rows, row / rows.R, row % rows.R);
+    const T *zr = row_at<T>(rows, place);
     const Part part = first_part(parts, nch);
     int id[2] = {-1, -1};
     float value[2] = {NEG_INF, NEG_INF};
@@ -167,7 +169,7 @@ __device__ inline void finish_row(const Rows &rows, const Teach &te, int row, in
             id[i] = te.ids[at + lane + 64 * i];
             value[i] = te.values[at + lane + 64 * i];
         }
-    if (!rows.counts(row / rows.R, row % rows.R))
+    if (!rows.counts(place.b, place.r))
         id[0] = id[1] = -1;
     double t[2] = {NINF, NINF}, z[2] = {NINF, NINF};
     bool valid[2];
@@ -313,10 +315,12 @@ __global__ __launch_bounds__(NT) void k_distill_final(Rows rows, Teach te, int n
 {
     __shared__ __align__(16) int s_id[NWAVE][MAX_IDS];
     __shared__ double s_p[NWAVE][MAX_IDS];
-    const int wave = threadIdx.x >> 6, row = blockIdx.x * NWAVE + wave;
-    if (row < n_all)
-        finish_row<T>(rows, te, row, nch, tau, parts + static_cast<int64_t>(row) * nch, loss,
-                      stats ? stats + static_cast<int64_t>(row) * (HEAD + te.k) : nullptr, s_id[wave], s_p[wave]);
+    const int wave = threadIdx.x >> 6, i = blockIdx.x * NWAVE + wave;
+    if (i >= n_all)
+        return;
+    const Place place = rows.place(i);
+    finish_row<T>(rows, te, place, nch, tau, parts + static_cast<int64_t>(place.row) * nch, loss,
+                  stats ? stats + static_cast<int64_t>(place.row) * (HEAD + te.k) : nullptr, s_id[wave], s_p[wave]);
 }
 
 // The chunk's elements become A exp((z - m) / tau), or 0 in rows left out.
@@ -344,18 +348,20 @@ __device__ inline void chunk_grad(typename Vec<T>::raw (&x)[NV], bool live, floa
 
 // dloss/dz of one chunk.  The elements that entries name are written again once the block's other stores are done.
 template <typename T, int NV>
-__global__ __launch_bounds__(NT) void k_distill_grad(Rows rows, int k, int nch, int cvec, const int32_t *ids,
+__global__ __launch_bounds__(NT) void k_distill_grad(Rows rows, int k, Split sp, const int32_t *ids,
                                                      const float *stats, const float *grad_loss, float tau, Scale sc,
                                                      Rows grad)
 {
-    const int row = rows.at_place(blockIdx.x / nch), c = blockIdx.x % nch, b = row / rows.R, r = row % rows.R;
-    T *out = const_cast<T *>(row_at<T>(grad, b, r));
+    const int i_row = static_cast<int>(sp.by.quotient(blockIdx.x)), c = static_cast<int>(blockIdx.x) - i_row * sp.nch;
+    const Place place = rows.place(i_row);
+    const int row = place.row, cvec = sp.cvec;
+    T *out = const_cast<T *>(row_at<T>(grad, place));
     const float *st = stats + static_cast<int64_t>(row) * (HEAD + k);
-    const bool counts = rows.counts(b, r);
+    const bool counts = rows.counts(place.b, place.r);
     const int v0 = chunk_begin<T>(c, cvec, rows.V), v1 = chunk_begin<T>(c + 1, cvec, rows.V);
     typename Vec<T>::raw x[NV];
     if (counts)
-        load_chunk<T, NV>(x, row_at<T>(rows, b, r), rows.V, c, cvec);
+        load_chunk<T, NV>(x, row_at<T>(rows, place), rows.V, c, cvec);
     const bool live = counts && st[2] != 0.f;
     const float g = grad_loss[row] * tau;
     chunk_grad<T, NV>(x, live, st[0], st[1] * g, sc);
@@ -384,17 +390,18 @@ __global__ __launch_bounds__(NT) void k_distill_row(Rows rows, Teach te, double 
     __shared__ __align__(16) int s_id[MAX_IDS];
     __shared__ double s_p[MAX_IDS];
     __shared__ float s_stat[HEAD + MAX_IDS];
-    const int row = rows.at_place(blockIdx.x), b = row / rows.R, r = row % rows.R;
+    const Place place = rows.place(blockIdx.x);
+    const int row = place.row;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     int id = -1;
-    if (static_cast<int>(threadIdx.x) < te.k && rows.counts(b, r))
+    if (static_cast<int>(threadIdx.x) < te.k && rows.counts(place.b, place.r))
         id = te.ids[static_cast<int64_t>(row) * te.k + threadIdx.x];
     if constexpr (TAIL)
         clear_mask(mask);
     typename VT::raw x[NV];
     const bool any = __syncthreads_or(in_row(id, rows.V));
     if (any) {
-        load_chunk<T, NV>(x, row_at<T>(rows, b, r), rows.V, 0, NV * NT);
+        load_chunk<T, NV>(x, row_at<T>(rows, place), rows.V, 0, NV * NT);
         if constexpr (TAIL)
             drop_named<T, NV>(x, mask, id, 0, rows.V);  // (their gradients are written last)
         const Part got = chunk_part<T, NV>(x, sc, red_m, red_s);
@@ -404,7 +411,7 @@ __global__ __launch_bounds__(NT) void k_distill_row(Rows rows, Teach te, double 
     __syncthreads();
     if (wave == 0) {
         if (any) {
-            finish_row<T>(rows, te, row, 1, tau, &part, loss, s_stat, s_id, s_p);
+            finish_row<T>(rows, te, place, 1, tau, &part, loss, s_stat, s_id, s_p);
         } else {
             for (int i = lane; i < HEAD + te.k; i += 64)
                 s_stat[i] = 0.f;
@@ -414,7 +421,7 @@ __global__ __launch_bounds__(NT) void k_distill_row(Rows rows, Teach te, double 
     }
     __syncthreads();
     if constexpr (GRAD) {
-        T *out = const_cast<T *>(row_at<T>(grad, b, r));
+        T *out = const_cast<T *>(row_at<T>(grad, place));
         const float g = grad_loss[row] * static_cast<float>(tau);
         const bool live = s_stat[2] != 0.f;
         chunk_grad<T, NV>(x, live, s_stat[0], s_stat[1] * g, sc);
@@ -457,24 +464,7 @@ Split split_of(const domino_logits &lg, int max_nv)
     int64_t n = rows ? (TARGET_BLOCKS + rows - 1) / rows : 1;
     n = n < nvec / NT ? n : nvec / NT;
     n = n > least ? n : least;
-    Split sp;
-    sp.cvec = static_cast<int>((nvec + n - 1) / n);
-    sp.nch = (nvec + sp.cvec - 1) / sp.cvec;
-    sp.nv = (sp.cvec + NT - 1) / NT;
-    return sp;
-}
-
-Rows rows_of(const domino_logits &lg, const int32_t *n_rows)
-{
-    Rows r;
-    r.data = lg.data;
-    r.bs = lg.batch_stride;
-    r.rs = lg.row_stride;
-    r.B = lg.B;
-    r.R = lg.R;
-    r.V = lg.V;
-    r.n_rows = n_rows;
-    return r;
+    return split(nvec, n);
 }
 
 struct PartCall {
@@ -490,11 +480,11 @@ struct PartCall {
     void run() const
     {
         if (te.lse)
-            hipLaunchKernelGGL((k_distill_part<T, NV, true>), dim3(grid), dim3(NT), 0, st, rows, te, sp.nch, sp.cvec,
-                               keep, sc, parts);
+            hipLaunchKernelGGL((k_distill_part<T, NV, true>), dim3(grid), dim3(NT), 0, st, rows, te, sp, keep, sc,
+                               parts);
         else
-            hipLaunchKernelGGL((k_distill_part<T, NV, false>), dim3(grid), dim3(NT), 0, st, rows, te, sp.nch, sp.cvec,
-                               keep, sc, parts);
+            hipLaunchKernelGGL((k_distill_part<T, NV, false>), dim3(grid), dim3(NT), 0, st, rows, te, sp, keep, sc,
+                               parts);
     }
 };
 
@@ -512,8 +502,8 @@ struct GradCall {
     void run() const
     {
         if constexpr (NV <= GRAD_NV)  // (its split makes no larger chunks)
-            hipLaunchKernelGGL((k_distill_grad<T, NV>), dim3(grid), dim3(NT), 0, st, rows, k, sp.nch, sp.cvec, ids,
-                               stats, grad_loss, tau, sc, grad);
+            hipLaunchKernelGGL((k_distill_grad<T, NV>), dim3(grid), dim3(NT), 0, st, rows, k, sp, ids, stats, grad_loss,
+                               tau, sc, grad);
     }
 };
 
@@ -586,9 +576,9 @@ bool by_rows(const domino_logits &lg, const Teacher &t, float tau, const int32_t
     RowCall c;
     if (vectors(lg) > NT * PART_NV)
         return false;
-    c.sp = Split{1, vectors(lg), (vectors(lg) + NT - 1) / NT};
-    c.rows = rows_of(lg, n_rows);
-    c.grad = grad ? rows_of(*grad, nullptr) : Rows{};
+    c.sp = split(vectors(lg), 1);
+    c.rows = rows_of(lg, n_rows, n_rows != nullptr);
+    c.grad = grad ? rows_of(*grad, nullptr, false) : Rows{};
     c.te = Teach{t.k, t.ids, t.values, t.lse};
     c.tau = tau;
     c.sc = scale_of(tau);
@@ -612,7 +602,7 @@ hipError_t forward(const domino_logits &lg, const Teacher &t, float tau, const i
     if (by_rows(lg, t, tau, n_rows, loss, stats, nullptr, nullptr, st))
         return hipGetLastError();
     PartCall c;
-    c.rows = rows_of(lg, n_rows);
+    c.rows = rows_of(lg, n_rows, n_rows != nullptr);
     c.te = Teach{t.k, t.ids, t.values, t.lse};
     c.sp = split_of(lg, PART_NV);
     c.sc = scale_of(tau);
@@ -646,8 +636,8 @@ hipError_t backward(const domino_logits &lg, int k, const int32_t *ids, const fl
                     float tau, const int32_t *n_rows, const domino_logits &grad, hipStream_t st)
 {
     GradCall c;
-    c.rows = rows_of(lg, n_rows);
-    c.grad = rows_of(grad, nullptr);
+    c.rows = rows_of(lg, n_rows, n_rows != nullptr);
+    c.grad = rows_of(grad, nullptr, false);
     c.k = k;
     c.ids = ids;
     c.stats = stats;

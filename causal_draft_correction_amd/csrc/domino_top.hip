@@ -10,20 +10,20 @@
 // the place of each is the number of greater ones.  Nothing is sorted and no element is compared more than twice.
 // k_top_merge joins the chunks' lists of a row in the same way; its bound is taken from the lists' heads.
 //
-// What bounds it, on one MI355X: 512 bf16 rows of 151936, k = 20 (156 MB): 33.2 + 4.6 us, 4.7 TB/s in the chunks'
-// launch, which issues 760 vector instructions a wave, 4 cycles each, and 59 exponentials at 16: about 31 us of issue
-// at 2.4 GHz, so the vector units bound bfloat16, not the 24 us the bytes take.  float32 has half the elements a
-// byte: 1024 rows of 50021, k = 16 (205 MB): 38 us in all, 5.4 TB/s.  Few rows are bound by latency: 17 f32 rows,
-// k = 64: 9.4 + 5.1 us.
+// What bounds it, on one MI355X: 512 bf16 rows of 151936, k = 20 (156 MB): 32.0 + 4.7 us, 4.9 TB/s in the chunks'
+// launch, which issues 708 vector instructions a wave (59 of them exponentials, at 16 cycles, the others at 4): 30 us
+// of issue at 2.4 GHz, so the vector units bound bfloat16, not the 24 us the bytes take.  float32 has half the elements
+// a byte: 1024 rows of 50021, k = 16 (205 MB): 38 us in all, 5.4 TB/s.  Few rows are bound by latency: 17 f32 rows,
+// k = 64: 9.0 + 5.3 us.
 //
-// Chunks of 8 vectors a thread against 16 (half the waves in flight): 33.2 against 35.8 us for the 512 rows.  More
-// chunks a row give few rows more blocks, and the join more candidates: 17 rows, k = 64, 31 chunks 9.4 + 5.1 us,
+// Chunks of 8 vectors a thread against 16 (half the waves in flight): 34.3 against 35.8 us for the 512 rows.  More
+// chunks a row give few rows more blocks, and the join more candidates: 17 rows, k = 64, 31 chunks 8.9 + 5.6 us,
 // 61 chunks 10.4 + 5.4 us; so half as many blocks are aimed at for k > 32.
 //
 // beam: W beams' candidates score s_w + log softmax(z_w)_v.  Within a beam they are ordered by their logits, so the
 // M best of all are among the M largest of each chunk, and k_top_chunk serves both.  k_beam_merge scores them in 64
 // bits, ranks them as k_top_merge does, and writes state and history in the new order: 32 x 8 bf16 beams of 151936,
-// 16 out of each, 4 KiB of state: 20.2 + 9.0 us (78 MB); four f32 beams of one request, 8 out: 5.4 + 8.0 us, latency.
+// 16 out of each, 4 KiB of state: 19.4 + 9.1 us (71 MB); four f32 beams of one request, 8 out: 5.2 + 8.2 us, latency.
 #define DH_NT 256
 #define DH_NS dht
 #include "dh_rows.h"
@@ -46,14 +46,13 @@ struct Live {
     const float *scores;
     const uint8_t *finished;
 };
-__device__ inline bool row_live(const Rows &rows, const Live &lv, int row)
+__device__ inline bool row_live(const Rows &rows, const Live &lv, const Place &at)
 {
-    const int b = row / rows.R, r = row % rows.R;
     if (lv.scores) {
-        const float s = lv.scores[row];
-        return s > NEG_INF && s < -NEG_INF && !(lv.finished && lv.finished[row]);
+        const float s = lv.scores[at.row];
+        return s > NEG_INF && s < -NEG_INF && !(lv.finished && lv.finished[at.row]);
     }
-    return rows.counts(b, r);
+    return rows.counts(at.b, at.r);
 }
 
 // Unsigned words in the order of finite and infinite floats, 0 below all of them.
@@ -310,15 +309,18 @@ __device__ inline void put_result(const TopOut &o, int row, int k, int place, ui
 
 // One chunk of a row: its k largest and its part of the row's sum, or the row's results where it is one chunk.
 template <typename T, int NV>
-__global__ __launch_bounds__(NT) void k_top_chunk(Rows rows, Live live, int k, int nch, int cvec, Scale sc,
+__global__ __launch_bounds__(NT) void k_top_chunk(Rows rows, Live live, int k, Split sp, Scale sc,
                                                   double inv_tau, TopOut out)
 {
     typedef Vec<T> VT;
     __shared__ ChunkShared sh;
-    const int row = rows.at_place(blockIdx.x / nch, live.scores != nullptr), c = blockIdx.x % nch;
+    const int nch = sp.nch, cvec = sp.cvec, i_row = static_cast<int>(sp.by.quotient(blockIdx.x));
+    const int c = static_cast<int>(blockIdx.x) - i_row * nch;
+    const Place place = rows.place(i_row);
+    const int row = place.row;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const bool direct = nch == 1 && out.ids;
-    if (!row_live(rows, live, row)) {
+    if (!row_live(rows, live, place)) {
         if (direct) {
             for (int i = threadIdx.x; i < k; i += NT) {
                 out.ids[static_cast<int64_t>(row) * k + i] = -1;
@@ -329,7 +331,7 @@ __global__ __launch_bounds__(NT) void k_top_chunk(Rows rows, Live live, int k, i
         }
         return;
     }
-    const T *z = row_at<T>(rows, row / rows.R, row % rows.R);
+    const T *z = row_at<T>(rows, place);
     const int v0 = chunk_begin<T>(c, cvec, rows.V), v1 = chunk_begin<T>(c + 1, cvec, rows.V);
     typename VT::raw x[NV];
     load_chunk<T, NV>(x, z, rows.V, c, cvec);
@@ -383,18 +385,18 @@ __global__ __launch_bounds__(NT) void k_top_chunk(Rows rows, Live live, int k, i
             const int j = i / VT::N, e = i % VT::N, v = j < nvec ? sh.at[j] + e : v1;
             const float f = VT::word_at(reinterpret_cast<const uint32_t *>(sh.vec), i);
             const bool one[1] = {v < v1 && f >= t};
-            int place[1];
-            wave_places(one, &sh.n, place);
-            if (one[0] && place[0] < LIST)
-                sh.list[place[0]] = argmax_key(f, static_cast<uint32_t>(v));
+            int to[1];
+            wave_places(one, &sh.n, to);
+            if (one[0] && to[0] < LIST)
+                sh.list[to[0]] = argmax_key(f, static_cast<uint32_t>(v));
         }
     __syncthreads();
     const int64_t slot = static_cast<int64_t>(row) * nch + c;
-    auto emit = [&](int place, uint64_t key) {
+    auto emit = [&](int at, uint64_t key) {
         if (direct)
-            put_result(out, row, k, place, key);
+            put_result(out, row, k, at, key);
         else
-            out.keys[slot * k + place] = key;
+            out.keys[slot * k + at] = key;
     };
     const int n = sh.n;
     bool infinite = false;
@@ -482,8 +484,9 @@ template <int PER>
 __global__ __launch_bounds__(NT) void k_top_merge(Rows rows, Live live, int k, int nch, double inv_tau, TopOut out)
 {
     __shared__ MergeShared sh;
-    const int row = blockIdx.x;
-    if (!row_live(rows, live, row)) {
+    const Place place = rows.place(blockIdx.x);
+    const int row = place.row;
+    if (!row_live(rows, live, place)) {
         for (int i = threadIdx.x; i < k; i += NT) {
             out.ids[static_cast<int64_t>(row) * k + i] = -1;
             out.values[static_cast<int64_t>(row) * k + i] = NEG_INF;
@@ -495,7 +498,7 @@ __global__ __launch_bounds__(NT) void k_top_merge(Rows rows, Live live, int k, i
     const int64_t slot = static_cast<int64_t>(row) * nch;
     const Part part = first_part(out.parts + slot, nch);
     const int n = merge_list<PER>(out.keys + slot * k, nch, k, sh);
-    emit_largest(sh.list, sh.place, n, k, [&](int place, uint64_t key) { put_result(out, row, k, place, key); });
+    emit_largest(sh.list, sh.place, n, k, [&](int at, uint64_t key) { put_result(out, row, k, at, key); });
     if (threadIdx.x >= NT - 64) {  // the wave with the least to rank
         float m;
         double s;
@@ -832,13 +835,7 @@ Split split_of(const domino_logits &lg, int k)
     n = n < MERGE_LIST / k ? n : MERGE_LIST / k;
     n = n < 64 ? n : 64;  // (a wave joins the parts of 64 at once)
     n = n > least ? n : least;
-    Split sp;
-    sp.cvec = static_cast<int>((nvec + n - 1) / n);
-    sp.nch = (nvec + sp.cvec - 1) / sp.cvec;
-    sp.nv = 1;
-    while (sp.nv * NT < sp.cvec)
-        sp.nv *= 2;
-    return sp;
+    return split(nvec, n);
 }
 
 size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
@@ -847,8 +844,8 @@ template <typename T, int NV>
 void launch_chunk(const Rows &rows, const Live &live, int k, const Split &sp, float tau, const TopOut &out,
                   unsigned grid, hipStream_t st)
 {
-    hipLaunchKernelGGL((k_top_chunk<T, NV>), dim3(grid), dim3(NT), 0, st, rows, live, k, sp.nch, sp.cvec,
-                       scale_of(tau), 1.0 / static_cast<double>(tau), out);
+    hipLaunchKernelGGL((k_top_chunk<T, NV>), dim3(grid), dim3(NT), 0, st, rows, live, k, sp, scale_of(tau),
+                       1.0 / static_cast<double>(tau), out);
 }
 
 template <typename T>
@@ -883,19 +880,6 @@ Scratch scratch_of(const domino_logits &lg, int k, const Split &sp, void *ws)
     return s;
 }
 
-Rows rows_of(const domino_logits &lg, const int32_t *n_rows)
-{
-    Rows r;
-    r.data = lg.data;
-    r.bs = lg.batch_stride;
-    r.rs = lg.row_stride;
-    r.B = lg.B;
-    r.R = lg.R;
-    r.V = lg.V;
-    r.n_rows = n_rows;
-    return r;
-}
-
 void chunks(const domino_logits &lg, const Rows &rows, const Live &live, int k, float tau, const Split &sp,
             const TopOut &out, hipStream_t st)
 {
@@ -923,7 +907,7 @@ hipError_t top(const domino_logits &lg, int k, float tau, const int32_t *n_rows,
     const Split sp = split_of(lg, k);
     const Scratch s = scratch_of(lg, k, sp, ws);
     const TopOut out = {s.keys, s.parts, ids, values, lse};
-    const Rows rows = rows_of(lg, n_rows);
+    const Rows rows = rows_of(lg, n_rows, n_rows != nullptr);
     const Live live = {nullptr, nullptr};
     chunks(lg, rows, live, k, tau, sp, out, st);
     const hipError_t e = hipGetLastError();
@@ -944,7 +928,7 @@ hipError_t beam(const domino_logits &lg, const domino_beam &bm, void *ws, hipStr
     const Split sp = split_of(lg, kc);
     const Scratch s = scratch_of(lg, kc, sp, ws);
     const TopOut out = {s.keys, s.parts, nullptr, nullptr, nullptr};
-    chunks(lg, rows_of(lg, nullptr), Live{bm.scores, bm.finished}, kc, 1.f, sp, out, st);
+    chunks(lg, rows_of(lg, nullptr, true), Live{bm.scores, bm.finished}, kc, 1.f, sp, out, st);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
