@@ -11,8 +11,8 @@
 //
 // The forward pass reads a row once (k_distill_part, one block per chunk, values in registers) and joins the
 // chunks and the k entries in 64 bits (k_distill_final).  The backward pass reads it once and writes it once
-// (k_distill_grad).  Rows of at most 8 vectors a thread go through one launch (k_distill_row): 32 f32 rows of 1024,
-// loss and gradient: 6.8 us, against 3.4 + 6.2 + 3.0 us and two more launches.
+// (k_distill_grad).  Rows that one block can hold go through one launch (k_distill_row): 32 f32 rows of 1024, loss and
+// gradient: 6.8 us, against 3.4 + 6.2 + 3.0 us and two more launches.
 //
 // What bounds them, on one MI355X.  1024 f32 rows of 151936 (622 MB), loss and gradient: 92 + 8.6 + 194 us, 6.8 TB/s
 // read, then 6.4 TB/s read and written; a large copy reaches 4.9 TB/s.  512 bf16 rows (156 MB): 30 + 5.4 + 46 us; in
@@ -45,8 +45,8 @@ __device__ inline bool in_row(int id, int V) { return id >= 0 && id < V; }
 template <typename T, int NV>
 constexpr int MASK_WORDS = (NV * Vec<T>::N + 31) / 32;
 
-template <int WORDS>
-__device__ inline void clear_mask(uint32_t (&mask)[WORDS][NT])
+template <int WORDS, int NTB>
+__device__ inline void clear_mask(uint32_t (&mask)[WORDS][NTB])
 {
 #pragma unroll
     for (int i = 0; i < WORDS; ++i)
@@ -55,13 +55,13 @@ __device__ inline void clear_mask(uint32_t (&mask)[WORDS][NT])
 
 // Named elements of the chunk [v0, v1) become -inf.  `id`: the thread's entry, or -1.  The mask was cleared before
 // the block's last barrier.
-template <typename T, int NV, int WORDS>
-__device__ inline void drop_named(typename Vec<T>::raw (&x)[NV], uint32_t (&mask)[WORDS][NT], int id, int v0, int v1)
+template <typename T, int NV, int WORDS, int NTB>
+__device__ inline void drop_named(typename Vec<T>::raw (&x)[NV], uint32_t (&mask)[WORDS][NTB], int id, int v0, int v1)
 {
     typedef Vec<T> VT;
     if (id >= v0 && id < v1) {
-        const int o = id - v0, i = o / VT::N, bit = i / NT * VT::N + o % VT::N;
-        atomicOr(&mask[bit >> 5][i % NT], 1u << (bit & 31));
+        const int o = id - v0, i = o / VT::N, bit = i / NTB * VT::N + o % VT::N;
+        atomicOr(&mask[bit >> 5][i % NTB], 1u << (bit & 31));
     }
     __syncthreads();
     uint32_t mine[WORDS], any = 0;
@@ -83,7 +83,7 @@ __device__ inline void drop_named(typename Vec<T>::raw (&x)[NV], uint32_t (&mask
 }
 
 // The block's maximum and sum of exponentials (a NaN or +inf makes both NaN: so the row's), in every thread.
-template <typename T, int NV>
+template <typename T, int NV, int NTB>
 __device__ inline Part chunk_part(typename Vec<T>::raw (&x)[NV], const Scale &sc, float *red_m, float *red_s)
 {
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -97,7 +97,7 @@ __device__ inline Part chunk_part(typename Vec<T>::raw (&x)[NV], const Scale &sc
     __syncthreads();
     m = red_m[0];
 #pragma unroll
-    for (int w = 1; w < NWAVE; ++w)
+    for (int w = 1; w < NTB / 64; ++w)
         m = fmaxf(m, red_m[w]);
     const Expo ex(m > NEG_INF ? m : 0.f, sc);
     float s = ex.small ? sum_exps<T, true>(x, ex, sc) : sum_exps<T, false>(x, ex, sc);
@@ -107,7 +107,7 @@ __device__ inline Part chunk_part(typename Vec<T>::raw (&x)[NV], const Scale &sc
     __syncthreads();
     double total = 0.0;
 #pragma unroll
-    for (int w = 0; w < NWAVE; ++w)
+    for (int w = 0; w < NTB / 64; ++w)
         total += static_cast<double>(red_s[w]);
     total *= ex.fix(sc);
     return Part{total != total ? __builtin_nanf("") : m, static_cast<float>(total)};
@@ -139,7 +139,7 @@ __global__ __launch_bounds__(NT) void k_distill_part(Rows rows, Teach te, Split 
         load_chunk<T, NV>(x, z, rows.V, c, cvec);
     if constexpr (TAIL)
         drop_named<T, NV>(x, mask, id, chunk_begin<T>(c, cvec, rows.V), chunk_begin<T>(c + 1, cvec, rows.V));
-    const Part part = chunk_part<T, NV>(x, sc, red_m, red_s);
+    const Part part = chunk_part<T, NV, NT>(x, sc, red_m, red_s);
     if (threadIdx.x == 0)
         parts[static_cast<int64_t>(row) * sp.nch + c] = part;
 }
@@ -378,15 +378,15 @@ __global__ __launch_bounds__(NT) void k_distill_grad(Rows rows, int k, Split sp,
 }
 
 // A row of at most NV vectors a thread, by one block: loss, and with GRAD its gradient (else the statistics for a
-// later backward pass).  The row stays in registers from its maximum to its gradient.
-template <typename T, int NV, bool TAIL, bool GRAD>
-__global__ __launch_bounds__(NT) void k_distill_row(Rows rows, Teach te, double tau, Scale sc, float *loss,
+// later backward pass).  The row stays in registers from its maximum to its gradient: it is read once.
+template <typename T, int NTB, int NV, bool TAIL, bool GRAD>
+__global__ __launch_bounds__(NTB) void k_distill_row(Rows rows, Teach te, double tau, Scale sc, float *loss,
                                                     float *stats, const float *grad_loss, Rows grad)
 {
     typedef Vec<T> VT;
-    __shared__ float red_m[NWAVE], red_s[NWAVE];
+    __shared__ float red_m[NTB / 64], red_s[NTB / 64];
     __shared__ Part part;
-    __shared__ uint32_t mask[TAIL ? MASK_WORDS<T, NV> : 1][NT];
+    __shared__ uint32_t mask[TAIL ? MASK_WORDS<T, NV> : 1][NTB];
     __shared__ __align__(16) int s_id[MAX_IDS];
     __shared__ double s_p[MAX_IDS];
     __shared__ float s_stat[HEAD + MAX_IDS];
@@ -401,10 +401,10 @@ __global__ __launch_bounds__(NT) void k_distill_row(Rows rows, Teach te, double 
     typename VT::raw x[NV];
     const bool any = __syncthreads_or(in_row(id, rows.V));
     if (any) {
-        load_chunk<T, NV>(x, row_at<T>(rows, place), rows.V, 0, NV * NT);
+        load_chunk<T, NV, NTB>(x, row_at<T>(rows, place), rows.V, 0, NV * NTB);
         if constexpr (TAIL)
             drop_named<T, NV>(x, mask, id, 0, rows.V);  // (their gradients are written last)
-        const Part got = chunk_part<T, NV>(x, sc, red_m, red_s);
+        const Part got = chunk_part<T, NV, NTB>(x, sc, red_m, red_s);
         if (threadIdx.x == 0)
             part = got;
     }
@@ -425,7 +425,7 @@ __global__ __launch_bounds__(NT) void k_distill_row(Rows rows, Teach te, double 
         const float g = grad_loss[row] * static_cast<float>(tau);
         const bool live = s_stat[2] != 0.f;
         chunk_grad<T, NV>(x, live, s_stat[0], s_stat[1] * g, sc);
-        store_chunk<T, NV>(x, out, 0, rows.V);
+        store_chunk<T, NV, NTB>(x, out, 0, rows.V);
         if (live) {
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the block's stores are done
             __syncthreads();
@@ -433,7 +433,7 @@ __global__ __launch_bounds__(NT) void k_distill_row(Rows rows, Teach te, double 
                 VT::put(out + id, s_stat[HEAD + threadIdx.x] * g);
         }
     } else if (stats) {
-        for (int i = threadIdx.x; i < HEAD + te.k; i += NT)
+        for (int i = threadIdx.x; i < HEAD + te.k; i += NTB)
             stats[static_cast<int64_t>(row) * (HEAD + te.k) + i] = s_stat[i];
     }
 }
@@ -454,6 +454,17 @@ int vectors(const domino_logits &lg)
 {
     const int per = lg.dtype == DOMINO_F32 ? 4 : 8;
     return static_cast<int>((static_cast<int64_t>(lg.V) + per - 1) / per);
+}
+
+// Rows that one block takes whole: up to 8 vectors for each of 1024 threads.  For the gradient always (read once
+// instead of twice): 16, 256 and 1024 f32 rows of 32000 in 12.7, 17.6 and 66.0 us a call, in three launches 17.8, 25.5
+// and 70.5 us; 1024 bf16 rows of 64000 72.7 and 72.0 us.  For the loss alone, where blocks of more than 512 threads
+// would wait for each other's phases, up to one row a compute unit: 256 and 1024 f32 rows of 32000 in 12.8 and 42.5
+// us, in two launches 15.9 and 30.5 us.
+bool whole_rows(const domino_logits &lg, bool grad)
+{
+    const int nvec = vectors(lg);
+    return nvec <= 512 * 8 || (nvec <= 1024 * 8 && (grad || static_cast<int64_t>(lg.B) * lg.R <= 256));
 }
 
 Split split_of(const domino_logits &lg, int max_nv)
@@ -510,30 +521,42 @@ struct GradCall {
 struct RowCall {
     Rows rows, grad;
     Teach te;
-    Split sp;
+    int nvec;
     float tau;
     Scale sc;
     float *loss, *stats;
     const float *grad_loss;
     unsigned n;
     hipStream_t st;
-    template <typename T, int NV, bool TAIL>
+    template <typename T, int NTB, int NV, bool TAIL>
     void launch() const
     {
         if (grad_loss)
-            hipLaunchKernelGGL((k_distill_row<T, NV, TAIL, true>), dim3(n), dim3(NT), 0, st, rows, te,
+            hipLaunchKernelGGL((k_distill_row<T, NTB, NV, TAIL, true>), dim3(n), dim3(NTB), 0, st, rows, te,
                                static_cast<double>(tau), sc, loss, stats, grad_loss, grad);
         else
-            hipLaunchKernelGGL((k_distill_row<T, NV, TAIL, false>), dim3(n), dim3(NT), 0, st, rows, te,
+            hipLaunchKernelGGL((k_distill_row<T, NTB, NV, TAIL, false>), dim3(n), dim3(NTB), 0, st, rows, te,
                                static_cast<double>(tau), sc, loss, stats, grad_loss, grad);
     }
-    template <typename T, int NV>
+    template <typename T, int NTB, int NV>
     void run() const
     {
         if (te.lse)
-            launch<T, NV, true>();
+            launch<T, NTB, NV, true>();
         else
-            launch<T, NV, false>();
+            launch<T, NTB, NV, false>();
+    }
+    template <typename T>
+    void pick() const
+    {
+        if (nvec <= 256 * 2)
+            run<T, 256, 2>();
+        else if (nvec <= 256 * 8)
+            run<T, 256, 8>();
+        else if (nvec <= 512 * 8)
+            run<T, 512, 8>();
+        else
+            run<T, 1024, 8>();
     }
 };
 
@@ -562,21 +585,21 @@ size_t parts_bytes(const domino_logits &lg)
 
 size_t workspace_bytes(const domino_logits &lg, int k)
 {
-    if (vectors(lg) <= NT * PART_NV)
+    if (whole_rows(lg, false))
         return 0;
     return parts_bytes(lg) + static_cast<size_t>(lg.B) * lg.R * (HEAD + k) * sizeof(float);
 }
 
 namespace {
 
-// Loss, and gradient or statistics, in one launch.  False: the rows are too long for it.
+// Loss, and gradient or statistics, in one launch.  False: not for these rows.
 bool by_rows(const domino_logits &lg, const Teacher &t, float tau, const int32_t *n_rows, float *loss, float *stats,
              const float *grad_loss, const domino_logits *grad, hipStream_t st)
 {
     RowCall c;
-    if (vectors(lg) > NT * PART_NV)
+    if (!whole_rows(lg, grad_loss))
         return false;
-    c.sp = split(vectors(lg), 1);
+    c.nvec = vectors(lg);
     c.rows = rows_of(lg, n_rows, n_rows != nullptr);
     c.grad = grad ? rows_of(*grad, nullptr, false) : Rows{};
     c.te = Teach{t.k, t.ids, t.values, t.lse};
@@ -588,9 +611,9 @@ bool by_rows(const domino_logits &lg, const Teacher &t, float tau, const int32_t
     c.n = static_cast<unsigned>(lg.B) * static_cast<unsigned>(lg.R);
     c.st = st;
     if (lg.dtype == DOMINO_F32)
-        pick<float>(c);
+        c.pick<float>();
     else
-        pick<bf16s>(c);
+        c.pick<bf16s>();
     return true;
 }
 

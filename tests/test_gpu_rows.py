@@ -307,6 +307,8 @@ def check_distill(z, ids, values, lse, tau, n_rows=None, label=""):
     (2, 1, 1025, 64, 0, 3, 2.0), (3, 2, 5003, 33, 1, 0, 1.0), (1, 1, 16384, 1, 0, 0, 1.0),
     (1, 2, 40001, 100, 7, 1, 3.0),
     (1, 1, 151936, 64, 0, 0, 1.0), (33, 40, 2049, 8, 0, 0, 1.0), (13, 16, 20011, 9, 0, 1, 1.0),
+    (1, 2, 32768, 17, 0, 0, 1.0), (1, 1, 32769, 3, 0, 1, 1.0), (9, 31, 16411, 33, 0, 0, 2.0),
+    (1, 2, 65551, 128, 3, 0, 1.0),
 ])
 def test_distill(B, R, V, k, pad, shift, tau, tail, dtype):
     z = rows(B, R, V, dtype, 3 * V + k, pad, shift)
@@ -316,7 +318,7 @@ def test_distill(B, R, V, k, pad, shift, tau, tail, dtype):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("tail", [False, True])
 def test_distill_of_special_rows(tail, dtype):
-    for V, k in ((300, 20), (9001, 128)):
+    for V, k in ((300, 20), (9001, 128), (70001, 40)):
         named = special_rows(V, dtype)
         z = torch.stack(list(named.values())).cuda().view(1, len(named), V)
         calm = rows(1, len(named), V, dtype, 1)
