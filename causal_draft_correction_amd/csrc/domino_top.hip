@@ -8,7 +8,8 @@
 // chunk from below; the waves' shares of it are found by ballots two bits at a time, 16 bits deep.  On rows in no
 // particular order 1.5 k to 3 k elements reach the bound: their vectors go to LDS, from there they go to a list, and
 // the place of each is the number of greater ones.  Nothing is sorted and no element is compared more than twice.
-// k_top_merge joins the chunks' lists of a row in the same way; its bound is taken from the lists' heads.
+// k_top_merge joins the chunks' lists of a row in the same way; its bound is taken from the lists' heads.  A row that
+// one block can hold (up to 1024 threads) is one chunk, and needs no join.
 //
 // What bounds it, on one MI355X: 512 bf16 rows of 151936, k = 20 (156 MB): 32.0 + 4.7 us, 4.9 TB/s in the chunks'
 // launch, which issues 708 vector instructions a wave (59 of them exponentials, at 16 cycles, the others at 4): 30 us
@@ -147,17 +148,18 @@ __device__ inline void wave_places(const bool (&hit)[N], int *count, int (&at)[N
 }
 
 // Sorts list[0, n) in descending order; the list has room up to the next power of two.
+template <int NTB>
 __device__ inline void block_sort(uint64_t *list, int n)
 {
     int len = 2;
     while (len < n)
         len <<= 1;
-    for (int i = n + static_cast<int>(threadIdx.x); i < len; i += NT)
+    for (int i = n + static_cast<int>(threadIdx.x); i < len; i += NTB)
         list[i] = 0;
     for (int size = 2; size <= len; size <<= 1)
         for (int step = size >> 1; step; step >>= 1) {
             __syncthreads();
-            for (int i = threadIdx.x; i < len / 2; i += NT) {
+            for (int i = threadIdx.x; i < len / 2; i += NTB) {
                 const int a = 2 * i - (i & (step - 1)), b = a + step;
                 const uint64_t x = list[a], y = list[b];
                 if ((x < y) == ((a & size) == 0))
@@ -168,22 +170,22 @@ __device__ inline void block_sort(uint64_t *list, int n)
 }
 
 // Hands the k largest of list[0, n) to emit(place, key), largest first; places past n get key 0.
-template <typename F>
+template <int NTB, typename F>
 __device__ inline void emit_largest(uint64_t *list, int *place, int n, int k, F emit)
 {
     if (n > COUNT_MAX) {
-        block_sort(list, n);
-        for (int i = threadIdx.x; i < k; i += NT)
+        block_sort<NTB>(list, n);
+        for (int i = threadIdx.x; i < k; i += NTB)
             emit(i, list[i]);
         return;
     }
-    // 2^shift threads take one key each, and 256 / 2^shift a slice of the others
+    // 2^shift threads take one key each, and NTB / 2^shift a slice of the others
     const int t = threadIdx.x, shift = n <= 64 ? 6 : n <= 128 ? 7 : 8;
     place[t] = 0;
     if (t == 0 && (n & 1))
         list[n] = 0;
     __syncthreads();
-    const int i = t & ((1 << shift) - 1), slices = NT >> shift, pairs = (n + 1) / 2;
+    const int i = t & ((1 << shift) - 1), slices = NTB >> shift, pairs = (n + 1) / 2;
     const int len = (pairs + slices - 1) / slices, j0 = (t >> shift) * len, j1 = j0 + len < pairs ? j0 + len : pairs;
     if (i < n) {
         const uint64_t key = list[i];
@@ -200,31 +202,32 @@ __device__ inline void emit_largest(uint64_t *list, int *place, int n, int k, F 
     __syncthreads();
     if (t < n && place[t] < k)
         emit(place[t], list[t]);
-    for (int at = n + t; at < k; at += NT)
+    for (int at = n + t; at < k; at += NTB)
         emit(at, 0ull);
 }
 
+template <int NTB>
 struct ChunkShared {
     alignas(16) uint64_t list[LIST];
     uint4 vec[VECS];
     int at[VECS];            // first element of each
-    uint32_t bound[NWAVE];
-    int place[NT];
-    uint64_t best[NWAVE];
-    float m[NWAVE], s[NWAVE];
-    uint32_t count[NWAVE];
+    uint32_t bound[NTB / 64];
+    int place[NTB];
+    uint64_t best[NTB / 64];
+    float m[NTB / 64], s[NTB / 64];
+    uint32_t count[NTB / 64];
     int nvec, n;
 };
 
 // The k largest of row[v0, v1) by k passes, each for the largest key below the last: any values, NaN and
 // infinities among them.  For rows with such values and for orders that overflow the list.
-template <typename T, typename F>
-__device__ inline void largest_by_rounds(const T *row, int v0, int v1, int k, ChunkShared &sh, F emit)
+template <typename T, int NTB, typename F>
+__device__ inline void largest_by_rounds(const T *row, int v0, int v1, int k, ChunkShared<NTB> &sh, F emit)
 {
     uint64_t last = ~0ull;
     for (int i = 0; i < k; ++i) {
         uint64_t best = 0;
-        for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += NT) {
+        for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += NTB) {
             const uint64_t key = argmax_key(Vec<T>::one(row + v), static_cast<uint32_t>(v));
             if (key < last && key > best)
                 best = key;
@@ -235,7 +238,7 @@ __device__ inline void largest_by_rounds(const T *row, int v0, int v1, int k, Ch
         __syncthreads();
         best = sh.best[0];
 #pragma unroll
-        for (int w = 1; w < NWAVE; ++w)
+        for (int w = 1; w < NTB / 64; ++w)
             best = max_u64(best, sh.best[w]);
         __syncthreads();
         if (threadIdx.x == 0)
@@ -247,15 +250,15 @@ __device__ inline void largest_by_rounds(const T *row, int v0, int v1, int k, Ch
 // More elements than the list holds reach the bound t, most of them equal to it (masked rows: all the rest is
 // -inf).  The greater ones go to the list, then the equal ones in the order of their ids until k are there.
 // False: too many are greater.
-template <typename T>
-__device__ inline bool list_with_ties(const T *row, int v0, int v1, float t, int k, ChunkShared &sh)
+template <typename T, int NTB>
+__device__ inline bool list_with_ties(const T *row, int v0, int v1, float t, int k, ChunkShared<NTB> &sh)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     __syncthreads();
     if (threadIdx.x == 0)
         sh.n = 0;
     __syncthreads();
-    for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += NT) {
+    for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += NTB) {
         const float z = Vec<T>::one(row + v);
         if (z > t) {
             const int at = atomicAdd(&sh.n, 1);
@@ -268,7 +271,7 @@ __device__ inline bool list_with_ties(const T *row, int v0, int v1, float t, int
     if (greater > LIST - MAX_TIES)
         return false;
     int have = 0;  // equal ones so far
-    for (int base = v0; base < v1 && greater + have < k; base += NT) {
+    for (int base = v0; base < v1 && greater + have < k; base += NTB) {
         const int v = base + static_cast<int>(threadIdx.x);
         const bool tie = v < v1 && Vec<T>::one(row + v) == t;
         const uint64_t mask = __ballot(tie);
@@ -277,7 +280,7 @@ __device__ inline bool list_with_ties(const T *row, int v0, int v1, float t, int
         __syncthreads();
         int before = have, all = have;
 #pragma unroll
-        for (int w = 0; w < NWAVE; ++w) {
+        for (int w = 0; w < NTB / 64; ++w) {
             before += w < wave ? static_cast<int>(sh.count[w]) : 0;
             all += static_cast<int>(sh.count[w]);
         }
@@ -308,12 +311,12 @@ __device__ inline void put_result(const TopOut &o, int row, int k, int place, ui
 }
 
 // One chunk of a row: its k largest and its part of the row's sum, or the row's results where it is one chunk.
-template <typename T, int NV>
-__global__ __launch_bounds__(NT) void k_top_chunk(Rows rows, Live live, int k, Split sp, Scale sc,
+template <typename T, int NTB, int NV>
+__global__ __launch_bounds__(NTB) void k_top_chunk(Rows rows, Live live, int k, Split sp, Scale sc,
                                                   double inv_tau, TopOut out)
 {
     typedef Vec<T> VT;
-    __shared__ ChunkShared sh;
+    __shared__ ChunkShared<NTB> sh;
     const int nch = sp.nch, cvec = sp.cvec, i_row = static_cast<int>(sp.by.quotient(blockIdx.x));
     const int c = static_cast<int>(blockIdx.x) - i_row * nch;
     const Place place = rows.place(i_row);
@@ -322,7 +325,7 @@ __global__ __launch_bounds__(NT) void k_top_chunk(Rows rows, Live live, int k, S
     const bool direct = nch == 1 && out.ids;
     if (!row_live(rows, live, place)) {
         if (direct) {
-            for (int i = threadIdx.x; i < k; i += NT) {
+            for (int i = threadIdx.x; i < k; i += NTB) {
                 out.ids[static_cast<int64_t>(row) * k + i] = -1;
                 out.values[static_cast<int64_t>(row) * k + i] = NEG_INF;
             }
@@ -334,7 +337,7 @@ __global__ __launch_bounds__(NT) void k_top_chunk(Rows rows, Live live, int k, S
     const T *z = row_at<T>(rows, place);
     const int v0 = chunk_begin<T>(c, cvec, rows.V), v1 = chunk_begin<T>(c + 1, cvec, rows.V);
     typename VT::raw x[NV];
-    load_chunk<T, NV>(x, z, rows.V, c, cvec);
+    load_chunk<T, NV, NTB>(x, z, rows.V, c, cvec);
     if (threadIdx.x == 0)
         sh.nvec = sh.n = 0;
 
@@ -350,10 +353,10 @@ __global__ __launch_bounds__(NT) void k_top_chunk(Rows rows, Live live, int k, S
     const float wm = wave_max(tm);
     if (lane == 0)
         sh.m[wave] = wm;
-    const uint32_t t_ord = block_bound<16, 26, NT>(top, k, sh.bound);
+    const uint32_t t_ord = block_bound<16, 26, NTB>(top, k, sh.bound);
     float m = sh.m[0];
 #pragma unroll
-    for (int w = 1; w < NWAVE; ++w)
+    for (int w = 1; w < NTB / 64; ++w)
         m = fmaxf(m, sh.m[w]);
     const float t = t_ord > ORD_NEG_INF ? unord_f32(t_ord) : NEG_INF;
     bool hit[NV];
@@ -366,7 +369,7 @@ __global__ __launch_bounds__(NT) void k_top_chunk(Rows rows, Live live, int k, S
     for (int u = 0; u < NV; ++u)
         if (hit[u] && at[u] < VECS) {
             sh.vec[at[u]] = make_uint4(word(x[u][0]), word(x[u][1]), word(x[u][2]), word(x[u][3]));
-            sh.at[at[u]] = v0 + (u * NT + static_cast<int>(threadIdx.x)) * VT::N;
+            sh.at[at[u]] = v0 + (u * NTB + static_cast<int>(threadIdx.x)) * VT::N;
         }
     const Expo ex(m > NEG_INF ? m : 0.f, sc);
     float s = ex.small ? sum_exps<T, true>(x, ex, sc) : sum_exps<T, false>(x, ex, sc);
@@ -377,11 +380,11 @@ __global__ __launch_bounds__(NT) void k_top_chunk(Rows rows, Live live, int k, S
     const int nvec = sh.nvec;
     bool nan = false;
 #pragma unroll
-    for (int w = 0; w < NWAVE; ++w)
+    for (int w = 0; w < NTB / 64; ++w)
         nan |= sh.s[w] != sh.s[w];
     // one element a thread
     if (nvec <= VECS)
-        for (int i = threadIdx.x; i < (nvec * VT::N + 63) / 64 * 64; i += NT) {
+        for (int i = threadIdx.x; i < (nvec * VT::N + 63) / 64 * 64; i += NTB) {
             const int j = i / VT::N, e = i % VT::N, v = j < nvec ? sh.at[j] + e : v1;
             const float f = VT::word_at(reinterpret_cast<const uint32_t *>(sh.vec), i);
             const bool one[1] = {v < v1 && f >= t};
@@ -403,7 +406,7 @@ __global__ __launch_bounds__(NT) void k_top_chunk(Rows rows, Live live, int k, S
     if (nan) {
         // NaN or +inf among the elements
         bool any_nan = false;
-        for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += NT) {
+        for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += NTB) {
             const float f = VT::one(z + v);
             any_nan |= f != f;
         }
@@ -411,19 +414,19 @@ __global__ __launch_bounds__(NT) void k_top_chunk(Rows rows, Live live, int k, S
         infinite = !nan;
         largest_by_rounds(z, v0, v1, k, sh, emit);
     } else if (nvec <= VECS && n <= LIST) {
-        emit_largest(sh.list, sh.place, n, k, emit);
+        emit_largest<NTB>(sh.list, sh.place, n, k, emit);
     } else {
         // more reach the bound than the lists hold: the exact one, since most of them may be equal to it
-        const uint32_t exact = block_bound<0, 26, NT>(top, k, sh.bound);
+        const uint32_t exact = block_bound<0, 26, NTB>(top, k, sh.bound);
         if (list_with_ties(z, v0, v1, exact ? unord_f32(exact) : NEG_INF, k, sh))
-            emit_largest(sh.list, sh.place, sh.n, k, emit);
+            emit_largest<NTB>(sh.list, sh.place, sh.n, k, emit);
         else
             largest_by_rounds(z, v0, v1, k, sh, emit);
     }
-    if (threadIdx.x == NT - 1) {  // (of the wave with the least to rank)
+    if (threadIdx.x == NTB - 1) {  // (of the wave with the least to rank)
         double total = 0.0;
 #pragma unroll
-        for (int w = 0; w < NWAVE; ++w)
+        for (int w = 0; w < NTB / 64; ++w)
             total += static_cast<double>(sh.s[w]);
         total *= ex.fix(sc);
         const Part part = nan ? Part{__builtin_nanf(""), 1.f} : infinite ? Part{-NEG_INF, 1.f}
@@ -498,7 +501,7 @@ __global__ __launch_bounds__(NT) void k_top_merge(Rows rows, Live live, int k, i
     const int64_t slot = static_cast<int64_t>(row) * nch;
     const Part part = first_part(out.parts + slot, nch);
     const int n = merge_list<PER>(out.keys + slot * k, nch, k, sh);
-    emit_largest(sh.list, sh.place, n, k, [&](int at, uint64_t key) { put_result(out, row, k, at, key); });
+    emit_largest<NT>(sh.list, sh.place, n, k, [&](int at, uint64_t key) { put_result(out, row, k, at, key); });
     if (threadIdx.x >= NT - 64) {  // the wave with the least to rank
         float m;
         double s;
@@ -821,10 +824,21 @@ constexpr int MAX_NV = 8, LAST_NV = 16;       // vectors a thread takes at most;
 
 int vec_len(int dtype) { return dtype == DOMINO_F32 ? 4 : 8; }
 
-Split split_of(const domino_logits &lg, int k)
+// Rows that need no join: of up to 8 vectors for each of 256 threads, or of 1024 where every row has a compute unit for
+// itself.  64 f32 rows of 32000, k = 8: 12.5 us a call and 9.0 us of kernel, split and joined 16.2 us and two kernels
+// of 17 us from the first one's start to the second one's end; 1024 rows 27.3 us either way.  Beams are joined with
+// each other in any case, and split rows reach that sooner.
+bool whole_rows(int64_t rows, int nvec, bool for_beams)
+{
+    return !for_beams && (nvec <= NT * MAX_NV || (nvec <= 1024 * MAX_NV && rows <= 256));
+}
+
+Split split_of(const domino_logits &lg, int k, bool for_beams)
 {
     const int64_t rows = static_cast<int64_t>(lg.B) * lg.R;
     const int nvec = (lg.V + vec_len(lg.dtype) - 1) / vec_len(lg.dtype);
+    if (whole_rows(rows, nvec, for_beams))
+        return split(nvec, 1);
     int least = (nvec + NT * MAX_NV - 1) / (NT * MAX_NV);
     if (least * k > MERGE_LIST)  // long rows and many logits of each: larger chunks
         least = (nvec + NT * LAST_NV - 1) / (NT * LAST_NV);
@@ -840,11 +854,11 @@ Split split_of(const domino_logits &lg, int k)
 
 size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
 
-template <typename T, int NV>
+template <typename T, int NTB, int NV>
 void launch_chunk(const Rows &rows, const Live &live, int k, const Split &sp, float tau, const TopOut &out,
                   unsigned grid, hipStream_t st)
 {
-    hipLaunchKernelGGL((k_top_chunk<T, NV>), dim3(grid), dim3(NT), 0, st, rows, live, k, sp, scale_of(tau),
+    hipLaunchKernelGGL((k_top_chunk<T, NTB, NV>), dim3(grid), dim3(NTB), 0, st, rows, live, k, sp, scale_of(tau),
                        1.0 / static_cast<double>(tau), out);
 }
 
@@ -852,14 +866,19 @@ template <typename T>
 void pick_chunk(const Rows &rows, const Live &live, int k, const Split &sp, float tau, const TopOut &out,
                 unsigned grid, hipStream_t st)
 {
+    // (one chunk a row: up to 1024 threads; else blocks of 256, which wait less for their own phases)
     if (sp.nv <= 2)
-        launch_chunk<T, 2>(rows, live, k, sp, tau, out, grid, st);
+        launch_chunk<T, 256, 2>(rows, live, k, sp, tau, out, grid, st);
     else if (sp.nv <= 4)
-        launch_chunk<T, 4>(rows, live, k, sp, tau, out, grid, st);
+        launch_chunk<T, 256, 4>(rows, live, k, sp, tau, out, grid, st);
     else if (sp.nv <= 8)
-        launch_chunk<T, 8>(rows, live, k, sp, tau, out, grid, st);
+        launch_chunk<T, 256, 8>(rows, live, k, sp, tau, out, grid, st);
+    else if (sp.nch > 1)
+        launch_chunk<T, 256, 16>(rows, live, k, sp, tau, out, grid, st);
+    else if (sp.nv <= 16)
+        launch_chunk<T, 512, 8>(rows, live, k, sp, tau, out, grid, st);
     else
-        launch_chunk<T, 16>(rows, live, k, sp, tau, out, grid, st);
+        launch_chunk<T, 1024, 8>(rows, live, k, sp, tau, out, grid, st);
 }
 
 struct Scratch {
@@ -897,14 +916,14 @@ static_assert((dhtop::MAX_V / 4 + NT * LAST_NV - 1) / (NT * LAST_NV) * dhtop::MA
 
 size_t workspace_bytes(const domino_logits &lg, int k, bool for_beams)
 {
-    const Split sp = split_of(lg, k);
+    const Split sp = split_of(lg, k, for_beams);
     return sp.nch == 1 && !for_beams ? 0 : scratch_of(lg, k, sp, nullptr).bytes;
 }
 
 hipError_t top(const domino_logits &lg, int k, float tau, const int32_t *n_rows, void *ws, int32_t *ids,
                float *values, float *lse, hipStream_t st)
 {
-    const Split sp = split_of(lg, k);
+    const Split sp = split_of(lg, k, false);
     const Scratch s = scratch_of(lg, k, sp, ws);
     const TopOut out = {s.keys, s.parts, ids, values, lse};
     const Rows rows = rows_of(lg, n_rows, n_rows != nullptr);
@@ -925,7 +944,7 @@ hipError_t top(const domino_logits &lg, int k, float tau, const int32_t *n_rows,
 hipError_t beam(const domino_logits &lg, const domino_beam &bm, void *ws, hipStream_t st)
 {
     const int kc = bm.n_out < lg.V ? bm.n_out : lg.V;
-    const Split sp = split_of(lg, kc);
+    const Split sp = split_of(lg, kc, true);
     const Scratch s = scratch_of(lg, kc, sp, ws);
     const TopOut out = {s.keys, s.parts, nullptr, nullptr, nullptr};
     chunks(lg, rows_of(lg, nullptr, true), Live{bm.scores, bm.finished}, kc, 1.f, sp, out, st);

@@ -69,6 +69,8 @@ def check_top(z, k, tau, n_rows=None, label=""):
     (2, 1, 1025, 64, 0, 3, 2.0), (1, 1, 2048, 1, 5, 1, 1.0), (3, 2, 5003, 33, 0, 0, 1.0), (1, 1, 16384, 128, 0, 0, 1.0),
     (2, 2, 16385, 100, 7, 1, 0.7), (1, 2, 40001, 128, 0, 0, 1.0), (1, 1, 151936, 64, 0, 0, 1.0),
     (200, 4, 2500, 3, 0, 1, 1.0), (30, 40, 4099, 17, 1, 0, 1.0), (1, 1, 524288, 128, 0, 0, 1.0),
+    (1, 2, 32768, 128, 0, 0, 1.0), (1, 1, 32769, 7, 0, 1, 1.0), (70, 4, 20011, 33, 0, 0, 1.0),
+    (3, 1, 65536, 100, 0, 0, 2.0), (2, 1, 65537, 5, 3, 0, 1.0),
 ])
 def test_top_logits(B, R, V, k, pad, shift, tau, dtype):
     check_top(rows(B, R, V, dtype, 7 * V + k, pad, shift), k, tau, label="B=%d R=%d V=%d k=%d" % (B, R, V, k))
@@ -117,7 +119,7 @@ def special_rows(V, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("V,k", [(300, 128), (2100, 100), (16000, 64), (70000, 128)])
+@pytest.mark.parametrize("V,k", [(300, 128), (2100, 100), (16000, 64), (30001, 100), (70000, 128)])
 def test_top_logits_of_special_rows(V, k, dtype):
     named = special_rows(V, dtype)
     for name, row in named.items():
