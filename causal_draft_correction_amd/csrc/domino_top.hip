@@ -7,7 +7,7 @@
 // chunk's k largest and its part of the sum.  The k-th largest of the threads' maxima bounds the k-th largest of the
 // chunk from below; the waves' shares of it are found by ballots two bits at a time, 16 bits deep.  On rows in no
 // particular order 1.5 k to 3 k elements reach the bound: their vectors go to LDS, from there they go to a list, and
-// the place of each is the number of greater ones.  Nothing is sorted and no element is compared more than twice.
+// the place of each is the number of greater ones (of a list longer than 256, which is rare, by sorting it).
 // k_top_merge joins the chunks' lists of a row in the same way; its bound is taken from the lists' heads.  A row that
 // one block can hold (up to 1024 threads) is one chunk, and needs no join.
 //

@@ -261,10 +261,10 @@ typedef struct domino_logits {
  *   values  [B, R, k] float32   their logits (-inf in rows left out)
  *   lse     [B, R]    float32   log sum_v exp(z_v / temperature): -inf where every logit is -inf and in rows
  *                               left out, +inf where one is +inf, NaN where one is NaN
- * 0 <= B, 1 <= R, 1 <= k <= 128, k <= V <= 524288, 1e-4 <= temperature <= 1e4; B = 0 is a no-op.  The result
- * does not depend on how a row is split over the device.  At most two launches, asynchronous on `stream`; no
- * allocation, no synchronization.  Pointers other than logits->data 16-byte aligned; outputs may not alias
- * inputs or the workspace.
+ * 0 <= B, 1 <= R, 1 <= k <= 128, k <= V <= 524288, 1e-4 <= temperature <= 1e4; B = 0 is a no-op.  ids
+ * and values do not depend on how a row is split over the device (V, k and B R decide that); the last place
+ * of lse may.  At most two launches, asynchronous on `stream`; no allocation, no synchronization.  Pointers
+ * other than logits->data 16-byte aligned; outputs may not alias inputs or the workspace.
  */
 int domino_top_logits_workspace_size(const domino_logits *logits, int32_t k, size_t *bytes);
 int domino_top_logits(const domino_logits *logits, int32_t k, float temperature, const int32_t *n_rows,
@@ -275,7 +275,8 @@ int domino_top_logits(const domino_logits *logits, int32_t k, float temperature,
  * candidates are all (w, v), with
  *     score(w, v) = scores[b][w] + z_wv - log sum_u exp(z_wu),
  * and the n_out best of them become the beams of the next step: higher scores first, equal ones by lowest
- * w, then lowest v (a beam's own candidates are ordered by their logits).  Scores are compared in 64 bits.
+ * w, then lowest v (a beam's own candidates are ordered by their logits).  Scores are compared in 64 bits,
+ * each row's sum of exponentials having been taken in float32 within a chunk of the row.
  *   - A beam whose score is -inf is dead: its candidates score -inf.  So do tokens whose logit is -inf, in a
  *     row of nothing but -inf too.
  *   - An ended beam (finished[b][w] != 0) has one candidate, (w, eos), with the score it has; the others
