@@ -169,16 +169,10 @@ __device__ inline void block_sort(uint64_t *list, int n)
     __syncthreads();
 }
 
-// Hands the k largest of list[0, n) to emit(place, key), largest first; places past n get key 0.
+// Hands the k largest of list[0, n), n <= COUNT_MAX, to emit(place, key), largest first; places past n get key 0.
 template <int NTB, typename F>
-__device__ inline void emit_largest(uint64_t *list, int *place, int n, int k, F emit)
+__device__ inline void emit_counted(uint64_t *list, int *place, int n, int k, F emit)
 {
-    if (n > COUNT_MAX) {
-        block_sort<NTB>(list, n);
-        for (int i = threadIdx.x; i < k; i += NTB)
-            emit(i, list[i]);
-        return;
-    }
     // 2^shift threads take one key each, and NTB / 2^shift a slice of the others
     const int t = threadIdx.x, shift = n <= 64 ? 6 : n <= 128 ? 7 : 8;
     place[t] = 0;
@@ -206,6 +200,19 @@ __device__ inline void emit_largest(uint64_t *list, int *place, int n, int k, F 
         emit(at, 0ull);
 }
 
+// The same for longer lists (room up to the next power of two), which are sorted.
+template <int NTB, typename F>
+__device__ inline void emit_largest(uint64_t *list, int *place, int n, int k, F emit)
+{
+    if (n <= COUNT_MAX) {
+        emit_counted<NTB>(list, place, n, k, emit);
+    } else {
+        block_sort<NTB>(list, n);
+        for (int i = threadIdx.x; i < k; i += NTB)
+            emit(i, list[i]);
+    }
+}
+
 template <int NTB>
 struct ChunkShared {
     alignas(16) uint64_t list[LIST];
@@ -213,87 +220,148 @@ struct ChunkShared {
     int at[VECS];            // first element of each
     uint32_t bound[NTB / 64];
     int place[NTB];
-    uint64_t best[NTB / 64];
     float m[NTB / 64], s[NTB / 64];
-    uint32_t count[NTB / 64];
+    uint32_t count[2][NTB / 64];
     int nvec, n;
 };
 
-// The k largest of row[v0, v1) by k passes, each for the largest key below the last: any values, NaN and
-// infinities among them.  For rows with such values and for orders that overflow the list.
+// The word by which argmax_key orders an element: NaN above +inf, -0 as +0.
+__device__ inline uint32_t key_word(float f) { return static_cast<uint32_t>(argmax_key(f, 0) >> 32); }
+
+// f(value, index, whether there is one) for the n elements at z, two vectors a thread at a time: more would halve the
+// waves of the common path.
 template <typename T, int NTB, typename F>
-__device__ inline void largest_by_rounds(const T *row, int v0, int v1, int k, ChunkShared<NTB> &sh, F emit)
+__device__ __forceinline__ void each(const T *z, int n, F f)
 {
-    uint64_t last = ~0ull;
-    for (int i = 0; i < k; ++i) {
-        uint64_t best = 0;
-        for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += NTB) {
-            const uint64_t key = argmax_key(Vec<T>::one(row + v), static_cast<uint32_t>(v));
-            if (key < last && key > best)
-                best = key;
-        }
-        best = wave_max_u64(best);
-        if ((threadIdx.x & 63) == 0)
-            sh.best[threadIdx.x >> 6] = best;
-        __syncthreads();
-        best = sh.best[0];
+    typedef Vec<T> VT;
+    constexpr int STEP = 2;
+#pragma unroll 1
+    for (int i = 0; i * STEP * NTB * VT::N < n; ++i) {
+        typename VT::raw x[STEP];
+        load_chunk<T, STEP, NTB, true>(x, z, n, i, STEP * NTB);
 #pragma unroll
-        for (int w = 1; w < NTB / 64; ++w)
-            best = max_u64(best, sh.best[w]);
-        __syncthreads();
-        if (threadIdx.x == 0)
-            emit(i, best);
-        last = best;  // 0 once nothing is left
+        for (int u = 0; u < STEP; ++u) {
+            const int at = ((i * STEP + u) * NTB + static_cast<int>(threadIdx.x)) * VT::N;
+#pragma unroll
+            for (int e = 0; e < VT::N; ++e)
+                f(VT::get(x[u], e), at + e, at + e < n);
+        }
     }
 }
 
-// More elements than the list holds reach the bound t, most of them equal to it (masked rows: all the rest is
-// -inf).  The greater ones go to the list, then the equal ones in the order of their ids until k are there.
-// False: too many are greater.
-template <typename T, int NTB>
-__device__ inline bool list_with_ties(const T *row, int v0, int v1, float t, int k, ChunkShared<NTB> &sh)
+// The sum of the threads' counts (at most 2^16 a wave, which float32 holds).  One barrier: calls take the two rows of
+// `count` in turn, so that a row's words were read before the other one's barrier (a bisection begins with row 0).
+template <int NTB>
+__device__ inline int block_count(int mine, int turn, uint32_t (&count)[2][NTB / 64])
+{
+    const float all = wave_sum(static_cast<float>(mine));
+    if ((threadIdx.x & 63) == 0)
+        count[turn][threadIdx.x >> 6] = static_cast<uint32_t>(all);
+    __syncthreads();
+    int sum = 0;
+#pragma unroll
+    for (int w = 0; w < NTB / 64; ++w)
+        sum += static_cast<int>(count[turn][w]);
+    return sum;
+}
+
+// A word that at least k of a block's words reach: at most `most` of them, or fewer than k exceed it.  By bisection
+// from `lo`, which more than `most` reach, to `hi`, which none does.  reach(c): how many of the thread's words reach c.
+template <int NTB, typename F>
+__device__ __forceinline__ uint32_t bisected(uint32_t lo, uint64_t hi, int k, int most,
+                                             uint32_t (&count)[2][NTB / 64], F reach)
+{
+    for (int turn = 0; hi - lo > 1; turn ^= 1) {  // (at most 32 turns)
+        const uint32_t c = static_cast<uint32_t>(lo + (hi - lo) / 2);
+        const int n = block_count<NTB>(reach(c), turn, count);
+        if (n < k)
+            hi = c;
+        else
+            lo = c;
+        if (n >= k && n <= most)
+            break;
+    }
+    return lo;
+}
+
+// The next entries of the list, in the threads' order: those with `tie`, behind the greater ones and the `have` equal
+// ones before them, up to place k.  Two barriers.
+template <int NTB>
+__device__ inline void list_ties(uint64_t *list, int greater, int &have, int k, bool tie, uint64_t key,
+                                 uint32_t (&count)[2][NTB / 64])
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint64_t mask = __ballot(tie);
+    if (lane == 0)
+        count[0][wave] = __popcll(mask);
+    __syncthreads();
+    int before = have, all = have;
+#pragma unroll
+    for (int w = 0; w < NTB / 64; ++w) {
+        before += w < wave ? static_cast<int>(count[0][w]) : 0;
+        all += static_cast<int>(count[0][w]);
+    }
+    const int at = greater + before + __popcll(mask & ((1ull << lane) - 1));
+    if (tie && at < k)
+        list[at] = key;
+    have = all;
+    __syncthreads();
+}
+
+// The elements whose words exceed t go to the list, as far as they have room; returns how many there are.
+template <typename T, int NTB>
+__device__ __forceinline__ int list_above(const T *z, int n, int v0, uint32_t t, ChunkShared<NTB> &sh)
+{
     __syncthreads();
     if (threadIdx.x == 0)
         sh.n = 0;
     __syncthreads();
-    for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += NTB) {
-        const float z = Vec<T>::one(row + v);
-        if (z > t) {
-            const int at = atomicAdd(&sh.n, 1);
-            if (at < LIST - MAX_TIES)
-                sh.list[at] = argmax_key(z, static_cast<uint32_t>(v));
-        }
-    }
+    each<T, NTB>(z, n, [&](float f, int i, bool in) {
+        const bool one[1] = {in && key_word(f) > t};
+        int to[1];
+        wave_places(one, &sh.n, to);
+        if (one[0] && to[0] < LIST - MAX_TIES)
+            sh.list[to[0]] = argmax_key(f, static_cast<uint32_t>(v0 + i));
+    });
     __syncthreads();
-    const int greater = sh.n;
-    if (greater > LIST - MAX_TIES)
-        return false;
+    return sh.n;
+}
+
+// The list of a chunk with any values: masked rows (most elements are -inf), sorted rows, few different values, NaN
+// and infinities.  The elements above a bound go to the list, then those equal to it in the order of their ids until
+// k are there.  `lo`: a bound that at least k elements reach (or all, where there are fewer); `hi`: one that none does.
+// 16 f32 rows of 32000 with 2000 neighbours left by a mask, k = 64: 51 us a call, where 64 passes for a maximum each
+// took 406; 512 rows of 151936 with a +inf each 64 us, instead of 425.
+template <typename T, int NTB>
+__device__ __forceinline__ void list_any(const T *row, int v0, int v1, int k, uint32_t lo, uint64_t hi,
+                                         ChunkShared<NTB> &sh)
+{
+    uint32_t t = lo;
+    int greater = 0;
+#pragma unroll 1
+    for (int attempt = 0; attempt < 2; ++attempt) {  // (the second has few enough)
+        if (attempt)
+            t = bisected<NTB>(lo + 1, hi, k, LIST - MAX_TIES, sh.count, [&](uint32_t c) {
+                int reach = 0;
+                each<T, NTB>(row + v0, v1 - v0,
+                             [&](float f, int, bool in) { reach += in & (key_word(f) >= c); });
+                return reach;
+            });
+        greater = list_above(row + v0, v1 - v0, v0, t, sh);
+        if (greater <= LIST - MAX_TIES)
+            break;
+        greater = LIST - MAX_TIES;  // (the list's length, whatever happens to the row meanwhile)
+    }
     int have = 0;  // equal ones so far
     for (int base = v0; base < v1 && greater + have < k; base += NTB) {
         const int v = base + static_cast<int>(threadIdx.x);
-        const bool tie = v < v1 && Vec<T>::one(row + v) == t;
-        const uint64_t mask = __ballot(tie);
-        if (lane == 0)
-            sh.count[wave] = __popcll(mask);
-        __syncthreads();
-        int before = have, all = have;
-#pragma unroll
-        for (int w = 0; w < NTB / 64; ++w) {
-            before += w < wave ? static_cast<int>(sh.count[w]) : 0;
-            all += static_cast<int>(sh.count[w]);
-        }
-        const int at = greater + before + __popcll(mask & ((1ull << lane) - 1));
-        if (tie && at < k)
-            sh.list[at] = argmax_key(t, static_cast<uint32_t>(v));
-        have = all;
-        __syncthreads();
+        const float z = v < v1 ? Vec<T>::one(row + v) : 0.f;
+        list_ties<NTB>(sh.list, greater, have, k, v < v1 && key_word(z) == t,
+                       argmax_key(z, static_cast<uint32_t>(v)), sh.count);
     }
     if (threadIdx.x == 0)
-        sh.n = greater + have < k ? greater + have : (greater > k ? greater : k);
+        sh.n = greater + have < k ? greater + have : greater > k ? greater : k;
     __syncthreads();
-    return true;
 }
 
 // What one block leaves of its chunk: keys and part, or (a row of one chunk) the results.
@@ -403,25 +471,22 @@ __global__ __launch_bounds__(NTB) void k_top_chunk(Rows rows, Live live, int k, 
     };
     const int n = sh.n;
     bool infinite = false;
-    if (nan) {
-        // NaN or +inf among the elements
-        bool any_nan = false;
-        for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += NTB) {
-            const float f = VT::one(z + v);
-            any_nan |= f != f;
-        }
-        nan = __syncthreads_or(any_nan);
-        infinite = !nan;
-        largest_by_rounds(z, v0, v1, k, sh, emit);
-    } else if (nvec <= VECS && n <= LIST) {
+    if (!nan && nvec <= VECS && n <= LIST) {
         emit_largest<NTB>(sh.list, sh.place, n, k, emit);
     } else {
-        // more reach the bound than the lists hold: the exact one, since most of them may be equal to it
-        const uint32_t exact = block_bound<0, 26, NTB>(top, k, sh.bound);
-        if (list_with_ties(z, v0, v1, exact ? unord_f32(exact) : NEG_INF, k, sh))
-            emit_largest<NTB>(sh.list, sh.place, sh.n, k, emit);
-        else
-            largest_by_rounds(z, v0, v1, k, sh, emit);
+        if (nan) {
+            // NaN or +inf among the elements
+            bool any_nan = false;
+            for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += NTB) {
+                const float f = VT::one(z + v);
+                any_nan |= f != f;
+            }
+            nan = __syncthreads_or(any_nan);
+            infinite = !nan;
+        }
+        const uint64_t hi = nan ? 1ull << 32 : static_cast<uint64_t>(key_word(m)) + 1;
+        list_any(z, v0, v1, k, t_ord > ORD_NEG_INF ? t_ord : ORD_NEG_INF, hi, sh);
+        emit_largest<NTB>(sh.list, sh.place, sh.n, k, emit);
     }
     if (threadIdx.x == NTB - 1) {  // (of the wave with the least to rank)
         double total = 0.0;
@@ -444,8 +509,20 @@ struct MergeShared {
     alignas(16) uint64_t list[MERGE_LIST];
     uint32_t bound[NWAVE];
     int place[NT];
+    uint32_t count[2][NWAVE];
     int n;
 };
+
+// How many of the thread's keys have a word above t.
+template <int PER>
+__device__ inline int above(const uint64_t (&keys)[PER], uint32_t t)
+{
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        n += static_cast<uint32_t>(keys[i] >> 32) > t;
+    return n;
+}
 
 // The candidates of nch sorted lists of k keys that reach the k-th largest of the lists' heads go to sh.list;
 // returns how many.  A thread takes PER keys; q heads of each list, one a thread (of more than NT lists, the first
@@ -479,7 +556,38 @@ __device__ inline int merge_list(const uint64_t *keys, int nch, int k, MergeShar
         if (hit[i])
             sh.list[at[i]] = mine[i];
     __syncthreads();
-    return sh.n;
+    const int all = sh.n;
+    if (all <= COUNT_MAX)
+        return all;
+    // Too many to count places: mostly equal ones (what a mask left out).  A bound that fewer exceed, then those equal
+    // to it in the order of the lists, which is that of their ids.  16 f32 rows of 151936 with 6000 neighbours left by
+    // a mask, k = 128: 24 us a call, where a sorted list took 91.
+    const uint32_t lo = t > ORD_NEG_INF ? t : ORD_NEG_INF;
+    uint32_t u = lo;
+    int greater = block_count<NT>(above<PER>(mine, lo), 1, sh.count);
+    if (greater > COUNT_MAX)
+        u = bisected<NT>(lo + 1, 1ull << 32, k, COUNT_MAX, sh.count,
+                         [&](uint32_t c) { return above<PER>(mine, c - 1); });
+    __syncthreads();
+    if (threadIdx.x == 0)
+        sh.n = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        hit[i] = static_cast<uint32_t>(mine[i] >> 32) > u;
+    wave_places(hit, &sh.n, at);
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (hit[i])
+            sh.list[at[i]] = mine[i];
+    __syncthreads();
+    greater = sh.n;
+    int have = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (greater + have < k)
+            list_ties<NT>(sh.list, greater, have, k, static_cast<uint32_t>(mine[i] >> 32) == u, mine[i], sh.count);
+    return greater + have < k ? greater + have : greater > k ? greater : k;
 }
 
 // The k largest of a row from its chunks' lists, and its log-sum-exp.
@@ -501,7 +609,7 @@ __global__ __launch_bounds__(NT) void k_top_merge(Rows rows, Live live, int k, i
     const int64_t slot = static_cast<int64_t>(row) * nch;
     const Part part = first_part(out.parts + slot, nch);
     const int n = merge_list<PER>(out.keys + slot * k, nch, k, sh);
-    emit_largest<NT>(sh.list, sh.place, n, k, [&](int at, uint64_t key) { put_result(out, row, k, at, key); });
+    emit_counted<NT>(sh.list, sh.place, n, k, [&](int at, uint64_t key) { put_result(out, row, k, at, key); });
     if (threadIdx.x >= NT - 64) {  // the wave with the least to rank
         float m;
         double s;

@@ -112,6 +112,9 @@ def special_rows(V, dtype):
     vec = 4 if dtype == torch.float32 else 8
     quiet = (torch.arange(V) // vec) % 256 < 64
     out["one quiet wave"] = torch.where(quiet, base.abs() * -1.0, 100.0 + base.abs())
+    x = torch.full((V,), -np.inf)
+    x[V // 3:V // 3 + min(V // 2, 2500)] = base[V // 3:V // 3 + min(V // 2, 2500)]
+    out["neighbours left"] = x
     x = torch.full((V,), 2.0)
     x[V // 7::V // 7] = 3.0
     out["ties below a few"] = x
