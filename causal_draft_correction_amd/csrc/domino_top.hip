@@ -221,7 +221,7 @@ struct ChunkShared {
     uint32_t bound[NTB / 64];
     int place[NTB];
     float m[NTB / 64], s[NTB / 64];
-    uint32_t count[2][NTB / 64];
+    uint32_t count[2 * (NTB / 64)];
     int nvec, n;
 };
 
@@ -249,30 +249,30 @@ __device__ __forceinline__ void each(const T *z, int n, F f)
     }
 }
 
-// The sum of the threads' counts (at most 2^16 a wave, which float32 holds).  One barrier: calls take the two rows of
-// `count` in turn, so that a row's words were read before the other one's barrier (a bisection begins with row 0).
+// The sum of the threads' counts (at most 2^16 a wave, which float32 holds).  One barrier.  `count`: two rows of a word
+// a wave, which calls take in turn, so that a row's words were read before the other one's barrier.
 template <int NTB>
-__device__ inline int block_count(int mine, int turn, uint32_t (&count)[2][NTB / 64])
+__device__ inline int block_count(int mine, int turn, uint32_t *count)
 {
     const float all = wave_sum(static_cast<float>(mine));
+    count += turn * (NTB / 64);
     if ((threadIdx.x & 63) == 0)
-        count[turn][threadIdx.x >> 6] = static_cast<uint32_t>(all);
+        count[threadIdx.x >> 6] = static_cast<uint32_t>(all);
     __syncthreads();
     int sum = 0;
 #pragma unroll
     for (int w = 0; w < NTB / 64; ++w)
-        sum += static_cast<int>(count[turn][w]);
+        sum += static_cast<int>(count[w]);
     return sum;
 }
 
-// A word that at least k of a block's words reach: at most `most` of them, or fewer than k exceed it.  By bisection
-// from `lo`, which more than `most` reach, to `hi`, which none does.  reach(c): how many of the thread's words reach c.
+// Narrows [lo, hi), of which at least k of a block's words reach lo and fewer than k reach hi, until at most `most`
+// reach lo, or to one word.  reach(c): how many of the thread's words reach c.  Begins with row 0 of `count`.
 template <int NTB, typename F>
-__device__ __forceinline__ uint32_t bisected(uint32_t lo, uint64_t hi, int k, int most,
-                                             uint32_t (&count)[2][NTB / 64], F reach)
+__device__ __forceinline__ void bisect(uint64_t &lo, uint64_t &hi, int k, int most, uint32_t *count, F reach)
 {
-    for (int turn = 0; hi - lo > 1; turn ^= 1) {  // (at most 32 turns)
-        const uint32_t c = static_cast<uint32_t>(lo + (hi - lo) / 2);
+    for (int turn = 0; hi - lo > 1; turn ^= 1) {  // (at most 64 turns)
+        const uint64_t c = lo + (hi - lo) / 2;
         const int n = block_count<NTB>(reach(c), turn, count);
         if (n < k)
             hi = c;
@@ -281,25 +281,24 @@ __device__ __forceinline__ uint32_t bisected(uint32_t lo, uint64_t hi, int k, in
         if (n >= k && n <= most)
             break;
     }
-    return lo;
 }
 
 // The next entries of the list, in the threads' order: those with `tie`, behind the greater ones and the `have` equal
 // ones before them, up to place k.  Two barriers.
 template <int NTB>
 __device__ inline void list_ties(uint64_t *list, int greater, int &have, int k, bool tie, uint64_t key,
-                                 uint32_t (&count)[2][NTB / 64])
+                                 uint32_t *count)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint64_t mask = __ballot(tie);
     if (lane == 0)
-        count[0][wave] = __popcll(mask);
+        count[wave] = __popcll(mask);
     __syncthreads();
     int before = have, all = have;
 #pragma unroll
     for (int w = 0; w < NTB / 64; ++w) {
-        before += w < wave ? static_cast<int>(count[0][w]) : 0;
-        all += static_cast<int>(count[0][w]);
+        before += w < wave ? static_cast<int>(count[w]) : 0;
+        all += static_cast<int>(count[w]);
     }
     const int at = greater + before + __popcll(mask & ((1ull << lane) - 1));
     if (tie && at < k)
@@ -340,13 +339,15 @@ __device__ __forceinline__ void list_any(const T *row, int v0, int v1, int k, ui
     int greater = 0;
 #pragma unroll 1
     for (int attempt = 0; attempt < 2; ++attempt) {  // (the second has few enough)
-        if (attempt)
-            t = bisected<NTB>(lo + 1, hi, k, LIST - MAX_TIES, sh.count, [&](uint32_t c) {
+        if (attempt) {
+            uint64_t least = static_cast<uint64_t>(lo) + 1;
+            bisect<NTB>(least, hi, k, LIST - MAX_TIES, sh.count, [&](uint64_t c) {
                 int reach = 0;
-                each<T, NTB>(row + v0, v1 - v0,
-                             [&](float f, int, bool in) { reach += in & (key_word(f) >= c); });
+                each<T, NTB>(row + v0, v1 - v0, [&](float f, int, bool in) { reach += in & (key_word(f) >= c); });
                 return reach;
             });
+            t = static_cast<uint32_t>(least);
+        }
         greater = list_above(row + v0, v1 - v0, v0, t, sh);
         if (greater <= LIST - MAX_TIES)
             break;
@@ -509,7 +510,7 @@ struct MergeShared {
     alignas(16) uint64_t list[MERGE_LIST];
     uint32_t bound[NWAVE];
     int place[NT];
-    uint32_t count[2][NWAVE];
+    uint32_t count[2 * NWAVE];
     int n;
 };
 
@@ -562,12 +563,12 @@ __device__ inline int merge_list(const uint64_t *keys, int nch, int k, MergeShar
     // Too many to count places: mostly equal ones (what a mask left out).  A bound that fewer exceed, then those equal
     // to it in the order of the lists, which is that of their ids.  16 f32 rows of 151936 with 6000 neighbours left by
     // a mask, k = 128: 24 us a call, where a sorted list took 91.
-    const uint32_t lo = t > ORD_NEG_INF ? t : ORD_NEG_INF;
-    uint32_t u = lo;
-    int greater = block_count<NT>(above<PER>(mine, lo), 1, sh.count);
+    uint64_t lo = t > ORD_NEG_INF ? t : ORD_NEG_INF, hi = 1ull << 32;
+    int greater = block_count<NT>(above<PER>(mine, static_cast<uint32_t>(lo)), 1, sh.count);
     if (greater > COUNT_MAX)
-        u = bisected<NT>(lo + 1, 1ull << 32, k, COUNT_MAX, sh.count,
-                         [&](uint32_t c) { return above<PER>(mine, c - 1); });
+        bisect<NT>(++lo, hi, k, COUNT_MAX, sh.count,
+                   [&](uint64_t c) { return above<PER>(mine, static_cast<uint32_t>(c - 1)); });
+    const uint32_t u = static_cast<uint32_t>(lo);
     __syncthreads();
     if (threadIdx.x == 0)
         sh.n = 0;
@@ -678,21 +679,15 @@ __device__ inline bool before(const Cand &a, const Cand &b)
     // (no branches)
     return (a.score > b.score) | ((a.score == b.score) & ((a.w < b.w) | ((a.w == b.w) & (a.place > b.place))));
 }
-__device__ inline void keep_first(Cand &best, const Cand &c, bool counts)
-{
-    const bool take = counts & before(c, best);
-    best.score = take ? c.score : best.score;
-    best.place = take ? c.place : best.place;
-    best.w = take ? c.w : best.w;
-}
 enum { LIVE, DEAD, ENDED, BAD };
 constexpr uint64_t ORD64_NEG_INF = 0x000FFFFFFFFFFFFFull;  // ord_f64(-inf)
 
 struct BeamShared {
     Cand list[BEAM_LIST];
     int place[BEAM_LIST];
-    uint32_t bound[16];
-    Cand best[16];
+    uint32_t bound[16], count[2 * 16];
+    uint64_t top[16];
+    int tie[MAX_BEAMS];
     double score[MAX_BEAMS], log_s[MAX_BEAMS];
     float max[MAX_BEAMS];
     int kind[MAX_BEAMS];
@@ -720,51 +715,95 @@ __device__ inline void put_beam(BeamShared &sh, const BeamArgs &a, int i, const 
     sh.o_token[i] = tok;
 }
 
-// The M best one by one: any mixture of dead, ended and live beams, NaN and -inf.
-__device__ inline void best_by_rounds(const BeamArgs &a, const uint64_t *keys, BeamShared &sh)
+// The list for any mixture of dead, ended and live beams, NaN, equal scores and -inf, where the bound leaves fewer than
+// M or too many: the candidates up to a score that at least M reach and at most BEAM_LIST, or up to the M-th of all, by
+// bisection of the scores, then of the places within the beam that the M-th belongs to.  Returns how many.
+// live(f): f(score, place, w) for the thread's candidates of live beams; beam(w, f): for those of beam w.  `kind`,
+// `first`: of beam threadIdx.x, and its only candidate's score where it has ended; n candidates reach `bound`; `top`:
+// the thread's best.  32 x 8 beams of 32000 f32, all of them ended, 16 out: 22 us a call, where 16 passes for the best
+// one each took 85; 4 x 32 of 151936 with 3 tokens left by a mask, 128 out: 331 us instead of 5264.
+template <int NTB, typename L, typename O>
+__device__ __forceinline__ int list_any_beams(const BeamArgs &a, int kind, uint64_t first, bool odd, int n,
+                                              uint64_t bound, uint64_t top, BeamShared &sh, L live, O beam)
 {
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, nwave = blockDim.x >> 6;
-    const int per = a.nch * a.kc;  // keys of a beam
-    Cand last = {~0ull, ~0ull, -1};
-    for (int i = 0; i < a.M; ++i) {
-        Cand best = {0, 0, a.W};
-        for (int w = 0; w < a.W; ++w) {
-            const int kind = sh.kind[w], n = kind == LIVE ? per : a.kc;
-            for (int j = threadIdx.x; j < n; j += blockDim.x) {
-                Cand c;
-                c.w = w;
-                if (kind == LIVE) {
-                    c.place = keys[static_cast<int64_t>(w) * per + j];
-                    if (!c.place)
-                        continue;
-                    c.score = ord_f64(cand_score(sh, w, c.place));
-                } else {
-                    c.place = 0xFFFFFFFFu - static_cast<uint32_t>(j);
-                    c.score = kind == BAD ? ~0ull : kind == ENDED && j == 0 ? ord_f64(sh.score[w]) : ORD64_NEG_INF;
-                }
-                keep_first(best, c, before(last, c));
-            }
-        }
-#pragma unroll
-        for (int o = 32; o; o >>= 1) {
-            Cand c;
-            c.score = __shfl_xor(best.score, o);
-            c.place = __shfl_xor(best.place, o);
-            c.w = __shfl_xor(best.w, o);
-            keep_first(best, c, true);
-        }
-        if (lane == 0)
-            sh.best[wave] = best;
+    const bool own = threadIdx.x < a.W;
+    const int kc = a.kc;  // candidates of a beam that is not live, the same score for all (but the ended one's first)
+    auto reach = [&](uint64_t c) {
+        int r = 0;
+        live([&](uint64_t score, uint64_t, int) { r += score >= c; });
+        if (own && kind != LIVE)
+            r += kind == BAD || ORD64_NEG_INF >= c ? kc : kind == ENDED && first >= c;
+        return r;
+    };
+    uint64_t lo = ORD64_NEG_INF, hi = ~0ull;  // (NaN is ~0)
+    if (odd) {
+        if (block_count<NTB>(reach(hi), 1, sh.count) >= a.M)
+            lo = hi;
+    } else if (n < a.M) {
+        hi = lo + 1;
+    } else {  // from the bound that too many reach to the best
+        lo = bound > lo ? bound : lo;
+        top = wave_max_u64(top);
+        if ((threadIdx.x & 63) == 0)
+            sh.top[threadIdx.x >> 6] = top;
         __syncthreads();
-        best = sh.best[0];
-        for (int v = 1; v < nwave; ++v)
-            keep_first(best, sh.best[v], true);
+        for (int w = 0; w < NTB / 64; ++w)
+            top = max_u64(top, sh.top[w]);
+        hi = top + 1;
+    }
+    bisect<NTB>(lo, hi, a.M, BEAM_LIST, sh.count, reach);
+    const uint64_t t = lo;
+    uint64_t p = 0;       // of the candidates that score t, those of beams before `last` count, and its own from place p
+    int last = a.W;
+    if (hi - lo <= 1) {
         __syncthreads();
-        if (threadIdx.x == 0)
-            put_beam(sh, a, i, best);
-        last = best;
+        if (own)
+            sh.tie[threadIdx.x] = 0;
+        __syncthreads();
+        live([&](uint64_t score, uint64_t, int w) {
+            if (score == t)
+                atomicAdd(&sh.tie[w], 1);
+        });
+        if (own && kind != LIVE)
+            sh.tie[threadIdx.x] = kind == BAD            ? kc * (t == ~0ull)
+                                  : t == ORD64_NEG_INF ? kc - (kind == ENDED)
+                                                       : kind == ENDED && first == t;
+        int need = a.M - block_count<NTB>(t == ~0ull ? 0 : reach(t + 1), 1, sh.count);
+        for (last = 0; last < a.W - 1 && sh.tie[last] < need; ++last)
+            need -= sh.tie[last];
+        if (sh.kind[last] == LIVE) {
+            uint64_t end = ~0ull;
+            if (sh.tie[last] > need)
+                bisect<NTB>(p, end, need, need, sh.count, [&](uint64_t c) {
+                    int r = 0;
+                    beam(last, [&](uint64_t score, uint64_t place, int) { r += score == t && place >= c; });
+                    return r;
+                });
+        } else {
+            const int j0 = sh.kind[last] == ENDED && t == ORD64_NEG_INF;
+            p = 0xFFFFFFFFu - static_cast<uint32_t>(j0 + need - 1);
+        }
     }
     __syncthreads();
+    if (threadIdx.x == 0)
+        sh.n = 0;
+    __syncthreads();
+    auto take = [&](uint64_t score, uint64_t place, int w) {
+        if (score > t || (score == t && (w < last || (w == last && place >= p)))) {
+            const int at = atomicAdd(&sh.n, 1);
+            if (at < BEAM_LIST)
+                sh.list[at] = Cand{score, place, w};
+        }
+    };
+    live(take);
+    for (int w = 0; w < a.W; ++w)
+        if (sh.kind[w] != LIVE)
+            for (int j = threadIdx.x; j < kc; j += NTB)
+                take(sh.kind[w] == BAD ? ~0ull
+                                       : sh.kind[w] == ENDED && j == 0 ? ord_f64(sh.score[w]) : ORD64_NEG_INF,
+                     0xFFFFFFFFu - static_cast<uint32_t>(j), w);
+    __syncthreads();
+    return sh.n < BEAM_LIST ? sh.n : BEAM_LIST;
 }
 
 // One batch entry.  Its blocks (blockIdx.y) all rank the candidates and share the copying of the state; block 0
@@ -867,31 +906,57 @@ __global__ __launch_bounds__(NTB) void k_beam_merge(BeamArgs a)
     }
     take(ended, 0xFFFFFFFFull, static_cast<int>(threadIdx.x));
     __syncthreads();
-    const int n = sh.n;
+    int n = sh.n;
     if (odd || n < a.M || n > BEAM_LIST) {
-        best_by_rounds(a, keys, sh);
-    } else {
-        // 2^shift threads take one candidate each, and NTB / 2^shift a slice of the others
-        const int shift = n <= 32 ? 5 : n <= 64 ? 6 : n <= 128 ? 7 : n <= 256 ? 8 : 9;
-        const int i = threadIdx.x & ((1 << shift) - 1), slices = NTB >> shift, len = (n + slices - 1) / slices;
-        const int j0 = (threadIdx.x >> shift) * len, j1 = j0 + len < n ? j0 + len : n;
-        if (threadIdx.x < BEAM_LIST)
-            sh.place[threadIdx.x] = 0;
-        __syncthreads();
-        if (i < n) {
-            const Cand c = sh.list[i];
-            int place = 0;
-#pragma unroll 2
-            for (int j = j0; j < j1; ++j)
-                place += before(sh.list[j], c);
-            if (place)
-                atomicAdd(&sh.place[i], place);
-        }
-        __syncthreads();
-        if (threadIdx.x < n && sh.place[threadIdx.x] < a.M)
-            put_beam(sh, a, sh.place[threadIdx.x], sh.list[threadIdx.x]);
-        __syncthreads();
+        auto live = [&](auto f) {
+            if constexpr (PER > 0) {
+#pragma unroll
+                for (int j = 0; j < PER; ++j)
+                    if (score[j])
+                        f(score[j], mine[j], w0);
+            } else {
+                for (int i = at0; i < n_cand; i += NTB) {
+                    int w;
+                    const uint64_t key = key_at(i, w), word = word_of(key, w);
+                    if (word)
+                        f(word, key, w);
+                }
+            }
+        };
+        auto beam = [&](int w, auto f) {
+            if constexpr (PER > 0) {
+                if (w == w0)
+                    live(f);
+            } else {
+                for (int i = threadIdx.x; i < a.nch * a.kc; i += NTB) {
+                    const uint64_t key = keys[static_cast<int64_t>(w) * a.nch * a.kc + i], word = word_of(key, w);
+                    if (word)
+                        f(word, key, w);
+                }
+            }
+        };
+        n = list_any_beams<NTB>(a, kind, ended, odd, n, static_cast<uint64_t>(t) << 32, top, sh, live, beam);
     }
+    // 2^shift threads take one candidate each, and NTB / 2^shift a slice of the others
+    const int shift = n <= 32 ? 5 : n <= 64 ? 6 : n <= 128 ? 7 : n <= 256 ? 8 : 9;
+    const int i = threadIdx.x & ((1 << shift) - 1), slices = NTB >> shift, len = (n + slices - 1) / slices;
+    const int j0 = (threadIdx.x >> shift) * len, j1 = j0 + len < n ? j0 + len : n;
+    if (threadIdx.x < BEAM_LIST)
+        sh.place[threadIdx.x] = 0;
+    __syncthreads();
+    if (i < n) {
+        const Cand c = sh.list[i];
+        int place = 0;
+#pragma unroll 2
+        for (int j = j0; j < j1; ++j)
+            place += before(sh.list[j], c);
+        if (place)
+            atomicAdd(&sh.place[i], place);
+    }
+    __syncthreads();
+    if (threadIdx.x < n && sh.place[threadIdx.x] < a.M)
+        put_beam(sh, a, sh.place[threadIdx.x], sh.list[threadIdx.x]);
+    __syncthreads();
     if (blockIdx.y == 0) {
         for (int j = threadIdx.x; j < a.M; j += NTB) {
             const int64_t o = static_cast<int64_t>(b) * a.M + j;

@@ -240,6 +240,37 @@ def test_beam_step_of_special_rows(dtype):
                        finished=torch.tensor([[True, True, True]]))
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B,W,V,M", [(2, 4, 700, 8), (1, 32, 3000, 128), (2, 8, 40000, 16), (1, 3, 50, 100)])
+def test_beam_step_with_little_left_or_much_equal(B, W, V, M, dtype):
+    base = rows(B, W, V, dtype, V + M)
+    scores = some_scores(B, W, M)
+    first = torch.full_like(scores, -np.inf)
+    first[:, W // 2] = -0.5
+    for left in (1, 3, min(200, V - 7)):
+        z = torch.full_like(base, -np.inf)
+        z[..., 7:7 + left] = base[..., 7:7 + left]
+        check_beam(z, scores, M, label="%d tokens left" % left)
+        check_beam(z, first, M, label="%d tokens left of one beam" % left)
+    zero = torch.zeros_like(base)
+    zero[..., 3] = -np.inf
+    lowest, nan = torch.full_like(scores, torch.finfo(torch.float32).min), scores.clone()
+    nan[:, W - 1] = np.nan
+    ended = torch.ones((B, W), dtype=torch.bool)
+    some = torch.arange(W).expand(B, W) % 2 == 1
+    # equal scores have an order: these are the same candidates in the same places
+    for label, z, sc, end in (("equal logits", zero, scores, None), ("all equal", zero, torch.ones_like(scores), None),
+                              ("lowest scores", base, lowest, None), ("all ended", base, scores, ended),
+                              ("all ended, equal scores", base, torch.ones_like(scores), ended),
+                              ("some ended, equal logits", zero, torch.ones_like(scores), some),
+                              ("a NaN score among ended ones", base, nan, ended), ("a NaN score", zero, nan, None)):
+        eos = -1 if end is None else 5
+        got = check_beam(z, sc, M, eos=eos, finished=end, label=label)
+        _, parent, token = plain.beam(host(z), sc.numpy(), M, eos, None if end is None else end.numpy())
+        assert np.array_equal(got["parent"].cpu().numpy(), parent), label
+        assert np.array_equal(got["token"].cpu().numpy(), token), label
+
+
 def test_beam_step_does_not_read_dead_and_ended_rows():
     z = rows(1, 3, 3000, torch.float32, 3)
     scores = torch.tensor([[-1.0, -np.inf, -0.5]])
