@@ -12,7 +12,7 @@
 // one block can hold (up to 1024 threads) is one chunk, and needs no join.
 //
 // What bounds it, on one MI355X: 512 bf16 rows of 151936, k = 20 (156 MB): 32.0 + 4.7 us, 4.9 TB/s in the chunks'
-// launch, which issues 708 vector instructions a wave (59 of them exponentials, at 16 cycles, the others at 4): 30 us
+// launch, which issues 711 vector instructions a wave (59 of them exponentials, at 16 cycles, the others at 4): 30 us
 // of issue at 2.4 GHz, so the vector units bound bfloat16, not the 24 us the bytes take.  float32 has half the elements
 // a byte: 1024 rows of 50021, k = 16 (205 MB): 38 us in all, 5.4 TB/s.  Few rows are bound by latency: 17 f32 rows,
 // k = 64: 9.0 + 5.3 us.
@@ -24,7 +24,7 @@
 // beam: W beams' candidates score s_w + log softmax(z_w)_v.  Within a beam they are ordered by their logits, so the
 // M best of all are among the M largest of each chunk, and k_top_chunk serves both.  k_beam_merge scores them in 64
 // bits, ranks them as k_top_merge does, and writes state and history in the new order: 32 x 8 bf16 beams of 151936,
-// 16 out of each, 4 KiB of state: 19.4 + 9.1 us (71 MB); four f32 beams of one request, 8 out: 5.2 + 8.2 us, latency.
+// 16 out of each, 4 KiB of state: 19.0 + 9.1 us (71 MB); four f32 beams of one request, 8 out: 5.0 + 8.1 us, latency.
 #define DH_NT 256
 #define DH_NS dht
 #include "dh_rows.h"
@@ -753,7 +753,8 @@ __device__ __forceinline__ int list_any_beams(const BeamArgs &a, int kind, uint6
     }
     bisect<NTB>(lo, hi, a.M, BEAM_LIST, sh.count, reach);
     const uint64_t t = lo;
-    uint64_t p = 0;       // of the candidates that score t, those of beams before `last` count, and its own from place p
+    // of the candidates that score t, those of beams before `last` are in, and its own from place p on
+    uint64_t p = 0;
     int last = a.W;
     if (hi - lo <= 1) {
         __syncthreads();
