@@ -162,7 +162,7 @@ __device__ inline void finish_row(const Rows &rows, const Teach &te, const Place
     const Part part = first_part(parts, nch);
     int id[2] = {-1, -1};
     float value[2] = {NEG_INF, NEG_INF};
-    const double L = te.lse ? te.lse[row] : 0.0;
+    const double L = te.lse ? static_cast<double>(te.lse[row]) : NINF;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
         if (lane + 64 * i < te.k) {
@@ -187,14 +187,13 @@ __device__ inline void finish_row(const Rows &rows, const Teach &te, const Place
     // t becomes the logarithm of an entry's mass (without L: of its mass times p_sum)
     bool live = __ballot(valid[0] || valid[1]) != 0;
     double p[2] = {0.0, 0.0};
-    double t_top = L;
-    if (live && !te.lse) {
-        t_top = wave_max_f64(fmax(t[0], t[1]));
-        if (!(t_top > NINF)) {  // nothing but -inf (no mass: left out) or NaN
-            live = __ballot((valid[0] && t[0] != t[0]) || (valid[1] && t[1] != t[1])) != 0;
-            t_top = __builtin_nan("");
-        }
+    double t_top = live ? wave_max_f64(fmax(t[0], t[1])) : NINF;
+    if (live && !(t_top > NINF) && L == NINF) {  // nothing but -inf (no mass: left out) or NaN
+        live = __ballot((valid[0] && t[0] != t[0]) || (valid[1] && t[1] != t[1])) != 0;
+        t_top = __builtin_nan("");
     }
+    if (te.lse)
+        t_top = L;
     if (!live) {
         if (lane == 0)
             loss[row] = 0.f;

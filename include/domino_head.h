@@ -322,8 +322,9 @@ int domino_beam_step(const domino_logits *logits, const domino_beam *beam, void 
  *         event), else 0;  Qr = the sum of q over the ids that no entry names
  *     loss = temperature^2 ( sum_j p_j (t_j - log q_j) + rest log(rest / Qr) )
  * An id outside [0, V) (-1 pads a row) is passed over; an id named twice has both masses.  A row without a
- * valid id, one whose entries' values are all -inf (without teacher_lse), and rows r >= n_rows[b] are left
- * out: loss 0, gradient 0, whatever their logits hold.  A row of nothing but -inf has
+ * valid id, one whose entries' values are all -inf (with teacher_lse: and that is -inf too, as domino_top_logits
+ * leaves a row of nothing but -inf), and rows r >= n_rows[b] are left out: loss 0, gradient 0, whatever their
+ * logits hold.  A row of nothing but -inf has
  * q = 0; a NaN or +inf among a row's logits makes its loss and gradient NaN.
  *   ids        [B, R, k] int32, values [B, R, k] float32, teacher_lse [B, R] float32 or NULL
  *   n_rows     [B] int32 or NULL (all R)

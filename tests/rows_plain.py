@@ -81,7 +81,7 @@ def distill(z, ids, values, teacher_lse, tau, n_rows=None):
                 continue
             i, t = ids[b, r][ok], np.asarray(values[b, r][ok], np.float64) / tau
             L = lse(t) if teacher_lse is None else float(teacher_lse[b, r])
-            if teacher_lse is None and L == NINF:
+            if L == NINF and (t == NINF).all():
                 continue
             t = log_softmax(t) if teacher_lse is None and np.isfinite(L) else t - L
             p = np.exp(t)
