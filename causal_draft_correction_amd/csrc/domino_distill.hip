@@ -7,7 +7,8 @@
 //     dloss/dz_v = tau [ Mm q_v - sum_{j: id_j = v} p_j ]     where an entry names v
 //                = tau (q_v / Qr) [ Mm Qr - rest ]             elsewhere
 // The sum over the ids that no entry names is taken by itself (named elements count as -inf), never as a
-// difference, and has a maximum of its own: it keeps its precision where the student is nearly certain.
+// difference, and has a maximum of its own; the named elements are added in 64 bits.  So log s and Qr both keep their
+// precision where the student is nearly certain of a named id and the loss is small.
 //
 // The forward pass reads a row once (k_distill_part, one block per chunk, values in registers) and joins the
 // chunks and the k entries in 64 bits (k_distill_final).  The backward pass reads it once and writes it once
@@ -113,11 +114,11 @@ __device__ inline Part chunk_part(typename Vec<T>::raw (&x)[NV], const Scale &sc
     return Part{total != total ? __builtin_nanf("") : m, static_cast<float>(total)};
 }
 
-// The chunk's part; with TAIL over the elements that no entry names.
-template <typename T, int NV, bool TAIL>
+// The chunk's part, over the elements that no entry names.
+template <typename T, int NV>
 __global__ __launch_bounds__(NT) void k_distill_part(Rows rows, Teach te, Split sp, bool keep, Scale sc, Part *parts)
 {
-    __shared__ uint32_t mask[TAIL ? MASK_WORDS<T, NV> : 1][NT];
+    __shared__ uint32_t mask[MASK_WORDS<T, NV>][NT];
     __shared__ float red_m[NWAVE], red_s[NWAVE];
     const int i_row = static_cast<int>(sp.by.quotient(blockIdx.x)), c = static_cast<int>(blockIdx.x) - i_row * sp.nch;
     const Place place = rows.place(i_row);
@@ -127,8 +128,7 @@ __global__ __launch_bounds__(NT) void k_distill_part(Rows rows, Teach te, Split 
     int id = -1;
     if (static_cast<int>(threadIdx.x) < te.k)
         id = te.ids[static_cast<int64_t>(row) * te.k + threadIdx.x];
-    if constexpr (TAIL)
-        clear_mask(mask);
+    clear_mask(mask);
     if (!__syncthreads_or(in_row(id, rows.V)))
         return;
     typename Vec<T>::raw x[NV];
@@ -137,15 +137,14 @@ __global__ __launch_bounds__(NT) void k_distill_part(Rows rows, Teach te, Split 
         load_chunk<T, NV, NT, true>(x, z, rows.V, c, cvec);
     else
         load_chunk<T, NV>(x, z, rows.V, c, cvec);
-    if constexpr (TAIL)
-        drop_named<T, NV>(x, mask, id, chunk_begin<T>(c, cvec, rows.V), chunk_begin<T>(c + 1, cvec, rows.V));
+    drop_named<T, NV>(x, mask, id, chunk_begin<T>(c, cvec, rows.V), chunk_begin<T>(c + 1, cvec, rows.V));
     const Part part = chunk_part<T, NV, NT>(x, sc, red_m, red_s);
     if (threadIdx.x == 0)
         parts[static_cast<int64_t>(row) * sp.nch + c] = part;
 }
 
 // One row, by one wave, from the parts of its nch chunks: its loss, and what the backward pass needs of it:
-//     stats = { m, A, 1 (0: a row that is left out), log-sum-exp, h_0 .. h_{k-1} }
+//     stats = { m of the other ids, A, 1 (0: a row that is left out), log-sum-exp, h_0 .. h_{k-1} }
 // so that dloss/dz_v = tau A exp((z_v - m) / tau), and tau h_j for v = id_j.  A lane takes the entries lane and
 // lane + 64.  Everything is in 64 bits; differences are taken from the maxima, before their logarithms: rows at the
 // type's lowest value keep them.
@@ -251,20 +250,19 @@ __device__ inline void finish_row(const Rows &rows, const Teach &te, const Place
                     first[i] = first[i] && j >= lane + 64 * i;
                 }
     }
-    double rest = 0.0, m = m_rest, s = s_rest, of_rest = s_rest;
-    if (te.lse) {
-        rest = 1.0 - mass;
-        rest = rest < 0.0 ? 0.0 : rest;
-        const double top = wave_max_f64(fmax(z[0], z[1]));
-        m = m > top || m != m ? m : top;
-        of_rest = m_rest == NEG_INF ? 0.0 : m_rest == m ? s_rest : s_rest * exp((m_rest - m) * inv_tau);
-    }
+    double rest = te.lse ? 1.0 - mass : 0.0;
+    rest = rest < 0.0 ? 0.0 : rest;
+    // the student's maximum; its sum over the other ids, and over all: the named ones, one by one, are in 64 bits, so
+    // that log s keeps its digits where they have nearly all of the mass
+    const double top = wave_max_f64(fmax(z[0], z[1]));
+    const double m = m_rest > top || m_rest != m_rest ? m_rest : top;
+    const double of_rest =
+        m_rest == NEG_INF ? 0.0 : m_rest == m ? s_rest : s_rest * exp((m_rest - m) * inv_tau);
     double q[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
         q[i] = !valid[i] || m == NINF ? 0.0 : z[i] == m ? 1.0 : exp((z[i] - m) * inv_tau);
-    if (te.lse)
-        s = wave_sum_f64((first[0] ? q[0] : 0.0) + (first[1] ? q[1] : 0.0)) + of_rest;
+    const double s = wave_sum_f64((first[0] ? q[0] : 0.0) + (first[1] ? q[1] : 0.0)) + of_rest;
     // four logarithms, one in each of the first lanes
     const double logs = log(lane == 0 ? s : lane == 1 ? s_rest : lane == 2 ? rest : p_sum);
     const double log_s = __shfl(logs, 0), log_s_rest = __shfl(logs, 1), log_r = __shfl(logs, 2);
@@ -280,14 +278,9 @@ __device__ inline void finish_row(const Rows &rows, const Teach &te, const Place
     }
     double sum = wave_sum_f64(terms);
     const double inv_s = s > 0.0 || s != s ? 1.0 / s : 0.0;
-    double A = total * inv_s;
-    double ref = m;
-    if (te.lse) {
-        if (rest > 0.0)
-            sum += rest * (log_r - (m_rest == NEG_INF ? NINF : (m_rest - m) * inv_tau + log_s_rest - log_s));
-        A = m_rest == NEG_INF ? 0.0 : (total * of_rest * inv_s - rest) / s_rest;
-        ref = m_rest;
-    }
+    if (rest > 0.0)
+        sum += rest * (log_r - (m_rest == NEG_INF ? NINF : (m_rest - m) * inv_tau + log_s_rest - log_s));
+    double A = m_rest == NEG_INF ? 0.0 : (total * of_rest * inv_s - rest) / s_rest;
     const bool none = !(lse < -NINF);  // a NaN or +inf among the logits: no distribution
     if (none)
         sum = A = __builtin_nan("");
@@ -295,7 +288,7 @@ __device__ inline void finish_row(const Rows &rows, const Teach &te, const Place
         loss[row] = static_cast<float>(tau * tau * sum);
     if (st) {
         if (lane == 0) {
-            st[0] = ref > NINF || ref != ref ? static_cast<float>(ref) : 0.f;
+            st[0] = m_rest > NEG_INF || m_rest != m_rest ? m_rest : 0.f;
             st[1] = static_cast<float>(A);
             st[2] = 1.f;
             st[3] = static_cast<float>(lse);
@@ -378,14 +371,14 @@ __global__ __launch_bounds__(NT) void k_distill_grad(Rows rows, int k, Split sp,
 
 // A row of at most NV vectors a thread, by one block: loss, and with GRAD its gradient (else the statistics for a
 // later backward pass).  The row stays in registers from its maximum to its gradient: it is read once.
-template <typename T, int NTB, int NV, bool TAIL, bool GRAD>
+template <typename T, int NTB, int NV, bool GRAD>
 __global__ __launch_bounds__(NTB) void k_distill_row(Rows rows, Teach te, double tau, Scale sc, float *loss,
                                                     float *stats, const float *grad_loss, Rows grad)
 {
     typedef Vec<T> VT;
     __shared__ float red_m[NTB / 64], red_s[NTB / 64];
     __shared__ Part part;
-    __shared__ uint32_t mask[TAIL ? MASK_WORDS<T, NV> : 1][NTB];
+    __shared__ uint32_t mask[MASK_WORDS<T, NV>][NTB];
     __shared__ __align__(16) int s_id[MAX_IDS];
     __shared__ double s_p[MAX_IDS];
     __shared__ float s_stat[HEAD + MAX_IDS];
@@ -395,14 +388,12 @@ __global__ __launch_bounds__(NTB) void k_distill_row(Rows rows, Teach te, double
     int id = -1;
     if (static_cast<int>(threadIdx.x) < te.k && rows.counts(place.b, place.r))
         id = te.ids[static_cast<int64_t>(row) * te.k + threadIdx.x];
-    if constexpr (TAIL)
-        clear_mask(mask);
+    clear_mask(mask);
     typename VT::raw x[NV];
     const bool any = __syncthreads_or(in_row(id, rows.V));
     if (any) {
         load_chunk<T, NV, NTB>(x, row_at<T>(rows, place), rows.V, 0, NV * NTB);
-        if constexpr (TAIL)
-            drop_named<T, NV>(x, mask, id, 0, rows.V);  // (their gradients are written last)
+        drop_named<T, NV>(x, mask, id, 0, rows.V);  // (their gradients are written last)
         const Part got = chunk_part<T, NV, NTB>(x, sc, red_m, red_s);
         if (threadIdx.x == 0)
             part = got;
@@ -489,12 +480,7 @@ struct PartCall {
     template <typename T, int NV>
     void run() const
     {
-        if (te.lse)
-            hipLaunchKernelGGL((k_distill_part<T, NV, true>), dim3(grid), dim3(NT), 0, st, rows, te, sp, keep, sc,
-                               parts);
-        else
-            hipLaunchKernelGGL((k_distill_part<T, NV, false>), dim3(grid), dim3(NT), 0, st, rows, te, sp, keep, sc,
-                               parts);
+        hipLaunchKernelGGL((k_distill_part<T, NV>), dim3(grid), dim3(NT), 0, st, rows, te, sp, keep, sc, parts);
     }
 };
 
@@ -527,23 +513,15 @@ struct RowCall {
     const float *grad_loss;
     unsigned n;
     hipStream_t st;
-    template <typename T, int NTB, int NV, bool TAIL>
-    void launch() const
-    {
-        if (grad_loss)
-            hipLaunchKernelGGL((k_distill_row<T, NTB, NV, TAIL, true>), dim3(n), dim3(NTB), 0, st, rows, te,
-                               static_cast<double>(tau), sc, loss, stats, grad_loss, grad);
-        else
-            hipLaunchKernelGGL((k_distill_row<T, NTB, NV, TAIL, false>), dim3(n), dim3(NTB), 0, st, rows, te,
-                               static_cast<double>(tau), sc, loss, stats, grad_loss, grad);
-    }
     template <typename T, int NTB, int NV>
     void run() const
     {
-        if (te.lse)
-            launch<T, NTB, NV, true>();
+        if (grad_loss)
+            hipLaunchKernelGGL((k_distill_row<T, NTB, NV, true>), dim3(n), dim3(NTB), 0, st, rows, te,
+                               static_cast<double>(tau), sc, loss, stats, grad_loss, grad);
         else
-            launch<T, NTB, NV, false>();
+            hipLaunchKernelGGL((k_distill_row<T, NTB, NV, false>), dim3(n), dim3(NTB), 0, st, rows, te,
+                               static_cast<double>(tau), sc, loss, stats, grad_loss, grad);
     }
     template <typename T>
     void pick() const

@@ -66,3 +66,48 @@ def test_teacher_rows_whose_mask_leaves_nothing_are_left_out(V, dtype):
     values[0, 1, 3] = np.nan
     one, two, _ = three_ways(z, top["ids"], values, top["lse"], g)
     assert np.isnan(float(one[0][0, 1])) and np.isnan(float(two[0][0, 1]))
+
+
+SUM = 140 * H  # a chunk's sum of exponentials, whatever the order of its additions (derived in test_gpu_rows.py)
+
+
+def certain_rows(B, R, V, dtype, seed, peak=22.0):
+    """Rows nearly certain of six ids, and those ids."""
+    g = torch.Generator().manual_seed(seed)
+    z = torch.randn((B, R, V), generator=g)
+    at = torch.stack([torch.randperm(V, generator=g)[:6] for _ in range(B * R)]).view(B, R, 6)
+    z.scatter_(2, at, peak - 0.7 * torch.arange(6).float() + torch.randn((B, R, 6), generator=g))
+    return z.to(dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("V,k,tau", [(300, 20, 1.0), (9001, 9, 0.7), (70001, 64, 1.442), (40000, 6, 1.0)])
+def test_small_losses_of_a_student_that_is_nearly_certain(V, k, tau, tail, dtype):
+    """Only the other ids' sum is taken in float32: log q of a named id is off by Qr SUM at most, the loss by the
+    masses times that (and rest times the sum's own error), and its rounding; so are the gradients of named ids."""
+    tau = float(np.float32(tau))  # what the entry point takes
+    z = certain_rows(2, 4, V, dtype, V + k)
+    t = z.float() + 0.05 * torch.randn(z.shape, generator=torch.Generator().manual_seed(k))
+    values, ids = t.topk(k)
+    lse = torch.logsumexp(t.double() / tau, -1).float() if tail else None
+    g = (0.5 + torch.rand((2, 4), generator=torch.Generator().manual_seed(V))).cuda()
+    dev = z.cuda()
+    one, two, _ = three_ways(dev, ids.int().cuda(), values.cuda(), None if lse is None else lse.cuda(), g,
+                             temperature=tau)
+    loss, grad, _ = plain.distill(z.float().numpy(), ids.numpy(), values.numpy(),
+                                  None if lse is None else lse.numpy(), tau)
+    y = z.double() / tau
+    q = torch.softmax(y, -1)
+    other = (1.0 - q.gather(2, ids).sum(-1)).clamp(min=0).numpy() + 1e-15
+    rest = np.zeros((2, 4)) if lse is None else np.maximum(0, 1 - np.exp(
+        values.numpy().astype(np.float64) / tau - lse.numpy()[..., None].astype(np.float64)).sum(-1))
+    most = tau * tau * SUM * (2 * other + 2 * rest) + np.abs(loss) * H + 1e-13
+    named = np.take_along_axis(grad, ids.numpy(), 2) * g.cpu().numpy()[..., None].astype(np.float64)
+    qn = q.gather(2, ids).numpy()
+    for got, gr in (one, two):
+        assert (np.abs(host(got).astype(np.float64) - loss) <= most).all(), np.abs(host(got) - loss).max()
+        if dtype == torch.float32:
+            off = np.abs(np.take_along_axis(host(gr).astype(np.float64), ids.numpy(), 2) - named)
+            # h, grad_loss * tau and their product are rounded to float32 (tau is: H of the product)
+            assert (off <= 1.5 * tau * qn * other[..., None] * SUM + 4 * H * np.abs(named) + 1e-13).all(), off.max()
