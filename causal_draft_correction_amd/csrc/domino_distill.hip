@@ -3,6 +3,7 @@
 // With y = z / tau, q = softmax(y), the teacher's entries j (id in [0, V)), t_j = value_j / tau - L with L the
 // teacher's log-sum-exp (given, or that of the entries alone), p_j = exp t_j, P = sum p_j,
 //     rest = max(0, 1 - P) where L is given, else 0;   Mm = P + rest;   Qr = sum of q over ids no entry names
+//     (where 1 - P and Qr are no more than the rounding of L leaves open: as if L were not given)
 //     loss = tau^2 [ sum_j p_j (t_j - log q_j) + rest log(rest / Qr) ]
 //     dloss/dz_v = tau [ Mm q_v - sum_{j: id_j = v} p_j ]     where an entry names v
 //                = tau (q_v / Qr) [ Mm Qr - rest ]             elsewhere
@@ -143,6 +144,13 @@ __global__ __launch_bounds__(NT) void k_distill_part(Rows rows, Teach te, Split 
         parts[static_cast<int64_t>(row) * sp.nch + c] = part;
 }
 
+// L is a float32, so the masses p_j carry its rounding, up to |L| 2^-24, and the error of the sum it was taken from
+// (LSE_STEPS half steps: an exponential's own 2, its argument's, 15 of a thread's additions).  Where neither the
+// teacher's entries nor the student leave more than that to the other ids, 1 - sum p is nothing but this noise, which
+// rest log(rest / Qr) would make an infinity of where Qr is 0 (entries that name every id, or a mask that both share).
+// An L so large that the noise reaches MAX_NOISE tells nothing of the other ids, and the formula stands as it is.
+constexpr double LSE_STEPS = 32.0, MAX_NOISE = 0x1p-6;
+
 // One row, by one wave, from the parts of its nch chunks: its loss, and what the backward pass needs of it:
 //     stats = { m of the other ids, A, 1 (0: a row that is left out), log-sum-exp, h_0 .. h_{k-1} }
 // so that dloss/dz_v = tau A exp((z_v - m) / tau), and tau h_j for v = id_j.  A lane takes the entries lane and
@@ -211,11 +219,6 @@ __device__ inline void finish_row(const Rows &rows, const Teach &te, const Place
     float m_rest;
     double s_rest;
     join_parts(part, parts, nch, inv_tau, m_rest, s_rest);
-    double mass = p_sum, log_p = 0.0;
-    if (!te.lse) {
-        p[0] /= p_sum, p[1] /= p_sum;
-        mass = wave_sum_f64(p[0] + p[1]);
-    }
     // entries that name an id again: the first of them stands for it, with the mass of all
     double named[2] = {p[0], p[1]};
     bool first[2] = {valid[0], valid[1]};
@@ -250,8 +253,6 @@ __device__ inline void finish_row(const Rows &rows, const Teach &te, const Place
                     first[i] = first[i] && j >= lane + 64 * i;
                 }
     }
-    double rest = te.lse ? 1.0 - mass : 0.0;
-    rest = rest < 0.0 ? 0.0 : rest;
     // the student's maximum; its sum over the other ids, and over all: the named ones, one by one, are in 64 bits, so
     // that log s keeps its digits where they have nearly all of the mass
     const double top = wave_max_f64(fmax(z[0], z[1]));
@@ -263,12 +264,23 @@ __device__ inline void finish_row(const Rows &rows, const Teach &te, const Place
     for (int i = 0; i < 2; ++i)
         q[i] = !valid[i] || m == NINF ? 0.0 : z[i] == m ? 1.0 : exp((z[i] - m) * inv_tau);
     const double s = wave_sum_f64((first[0] ? q[0] : 0.0) + (first[1] ? q[1] : 0.0)) + of_rest;
+    bool alone = !te.lse;  // the entries are all of the teacher: their masses are brought to a sum of 1
+    double rest = 0.0;
+    if (te.lse) {
+        rest = 1.0 - p_sum;
+        const double noise = fmin((fabs(L) + LSE_STEPS) * 0x1p-24, MAX_NOISE);
+        alone = fabs(rest) <= noise && of_rest <= noise * s;
+        rest = alone || rest < 0.0 ? 0.0 : rest;
+    }
+    const double scale = alone ? 1.0 / p_sum : 1.0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        p[i] *= scale, named[i] *= scale;
     // four logarithms, one in each of the first lanes
     const double logs = log(lane == 0 ? s : lane == 1 ? s_rest : lane == 2 ? rest : p_sum);
     const double log_s = __shfl(logs, 0), log_s_rest = __shfl(logs, 1), log_r = __shfl(logs, 2);
-    if (!te.lse)
-        log_p = __shfl(logs, 3);
-    const double total = mass + rest;
+    const double log_p = alone ? __shfl(logs, 3) : 0.0;
+    const double total = p_sum * scale + rest;
     const double lse = m == NINF ? NINF : m * inv_tau + log_s;
     double terms = 0.0;
 #pragma unroll

@@ -95,6 +95,10 @@ def distill(z, ids, values, teacher_lse, tau, n_rows=None):
             rest = 0.0 if teacher_lse is None else max(0.0, 1.0 - p.sum())
             other = np.ones(V, bool)
             other[i] = False
+            if teacher_lse is not None:  # what a float32 log-sum-exp cannot tell from no mass
+                noise = min((abs(L) + 32) * 2.0 ** -24, 2.0 ** -6)
+                if abs(1.0 - p.sum()) <= noise and q[other].sum() <= noise:
+                    rest, t, p = 0.0, t - np.log(p.sum()), p / p.sum()
             with np.errstate(divide="ignore", invalid="ignore"):
                 kl = sum(pj * (tj - logq[v]) for pj, tj, v in zip(p, t, i) if pj > 0)
                 log_rest = lse(logq[other]) if other.any() else NINF
@@ -103,7 +107,7 @@ def distill(z, ids, values, teacher_lse, tau, n_rows=None):
             mass = p.sum() + rest
             g = mass * q
             s = mass * q
-            if teacher_lse is not None and log_rest > NINF:
+            if rest > 0 and log_rest > NINF:
                 share = np.exp(log_softmax(y[other]))
                 g[other] -= rest * share
                 s[other] += rest * share

@@ -111,3 +111,68 @@ def test_small_losses_of_a_student_that_is_nearly_certain(V, k, tau, tail, dtype
             off = np.abs(np.take_along_axis(host(gr).astype(np.float64), ids.numpy(), 2) - named)
             # h, grad_loss * tau and their product are rounded to float32 (tau is: H of the product)
             assert (off <= 1.5 * tau * qn * other[..., None] * SUM + 4 * H * np.abs(named) + 1e-13).all(), off.max()
+
+
+def noise_of(lse):
+    """What a float32 log-sum-exp leaves open of a mass (include/domino_head.h)."""
+    return np.minimum((np.abs(lse.astype(np.float64)) + 32) * H, 2.0 ** -6)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("V,k,left,tau,fill", [
+    (7, 7, 7, 1.0, None), (50, 50, 50, 0.5, None), (128, 128, 128, 2.0, None),
+    *[(V, k, left, 1.0, fill) for V, k, left in ((2000, 64, 40), (20000, 128, 100), (70001, 64, 5))
+      for fill in ("-inf", "lowest")]])
+def test_a_student_that_is_its_teacher_where_the_entries_hold_all_there_is(V, k, left, tau, fill, dtype):
+    """Masses brought to a sum of 1 and a sum of q that is all named: equal in 64 bits, whatever way the teacher's
+    log-sum-exp was rounded."""
+    z = logits(8, 25, V, dtype, V + k)
+    if fill:
+        at = torch.rand((8, 25, V), generator=torch.Generator().manual_seed(k)).argsort(-1)[..., :left].cuda()
+        x = torch.full_like(z, -np.inf if fill == "-inf" else torch.finfo(dtype).min)
+        z = x.scatter(2, at, z.gather(2, at))
+    top = dca.top_logits(z, k, temperature=tau)
+    g = torch.ones((8, 25), device="cuda")
+    one, two, _ = three_ways(z, top["ids"], top["values"], top["lse"], g, temperature=tau)
+    for loss, grad in (one, two):
+        assert float(loss.abs().max()) <= 1e-12
+        assert float(grad.float().abs().max()) <= 1e-12
+
+
+@pytest.mark.parametrize("V,k", [(2000, 64), (9001, 128), (70001, 64)])
+@pytest.mark.parametrize("tau", [1.0, 0.1, 0.05, 0.01, 0.001])
+def test_top_logits_into_distill_at_low_temperatures(V, k, tau):
+    """Against the loss with the teacher's log-sum-exp in 64 bits: a mass is off by the noise of L (the other ids' by
+    that too), and x log(x / Qr) over such a step, or up to twice that where a row counts as without L, by the step
+    times |log Qr| + |log noise| + 1; a student that is its teacher by a few times the noise."""
+    tau = float(np.float32(tau))
+    target = logits(1, 6, V, torch.float32, V, 4.0)
+    g = torch.ones((1, 6), device="cuda")
+    top = dca.top_logits(target, k, temperature=tau)
+    ids = top["ids"].long()
+    noise = noise_of(host(top["lse"]))
+    t = target.double() / tau
+    logp = torch.log_softmax(t, -1)
+
+    def other_mass(y):  # log of the other ids' sum
+        return y.scatter(2, ids, -np.inf).logsumexp(-1)
+
+    log_rest = other_mass(logp)
+    for name, z in (("itself", target), ("another", logits(1, 6, V, torch.float32, V + 1, 1.0) + target)):
+        logq = torch.log_softmax(z.double() / tau, -1)
+        log_qr = other_mass(logq)
+        p, lq = logp.gather(2, ids).exp(), logq.gather(2, ids)
+        terms = torch.where(p > 0, p * (logp.gather(2, ids) - lq), 0.0)
+        rest = log_rest.exp()
+        want = (terms.sum(-1) + torch.where(rest > 0, rest * (log_rest - log_qr), 0.0)).cpu().numpy()
+        if name == "itself":
+            most = 4 * noise + 2 * SUM * rest.cpu().numpy()
+        else:
+            size = (terms.abs().sum(-1) + log_qr.abs()).cpu().numpy()
+            most = 2 * noise * (size + 3 + np.abs(np.log(noise))) + 2 * SUM + np.abs(want) * H
+        one, two, _ = three_ways(z, top["ids"], top["values"], top["lse"], g, temperature=tau)
+        for loss, grad in (one, two):
+            off = np.abs(host(loss).astype(np.float64) / tau ** 2 - want)
+            assert (off <= most).all(), (name, off, most)
+            if name == "itself":
+                assert (np.abs(host(grad) / tau).max(-1) <= 4 * noise + 2 * SUM).all(), name
