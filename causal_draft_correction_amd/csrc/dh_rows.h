@@ -371,14 +371,15 @@ __device__ inline double wave_max_f64(double v)
 // What the chunks of a row leave of its log-sum-exp: the maximum m (NaN: the chunk holds a NaN) and
 // s = sum exp((z - m) / tau), (-inf, 0) for a chunk of nothing but -inf.
 struct Part {
-    float m, s;
+    float m;
+    double s;
 };
 
 // The first part a lane has to join (loaded early, ahead of what else the caller waits for).
 __device__ inline Part first_part(const Part *parts, int nch)
 {
     const int lane = threadIdx.x & 63;
-    return lane < nch ? parts[lane] : Part{NEG_INF, 0.f};
+    return lane < nch ? parts[lane] : Part{NEG_INF, 0.0};
 }
 
 // A row's maximum and its sum of exponentials from its chunks' parts, in 64 bits; every lane of the wave gets
@@ -397,11 +398,11 @@ __device__ inline void join_parts(const Part &first, const Part *parts, int nch,
     bad = __ballot(bad) != 0;
     double t = 0.0;
     if (first.m > NEG_INF)
-        t = static_cast<double>(first.s) * (first.m == m ? 1.0 : exp((static_cast<double>(first.m) - m) * inv_tau));
+        t = first.s * (first.m == m ? 1.0 : exp((static_cast<double>(first.m) - m) * inv_tau));
     for (int c = lane + 64; c < nch; c += 64) {
         const Part p = parts[c];
         if (p.m > NEG_INF)
-            t += static_cast<double>(p.s) * (p.m == m ? 1.0 : exp((static_cast<double>(p.m) - m) * inv_tau));
+            t += p.s * (p.m == m ? 1.0 : exp((static_cast<double>(p.m) - m) * inv_tau));
     }
     s = wave_sum_f64(t);
     if (bad)

@@ -112,7 +112,7 @@ __device__ inline Part chunk_part(typename Vec<T>::raw (&x)[NV], const Scale &sc
     for (int w = 0; w < NTB / 64; ++w)
         total += static_cast<double>(red_s[w]);
     total *= ex.fix(sc);
-    return Part{total != total ? __builtin_nanf("") : m, static_cast<float>(total)};
+    return Part{total != total ? __builtin_nanf("") : m, total};
 }
 
 // The chunk's part, over the elements that no entry names.

@@ -220,7 +220,8 @@ struct ChunkShared {
     int at[VECS];            // first element of each
     uint32_t bound[NTB / 64];
     int place[NTB];
-    float m[NTB / 64], s[NTB / 64];
+    float m[NTB / 64];
+    double s[NTB / 64];
     uint32_t count[2 * (NTB / 64)];
     int nvec, n;
 };
@@ -441,8 +442,8 @@ __global__ __launch_bounds__(NTB) void k_top_chunk(Rows rows, Live live, int k, 
             sh.at[at[u]] = v0 + (u * NTB + static_cast<int>(threadIdx.x)) * VT::N;
         }
     const Expo ex(m > NEG_INF ? m : 0.f, sc);
-    float s = ex.small ? sum_exps<T, true>(x, ex, sc) : sum_exps<T, false>(x, ex, sc);
-    s = wave_sum(s);
+    // (a thread's sum in float32, all others in 64 bits: continuations of different beams lie close to each other)
+    const double s = wave_sum_f64(ex.small ? sum_exps<T, true>(x, ex, sc) : sum_exps<T, false>(x, ex, sc));
     if (lane == 0)
         sh.s[wave] = s;
     __syncthreads();
@@ -493,10 +494,9 @@ __global__ __launch_bounds__(NTB) void k_top_chunk(Rows rows, Live live, int k, 
         double total = 0.0;
 #pragma unroll
         for (int w = 0; w < NTB / 64; ++w)
-            total += static_cast<double>(sh.s[w]);
+            total += sh.s[w];
         total *= ex.fix(sc);
-        const Part part = nan ? Part{__builtin_nanf(""), 1.f} : infinite ? Part{-NEG_INF, 1.f}
-                                                                         : Part{m, static_cast<float>(total)};
+        const Part part = nan ? Part{__builtin_nanf(""), 1.0} : infinite ? Part{-NEG_INF, 1.0} : Part{m, total};
         if (direct)
             out.lse[row] = part.m == NEG_INF ? NEG_INF
                            : nan || infinite ? part.m

@@ -275,8 +275,9 @@ int domino_top_logits(const domino_logits *logits, int32_t k, float temperature,
  * candidates are all (w, v), with
  *     score(w, v) = scores[b][w] + z_wv - log sum_u exp(z_wu),
  * and the n_out best of them become the beams of the next step: higher scores first, equal ones by lowest
- * w, then lowest v (a beam's own candidates are ordered by their logits).  Scores are compared in 64 bits,
- * each row's sum of exponentials having been taken in float32 within a chunk of the row.
+ * w, then lowest v (a beam's own candidates are ordered by their logits).  Scores are compared in 64 bits, and so are
+ * the rows' sums of exponentials joined: exponentials, and the sums of the 64 at most that one thread takes, are
+ * float32.
  *   - A beam whose score is -inf is dead: its candidates score -inf.  So do tokens whose logit is -inf, in a
  *     row of nothing but -inf too.
  *   - An ended beam (finished[b][w] != 0) has one candidate, (w, eos), with the score it has; the others

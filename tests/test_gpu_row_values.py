@@ -176,3 +176,22 @@ def test_top_logits_into_distill_at_low_temperatures(V, k, tau):
             assert (off <= most).all(), (name, off, most)
             if name == "itself":
                 assert (np.abs(host(grad) / tau).max(-1) <= 4 * noise + 2 * SUM).all(), name
+
+
+def test_sums_of_beams_keep_what_other_threads_add():
+    """One logit of 0 and one of -25 log 2, in another thread of the same wave, another wave or another chunk: the
+    sum is 1 + 2^-25, of which float32 leaves nothing.  The exponential is good to 2 H and its argument to 25 log2(e) H
+    (fused, rounded once: less than 32 H); log(1 + x) = x within x^2."""
+    V, low, small = 40000, -25 * np.log(2.0), 2.0 ** -25
+    for far in (8, 300, 20000, 39999):
+        z = torch.full((1, 2, V), -np.inf)
+        z[0, :, 0] = 0.0
+        z[0, 0, far] = low
+        x = float(np.exp(np.float64(np.float32(low))))  # what the float32 logit stands for
+        lse = float(dca.top_logits(z.cuda(), 2)["lse"][0, 0])
+        assert abs(lse - np.log1p(x)) <= 64 * H * small, far
+        # -2^-25 against -1e-8: the second beam's only token is the better one
+        got = dca.beam_step(z.cuda(), torch.tensor([[0.0, -1e-8]]).cuda(), n_out=2)
+        assert got["parent"][0].tolist() == [1, 0] and got["token"][0].tolist() == [0, 0], far
+        assert float(got["scores"][0, 0]) == np.float32(-1e-8)
+        assert abs(float(got["scores"][0, 1]) + np.log1p(x)) <= 64 * H * small, far
