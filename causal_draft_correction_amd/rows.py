@@ -122,8 +122,10 @@ def _scratch(given: Optional[torch.Tensor], need: int, index: int):
     return given, given.data_ptr(), given.numel()
 
 
-# The current stream's handle of a GPU (torch.cuda.current_stream() builds a Stream object around it each time).
-_stream = torch._C._cuda_getCurrentRawStream
+# The current stream's handle of a GPU: by the name that torch's own generated code takes it by where there is one
+# (torch.cuda.current_stream() builds a Stream object around it each time).
+_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda gpu: torch.cuda.current_stream(gpu).cuda_stream)
 
 
 def _size_of(fn, lg: Logits, *args) -> int:
