@@ -23,6 +23,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <algorithm>
+#include <initializer_list>
 #include <string>
 
 #include "../../include/domino_head.h"
@@ -1194,6 +1195,109 @@ static int logits_data(const domino_logits *lg, const char *what)
     return DOMINO_OK;
 }
 
+// Bytes [p, p + bytes) of an argument (p NULL: not given).
+struct Range {
+    const void *p;
+    int64_t bytes;
+};
+
+static Range range(const void *p, __int128 bytes)
+{
+    const __int128 most = static_cast<__int128>(1) << 62;
+    return Range{bytes > 0 ? p : nullptr, static_cast<int64_t>(bytes < most ? bytes : most)};
+}
+
+static bool meet(const Range &a, const Range &b)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return x && y && x < y + static_cast<uintptr_t>(b.bytes) && y < x + static_cast<uintptr_t>(a.bytes);
+}
+
+// Rows that lie apart, in bytes: `outer` steps of `inner` rows; a step is no shorter than its rows' reach.
+struct Apart {
+    const char *base;
+    int64_t outer_stride, inner_stride, outer, inner, width;
+};
+
+static int64_t size_of(const domino_logits &lg) { return lg.dtype == DOMINO_F32 ? 4 : 2; }
+
+static Apart apart(const Range &r)
+{
+    return Apart{static_cast<const char *>(r.p), INT64_MAX, INT64_MAX, 1, 1, r.bytes};
+}
+
+// (rows that grad_args took)
+static Apart apart(const domino_logits &lg)
+{
+    const int64_t es = size_of(lg), rows_span = (lg.R - 1) * lg.row_stride + lg.V;
+    const int64_t bs = lg.B > 1 ? lg.batch_stride * es : INT64_MAX, rs = lg.R > 1 ? lg.row_stride * es : INT64_MAX;
+    const bool by_batch = lg.R == 1 || (lg.B > 1 && lg.batch_stride >= rows_span);
+    const char *base = static_cast<const char *>(lg.data);
+    return by_batch ? Apart{base, bs, rs, lg.B, lg.R, lg.V * es} : Apart{base, rs, bs, lg.R, lg.B, lg.V * es};
+}
+
+// Whether one of the rows meets [p, p + bytes): the first that ends past p, in the order of their addresses, does or none.
+static bool meets(const Apart &a, const Range &r)
+{
+    const int64_t at = static_cast<const char *>(r.p) - a.base, from = at - a.width + 1;  // of a row's first byte
+    int64_t o = 0, i = 0;
+    if (from > 0) {
+        o = from / a.outer_stride;
+        const int64_t within = from - o * a.outer_stride;
+        i = within / a.inner_stride + (within % a.inner_stride != 0);
+        if (i >= a.inner)
+            ++o, i = 0;
+    }
+    return o < a.outer && (o ? o * a.outer_stride : 0) + (i ? i * a.inner_stride : 0) < at + r.bytes;
+}
+
+static Range span_of(const domino_logits &lg)
+{
+    return range(lg.data, (static_cast<__int128>(lg.B - 1) * lg.batch_stride +
+                           static_cast<__int128>(lg.R - 1) * lg.row_stride + lg.V) * size_of(lg));
+}
+
+// Row by row only where the reach of all of them meets: slices of one buffer that lie side by side.
+static bool rows_meet(const domino_logits &lg, const Apart &a, const Range &reach)
+{
+    if (!meet(span_of(lg), reach))
+        return false;
+    const int64_t es = size_of(lg);
+    for (int64_t b = 0; b < lg.B; ++b)
+        for (int64_t r = 0; r < lg.R; ++r)
+            if (meets(a, Range{static_cast<const char *>(lg.data) + (b * lg.batch_stride + r * lg.row_stride) * es,
+                               lg.V * es}))
+                return true;
+    return false;
+}
+
+// Outputs (scratch among them) that lie on an input or on each other.  `grad`: rows that are written, the logits' own or
+// apart from them.
+static int alias_args(const domino_logits &lg, const domino_logits *grad, std::initializer_list<Range> outs,
+                      std::initializer_list<Range> ins)
+{
+    bool bad = false;
+    for (const Range *o = outs.begin(); o != outs.end(); ++o) {
+        if (!o->p)
+            continue;
+        for (const Range *p = o + 1; p != outs.end(); ++p)
+            bad |= meet(*o, *p);
+        for (const Range &p : ins)
+            bad |= meet(*o, p);
+        bad = bad || rows_meet(lg, apart(*o), *o) || (grad && rows_meet(*grad, apart(*o), *o));
+    }
+    if (grad) {
+        for (const Range &p : ins)
+            bad = bad || (p.p && rows_meet(*grad, apart(p), p));
+        const bool own = grad->data == lg.data && (lg.B == 1 || grad->batch_stride == lg.batch_stride) &&
+                         (lg.R == 1 || grad->row_stride == lg.row_stride);
+        bad = bad || (!own && rows_meet(lg, apart(*grad), span_of(*grad)));
+    }
+    if (bad)
+        return fail(DOMINO_EINVAL, "an output overlaps an input, another output or the workspace");
+    return DOMINO_OK;
+}
+
 static int temperature_arg(float t)
 {
     if (!(t >= 1e-4f && t <= 1e4f))
@@ -1266,7 +1370,14 @@ int domino_top_logits(const domino_logits *lg, int32_t k, float temperature, con
         return fail(DOMINO_EINVAL, "NULL pointer");
     if (!aligned16(ids) || !aligned16(values) || !aligned16(lse) || !aligned16(n_rows))
         return fail(DOMINO_EINVAL, "pointers must be 16-byte aligned");
-    if ((rc = workspace_arg(workspace, workspace_bytes, dhtop::workspace_bytes(*lg, k, false))))
+    const size_t need = dhtop::workspace_bytes(*lg, k, false);
+    if ((rc = workspace_arg(workspace, workspace_bytes, need)))
+        return rc;
+    const __int128 rows = static_cast<__int128>(lg->B) * lg->R;
+    if ((rc = alias_args(*lg, nullptr,
+                         {range(ids, rows * k * 4), range(values, rows * k * 4), range(lse, rows * 4),
+                          range(workspace, need)},
+                         {range(n_rows, lg->B * 4ll)})))
         return rc;
     HIP_TRY(dhtop::top(*lg, k, temperature, n_rows, workspace, ids, values, lse, static_cast<hipStream_t>(stream)),
             "launch top_logits");
@@ -1313,7 +1424,17 @@ int domino_beam_step(const domino_logits *lg, const domino_beam *bm, void *works
                           static_cast<const void *>(bm->out_history)})
         if (!aligned16(p))
             return fail(DOMINO_EINVAL, "pointers must be 16-byte aligned");
-    if ((rc = workspace_arg(workspace, workspace_bytes, dhtop::workspace_bytes(*lg, std::min(bm->n_out, lg->V), true))))
+    const size_t need = dhtop::workspace_bytes(*lg, std::min(bm->n_out, lg->V), true);
+    if ((rc = workspace_arg(workspace, workspace_bytes, need)))
+        return rc;
+    const __int128 in = static_cast<__int128>(lg->B) * lg->R, out = static_cast<__int128>(lg->B) * bm->n_out;
+    const int64_t state = bm->state ? bm->state_bytes : 0, history = bm->history ? bm->T * 4ll : 0;
+    if ((rc = alias_args(*lg, nullptr,
+                         {range(bm->out_scores, out * 4), range(bm->out_parent, out * 4), range(bm->out_token, out * 4),
+                          range(bm->out_finished, out), range(bm->out_state, out * state),
+                          range(bm->out_history, out * history), range(workspace, need)},
+                         {range(bm->scores, in * 4), range(bm->finished, in), range(bm->state, in * state),
+                          range(bm->history, in * history)})))
         return rc;
     HIP_TRY(dhtop::beam(*lg, *bm, workspace, static_cast<hipStream_t>(stream)), "launch beam_step");
     return DOMINO_OK;
@@ -1347,8 +1468,6 @@ static int grad_args(const domino_logits *lg, const domino_logits *grad)
         return DOMINO_OK;
     if ((rc = logits_data(grad, "grad")))
         return rc;
-    if (grad->data == lg->data && (grad->batch_stride != lg->batch_stride || grad->row_stride != lg->row_stride))
-        return fail(DOMINO_EINVAL, "grad in the logits' place has other strides");
     return DOMINO_OK;
 }
 
@@ -1387,7 +1506,15 @@ int domino_distill(const domino_logits *lg, int32_t k, const int32_t *ids, const
                           static_cast<const void *>(grad_loss)})
         if (!aligned16(p))
             return fail(DOMINO_EINVAL, "pointers must be 16-byte aligned");
-    if ((rc = workspace_arg(workspace, workspace_bytes, dhdistill::workspace_bytes(*lg, k))))
+    const size_t need = dhdistill::workspace_bytes(*lg, k);
+    if ((rc = workspace_arg(workspace, workspace_bytes, need)))
+        return rc;
+    const __int128 rows = static_cast<__int128>(lg->B) * lg->R;
+    if ((rc = alias_args(*lg, grad,
+                         {range(loss, rows * 4), range(stats, rows * (dhdistill::STAT_HEAD + k) * 4),
+                          range(workspace, need)},
+                         {range(ids, rows * k * 4), range(values, rows * k * 4), range(teacher_lse, rows * 4),
+                          range(grad_loss, rows * 4), range(n_rows, lg->B * 4ll)})))
         return rc;
     const dhdistill::Teacher t = {k, ids, values, teacher_lse};
     hipStream_t st = static_cast<hipStream_t>(stream);
@@ -1411,6 +1538,11 @@ int domino_distill_backward(const domino_logits *lg, int32_t k, const int32_t *i
         return fail(DOMINO_EINVAL, "NULL pointer");
     if (!aligned16(ids) || !aligned16(stats) || !aligned16(grad_loss) || !aligned16(n_rows))
         return fail(DOMINO_EINVAL, "pointers must be 16-byte aligned");
+    const __int128 rows = static_cast<__int128>(lg->B) * lg->R;
+    if ((rc = alias_args(*lg, grad, {},
+                         {range(ids, rows * k * 4), range(stats, rows * (dhdistill::STAT_HEAD + k) * 4),
+                          range(grad_loss, rows * 4), range(n_rows, lg->B * 4ll)})))
+        return rc;
     HIP_TRY(dhdistill::backward(*lg, k, ids, stats, grad_loss, temperature, n_rows, *grad,
                                 static_cast<hipStream_t>(stream)),
             "launch distill_backward");

@@ -241,7 +241,9 @@ int domino_verify_noalloc(int32_t B, int32_t K, int32_t V, const float *logits, 
  * search).  `data` is a device pointer of `dtype` (DOMINO_F32, or DOMINO_BF16 as raw 16-bit patterns) with
  * any element alignment; strides count elements, so that a slice of a larger tensor or a padded vocabulary
  * is passed as it is.  0 <= batch_stride, 0 <= row_stride; an output's rows may not overlap.  Every call takes
- * B R (V / 1024 + 1) < 2^24 (DOMINO_EUNSUPPORTED above).
+ * B R (V / 1024 + 1) < 2^24 (DOMINO_EUNSUPPORTED above).  An output that shares memory with an input, another
+ * output or the workspace is refused (DOMINO_EINVAL), but for the gradient in the logits' own rows; rows that lie
+ * between each other's in one buffer share none.
  */
 typedef struct domino_logits {
     const void *data;
@@ -341,8 +343,8 @@ int domino_beam_step(const domino_logits *logits, const domino_beam *beam, void 
  *   stats      [B, R, 4 + k] float32: what the backward pass needs of the forward pass; NULL = not stored
  *   grad_loss  [B, R] float32 or NULL.  Given, the call also writes the gradient grad_loss[b][r] *
  *              dloss/dz to `grad` (then not NULL), and stats must be NULL
- *   grad       same dtype, B, R and V as the logits; its rows may be the logits' own (same data and strides:
- *              the gradient takes their place) or lie apart from them
+ *   grad       same dtype, B, R and V as the logits; its rows may be the logits' own (same data, and strides
+ *              where a dimension is longer than 1: the gradient takes their place) or lie apart from them
  * domino_distill_backward writes the gradient from the forward pass' stats, with the same logits, ids,
  * temperature and n_rows.  0 <= B, 1 <= R, 1 <= V, 1 <= k <= 128, 1e-4 <= temperature <= 1e4; B = 0 is a
  * no-op.  Sums and statistics are float32 within a chunk of a row and 64 bits across; results do not change

@@ -195,3 +195,25 @@ def test_sums_of_beams_keep_what_other_threads_add():
         assert got["parent"][0].tolist() == [1, 0] and got["token"][0].tolist() == [0, 0], far
         assert float(got["scores"][0, 0]) == np.float32(-1e-8)
         assert abs(float(got["scores"][0, 1]) + np.log1p(x)) <= 64 * H * small, far
+
+
+@pytest.mark.parametrize("V", [300, 40000])
+def test_gradients_beside_the_logits_in_one_buffer(V):
+    z = logits(2, 3, V, torch.float32, V)
+    top = dca.top_logits(z + 1.0, 8)
+    teach = dict(ids=top["ids"], values=top["values"], teacher_lse=top["lse"], grad_loss=torch.ones((2, 3), device="cuda"))
+    want = dca.distill(z, **teach)["grad"]
+    room = torch.cat([z, torch.zeros_like(z)], -1)  # the right half of every row
+    got = dca.distill(room[..., :V], out={"grad": room[..., V:]}, **teach)["grad"]
+    assert torch.equal(got, want) and torch.equal(room[..., :V], z)
+    room = torch.stack([z, torch.zeros_like(z)])  # one behind the other
+    assert torch.equal(dca.distill(room[0], out={"grad": room[1]}, **teach)["grad"], want)
+    # one row of each batch entry, and one entry: the stride of a dimension of length 1 says nothing
+    one = {n: x[:, :1].contiguous() for n, x in teach.items()}
+    own = z[:, :1].clone()
+    place = torch.as_strided(own, (2, 1, V), (V, 3, 1))
+    assert torch.equal(dca.distill(own, out={"grad": place}, **one)["grad"], want[:, :1])
+    for shift in (1, V - 1):
+        with pytest.raises(dca.DominoError, match="overlaps"):
+            flat = torch.zeros(6 * V + V, device="cuda")
+            dca.distill(flat[:6 * V].view(2, 3, V), out={"grad": flat[shift:shift + 6 * V].view(2, 3, V)}, **teach)
