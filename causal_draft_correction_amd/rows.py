@@ -252,6 +252,10 @@ def distill(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor, teach
     dloss/dlogits, of the logits' shape and type.  ``out`` may supply these tensors (grad may be the logits
     themselves, or any tensor of their shape and type with a contiguous last dimension), ``workspace`` (uint8)
     the scratch.
+
+    No graph is recorded: the gradient is the one this call or `distill_backward` returns, so without grad_loss
+    logits that require one are refused (under no_grad they are taken).  The teacher's entries are constants.
+    teacher_lse is a float32: include/domino_head.h says what that leaves open at low temperatures.
     """
     lib = _declared or _lib()
     lg, B, R, V, gpu = _logits("logits", logits)
@@ -263,6 +267,9 @@ def distill(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor, teach
     rows = None if n_rows is None else _need("n_rows", n_rows, (B,), torch.int32, gpu)
     i_grad = stats = gd = None
     if grad_loss is None:
+        if logits.requires_grad and torch.is_grad_enabled():
+            raise ValueError("logits require a gradient, of which the loss records nothing: give grad_loss, or "
+                             "logits.detach() and call distill_backward")
         out = _known(out, _LOSS_OUT)
         stats = _output(out, "stats", lead + (STAT_HEAD + k,), torch.float32, gpu)
     else:

@@ -217,3 +217,19 @@ def test_gradients_beside_the_logits_in_one_buffer(V):
         with pytest.raises(dca.DominoError, match="overlaps"):
             flat = torch.zeros(6 * V + V, device="cuda")
             dca.distill(flat[:6 * V].view(2, 3, V), out={"grad": flat[shift:shift + 6 * V].view(2, 3, V)}, **teach)
+
+
+def test_logits_that_require_a_gradient():
+    """A loss without a graph is not handed out in its place; the gradient that the operator computes can go on."""
+    z = logits(2, 3, 500, torch.float32, 1)
+    top = dca.top_logits(z + 1.0, 8)
+    leaf = z.clone().requires_grad_()
+    teach = dict(ids=top["ids"], values=top["values"], teacher_lse=top["lse"])
+    with pytest.raises(ValueError, match="detach"):
+        dca.distill(leaf, **teach)
+    with torch.no_grad():
+        first = dca.distill(leaf, **teach)
+    g = torch.ones((2, 3), device="cuda")
+    two = dca.distill_backward(leaf, top["ids"], first["stats"], g)
+    leaf.backward(dca.distill(leaf, grad_loss=g, **teach)["grad"])
+    assert torch.equal(leaf.grad, two) and torch.equal(two, dca.distill(z, grad_loss=g, **teach)["grad"])
