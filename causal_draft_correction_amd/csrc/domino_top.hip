@@ -1098,6 +1098,8 @@ hipError_t top(const domino_logits &lg, int k, float tau, const int32_t *n_rows,
                float *values, float *lse, hipStream_t st)
 {
     const Split sp = split_of(lg, k, false);
+    if (sp.nch > 1 && sp.nch > MERGE_LIST / k)  // (split_of makes no such split; the join would drop candidates)
+        return hipErrorInvalidValue;
     const Scratch s = scratch_of(lg, k, sp, ws);
     const TopOut out = {s.keys, s.parts, ids, values, lse};
     const Rows rows = rows_of(lg, n_rows, n_rows != nullptr);

@@ -164,3 +164,22 @@ def test_overlaps_of_rows_against_every_byte():
             assert got == EINVAL
         else:
             assert (got == EINVAL) == (bool(set(x) & set(g)) and not own), (B, R, V, bs, rs, off, gbs, grs)
+
+
+# ---- workspaces ----
+
+@pytest.mark.parametrize("dtype,per", [(torch.float32, 4), (torch.bfloat16, 8)])
+def test_candidates_of_all_chunks_fit_the_list_that_joins_them(dtype, per):
+    """8 bytes a candidate and at most 4096 of a row, 16 bytes for each of at most 64 chunks."""
+    edges = [256 * 8 * per * n + d for n in (1, 2, 3, 4, 5, 8, 16, 17, 31, 32, 33) for d in (-1, 0, 1)]
+    lengths = sorted({V for V in edges + [1, 100, 5003, 50021, 151936, 2 ** 19 - 1, 2 ** 19] if 1 <= V <= 2 ** 19})
+    for V in lengths:
+        for k in (1, 5, 31, 32, 33, 63, 64, 65, 127, 128):
+            for B, R in ((1, 1), (1, 2), (1, 17), (3, 20), (255, 1), (16, 16), (257, 1), (64, 16)):
+                if k <= V:
+                    need = dca.top_logits_workspace_size(B, R, V, k, dtype)
+                    rows = B * R
+                    assert need % 16 == 0 and need <= rows * (4096 * 8 + 64 * 16) + 32, (V, k, rows)
+                    if need:  # chunks of k candidates and a part each
+                        assert any(need == (rows * n * k * 8 + 15) // 16 * 16 + rows * n * 16
+                                   for n in range(1, 65)), (V, k, rows)
