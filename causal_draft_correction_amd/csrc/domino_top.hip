@@ -1047,9 +1047,10 @@ void pick_chunk(const Rows &rows, const Live &live, int k, const Split &sp, floa
         launch_chunk<T, 256, 4>(rows, live, k, sp, tau, out, grid, st);
     else if (sp.nv <= 8)
         launch_chunk<T, 256, 8>(rows, live, k, sp, tau, out, grid, st);
-    else if (sp.nch > 1)
-        launch_chunk<T, 256, 16>(rows, live, k, sp, tau, out, grid, st);
-    else if (sp.nv <= 16)
+    else if (sp.nch > 1) {
+        if constexpr (Vec<T>::N == 4)  // (split_of gives bfloat16 rows no such chunks)
+            launch_chunk<T, 256, 16>(rows, live, k, sp, tau, out, grid, st);
+    } else if (sp.nv <= 16)
         launch_chunk<T, 512, 8>(rows, live, k, sp, tau, out, grid, st);
     else
         launch_chunk<T, 1024, 8>(rows, live, k, sp, tau, out, grid, st);
@@ -1085,6 +1086,8 @@ void chunks(const domino_logits &lg, const Rows &rows, const Live &live, int k, 
 
 static_assert((dhtop::MAX_V / 4 + NT * LAST_NV - 1) / (NT * LAST_NV) * dhtop::MAX_K <= MERGE_LIST,
               "the candidates of the longest row fit one block's list");
+static_assert((dhtop::MAX_V / 8 + NT * MAX_NV - 1) / (NT * MAX_NV) * dhtop::MAX_K <= MERGE_LIST,
+              "bfloat16 rows are never cut into chunks of more than MAX_NV vectors a thread");
 
 }  // namespace
 
