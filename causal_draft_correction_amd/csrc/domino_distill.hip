@@ -608,21 +608,19 @@ bool by_rows(const domino_logits &lg, const Teacher &t, float tau, const int32_t
 
 }  // namespace
 
-hipError_t forward(const domino_logits &lg, const Teacher &t, float tau, const int32_t *n_rows, void *ws, float *loss,
-                   float *stats, hipStream_t st)
+namespace {
+
+// keep: the logits may stay in the caches, for a gradient that follows.
+hipError_t in_parts(const domino_logits &lg, const Teacher &t, float tau, const int32_t *n_rows, void *ws, float *loss,
+                    float *stats, bool keep, hipStream_t st)
 {
-    if (by_rows(lg, t, tau, n_rows, loss, stats, nullptr, nullptr, st))
-        return hipGetLastError();
     PartCall c;
     c.rows = rows_of(lg, n_rows, n_rows != nullptr);
     c.te = Teach{t.k, t.ids, t.values, t.lse};
     c.sp = split_of(lg, PART_NV);
     c.sc = scale_of(tau);
     c.parts = static_cast<Part *>(ws);
-    // Logits that the 256 MB last-level cache holds beside the gradient are read to stay there for the backward
-    // pass.  512 bf16 rows of 151936 (156 MB): both passes 83.0 us without, 80.0 us with; 1024 f32 rows (622 MB):
-    // 294 us without, 297 us with.
-    c.keep = stats && static_cast<double>(lg.B) * lg.R * lg.V * (lg.dtype == DOMINO_F32 ? 4 : 2) <= 192e6;
+    c.keep = keep;
     const unsigned n = static_cast<unsigned>(lg.B) * static_cast<unsigned>(lg.R);
     c.grid = n * c.sp.nch;
     c.st = st;
@@ -642,6 +640,28 @@ hipError_t forward(const domino_logits &lg, const Teacher &t, float tau, const i
                            static_cast<int>(n), c.sp.nch,
                            static_cast<double>(tau), c.parts, loss, stats);
     return hipGetLastError();
+}
+
+// Reading the logits so that the caches keep them, against passing the caches by, for rows of 151936, float32 (bfloat16
+// alike): loss and gradient 80 against 87 us (156 MB), 115 against 123 (233 MB), 152 against 160 (311 MB), 229 against
+// 234 (467 MB), 304.6 against 303.4 (622 MB); the loss alone 35 against 33, 48 against 44, 61 against 56, 87 against 79,
+// 113 against 102.  So with the gradient up to twice the last-level cache's 256 MB, and without statistics never; with
+// statistics the gradient is likely to follow but may not: up to 256 MB it gains as much as a loss without it would pay.
+constexpr double KEEP_FOR_GRAD = 512e6, KEEP_FOR_STATS = 256e6;
+
+double bytes_of(const domino_logits &lg)
+{
+    return static_cast<double>(lg.B) * lg.R * lg.V * (lg.dtype == DOMINO_F32 ? 4 : 2);
+}
+
+}  // namespace
+
+hipError_t forward(const domino_logits &lg, const Teacher &t, float tau, const int32_t *n_rows, void *ws, float *loss,
+                   float *stats, hipStream_t st)
+{
+    if (by_rows(lg, t, tau, n_rows, loss, stats, nullptr, nullptr, st))
+        return hipGetLastError();
+    return in_parts(lg, t, tau, n_rows, ws, loss, stats, stats && bytes_of(lg) <= KEEP_FOR_STATS, st);
 }
 
 hipError_t backward(const domino_logits &lg, int k, const int32_t *ids, const float *stats, const float *grad_loss,
@@ -672,7 +692,7 @@ hipError_t both(const domino_logits &lg, const Teacher &t, float tau, const int3
     if (by_rows(lg, t, tau, n_rows, loss, nullptr, grad_loss, &grad, st))
         return hipGetLastError();
     float *stats = reinterpret_cast<float *>(static_cast<char *>(ws) + parts_bytes(lg));
-    const hipError_t e = forward(lg, t, tau, n_rows, ws, loss, stats, st);
+    const hipError_t e = in_parts(lg, t, tau, n_rows, ws, loss, stats, bytes_of(lg) <= KEEP_FOR_GRAD, st);
     return e == hipSuccess ? backward(lg, t.k, t.ids, stats, grad_loss, tau, n_rows, grad, st) : e;
 }
 

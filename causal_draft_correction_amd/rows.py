@@ -17,7 +17,7 @@ import torch
 from .binding import DOMINO_BF16, DOMINO_F32, _check, load_library
 
 STAT_HEAD = 4  # floats of a row's statistics before those of its ids
-_TOP_OUT, _LOSS_OUT, _GRAD_OUT = {"ids", "values", "lse"}, {"loss", "stats"}, {"loss", "grad"}
+_TOP_OUT, _LOSS_ONLY, _LOSS_OUT, _GRAD_OUT = {"ids", "values", "lse"}, {"loss"}, {"loss", "stats"}, {"loss", "grad"}
 _BEAM_OUT = {"scores", "parent", "token", "finished", "state", "history"}
 _DTYPES = {torch.float32: DOMINO_F32, torch.bfloat16: DOMINO_BF16}
 
@@ -239,7 +239,7 @@ def beam_step(logits: torch.Tensor, scores: torch.Tensor, n_out: Optional[int] =
 
 def distill(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor, teacher_lse: Optional[torch.Tensor] = None,
             temperature: float = 1.0, n_rows: Optional[torch.Tensor] = None, grad_loss: Optional[torch.Tensor] = None,
-            workspace: Optional[torch.Tensor] = None, out: Optional[dict] = None) -> dict:
+            workspace: Optional[torch.Tensor] = None, out: Optional[dict] = None, want_stats: bool = True) -> dict:
     """Loss of the student's rows against a teacher's top logits, and with `grad_loss` its gradient.
 
     logits [B, R, V] (or [N, V]) of the student; ids int32 and values float32 [B, R, k] of the teacher
@@ -248,8 +248,9 @@ def distill(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor, teach
     out (loss and gradient 0).
 
     Returns loss [B, R] float32 (temperature^2 times the divergence).  Without grad_loss also stats
-    [B, R, 4 + k] float32 for `distill_backward`; with grad_loss [B, R] float32 instead grad = grad_loss *
-    dloss/dlogits, of the logits' shape and type.  ``out`` may supply these tensors (grad may be the logits
+    [B, R, 4 + k] float32 for `distill_backward` (want_stats=False, where no gradient follows: the loss alone,
+    read past the caches); with grad_loss [B, R] float32 instead grad = grad_loss * dloss/dlogits, of the
+    logits' shape and type.  ``out`` may supply these tensors (grad may be the logits
     themselves, or any tensor of their shape and type with a contiguous last dimension), ``workspace`` (uint8)
     the scratch.
 
@@ -270,8 +271,9 @@ def distill(logits: torch.Tensor, ids: torch.Tensor, values: torch.Tensor, teach
         if logits.requires_grad and torch.is_grad_enabled():
             raise ValueError("logits require a gradient, of which the loss records nothing: give grad_loss, or "
                              "logits.detach() and call distill_backward")
-        out = _known(out, _LOSS_OUT)
-        stats = _output(out, "stats", lead + (STAT_HEAD + k,), torch.float32, gpu)
+        out = _known(out, _LOSS_OUT if want_stats else _LOSS_ONLY)
+        if want_stats:
+            stats = _output(out, "stats", lead + (STAT_HEAD + k,), torch.float32, gpu)
     else:
         i_grad = _need("grad_loss", grad_loss, lead, torch.float32, gpu)
         out = _known(out, _GRAD_OUT)

@@ -233,3 +233,14 @@ def test_logits_that_require_a_gradient():
     two = dca.distill_backward(leaf, top["ids"], first["stats"], g)
     leaf.backward(dca.distill(leaf, grad_loss=g, **teach)["grad"])
     assert torch.equal(leaf.grad, two) and torch.equal(two, dca.distill(z, grad_loss=g, **teach)["grad"])
+
+
+@pytest.mark.parametrize("V", LENGTHS)
+def test_loss_without_statistics(V):
+    z = logits(2, 3, V, torch.bfloat16, V)
+    top = dca.top_logits(logits(2, 3, V, torch.float32, V + 1), 12)
+    want = dca.distill(z, top["ids"], top["values"], top["lse"])
+    got = dca.distill(z, top["ids"], top["values"], top["lse"], want_stats=False)
+    assert set(got) == {"loss"} and torch.equal(got["loss"], want["loss"])
+    with pytest.raises(ValueError, match="out"):
+        dca.distill(z, top["ids"], top["values"], out={"stats": want["stats"]}, want_stats=False)
