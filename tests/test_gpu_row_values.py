@@ -244,3 +244,52 @@ def test_loss_without_statistics(V):
     assert set(got) == {"loss"} and torch.equal(got["loss"], want["loss"])
     with pytest.raises(ValueError, match="out"):
         dca.distill(z, top["ids"], top["values"], out={"stats": want["stats"]}, want_stats=False)
+
+
+def candidate_scores(z, scores, eos, finished):
+    """[W, V] of one batch entry, in 64 bits, from the definition."""
+    out = np.full(z.shape, -np.inf)
+    for w, row in enumerate(z.astype(np.float64)):
+        s = float(scores[w])
+        if s == -np.inf:
+            continue
+        if finished is not None and finished[w]:
+            out[w, eos] = s
+        elif not s < np.inf or np.isnan(row).any() or (row == np.inf).any():
+            out[w] = np.nan
+        elif (row > -np.inf).any():
+            out[w] = s + plain.log_softmax(row)
+    return out
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B,W,V,M,eos", [
+    (3, 1, 2, 1, -1), (2, 4, 700, 1, -1), (2, 4, 5003, 1, 5), (1, 32, 3000, 1, 2999), (1, 4, 151936, 1, -1),
+    (4, 6, 40001, 1, 0), (2, 4, 151936, 8, 7), (1, 32, 4099, 128, 3), (9, 5, 20011, 17, -1), (3, 3, 50, 100, 49)])
+def test_every_beam_has_the_score_of_its_parent_and_token(B, W, V, M, eos, dtype):
+    """Each place by its own candidate's score, the last one too: it is the reported one within a sum's bound and its
+    rounding, and the one that belongs in that place within twice the bound."""
+    g = torch.Generator().manual_seed(V + M)
+    z = logits(B, W, V, dtype, V)
+    scores = -torch.cumsum(0.1 + torch.rand((B, W), generator=g), 1)
+    finished = torch.rand((B, W), generator=g) < 0.3 if eos >= 0 else None
+    scores[:, W // 2 + 1:][torch.rand(scores[:, W // 2 + 1:].shape, generator=g) < 0.2] = -np.inf
+    state = torch.randn((B, W, 12), generator=g)
+    history = torch.randint(0, V, (B, W, 3), generator=g, dtype=torch.int32)
+    got = dca.beam_step(z, scores.cuda(), n_out=M, eos=eos, finished=None if eos < 0 else finished.cuda(),
+                        state=state.cuda(), history=history.cuda(), step=1)
+    torch.cuda.synchronize()
+    p, t, s = (got[n].cpu().numpy() for n in ("parent", "token", "scores"))
+    for b in range(B):
+        each = candidate_scores(host(z[b]), scores[b].numpy(), eos, None if eos < 0 else finished[b].numpy())
+        own = each[p[b], t[b]]
+        want = np.sort(each.reshape(-1))[::-1][:M]
+        assert len({*zip(p[b], t[b])}) == M
+        fine = np.isfinite(want)
+        assert np.array_equal(np.isneginf(own), np.isneginf(want)) and np.array_equal(np.isneginf(s[b]), ~fine)
+        assert (np.abs(own[fine] - want[fine]) <= 2 * SUM).all()
+        assert (np.abs(s[b][fine] - own[fine]) <= SUM + np.abs(own[fine]) * H).all()
+        assert np.array_equal(got["state"][b].cpu().numpy(), state[b].numpy()[p[b]])
+        moved = history[b].numpy()[p[b]]
+        moved[:, 1] = t[b]
+        assert np.array_equal(got["history"][b].cpu().numpy(), moved)
