@@ -3,7 +3,7 @@
 // With y = z / tau, q = softmax(y), the teacher's entries j (id in [0, V)), t_j = value_j / tau - L with L the
 // teacher's log-sum-exp (given, or that of the entries alone), p_j = exp t_j, P = sum p_j,
 //     rest = max(0, 1 - P) where L is given, else 0;   Mm = P + rest;   Qr = sum of q over ids no entry names
-//     (where 1 - P and Qr are no more than the rounding of L leaves open: as if L were not given)
+//     (where 1 - P is no more than the rounding of L leaves open, and Qr than the square of that: as if L were not given)
 //     loss = tau^2 [ sum_j p_j (t_j - log q_j) + rest log(rest / Qr) ]
 //     dloss/dz_v = tau [ Mm q_v - sum_{j: id_j = v} p_j ]     where an entry names v
 //                = tau (q_v / Qr) [ Mm Qr - rest ]             elsewhere
@@ -145,9 +145,9 @@ __global__ __launch_bounds__(NT) void k_distill_part(Rows rows, Teach te, Split 
 }
 
 // L is a float32, so the masses p_j carry its rounding, up to |L| 2^-24, and the error of the sum it was taken from
-// (LSE_STEPS half steps: an exponential's own 2, its argument's, 15 of a thread's additions).  Where neither the
-// teacher's entries nor the student leave more than that to the other ids, 1 - sum p is nothing but this noise, which
-// rest log(rest / Qr) would make an infinity of where Qr is 0 (entries that name every id, or a mask that both share).
+// (LSE_STEPS half steps: an exponential's own 2, its argument's, 15 of a thread's additions).  Where 1 - sum p is no more
+// than that noise, rest log(rest / Qr) is at most noise log(1 / noise) while Qr exceeds noise^2; below, it would be as
+// large as Qr is small, up to an infinity (entries that name every id, or a mask that both share), made of nothing.
 // An L so large that the noise reaches MAX_NOISE tells nothing of the other ids, and the formula stands as it is.
 constexpr double LSE_STEPS = 32.0, MAX_NOISE = 0x1p-6;
 
@@ -269,7 +269,7 @@ __device__ inline void finish_row(const Rows &rows, const Teach &te, const Place
     if (te.lse) {
         rest = 1.0 - p_sum;
         const double noise = fmin((fabs(L) + LSE_STEPS) * 0x1p-24, MAX_NOISE);
-        alone = fabs(rest) <= noise && of_rest <= noise * s;
+        alone = fabs(rest) <= noise && of_rest <= noise * noise * s;
         rest = alone || rest < 0.0 ? 0.0 : rest;
     }
     const double scale = alone ? 1.0 / p_sum : 1.0;

@@ -325,12 +325,14 @@ int domino_beam_step(const domino_logits *logits, const domino_beam *beam, void 
  *         event), else 0;  Qr = the sum of q over the ids that no entry names
  *     loss = temperature^2 ( sum_j p_j (t_j - log q_j) + rest log(rest / Qr) )
  * teacher_lse is a float32, which leaves a relative error of |L| 2^-24 in every p_j and as much of a mass open: at a
- * logit of 20, 1e-6 at temperature 1 and 1e-5 at 0.1.  Where | 1 - sum_j p_j | and Qr are both at most
+ * logit of 20, 1e-6 at temperature 1 and 1e-5 at 0.1.  With
  *     noise = min((|L| + 32) 2^-24, 2^-6)
- * the other ids have no mass that it could tell from none, and the row counts as given without teacher_lse (rest = 0,
- * the p_j brought to a sum of 1): so a student that equals its teacher has a loss of 0 where the entries hold all
- * there is (k = V, or a mask that leaves no more than k).  An |L| of 2^18 or more (temperatures near 1e-4; rows at the
- * type's lowest value) says little of the other ids' mass: give such rows without it.
+ * a row counts as given without teacher_lse (rest = 0, the p_j brought to a sum of 1) where | 1 - sum_j p_j | <= noise
+ * and Qr <= noise^2: the teacher's mass of the other ids cannot be told from none there, and the student has none.  So
+ * a student that equals its teacher has a loss of 0 where the entries hold all there is (k = V, or a mask that leaves
+ * no more than k), and one of at most about temperature^2 noise log(1 / noise) elsewhere.  An |L| of 2^18 or more
+ * (temperatures near 1e-4; rows at the type's lowest value) says little of the other ids' mass: give such rows
+ * without it.
  * An id outside [0, V) (-1 pads a row) is passed over; an id named twice has both masses.  A row without a
  * valid id, one whose entries' values are all -inf (with teacher_lse: and that is -inf too, as domino_top_logits
  * leaves a row of nothing but -inf), and rows r >= n_rows[b] are left out: loss 0, gradient 0, whatever their

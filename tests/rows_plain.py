@@ -95,9 +95,9 @@ def distill(z, ids, values, teacher_lse, tau, n_rows=None):
             rest = 0.0 if teacher_lse is None else max(0.0, 1.0 - p.sum())
             other = np.ones(V, bool)
             other[i] = False
-            if teacher_lse is not None:  # what a float32 log-sum-exp cannot tell from no mass
+            if teacher_lse is not None:  # a mass that a float32 log-sum-exp cannot tell from none, and no student's
                 noise = min((abs(L) + 32) * 2.0 ** -24, 2.0 ** -6)
-                if abs(1.0 - p.sum()) <= noise and q[other].sum() <= noise:
+                if abs(1.0 - p.sum()) <= noise and q[other].sum() <= noise ** 2:
                     rest, t, p = 0.0, t - np.log(p.sum()), p / p.sum()
             with np.errstate(divide="ignore", invalid="ignore"):
                 kl = sum(pj * (tj - logq[v]) for pj, tj, v in zip(p, t, i) if pj > 0)

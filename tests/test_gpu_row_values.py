@@ -144,7 +144,8 @@ def test_a_student_that_is_its_teacher_where_the_entries_hold_all_there_is(V, k,
 def test_top_logits_into_distill_at_low_temperatures(V, k, tau):
     """Against the loss with the teacher's log-sum-exp in 64 bits: a mass is off by the noise of L (the other ids' by
     that too), and x log(x / Qr) over such a step, or up to twice that where a row counts as without L, by the step
-    times |log Qr| + |log noise| + 1; a student that is its teacher by a few times the noise."""
+    times |log Qr| + |log noise| + 1.  For a student that is its teacher x is at most Qr + noise: below twice the noise
+    times 1 + |log noise| while Qr exceeds noise^2, and no such term below."""
     tau = float(np.float32(tau))
     target = logits(1, 6, V, torch.float32, V, 4.0)
     g = torch.ones((1, 6), device="cuda")
@@ -166,7 +167,7 @@ def test_top_logits_into_distill_at_low_temperatures(V, k, tau):
         rest = log_rest.exp()
         want = (terms.sum(-1) + torch.where(rest > 0, rest * (log_rest - log_qr), 0.0)).cpu().numpy()
         if name == "itself":
-            most = 4 * noise + 2 * SUM * rest.cpu().numpy()
+            most = 2 * noise * (1 + np.abs(np.log(noise))) + 2 * SUM * rest.cpu().numpy()
         else:
             size = (terms.abs().sum(-1) + log_qr.abs()).cpu().numpy()
             most = 2 * noise * (size + 3 + np.abs(np.log(noise))) + 2 * SUM + np.abs(want) * H
