@@ -251,7 +251,9 @@ __device__ inline int chunk_begin(int c, int cvec, int V)
 //
 // Where |ref s| < 1024 (SMALL) it is 2^(z near + c): near is s rounded to float32, c = -ref near rounded, so that an
 // element takes one fused multiply-add.  The rounding of c is the same factor in every term of a sum, and taken
-// out of it (fix); that of near weighs |log2 q| 2^-25 in a term q, below 4e-7 of a sum over any distribution.
+// out of it (fix); that of near weighs up to |ln q| 2^-24 in a term q, below 6e-7 of a sum over any distribution of
+// 2^19 elements (n terms exp(-d) beside a term 1 weigh at most d - 1 where n exp(-d) = d - 1, which is 9.8); at
+// tau = 1, where near is off by 2^-26.2 of itself, 1.3e-7.
 // Elsewhere it is 2^(d hi + d lo) with d = z - ref, hi + lo = s and both above 0, so that d = -inf gives 0.
 // (v_exp_f32 flushes results below 2^-126.)
 struct Scale {

@@ -16,9 +16,9 @@
 // (k_distill_grad).  Rows that one block can hold go through one launch (k_distill_row): 32 f32 rows of 1024, loss and
 // gradient: 6.8 us, against 3.4 + 6.2 + 3.0 us and two more launches.
 //
-// What bounds them, on one MI355X.  1024 f32 rows of 151936 (622 MB), loss and gradient: 92 + 8.6 + 194 us, 6.8 TB/s
-// read, then 6.4 TB/s read and written; a large copy reaches 4.9 TB/s.  512 bf16 rows (156 MB): 30 + 5.4 + 46 us; in
-// bfloat16 the forward pass is bound by the vector units (525 instructions a wave, 59 of them exponentials: 23 us of
+// What bounds them, on one MI355X.  1024 f32 rows of 151936 (622 MB), loss and gradient: 92 + 8.3 + 196 us, 6.8 TB/s
+// read, then 6.4 TB/s read and written; a large copy reaches 4.9 TB/s.  512 bf16 rows (156 MB): 29 + 5.5 + 46 us; in
+// bfloat16 the forward pass is bound by the vector units (552 instructions a wave, 59 of them exponentials: 24 us of
 // issue) as much as by the bytes (24 us).  The gradient needs the row's sum, so a row is read twice, from HBM where
 // the last-level cache does not hold it.  Keeping a row on chip between the two passes, one block of 256 to 1024
 // threads per row that reads its tiles again in the opposite order, was measured at 303 to 314 us for the f32 rows

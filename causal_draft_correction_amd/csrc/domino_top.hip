@@ -11,11 +11,11 @@
 // k_top_merge joins the chunks' lists of a row in the same way; its bound is taken from the lists' heads.  A row that
 // one block can hold (up to 1024 threads) is one chunk, and needs no join.
 //
-// What bounds it, on one MI355X: 512 bf16 rows of 151936, k = 20 (156 MB): 32.0 + 4.7 us, 4.9 TB/s in the chunks'
-// launch, which issues 711 vector instructions a wave (59 of them exponentials, at 16 cycles, the others at 4): 30 us
+// What bounds it, on one MI355X: 512 bf16 rows of 151936, k = 20 (156 MB): 32.4 + 4.6 us, 4.8 TB/s in the chunks'
+// launch, which issues 731 vector instructions a wave (59 of them exponentials, at 16 cycles, the others at 4): 30 us
 // of issue at 2.4 GHz, so the vector units bound bfloat16, not the 24 us the bytes take.  float32 has half the elements
 // a byte: 1024 rows of 50021, k = 16 (205 MB): 38 us in all, 5.4 TB/s.  Few rows are bound by latency: 17 f32 rows,
-// k = 64: 9.0 + 5.3 us.
+// k = 64: 8.8 + 5.6 us.
 //
 // Chunks of 8 vectors a thread against 16 (half the waves in flight): 34.3 against 35.8 us for the 512 rows.  More
 // chunks a row give few rows more blocks, and the join more candidates: 17 rows, k = 64, 31 chunks 8.9 + 5.6 us,
@@ -24,7 +24,9 @@
 // beam: W beams' candidates score s_w + log softmax(z_w)_v.  Within a beam they are ordered by their logits, so the
 // M best of all are among the M largest of each chunk, and k_top_chunk serves both.  k_beam_merge scores them in 64
 // bits, ranks them as k_top_merge does, and writes state and history in the new order: 32 x 8 bf16 beams of 151936,
-// 16 out of each, 4 KiB of state: 19.0 + 9.1 us (71 MB); four f32 beams of one request, 8 out: 5.0 + 8.1 us, latency.
+// 16 out of each, 4 KiB of state, one beam of each ended: 19.3 + 9.1 us (71 MB); its 2240 blocks with work are more than
+// the 2048 that the device holds (8 a compute unit, by 61 registers and 20 KB of LDS), so the last 192 run almost alone.
+// Four f32 beams of one request, 8 out: 5.2 + 8.2 us, latency.
 #define DH_NT 256
 #define DH_NS dht
 #include "dh_rows.h"
@@ -721,7 +723,10 @@ __device__ inline void put_beam(BeamShared &sh, const BeamArgs &a, int i, const 
 // live(f): f(score, place, w) for the thread's candidates of live beams; beam(w, f): for those of beam w.  `kind`,
 // `first`: of beam threadIdx.x, and its only candidate's score where it has ended; n candidates reach `bound`; `top`:
 // the thread's best.  32 x 8 beams of 32000 f32, all of them ended, 16 out: 22 us a call, where 16 passes for the best
-// one each took 85; 4 x 32 of 151936 with 3 tokens left by a mask, 128 out: 331 us instead of 5264.
+// one each took 85; 4 x 32 of 151936 with 3 tokens left by a mask, 128 out: 331 us instead of 5264.  Slow where wide beams
+// hold many equal candidates: with PER = 0 every turn reads and scores all of them again (up to 64 turns for the score,
+// up to 64 more for the place): 32 f32 beams of 151936 equal logits, 128 out, 2.2 ms; 16 beams, 64 out, 0.97 ms; 8 beams,
+// 16 out, 0.3 ms; without equal ones 134, 58 and 24 us.
 template <int NTB, typename L, typename O>
 __device__ __forceinline__ int list_any_beams(const BeamArgs &a, int kind, uint64_t first, bool odd, int n,
                                               uint64_t bound, uint64_t top, BeamShared &sh, L live, O beam)

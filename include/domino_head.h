@@ -336,8 +336,8 @@ int domino_beam_step(const domino_logits *logits, const domino_beam *beam, void 
  * An id outside [0, V) (-1 pads a row) is passed over; an id named twice has both masses.  A row without a
  * valid id, one whose entries' values are all -inf (with teacher_lse: and that is -inf too, as domino_top_logits
  * leaves a row of nothing but -inf), and rows r >= n_rows[b] are left out: loss 0, gradient 0, whatever their
- * logits hold.  A row of nothing but -inf has
- * q = 0; a NaN or +inf among a row's logits makes its loss and gradient NaN.
+ * logits hold.  A row of nothing but -inf has q = 0; a NaN or +inf among a row's logits makes its loss and
+ * gradient NaN.
  *   ids        [B, R, k] int32, values [B, R, k] float32, teacher_lse [B, R] float32 or NULL
  *   n_rows     [B] int32 or NULL (all R)
  *   workspace  >= domino_distill_workspace_size bytes; scratch of this call (where that is 0, NULL will do)
@@ -349,8 +349,8 @@ int domino_beam_step(const domino_logits *logits, const domino_beam *beam, void 
  *              where a dimension is longer than 1: the gradient takes their place) or lie apart from them
  * domino_distill_backward writes the gradient from the forward pass' stats, with the same logits, ids,
  * temperature and n_rows.  0 <= B, 1 <= R, 1 <= V, 1 <= k <= 128, 1e-4 <= temperature <= 1e4; B = 0 is a
- * no-op.  Sums and statistics are float32 within a chunk of a row and 64 bits across; results do not change
- * from call to call.  At most two launches for the loss and one for the gradient, asynchronous on `stream`; no
+ * no-op.  The sum over the ids that no entry names is float32 within a wave's elements and 64 bits across, the
+ * entries' terms are in 64 bits, stats are float32; results do not change from call to call.  At most two launches for the loss and one for the gradient, asynchronous on `stream`; no
  * allocation, no synchronization.  Pointers other than the logits' and the gradient's data 16-byte aligned;
  * apart from what is said of grad, outputs may not alias inputs or the workspace.
  */
