@@ -148,7 +148,8 @@ __global__ __launch_bounds__(NT) void k_distill_part(Rows rows, Teach te, Split 
 // (LSE_STEPS half steps: an exponential's own 2, its argument's, 15 of a thread's additions).  Where 1 - sum p is no more
 // than that noise, rest log(rest / Qr) is at most noise log(1 / noise) while Qr exceeds noise^2; below, it would be as
 // large as Qr is small, up to an infinity (entries that name every id, or a mask that both share), made of nothing.
-// An L so large that the noise reaches MAX_NOISE tells nothing of the other ids, and the formula stands as it is.
+// An L so large that the noise exceeds MAX_NOISE tells nothing of the other ids (a row at the type's lowest value, whose L
+// is -inf in float32 at temperatures below 1): such a row counts as given without it.
 constexpr double LSE_STEPS = 32.0, MAX_NOISE = 0x1p-6;
 
 // One row, by one wave, from the parts of its nch chunks: its loss, and what the backward pass needs of it:
@@ -170,6 +171,8 @@ __device__ inline void finish_row(const Rows &rows, const Teach &te, const Place
     int id[2] = {-1, -1};
     float value[2] = {NEG_INF, NEG_INF};
     const double L = te.lse ? static_cast<double>(te.lse[row]) : NINF;
+    const double noise = (fabs(L) + LSE_STEPS) * 0x1p-24;
+    const bool told = te.lse && !(noise > MAX_NOISE && L < -NINF);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
         if (lane + 64 * i < te.k) {
@@ -195,11 +198,11 @@ __device__ inline void finish_row(const Rows &rows, const Teach &te, const Place
     bool live = __ballot(valid[0] || valid[1]) != 0;
     double p[2] = {0.0, 0.0};
     double t_top = live ? wave_max_f64(fmax(t[0], t[1])) : NINF;
-    if (live && !(t_top > NINF) && L == NINF) {  // nothing but -inf (no mass: left out) or NaN
+    if (live && !told && !(t_top > NINF)) {  // nothing but -inf (no mass: left out) or NaN
         live = __ballot((valid[0] && t[0] != t[0]) || (valid[1] && t[1] != t[1])) != 0;
         t_top = __builtin_nan("");
     }
-    if (te.lse)
+    if (told)
         t_top = L;
     if (!live) {
         if (lane == 0)
@@ -264,12 +267,11 @@ __device__ inline void finish_row(const Rows &rows, const Teach &te, const Place
     for (int i = 0; i < 2; ++i)
         q[i] = !valid[i] || m == NINF ? 0.0 : z[i] == m ? 1.0 : exp((z[i] - m) * inv_tau);
     const double s = wave_sum_f64((first[0] ? q[0] : 0.0) + (first[1] ? q[1] : 0.0)) + of_rest;
-    bool alone = !te.lse;  // the entries are all of the teacher: their masses are brought to a sum of 1
+    bool alone = !told;  // the entries are all of the teacher: their masses are brought to a sum of 1
     double rest = 0.0;
-    if (te.lse) {
+    if (told) {
         rest = 1.0 - p_sum;
-        const double noise = fmin((fabs(L) + LSE_STEPS) * 0x1p-24, MAX_NOISE);
-        alone = fabs(rest) <= noise && of_rest <= noise * noise * s;
+        alone = noise <= MAX_NOISE && fabs(rest) <= noise && of_rest <= noise * noise * s;
         rest = alone || rest < 0.0 ? 0.0 : rest;
     }
     const double scale = alone ? 1.0 / p_sum : 1.0;

@@ -262,7 +262,8 @@ typedef struct domino_logits {
  *                               larger than any number, -0 equals +0; -1 in rows left out
  *   values  [B, R, k] float32   their logits (-inf in rows left out)
  *   lse     [B, R]    float32   log sum_v exp(z_v / temperature): -inf where every logit is -inf and in rows
- *                               left out, +inf where one is +inf, NaN where one is NaN
+ *                               left out, +inf where one is +inf, NaN where one is NaN; infinite, too, where it
+ *                               exceeds float32 (logits at the type's lowest value, temperatures below 1)
  * 0 <= B, 1 <= R, 1 <= k <= 128, k <= V <= 524288, 1e-4 <= temperature <= 1e4; B = 0 is a no-op.  ids
  * and values do not depend on how a row is split over the device (V, k and B R decide that); the last place
  * of lse may.  At most two launches, asynchronous on `stream`; no allocation, no synchronization.  Pointers
@@ -326,13 +327,13 @@ int domino_beam_step(const domino_logits *logits, const domino_beam *beam, void 
  *     loss = temperature^2 ( sum_j p_j (t_j - log q_j) + rest log(rest / Qr) )
  * teacher_lse is a float32, which leaves a relative error of |L| 2^-24 in every p_j and as much of a mass open: at a
  * logit of 20, 1e-6 at temperature 1 and 1e-5 at 0.1.  With
- *     noise = min((|L| + 32) 2^-24, 2^-6)
+ *     noise = (|L| + 32) 2^-24
  * a row counts as given without teacher_lse (rest = 0, the p_j brought to a sum of 1) where | 1 - sum_j p_j | <= noise
  * and Qr <= noise^2: the teacher's mass of the other ids cannot be told from none there, and the student has none.  So
  * a student that equals its teacher has a loss of 0 where the entries hold all there is (k = V, or a mask that leaves
- * no more than k), and one of at most about temperature^2 noise log(1 / noise) elsewhere.  An |L| of 2^18 or more
- * (temperatures near 1e-4; rows at the type's lowest value) says little of the other ids' mass: give such rows
- * without it.
+ * no more than k), and one of at most about temperature^2 noise log(1 / noise) elsewhere.  An L whose noise exceeds
+ * 2^-6 (|L| near 2^18: temperatures near 1e-4; rows at the type's lowest value, an L of -inf beside values that are
+ * not) says nothing of the other ids' mass: such a row counts as given without it, too.
  * An id outside [0, V) (-1 pads a row) is passed over; an id named twice has both masses.  A row without a
  * valid id, one whose entries' values are all -inf (with teacher_lse: and that is -inf too, as domino_top_logits
  * leaves a row of nothing but -inf), and rows r >= n_rows[b] are left out: loss 0, gradient 0, whatever their

@@ -80,10 +80,14 @@ def distill(z, ids, values, teacher_lse, tau, n_rows=None):
             if not ok.any():
                 continue
             i, t = ids[b, r][ok], np.asarray(values[b, r][ok], np.float64) / tau
-            L = lse(t) if teacher_lse is None else float(teacher_lse[b, r])
+            L = NINF if teacher_lse is None else float(teacher_lse[b, r])
+            noise = (abs(L) + 32) * 2.0 ** -24  # of a mass, by the rounding of L
+            told = teacher_lse is not None and not (noise > 2.0 ** -6 and L < np.inf)
+            if not told:
+                L = lse(t)
             if L == NINF and (t == NINF).all():
                 continue
-            t = log_softmax(t) if teacher_lse is None and np.isfinite(L) else t - L
+            t = log_softmax(t) if not told and np.isfinite(L) else t - L
             p = np.exp(t)
             y = z[b, r] / tau
             total = lse(y)
@@ -92,13 +96,12 @@ def distill(z, ids, values, teacher_lse, tau, n_rows=None):
                 continue
             logq = np.full(V, NINF) if total == NINF else log_softmax(y)
             q = np.exp(logq)
-            rest = 0.0 if teacher_lse is None else max(0.0, 1.0 - p.sum())
+            rest = max(0.0, 1.0 - p.sum()) if told else 0.0
             other = np.ones(V, bool)
             other[i] = False
-            if teacher_lse is not None:  # a mass that a float32 log-sum-exp cannot tell from none, and no student's
-                noise = min((abs(L) + 32) * 2.0 ** -24, 2.0 ** -6)
-                if abs(1.0 - p.sum()) <= noise and q[other].sum() <= noise ** 2:
-                    rest, t, p = 0.0, t - np.log(p.sum()), p / p.sum()
+            if told and noise <= 2.0 ** -6 and abs(1.0 - p.sum()) <= noise and q[other].sum() <= noise ** 2:
+                # a mass that cannot be told from none, and none of the student's
+                rest, t, p = 0.0, t - np.log(p.sum()), p / p.sum()
             with np.errstate(divide="ignore", invalid="ignore"):
                 kl = sum(pj * (tj - logq[v]) for pj, tj, v in zip(p, t, i) if pj > 0)
                 log_rest = lse(logq[other]) if other.any() else NINF

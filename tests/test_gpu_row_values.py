@@ -115,7 +115,7 @@ def test_small_losses_of_a_student_that_is_nearly_certain(V, k, tau, tail, dtype
 
 def noise_of(lse):
     """What a float32 log-sum-exp leaves open of a mass (include/domino_head.h)."""
-    return np.minimum((np.abs(lse.astype(np.float64)) + 32) * H, 2.0 ** -6)
+    return (np.abs(lse.astype(np.float64)) + 32) * H
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -294,3 +294,33 @@ def test_every_beam_has_the_score_of_its_parent_and_token(B, W, V, M, eos, dtype
         moved = history[b].numpy()[p[b]]
         moved[:, 1] = t[b]
         assert np.array_equal(got["history"][b].cpu().numpy(), moved)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("V", LENGTHS)
+@pytest.mark.parametrize("tau", [2.0, 1.0, 0.5, 1e-4])
+def test_teacher_rows_at_the_lowest_value(V, tau, dtype):
+    """Their log-sum-exp is -3e38, or -inf in float32: nothing of it can be the other ids', so they are rows without it.
+    So is a row whose temperature leaves of it less than a mass of 2^-6 can be told by."""
+    k, tau = 20, float(np.float32(tau))
+    z = logits(1, 4, V, dtype, V)
+    target = logits(1, 4, V, dtype, V + 1)
+    target[0, 1] = torch.finfo(dtype).min
+    target[0, 2] = 40.0
+    target[0, 2, V // 2] = 41.0
+    top = dca.top_logits(target, k, temperature=tau)
+    assert float(top["lse"][0, 1]) <= -3e38 / max(1.0, tau)
+    g = torch.ones((1, 4), device="cuda")
+    blind = [1] + ([2] if tau < 1e-3 else [])
+    told = three_ways(z, top["ids"], top["values"], top["lse"], g, temperature=tau)
+    alone = three_ways(z, top["ids"], top["values"], None, g, temperature=tau)
+    for (loss, grad), (want, want_grad) in zip(told[:2], alone[:2]):
+        assert bool(torch.isfinite(loss).all()) and bool(torch.isfinite(grad.float()).all())
+        for r in blind:
+            assert torch.equal(loss[0, r], want[0, r]) and torch.equal(grad[0, r], want_grad[0, r])
+        if tau > 1e-3:
+            assert not torch.equal(loss[0, 2], want[0, 2])  # (most of this row's mass is the other ids')
+    # a row of equal values over k entries: log(1 / k) - mean log q
+    logq = torch.log_softmax(z.double() / tau, -1)[0, 1].gather(0, top["ids"][0, 1].long())
+    want = float(tau ** 2 * (-np.log(k) - logq.mean()))
+    assert abs(float(told[0][0][0, 1]) - want) <= 2 * tau ** 2 * SUM + 2 * abs(want) * H
