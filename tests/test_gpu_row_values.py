@@ -324,3 +324,18 @@ def test_teacher_rows_at_the_lowest_value(V, tau, dtype):
     logq = torch.log_softmax(z.double() / tau, -1)[0, 1].gather(0, top["ids"][0, 1].long())
     want = float(tau ** 2 * (-np.log(k) - logq.mean()))
     assert abs(float(told[0][0][0, 1]) - want) <= 2 * tau ** 2 * SUM + 2 * abs(want) * H
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B,R,V,tau", [(1, 1, 300, 1.0), (40, 3, 2049, 0.7), (2, 2, 32000, 1.442), (300, 2, 16385, 1.0),
+                                       (2, 3, 151936, 1.442), (1, 1, 524288, 2.0)])
+def test_log_sum_exps_by_the_depth_of_their_sums(B, R, V, tau, dtype):
+    """Half steps of a sum: 2 of an exponential; the rounding of its argument, and that of log2(e) / tau, |d| of a term
+    exp(-d) each, which over 2^19 terms is 9.8 of the sum at most; 19 additions of a thread (4 elements, 16 vectors),
+    and none after, in 64 bits.  41 H, and the result's rounding."""
+    tau = float(np.float32(tau))
+    for scale in (0.01, 1.0, 3.0, 9.0):
+        z = logits(B, R, V, dtype, V + int(scale), scale)
+        got = host(dca.top_logits(z, 3, temperature=tau)["lse"]).astype(np.float64)
+        want = torch.logsumexp(z.double() / tau, -1).cpu().numpy()
+        assert (np.abs(got - want) <= 41 * H + np.abs(want) * H).all(), (scale, np.abs(got - want).max() / H)
