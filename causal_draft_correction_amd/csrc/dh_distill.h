@@ -24,11 +24,11 @@ struct Teacher {
 };
 
 // Arguments were checked by the caller.
-hipError_t forward(const domino_logits &lg, const Teacher &t, float tau, const int32_t *n_rows, void *ws, float *loss,
+hipError_t forward(const domino_logits &lg, const Teacher &t, double tau, const int32_t *n_rows, void *ws, float *loss,
                    float *stats, hipStream_t st);
-hipError_t both(const domino_logits &lg, const Teacher &t, float tau, const int32_t *n_rows, void *ws, float *loss,
+hipError_t both(const domino_logits &lg, const Teacher &t, double tau, const int32_t *n_rows, void *ws, float *loss,
                 const float *grad_loss, const domino_logits &grad, hipStream_t st);
 hipError_t backward(const domino_logits &lg, int k, const int32_t *ids, const float *stats, const float *grad_loss,
-                    float tau, const int32_t *n_rows, const domino_logits &grad, hipStream_t st);
+                    double tau, const int32_t *n_rows, const domino_logits &grad, hipStream_t st);
 
 }  // namespace dhdistill

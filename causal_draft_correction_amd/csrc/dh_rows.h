@@ -259,9 +259,9 @@ __device__ inline int chunk_begin(int c, int cvec, int V)
 struct Scale {
     float near, hi, lo;
 };
-inline Scale scale_of(float tau)
+inline Scale scale_of(double tau)
 {
-    const double s = 1.4426950408889634074 / static_cast<double>(tau);
+    const double s = 1.4426950408889634074 / tau;
     Scale sc;
     sc.near = sc.hi = static_cast<float>(s);
     if (static_cast<double>(sc.hi) >= s)

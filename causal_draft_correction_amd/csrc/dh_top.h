@@ -17,7 +17,7 @@ constexpr int MAX_V = 1 << 19;     // longest row: its chunks' candidates have t
 size_t workspace_bytes(const domino_logits &lg, int k, bool for_beams);
 
 // Arguments were checked by the caller.
-hipError_t top(const domino_logits &lg, int k, float tau, const int32_t *n_rows, void *ws, int32_t *ids,
+hipError_t top(const domino_logits &lg, int k, double tau, const int32_t *n_rows, void *ws, int32_t *ids,
                float *values, float *lse, hipStream_t st);
 hipError_t beam(const domino_logits &lg, const domino_beam &bm, void *ws, hipStream_t st);
 

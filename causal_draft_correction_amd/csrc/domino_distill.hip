@@ -503,7 +503,7 @@ struct GradCall {
     int k;
     const int32_t *ids;
     const float *stats, *grad_loss;
-    float tau;
+    double tau;
     Split sp;
     Scale sc;
     unsigned grid;
@@ -513,7 +513,7 @@ struct GradCall {
     {
         if constexpr (NV <= GRAD_NV)  // (its split makes no larger chunks)
             hipLaunchKernelGGL((k_distill_grad<T, NV>), dim3(grid), dim3(NT), 0, st, rows, k, sp, ids, stats, grad_loss,
-                               tau, sc, grad);
+                               static_cast<float>(tau), sc, grad);
     }
 };
 
@@ -521,7 +521,7 @@ struct RowCall {
     Rows rows, grad;
     Teach te;
     int nvec;
-    float tau;
+    double tau;
     Scale sc;
     float *loss, *stats;
     const float *grad_loss;
@@ -531,11 +531,11 @@ struct RowCall {
     void run() const
     {
         if (grad_loss)
-            hipLaunchKernelGGL((k_distill_row<T, NTB, NV, true>), dim3(n), dim3(NTB), 0, st, rows, te,
-                               static_cast<double>(tau), sc, loss, stats, grad_loss, grad);
+            hipLaunchKernelGGL((k_distill_row<T, NTB, NV, true>), dim3(n), dim3(NTB), 0, st, rows, te, tau, sc,
+                               loss, stats, grad_loss, grad);
         else
-            hipLaunchKernelGGL((k_distill_row<T, NTB, NV, false>), dim3(n), dim3(NTB), 0, st, rows, te,
-                               static_cast<double>(tau), sc, loss, stats, grad_loss, grad);
+            hipLaunchKernelGGL((k_distill_row<T, NTB, NV, false>), dim3(n), dim3(NTB), 0, st, rows, te, tau, sc,
+                               loss, stats, grad_loss, grad);
     }
     template <typename T>
     void pick() const
@@ -584,7 +584,7 @@ size_t workspace_bytes(const domino_logits &lg, int k)
 namespace {
 
 // Loss, and gradient or statistics, in one launch.  False: not for these rows.
-bool by_rows(const domino_logits &lg, const Teacher &t, float tau, const int32_t *n_rows, float *loss, float *stats,
+bool by_rows(const domino_logits &lg, const Teacher &t, double tau, const int32_t *n_rows, float *loss, float *stats,
              const float *grad_loss, const domino_logits *grad, hipStream_t st)
 {
     RowCall c;
@@ -613,7 +613,7 @@ bool by_rows(const domino_logits &lg, const Teacher &t, float tau, const int32_t
 namespace {
 
 // keep: the logits may stay in the caches, for a gradient that follows.
-hipError_t in_parts(const domino_logits &lg, const Teacher &t, float tau, const int32_t *n_rows, void *ws, float *loss,
+hipError_t in_parts(const domino_logits &lg, const Teacher &t, double tau, const int32_t *n_rows, void *ws, float *loss,
                     float *stats, bool keep, hipStream_t st)
 {
     PartCall c;
@@ -635,12 +635,10 @@ hipError_t in_parts(const domino_logits &lg, const Teacher &t, float tau, const 
         return e;
     if (lg.dtype == DOMINO_F32)
         hipLaunchKernelGGL((k_distill_final<float>), dim3((n + NWAVE - 1) / NWAVE), dim3(NT), 0, st, c.rows, c.te,
-                           static_cast<int>(n), c.sp.nch,
-                           static_cast<double>(tau), c.parts, loss, stats);
+                           static_cast<int>(n), c.sp.nch, tau, c.parts, loss, stats);
     else
         hipLaunchKernelGGL((k_distill_final<bf16s>), dim3((n + NWAVE - 1) / NWAVE), dim3(NT), 0, st, c.rows, c.te,
-                           static_cast<int>(n), c.sp.nch,
-                           static_cast<double>(tau), c.parts, loss, stats);
+                           static_cast<int>(n), c.sp.nch, tau, c.parts, loss, stats);
     return hipGetLastError();
 }
 
@@ -658,7 +656,7 @@ double bytes_of(const domino_logits &lg)
 
 }  // namespace
 
-hipError_t forward(const domino_logits &lg, const Teacher &t, float tau, const int32_t *n_rows, void *ws, float *loss,
+hipError_t forward(const domino_logits &lg, const Teacher &t, double tau, const int32_t *n_rows, void *ws, float *loss,
                    float *stats, hipStream_t st)
 {
     if (by_rows(lg, t, tau, n_rows, loss, stats, nullptr, nullptr, st))
@@ -667,7 +665,7 @@ hipError_t forward(const domino_logits &lg, const Teacher &t, float tau, const i
 }
 
 hipError_t backward(const domino_logits &lg, int k, const int32_t *ids, const float *stats, const float *grad_loss,
-                    float tau, const int32_t *n_rows, const domino_logits &grad, hipStream_t st)
+                    double tau, const int32_t *n_rows, const domino_logits &grad, hipStream_t st)
 {
     GradCall c;
     c.rows = rows_of(lg, n_rows, n_rows != nullptr);
@@ -688,7 +686,7 @@ hipError_t backward(const domino_logits &lg, int k, const int32_t *ids, const fl
     return hipGetLastError();
 }
 
-hipError_t both(const domino_logits &lg, const Teacher &t, float tau, const int32_t *n_rows, void *ws, float *loss,
+hipError_t both(const domino_logits &lg, const Teacher &t, double tau, const int32_t *n_rows, void *ws, float *loss,
                 const float *grad_loss, const domino_logits &grad, hipStream_t st)
 {
     if (by_rows(lg, t, tau, n_rows, loss, nullptr, grad_loss, &grad, st))

@@ -1298,10 +1298,10 @@ static int alias_args(const domino_logits &lg, const domino_logits *grad, std::i
     return DOMINO_OK;
 }
 
-static int temperature_arg(float t)
+static int temperature_arg(double t)
 {
-    if (!(t >= 1e-4f && t <= 1e4f))
-        return fail(DOMINO_EINVAL, "temperature %g outside [1e-4, 1e4]", static_cast<double>(t));
+    if (!(t >= 1e-4f && t <= 1e4))  // (1e-4f, so that a float32 1e-4 is inside)
+        return fail(DOMINO_EINVAL, "temperature %g outside [1e-4, 1e4]", t);
     return DOMINO_OK;
 }
 
@@ -1356,7 +1356,7 @@ int domino_top_logits_workspace_size(const domino_logits *lg, int32_t k, size_t 
     return DOMINO_OK;
 }
 
-int domino_top_logits(const domino_logits *lg, int32_t k, float temperature, const int32_t *n_rows, void *workspace,
+int domino_top_logits(const domino_logits *lg, int32_t k, double temperature, const int32_t *n_rows, void *workspace,
                       size_t workspace_bytes, int32_t *ids, float *values, float *lse, void *stream)
 {
     int rc = top_args(lg, k);
@@ -1440,7 +1440,7 @@ int domino_beam_step(const domino_logits *lg, const domino_beam *bm, void *works
     return DOMINO_OK;
 }
 
-static int distill_args(const domino_logits *lg, int32_t k, float temperature)
+static int distill_args(const domino_logits *lg, int32_t k, double temperature)
 {
     const int rc = logits_args(lg, "logits");
     if (rc)
@@ -1483,7 +1483,7 @@ int domino_distill_workspace_size(const domino_logits *lg, int32_t k, size_t *by
 }
 
 int domino_distill(const domino_logits *lg, int32_t k, const int32_t *ids, const float *values,
-                   const float *teacher_lse, float temperature, const int32_t *n_rows, void *workspace,
+                   const float *teacher_lse, double temperature, const int32_t *n_rows, void *workspace,
                    size_t workspace_bytes, float *loss, float *stats, const float *grad_loss,
                    const domino_logits *grad, void *stream)
 {
@@ -1526,7 +1526,7 @@ int domino_distill(const domino_logits *lg, int32_t k, const int32_t *ids, const
 }
 
 int domino_distill_backward(const domino_logits *lg, int32_t k, const int32_t *ids, const float *stats,
-                            const float *grad_loss, float temperature, const int32_t *n_rows,
+                            const float *grad_loss, double temperature, const int32_t *n_rows,
                             const domino_logits *grad, void *stream)
 {
     int rc = distill_args(lg, k, temperature);

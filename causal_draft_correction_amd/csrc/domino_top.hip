@@ -1034,15 +1034,15 @@ Split split_of(const domino_logits &lg, int k, bool for_beams)
 size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
 
 template <typename T, int NTB, int NV>
-void launch_chunk(const Rows &rows, const Live &live, int k, const Split &sp, float tau, const TopOut &out,
+void launch_chunk(const Rows &rows, const Live &live, int k, const Split &sp, double tau, const TopOut &out,
                   unsigned grid, hipStream_t st)
 {
     hipLaunchKernelGGL((k_top_chunk<T, NTB, NV>), dim3(grid), dim3(NTB), 0, st, rows, live, k, sp, scale_of(tau),
-                       1.0 / static_cast<double>(tau), out);
+                       1.0 / tau, out);
 }
 
 template <typename T>
-void pick_chunk(const Rows &rows, const Live &live, int k, const Split &sp, float tau, const TopOut &out,
+void pick_chunk(const Rows &rows, const Live &live, int k, const Split &sp, double tau, const TopOut &out,
                 unsigned grid, hipStream_t st)
 {
     // (one chunk a row: up to 1024 threads; else blocks of 256, which wait less for their own phases)
@@ -1079,7 +1079,7 @@ Scratch scratch_of(const domino_logits &lg, int k, const Split &sp, void *ws)
     return s;
 }
 
-void chunks(const domino_logits &lg, const Rows &rows, const Live &live, int k, float tau, const Split &sp,
+void chunks(const domino_logits &lg, const Rows &rows, const Live &live, int k, double tau, const Split &sp,
             const TopOut &out, hipStream_t st)
 {
     const unsigned n = static_cast<unsigned>(lg.B) * static_cast<unsigned>(lg.R);
@@ -1102,7 +1102,7 @@ size_t workspace_bytes(const domino_logits &lg, int k, bool for_beams)
     return sp.nch == 1 && !for_beams ? 0 : scratch_of(lg, k, sp, nullptr).bytes;
 }
 
-hipError_t top(const domino_logits &lg, int k, float tau, const int32_t *n_rows, void *ws, int32_t *ids,
+hipError_t top(const domino_logits &lg, int k, double tau, const int32_t *n_rows, void *ws, int32_t *ids,
                float *values, float *lse, hipStream_t st)
 {
     const Split sp = split_of(lg, k, false);
@@ -1117,7 +1117,7 @@ hipError_t top(const domino_logits &lg, int k, float tau, const int32_t *n_rows,
     if (e != hipSuccess || sp.nch == 1)
         return e;
     const dim3 grid(static_cast<unsigned>(lg.B) * static_cast<unsigned>(lg.R));
-    const double inv_tau = 1.0 / static_cast<double>(tau);
+    const double inv_tau = 1.0 / tau;
     if (sp.nch * k <= NT * 4)
         hipLaunchKernelGGL((k_top_merge<4>), grid, dim3(NT), 0, st, rows, live, k, sp.nch, inv_tau, out);
     else

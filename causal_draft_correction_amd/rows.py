@@ -47,14 +47,14 @@ def _lib():
     global _declared
     lib = load_library()
     if _declared is not lib:
-        P, I32, F32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
+        P, I32, F64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_double, ctypes.c_size_t
         lib.domino_top_logits_workspace_size.argtypes = [P, I32, ctypes.POINTER(SZ)]
-        lib.domino_top_logits.argtypes = [P, I32, F32, P, P, SZ, P, P, P, P]
+        lib.domino_top_logits.argtypes = [P, I32, F64, P, P, SZ, P, P, P, P]
         lib.domino_beam_step_workspace_size.argtypes = [P, I32, ctypes.POINTER(SZ)]
         lib.domino_beam_step.argtypes = [P, P, P, SZ, P]
         lib.domino_distill_workspace_size.argtypes = [P, I32, ctypes.POINTER(SZ)]
-        lib.domino_distill.argtypes = [P, I32, P, P, P, F32, P, P, SZ, P, P, P, P, P]
-        lib.domino_distill_backward.argtypes = [P, I32, P, P, P, F32, P, P, P]
+        lib.domino_distill.argtypes = [P, I32, P, P, P, F64, P, P, SZ, P, P, P, P, P]
+        lib.domino_distill_backward.argtypes = [P, I32, P, P, P, F64, P, P, P]
         _declared = lib
     return lib
 

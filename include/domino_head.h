@@ -241,7 +241,8 @@ int domino_verify_noalloc(int32_t B, int32_t K, int32_t V, const float *logits, 
  * search).  `data` is a device pointer of `dtype` (DOMINO_F32, or DOMINO_BF16 as raw 16-bit patterns) with
  * any element alignment; strides count elements, so that a slice of a larger tensor or a padded vocabulary
  * is passed as it is.  0 <= batch_stride, 0 <= row_stride; an output's rows may not overlap.  Every call takes
- * B R (V / 1024 + 1) < 2^24 (DOMINO_EUNSUPPORTED above).  An output that shares memory with an input, another
+ * B R (V / 1024 + 1) < 2^24 (DOMINO_EUNSUPPORTED above).  A temperature is a double: one of 0.7 in float32 moves
+ * z / temperature by 1.7e-8 of itself, which a loss of rows whose logits reach 20 shows.  An output that shares memory with an input, another
  * output or the workspace is refused (DOMINO_EINVAL), but for the gradient in the logits' own rows; rows that lie
  * between each other's in one buffer share none.
  */
@@ -270,7 +271,7 @@ typedef struct domino_logits {
  * other than logits->data 16-byte aligned; outputs may not alias inputs or the workspace.
  */
 int domino_top_logits_workspace_size(const domino_logits *logits, int32_t k, size_t *bytes);
-int domino_top_logits(const domino_logits *logits, int32_t k, float temperature, const int32_t *n_rows,
+int domino_top_logits(const domino_logits *logits, int32_t k, double temperature, const int32_t *n_rows,
                       void *workspace, size_t workspace_bytes, int32_t *ids, float *values, float *lse, void *stream);
 
 /*
@@ -357,11 +358,11 @@ int domino_beam_step(const domino_logits *logits, const domino_beam *beam, void 
  */
 int domino_distill_workspace_size(const domino_logits *logits, int32_t k, size_t *bytes);
 int domino_distill(const domino_logits *logits, int32_t k, const int32_t *ids, const float *values,
-                   const float *teacher_lse, float temperature, const int32_t *n_rows, void *workspace,
+                   const float *teacher_lse, double temperature, const int32_t *n_rows, void *workspace,
                    size_t workspace_bytes, float *loss, float *stats, const float *grad_loss,
                    const domino_logits *grad, void *stream);
 int domino_distill_backward(const domino_logits *logits, int32_t k, const int32_t *ids, const float *stats,
-                            const float *grad_loss, float temperature, const int32_t *n_rows,
+                            const float *grad_loss, double temperature, const int32_t *n_rows,
                             const domino_logits *grad, void *stream);
 
 /*

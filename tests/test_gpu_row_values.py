@@ -86,7 +86,21 @@ def certain_rows(B, R, V, dtype, seed, peak=22.0):
 def test_small_losses_of_a_student_that_is_nearly_certain(V, k, tau, tail, dtype):
     """Only the other ids' sum is taken in float32: log q of a named id is off by Qr SUM at most, the loss by the
     masses times that (and rest times the sum's own error), and its rounding; so are the gradients of named ids."""
-    tau = float(np.float32(tau))  # what the entry point takes
+    check_small_losses(V, k, float(np.float32(tau)), tail, dtype)
+
+
+@pytest.mark.parametrize("tau", [0.7, 1.442, 1 / 3])
+@pytest.mark.parametrize("V", LENGTHS)
+def test_temperatures_that_float32_does_not_hold(V, tau):
+    """The same bounds: a temperature off by H of itself would move a loss by |log p| H of its masses."""
+    check_small_losses(V, 9, tau, True, torch.float32)
+    z = logits(1, 3, V, torch.float32, V, 9.0)
+    got = host(dca.top_logits(z, 3, temperature=tau)["lse"]).astype(np.float64)
+    want = torch.logsumexp(z.double() / tau, -1).cpu().numpy()
+    assert (np.abs(got - want) <= 41 * H + np.abs(want) * H).all()
+
+
+def check_small_losses(V, k, tau, tail, dtype):
     z = certain_rows(2, 4, V, dtype, V + k)
     t = z.float() + 0.05 * torch.randn(z.shape, generator=torch.Generator().manual_seed(k))
     values, ids = t.topk(k)
