@@ -23,6 +23,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <algorithm>
+#include <cmath>
 #include <initializer_list>
 #include <string>
 
@@ -33,6 +34,7 @@
 #include "dh_verify.h"
 #include "dh_top.h"
 #include "dh_distill.h"
+#include "dh_embed.h"
 #include "dh_rbatch.h"
 
 using namespace dh;
@@ -1450,6 +1452,18 @@ static int distill_args(const domino_logits *lg, int32_t k, double temperature)
     return temperature_arg(temperature);
 }
 
+// Rows that are written: either those of a batch entry lie within its stride, or the batch entries of a row within the
+// row's.
+static int written_rows(const domino_rows *m, const char *what)
+{
+    const int64_t rows_span = (m->R - 1) * m->row_stride + m->V;
+    const int64_t batch_span = (m->B - 1) * m->batch_stride + m->V;
+    if ((m->R > 1 && m->row_stride < m->V) || (m->B > 1 && m->batch_stride < m->V) ||
+        (m->R > 1 && m->B > 1 && m->batch_stride < rows_span && m->row_stride < batch_span))
+        return fail(DOMINO_EINVAL, "%s's rows overlap", what);
+    return DOMINO_OK;
+}
+
 // grad: the logits' own rows, or memory apart from them.
 static int grad_args(const domino_logits *lg, const domino_logits *grad)
 {
@@ -1458,12 +1472,8 @@ static int grad_args(const domino_logits *lg, const domino_logits *grad)
         return rc;
     if (grad->dtype != lg->dtype || grad->B != lg->B || grad->R != lg->R || grad->V != lg->V)
         return fail(DOMINO_EINVAL, "grad differs from the logits in type or shape");
-    // either the rows of a batch entry lie within its stride, or the batch entries of a row within the row's
-    const int64_t rows_span = (grad->R - 1) * grad->row_stride + grad->V;
-    const int64_t batch_span = (grad->B - 1) * grad->batch_stride + grad->V;
-    if ((grad->R > 1 && grad->row_stride < grad->V) || (grad->B > 1 && grad->batch_stride < grad->V) ||
-        (grad->R > 1 && grad->B > 1 && grad->batch_stride < rows_span && grad->row_stride < batch_span))
-        return fail(DOMINO_EINVAL, "grad's rows overlap");
+    if ((rc = written_rows(grad, "grad")))
+        return rc;
     if (lg->B == 0)
         return DOMINO_OK;
     if ((rc = logits_data(grad, "grad")))
@@ -1546,6 +1556,124 @@ int domino_distill_backward(const domino_logits *lg, int32_t k, const int32_t *i
     HIP_TRY(dhdistill::backward(*lg, k, ids, stats, grad_loss, temperature, n_rows, *grad,
                                 static_cast<hipStream_t>(stream)),
             "launch distill_backward");
+    return DOMINO_OK;
+}
+
+// Operands of rows, and memory, that are written: none may share memory with another, or with what is read.  NULL, and
+// operands without rows, share none.
+static int separate(std::initializer_list<const domino_rows *> written, std::initializer_list<const domino_rows *> read,
+                    std::initializer_list<Range> outs, std::initializer_list<Range> ins)
+{
+    const auto none = [](const domino_rows *m) { return !m || m->B == 0; };
+    bool bad = false;
+    for (const domino_rows *const *w = written.begin(); w != written.end(); ++w) {
+        if (none(*w))
+            continue;
+        for (const domino_rows *r : read)
+            bad = bad || (!none(r) && rows_meet(*r, apart(**w), span_of(**w)));
+        for (const domino_rows *const *o = w + 1; o != written.end(); ++o)
+            bad = bad || (!none(*o) && rows_meet(**o, apart(**w), span_of(**w)));
+        for (const Range &p : ins)
+            bad = bad || (p.p && rows_meet(**w, apart(p), p));
+    }
+    for (const Range *o = outs.begin(); o != outs.end(); ++o) {
+        if (!o->p)
+            continue;
+        for (const Range *p = o + 1; p != outs.end(); ++p)
+            bad |= meet(*o, *p);
+        for (const Range &p : ins)
+            bad |= meet(*o, p);
+        for (const auto &list : {read, written})
+            for (const domino_rows *r : list)
+                bad = bad || (!none(r) && rows_meet(*r, apart(*o), *o));
+    }
+    if (bad)
+        return fail(DOMINO_EINVAL, "an output overlaps an input, another output or the workspace");
+    return DOMINO_OK;
+}
+
+// One matrix (a table, weights): B = 1.
+static int matrix_args(const domino_rows *m, const char *what)
+{
+    const int rc = logits_args(m, what);
+    if (rc)
+        return rc;
+    if (m->B != 1)
+        return fail(DOMINO_EINVAL, "%s: B=%d, expected one matrix", what, m->B);
+    return DOMINO_OK;
+}
+
+// rows: [B, R, d], one for each token; table: [1, V, d].
+static int embed_args(const domino_rows *rows, const char *what, const domino_rows *table, double scale)
+{
+    int rc = matrix_args(table, "table");
+    if (rc || (rc = logits_args(rows, what)))
+        return rc;
+    if (rows->V != table->V)
+        return fail(DOMINO_EINVAL, "%s has rows of %d elements, the table of %d", what, rows->V, table->V);
+    if (rows->V > 1 << 20)
+        return fail(DOMINO_EUNSUPPORTED, "rows of %d elements: at most %d", rows->V, 1 << 20);
+    if (!std::isfinite(static_cast<float>(scale)))
+        return fail(DOMINO_EINVAL, "scale %g is not finite in float32", scale);
+    return DOMINO_OK;
+}
+
+int domino_embed(const domino_rows *table, const int32_t *ids, double scale, const domino_rows *out, void *stream)
+{
+    int rc = embed_args(out, "out", table, scale);
+    if (rc || (rc = written_rows(out, "out")) || out->B == 0)
+        return rc;
+    if ((rc = logits_data(table, "table")) || (rc = logits_data(out, "out")))
+        return rc;
+    if (!ids)
+        return fail(DOMINO_EINVAL, "NULL pointer");
+    if (reinterpret_cast<uintptr_t>(ids) % 4)
+        return fail(DOMINO_EINVAL, "ids are not aligned to their elements");
+    if ((rc = separate({out}, {table}, {}, {range(ids, static_cast<__int128>(out->B) * out->R * 4)})))
+        return rc;
+    HIP_TRY(dhembed::forward(*table, ids, static_cast<float>(scale), *out, static_cast<hipStream_t>(stream)),
+            "launch embed");
+    return DOMINO_OK;
+}
+
+int domino_embed_backward_workspace_size(const domino_rows *grad, size_t *bytes)
+{
+    const int rc = logits_args(grad, "grad");
+    if (rc)
+        return rc;
+    if (!bytes)
+        return fail(DOMINO_EINVAL, "bytes is NULL");
+    *bytes = grad->B ? dhembed::workspace_bytes(*grad) : 0;
+    return DOMINO_OK;
+}
+
+int domino_embed_backward(const domino_rows *grad, const int32_t *ids, double scale, int32_t accumulate,
+                          void *workspace, size_t workspace_bytes, const domino_rows *table, void *stream)
+{
+    int rc = embed_args(grad, "grad", table, scale);
+    if (rc || (rc = written_rows(table, "table")))
+        return rc;
+    if (accumulate && grad->B == 0)
+        return DOMINO_OK;
+    if ((rc = logits_data(table, "table")))
+        return rc;
+    const size_t need = grad->B ? dhembed::workspace_bytes(*grad) : 0;
+    if (grad->B) {
+        if ((rc = logits_data(grad, "grad")))
+            return rc;
+        if (!ids)
+            return fail(DOMINO_EINVAL, "NULL pointer");
+        if (reinterpret_cast<uintptr_t>(ids) % 4)
+            return fail(DOMINO_EINVAL, "ids are not aligned to their elements");
+        if ((rc = workspace_arg(workspace, workspace_bytes, need)))
+            return rc;
+    }
+    if ((rc = separate({table}, {grad}, {range(workspace, need)},
+                       {range(ids, static_cast<__int128>(grad->B) * grad->R * 4)})))
+        return rc;
+    HIP_TRY(dhembed::backward(*grad, ids, static_cast<float>(scale), accumulate != 0, workspace, *table,
+                              static_cast<hipStream_t>(stream)),
+            "launch embed_backward");
     return DOMINO_OK;
 }
 

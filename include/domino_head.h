@@ -251,6 +251,7 @@ typedef struct domino_logits {
     int64_t batch_stride, row_stride;
     int32_t B, R, V, dtype;
 } domino_logits;
+typedef domino_logits domino_rows; /* the same for other operands: rows of V elements each */
 
 /*
  * The k largest logits of every row, and the row's log-sum-exp: what a teacher leaves behind for
@@ -364,6 +365,30 @@ int domino_distill(const domino_logits *logits, int32_t k, const int32_t *ids, c
 int domino_distill_backward(const domino_logits *logits, int32_t k, const int32_t *ids, const float *stats,
                             const float *grad_loss, double temperature, const int32_t *n_rows,
                             const domino_logits *grad, void *stream);
+
+/*
+ * ---- layers: embedding, linear, and their gradients ----
+ *
+ * Operands are rows of V elements, [B, R, V] as for logits: any element alignment and strides, float32 or bfloat16 each
+ * for itself.  A table or a weight matrix has B = 1.  An output that shares memory with an input, another output or
+ * the workspace is refused (DOMINO_EINVAL) but where it says otherwise, as are outputs whose rows overlap.
+ *
+ * Embedding: out_i = scale * table[ids_i], 0 where ids_i is outside [0, rows of the table).  ids [B, R] int32.
+ * Computed in float32 and rounded once.  One launch.
+ *
+ * domino_embed_backward: table[v] = scale * sum of grad_i over the i with ids_i = v, for every row v; with accumulate
+ * != 0 that is added to the rows that ids name, and the others stay as they are.  Ids outside the table are passed
+ * over.  The tokens are sorted, and each one's rows added in float32: the tile of up to 64 tokens in the order of their
+ * places, tiles in theirs; the result does not change from call to call.  `table` is the gradient, of type and shape of
+ * its own ([1, rows, V]).  workspace >= domino_embed_backward_workspace_size bytes, 16-byte aligned.  At most three
+ * launches for 8192 tokens, above that 3 for each 6 bits of the table's rows besides.
+ * V <= 2^20, scale finite in float32.  B = 0: nothing to look up; the gradient is 0 (without accumulate).
+ * Asynchronous on `stream`; no allocation, no synchronization.
+ */
+int domino_embed(const domino_rows *table, const int32_t *ids, double scale, const domino_rows *out, void *stream);
+int domino_embed_backward_workspace_size(const domino_rows *grad, size_t *bytes);
+int domino_embed_backward(const domino_rows *grad, const int32_t *ids, double scale, int32_t accumulate,
+                          void *workspace, size_t workspace_bytes, const domino_rows *table, void *stream);
 
 /*
  * Synchronizes the device (every stream, so drafts replayed from a captured
