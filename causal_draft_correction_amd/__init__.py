@@ -8,7 +8,10 @@ from .binding import (  # noqa: F401
     LIB_PATH, SYMBOLS, DominoError, DominoHead, accept_len, load_library, verify, verify_noalloc,
     verify_workspace_size,
 )
-from .layers import embed, embed_backward, embed_backward_workspace_size  # noqa: F401
+from .layers import (  # noqa: F401
+    embed, embed_backward, embed_backward_workspace_size, linear, linear_backward, linear_backward_workspace_size,
+    linear_workspace_size,
+)
 from .rows import (  # noqa: F401
     beam_step, beam_step_workspace_size, distill, distill_backward, distill_workspace_size, top_logits,
     top_logits_workspace_size,

@@ -38,7 +38,8 @@ SYMBOLS = ("domino_head_workspace_size", "domino_head_create", "domino_head_draf
            "domino_top_logits_workspace_size", "domino_top_logits", "domino_beam_step_workspace_size",
            "domino_beam_step", "domino_distill_workspace_size", "domino_distill", "domino_distill_backward",
            "domino_embed", "domino_embed_backward_workspace_size", "domino_embed_backward",
-           "domino_head_check_error", "domino_head_exec_info",
+           "domino_linear_workspace_size", "domino_linear", "domino_linear_backward_workspace_size",
+           "domino_linear_backward", "domino_head_check_error", "domino_head_exec_info",
            "domino_head_set_spin_limit", "domino_head_param_count", "domino_head_destroy", "domino_last_error")
 
 

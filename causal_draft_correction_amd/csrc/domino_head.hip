@@ -35,6 +35,7 @@
 #include "dh_top.h"
 #include "dh_distill.h"
 #include "dh_embed.h"
+#include "dh_linear.h"
 #include "dh_rbatch.h"
 
 using namespace dh;
@@ -1674,6 +1675,143 @@ int domino_embed_backward(const domino_rows *grad, const int32_t *ids, double sc
     HIP_TRY(dhembed::backward(*grad, ids, static_cast<float>(scale), accumulate != 0, workspace, *table,
                               static_cast<hipStream_t>(stream)),
             "launch embed_backward");
+    return DOMINO_OK;
+}
+
+static int activation_arg(int32_t act)
+{
+    if (act < DOMINO_NO_ACT || act > DOMINO_RELU)
+        return fail(DOMINO_EINVAL, "activation %d is none of DOMINO_NO_ACT to DOMINO_RELU", act);
+    return DOMINO_OK;
+}
+
+// x [B, R, K] and weight [1, N, K].
+static int linear_args(const domino_rows *x, const domino_rows *weight)
+{
+    int rc = logits_args(x, "x");
+    if (rc || (rc = matrix_args(weight, "weight")))
+        return rc;
+    if (x->V != weight->V)
+        return fail(DOMINO_EINVAL, "x has rows of %d elements, weight of %d", x->V, weight->V);
+    if (x->V >= 1 << 24)
+        return fail(DOMINO_EUNSUPPORTED, "K=%d: less than %d", x->V, 1 << 24);
+    return DOMINO_OK;
+}
+
+// m: [B, R, V]; `written`: an output.
+static int like_rows(const domino_rows *m, const char *what, int32_t B, int32_t R, int32_t V, bool written)
+{
+    int rc = logits_args(m, what);
+    if (rc)
+        return rc;
+    if (m->B != B || m->R != R || m->V != V)
+        return fail(DOMINO_EINVAL, "%s is [%d, %d, %d], expected [%d, %d, %d]", what, m->B, m->R, m->V, B, R, V);
+    if (written && (rc = written_rows(m, what)))
+        return rc;
+    return m->B ? logits_data(m, what) : DOMINO_OK;
+}
+
+static bool same_rows(const domino_rows *a, const domino_rows *b)
+{
+    return a && b && a->data == b->data && a->dtype == b->dtype &&
+           (a->B == 1 || a->batch_stride == b->batch_stride) && (a->R == 1 || a->row_stride == b->row_stride);
+}
+
+int domino_linear_workspace_size(const domino_rows *x, const domino_rows *weight, size_t *bytes)
+{
+    const int rc = linear_args(x, weight);
+    if (rc)
+        return rc;
+    if (!bytes)
+        return fail(DOMINO_EINVAL, "bytes is NULL");
+    dhlinear::Forward f = {};
+    f.x = x, f.weight = weight;
+    *bytes = x->B ? dhlinear::workspace_bytes(f) : 0;
+    return DOMINO_OK;
+}
+
+int domino_linear(const domino_rows *x, const domino_rows *weight, const domino_rows *bias, int32_t activation,
+                  const domino_rows *residual, void *workspace, size_t workspace_bytes, const domino_rows *y,
+                  const domino_rows *pre, void *stream)
+{
+    int rc = linear_args(x, weight);
+    if (rc || (rc = activation_arg(activation)))
+        return rc;
+    const int32_t B = x->B, R = x->R, N = weight->R;
+    if ((rc = like_rows(y, "y", B, R, N, true)) || (residual && (rc = like_rows(residual, "residual", B, R, N, false))) ||
+        (pre && (rc = like_rows(pre, "pre", B, R, N, true))) ||
+        (bias && (rc = like_rows(bias, "bias", 1, 1, N, false))) || B == 0)
+        return rc;
+    if ((rc = logits_data(x, "x")) || (rc = logits_data(weight, "weight")))
+        return rc;
+    const dhlinear::Forward f = {x, weight, bias, residual, y, pre, activation};
+    const size_t need = dhlinear::workspace_bytes(f);
+    if ((rc = workspace_arg(workspace, workspace_bytes, need)) ||
+        (rc = separate({y, pre}, {x, weight, bias, same_rows(residual, y) ? nullptr : residual},
+                       {range(workspace, need)}, {})))
+        return rc;
+    HIP_TRY(dhlinear::forward(f, workspace, static_cast<hipStream_t>(stream)), "launch linear");
+    return DOMINO_OK;
+}
+
+static int linear_backward_args(const domino_rows *grad, const domino_rows *x, const domino_rows *weight,
+                                int32_t activation)
+{
+    int rc = linear_args(x, weight);
+    if (rc || (rc = activation_arg(activation)) || (rc = logits_args(grad, "grad")))
+        return rc;
+    if (grad->B != x->B || grad->R != x->R || grad->V != weight->R)
+        return fail(DOMINO_EINVAL, "grad is [%d, %d, %d], expected [%d, %d, %d]", grad->B, grad->R, grad->V, x->B, x->R,
+                    weight->R);
+    return DOMINO_OK;
+}
+
+int domino_linear_backward_workspace_size(const domino_rows *grad, const domino_rows *x, const domino_rows *weight,
+                                          int32_t activation, int32_t want_x, int32_t want_weight, int32_t want_bias,
+                                          size_t *bytes)
+{
+    const int rc = linear_backward_args(grad, x, weight, activation);
+    if (rc)
+        return rc;
+    if (!bytes)
+        return fail(DOMINO_EINVAL, "bytes is NULL");
+    dhlinear::Backward b = {};
+    b.grad = grad, b.x = x, b.weight = weight, b.act = activation;
+    // (only whether they are wanted counts)
+    b.grad_x = want_x ? x : nullptr, b.grad_weight = want_weight ? weight : nullptr;
+    b.grad_bias = want_bias ? weight : nullptr;
+    *bytes = dhlinear::workspace_bytes(b);
+    return DOMINO_OK;
+}
+
+int domino_linear_backward(const domino_rows *grad, const domino_rows *x, const domino_rows *weight,
+                           const domino_rows *pre, int32_t activation, int32_t accumulate, void *workspace,
+                           size_t workspace_bytes, const domino_rows *grad_x, const domino_rows *grad_weight,
+                           const domino_rows *grad_bias, void *stream)
+{
+    int rc = linear_backward_args(grad, x, weight, activation);
+    if (rc)
+        return rc;
+    const int32_t B = x->B, R = x->R, N = weight->R, K = x->V;
+    if (!grad_x && !grad_weight && !grad_bias)
+        return fail(DOMINO_EINVAL, "no gradient is wanted");
+    if (!pre != (activation == DOMINO_NO_ACT))
+        return fail(DOMINO_EINVAL, "pre goes with an activation");
+    if ((pre && (rc = like_rows(pre, "pre", B, R, N, false))) ||
+        (grad_x && (rc = like_rows(grad_x, "grad_x", B, R, K, true))) ||
+        (grad_weight && (rc = like_rows(grad_weight, "grad_weight", 1, N, K, true))) ||
+        (grad_bias && (rc = like_rows(grad_bias, "grad_bias", 1, 1, N, true))))
+        return rc;
+    if (B && ((rc = logits_data(grad, "grad")) || (rc = logits_data(x, "x")) || (rc = logits_data(weight, "weight"))))
+        return rc;
+    const dhlinear::Backward b = {grad, x, weight, pre, grad_x, grad_weight, grad_bias, activation, accumulate != 0};
+    const size_t need = dhlinear::workspace_bytes(b);
+    // (without rows, weight's memory is not read)
+    if ((rc = workspace_arg(workspace, workspace_bytes, need)) ||
+        (rc = separate({grad_x, grad_weight, grad_bias}, {grad, x, B ? weight : nullptr, pre}, {range(workspace, need)},
+                       {})))
+        return rc;
+    HIP_TRY(dhlinear::backward(b, workspace, static_cast<hipStream_t>(stream)), "launch linear_backward");
     return DOMINO_OK;
 }
 

@@ -1,0 +1,273 @@
+// Linear layers: y = act(x w^T + bias) + residual, and the gradients of x, w and bias.
+//
+//     pre = x w^T + bias            y = act(pre) + residual
+//     dpre = g act'(pre)            dx = dpre w      dw = dpre^T x      dbias = sum over the rows of dpre
+//
+// The products are k_gemm's (dh_gemm.h).  Here: how a product is cut into tiles and parts of its sum, the join of
+// those parts, and what comes before the backward products (dpre, in float32, and the sums over its rows).
+#define DH_NT 256
+#define DH_NS dhl
+#include "dh_gemm.h"
+
+namespace DH_NS {
+
+hipError_t product_y(const Gemm &g, int shape, hipStream_t st);
+hipError_t product_dx(const Gemm &g, int shape, hipStream_t st);
+hipError_t product_dw(const Gemm &g, int shape, hipStream_t st);
+
+// The parts of a product's sums, in order, and the epilogue.  Four elements a thread.
+__global__ __launch_bounds__(NT) void k_gemm_join(Gemm g, Divisor per)
+{
+    const uint32_t at = blockIdx.x * NT + threadIdx.x;
+    const int j = static_cast<int>(per.quotient(at)), i = 4 * static_cast<int>(at - j * per.d);
+    if (j >= g.J)
+        return;
+    const int64_t step = static_cast<int64_t>(g.J) * g.pitch;
+    const float *p = g.partial + static_cast<int64_t>(j) * g.pitch + i;
+    f32x4 sum = *reinterpret_cast<const f32x4 *>(p);
+#pragma unroll 8
+    for (int s = 1; s < g.splits; ++s)
+        sum += *reinterpret_cast<const f32x4 *>(p + s * step);
+    float v[4] = {sum[0], sum[1], sum[2], sum[3]};
+    emit(g.e, i, g.I, g.e.out.row(j), g.e.pre.data ? g.e.pre.row(j) : 0, g.e.residual.data ? g.e.residual.row(j) : 0, v);
+}
+
+constexpr int SUM_COLS = 256;  // columns of a block of k_dpre
+
+struct Dpre {
+    Mat grad, pre;       // pre: data NULL without an activation
+    int M, N, act, rows;  // rows of a block
+    float *dpre;         // [M, pitch]; NULL: not wanted
+    int pitch;
+    float *sums;         // [blocks of rows, N4]; NULL: not wanted
+    int N4;
+};
+
+// dpre of a block's rows and columns, and their sums over the rows: 4 waves take every 4th row, 4 columns a lane.
+__global__ __launch_bounds__(NT) void k_dpre(Dpre d)
+{
+    __shared__ float part[NWAVE][SUM_COLS];
+    const int wave = threadIdx.x >> 6, c = static_cast<int>(blockIdx.x) * SUM_COLS + 4 * (threadIdx.x & 63);
+    const int m0 = static_cast<int>(blockIdx.y) * d.rows, m1 = m0 + d.rows < d.M ? m0 + d.rows : d.M, n = d.N - c;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    if (n > 0) {
+#pragma unroll 4
+        for (int m = m0 + wave; m < m1; m += NWAVE) {
+            float g[4], p[4];
+            get4(d.grad.data, d.grad.f32, d.grad.row(m) + c, n, g);
+            if (d.pre.data) {
+                get4(d.pre.data, d.pre.f32, d.pre.row(m) + c, n, p);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    g[e] *= slope_of(p[e], d.act);
+            }
+            if (d.dpre)
+                *reinterpret_cast<f32x4 *>(d.dpre + static_cast<int64_t>(m) * d.pitch + c) =
+                    f32x4{g[0], g[1], g[2], g[3]};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                sum[e] += g[e];
+        }
+    }
+    if (!d.sums)
+        return;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        part[wave][4 * (threadIdx.x & 63) + e] = sum[e];
+    __syncthreads();
+    const int col = static_cast<int>(blockIdx.x) * SUM_COLS + static_cast<int>(threadIdx.x);
+    if (col < d.N)
+        d.sums[static_cast<int64_t>(blockIdx.y) * d.N4 + col] =
+            (part[0][threadIdx.x] + part[1][threadIdx.x]) + (part[2][threadIdx.x] + part[3][threadIdx.x]);
+}
+
+__global__ __launch_bounds__(NT) void k_bias_join(const float *sums, int blocks, int N, int N4, Mat out, bool accumulate)
+{
+    const int c = static_cast<int>(blockIdx.x) * NT + static_cast<int>(threadIdx.x);
+    if (c >= N)
+        return;
+    float sum = 0.f;
+#pragma unroll 8
+    for (int b = 0; b < blocks; ++b)
+        sum += sums[static_cast<int64_t>(b) * N4 + c];
+    if (out.f32) {
+        float *p = static_cast<float *>(const_cast<void *>(out.data)) + c;
+        *p = accumulate ? *p + sum : sum;
+    } else {
+        bf16s *p = static_cast<bf16s *>(const_cast<void *>(out.data)) + c;
+        Vec<bf16s>::put(p, accumulate ? Vec<bf16s>::one(p) + sum : sum);
+    }
+}
+
+}  // namespace DH_NS
+
+namespace dhlinear {
+
+using namespace dhl;
+
+namespace {
+
+int up(int64_t n, int64_t d) { return static_cast<int>((n + d - 1) / d); }
+size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
+
+struct Cut {
+    int shape, ti, tj, splits, k_split, pitch;
+    size_t bytes;  // of the parts
+};
+
+// Tiles of 128 x 128 where both sides fill them, of 64 x 16 for up to 16 rows.  Few tiles share out their sums until
+// there are two blocks a compute unit, in parts of 256 of k at least.
+Cut cut_of(int64_t I, int64_t J, int64_t K)
+{
+    Cut c;
+    c.shape = J <= 16 ? FEW : I >= 128 && J >= 128 ? LARGE : MEDIUM;
+    const int bi = c.shape == LARGE ? 128 : 64, bj = c.shape == LARGE ? 128 : c.shape == MEDIUM ? 64 : 16;
+    c.ti = up(I, bi), c.tj = up(J, bj);
+    const int64_t tiles = static_cast<int64_t>(c.ti) * c.tj;
+    int64_t n = tiles ? 512 / tiles : 1;
+    n = n < K / 256 ? n : K / 256;
+    n = n < 1 ? 1 : n;
+    c.k_split = up(up(K, n), 64) * 64;
+    c.splits = K ? up(K, c.k_split) : 1;
+    c.pitch = up(I, 4) * 4;
+    c.bytes = c.splits > 1 ? static_cast<size_t>(c.splits) * J * c.pitch * sizeof(float) : 0;
+    return c;
+}
+
+Gemm gemm_of(const Cut &c, const Mat &a, const Mat &b, int64_t I, int64_t J, int64_t K, void *ws)
+{
+    Gemm g = {};
+    g.a = a, g.b = b;
+    g.I = static_cast<int>(I), g.J = static_cast<int>(J), g.K = static_cast<int>(K);
+    g.ti = c.ti, g.tj = c.tj, g.splits = c.splits, g.k_split = c.k_split;
+    g.i_inner = c.ti <= c.tj;
+    g.partial = static_cast<float *>(ws);
+    g.pitch = c.pitch;
+    return g;
+}
+
+template <typename F>
+hipError_t run(const Gemm &g, const Cut &c, F product, hipStream_t st)
+{
+    hipError_t e = product(g, c.shape, st);
+    if (e != hipSuccess || g.splits == 1)
+        return e;
+    const int per = g.pitch / 4;
+    hipLaunchKernelGGL(k_gemm_join, dim3(up(static_cast<int64_t>(g.J) * per, NT)), dim3(NT), 0, st, g,
+                       divisor(static_cast<uint32_t>(per)));
+    return hipGetLastError();
+}
+
+int64_t rows(const domino_rows &m) { return static_cast<int64_t>(m.B) * m.R; }
+
+}  // namespace
+
+size_t workspace_bytes(const Forward &f) { return cut_of(f.weight->R, rows(*f.x), f.x->V).bytes; }
+
+hipError_t forward(const Forward &f, void *ws, hipStream_t st)
+{
+    const int64_t M = rows(*f.x), N = f.weight->R, K = f.x->V;
+    const Cut c = cut_of(N, M, K);
+    Gemm g = gemm_of(c, mat_of(*f.weight), mat_of(*f.x), N, M, K, ws);
+    g.e.out = mat_of(*f.y);
+    if (f.pre)
+        g.e.pre = mat_of(*f.pre);
+    if (f.residual)
+        g.e.residual = mat_of(*f.residual);
+    if (f.bias)
+        g.e.bias = f.bias->data, g.e.bias_f32 = f.bias->dtype == DOMINO_F32;
+    g.e.act = f.act;
+    return run(g, c, product_y, st);
+}
+
+namespace {
+
+struct Layout {
+    Cut x, w;
+    int pitch, sum_rows, sum_blocks, N4;
+    size_t dpre, sums, parts, bytes;
+};
+
+Layout layout_of(const Backward &b)
+{
+    Layout l = {};
+    const int64_t M = rows(*b.grad), N = b.weight->R, K = b.x->V;
+    size_t at = 0, parts = 0;
+    l.pitch = l.N4 = up(N, 4) * 4;
+    l.dpre = at;
+    if (b.act != DOMINO_NO_ACT)
+        at += static_cast<size_t>(M) * l.pitch * sizeof(float);
+    // blocks of 64 rows, and more where that would be more than 64 blocks
+    l.sum_rows = M > 64 * 64 ? up(M, 64) : 64;
+    l.sum_blocks = up(M, l.sum_rows);
+    l.sums = at;
+    if (b.grad_bias)
+        at += round16(static_cast<size_t>(l.sum_blocks) * l.N4 * sizeof(float));
+    if (b.grad_x && M) {
+        l.x = cut_of(K, M, N);
+        parts = l.x.bytes;
+    }
+    if (b.grad_weight) {
+        l.w = cut_of(K, N, M);
+        parts = parts > l.w.bytes ? parts : l.w.bytes;
+    }
+    l.parts = at;
+    l.bytes = at + parts;
+    return l;
+}
+
+}  // namespace
+
+size_t workspace_bytes(const Backward &b) { return layout_of(b).bytes; }
+
+hipError_t backward(const Backward &b, void *ws, hipStream_t st)
+{
+    const Layout l = layout_of(b);
+    const int64_t M = rows(*b.grad), N = b.weight->R, K = b.x->V;
+    char *base = static_cast<char *>(ws);
+    Mat grad = mat_of(*b.grad);
+    hipError_t e = hipSuccess;
+    const bool act = b.act != DOMINO_NO_ACT;
+    if (M && (act || b.grad_bias)) {
+        Dpre d = {};
+        d.grad = grad;
+        if (act) {
+            d.pre = mat_of(*b.pre);
+            d.dpre = b.grad_x || b.grad_weight ? reinterpret_cast<float *>(base + l.dpre) : nullptr;
+        }
+        d.M = static_cast<int>(M), d.N = static_cast<int>(N), d.act = b.act, d.rows = l.sum_rows;
+        d.pitch = l.pitch, d.N4 = l.N4;
+        d.sums = b.grad_bias ? reinterpret_cast<float *>(base + l.sums) : nullptr;
+        hipLaunchKernelGGL(k_dpre, dim3(up(N, SUM_COLS), l.sum_blocks), dim3(NT), 0, st, d);
+        if ((e = hipGetLastError()) != hipSuccess)
+            return e;
+    }
+    if (act) {
+        grad = Mat{};
+        grad.data = base + l.dpre;
+        grad.rs = l.pitch;
+        grad.flat = grad.f32 = true;
+    }
+    if (b.grad_bias) {
+        hipLaunchKernelGGL(k_bias_join, dim3(up(N, NT)), dim3(NT), 0, st, reinterpret_cast<float *>(base + l.sums),
+                           l.sum_blocks, static_cast<int>(N), l.N4, mat_of(*b.grad_bias), b.accumulate);
+        if ((e = hipGetLastError()) != hipSuccess)
+            return e;
+    }
+    if (b.grad_x && M) {
+        Gemm g = gemm_of(l.x, mat_of(*b.weight), grad, K, M, N, base + l.parts);
+        g.e.out = mat_of(*b.grad_x);
+        if ((e = run(g, l.x, product_dx, st)) != hipSuccess)
+            return e;
+    }
+    if (b.grad_weight) {
+        Gemm g = gemm_of(l.w, mat_of(*b.x), grad, K, N, M, base + l.parts);
+        g.e.out = mat_of(*b.grad_weight);
+        if (b.accumulate)
+            g.e.residual = g.e.out;
+        e = run(g, l.w, product_dw, st);
+    }
+    return e;
+}
+
+}  // namespace dhlinear

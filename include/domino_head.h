@@ -391,6 +391,43 @@ int domino_embed_backward(const domino_rows *grad, const int32_t *ids, double sc
                           void *workspace, size_t workspace_bytes, const domino_rows *table, void *stream);
 
 /*
+ * Linear layer: y = act(x weight^T + bias) + residual.
+ *   x [B, R, K], weight [1, N, K], bias [1, 1, N] or NULL, residual [B, R, N] or NULL, y [B, R, N], pre [B, R, N] or
+ *   NULL: x weight^T + bias, which the backward pass of an activation takes
+ *   activation: DOMINO_NO_ACT, DOMINO_SILU (a sigmoid(a)), DOMINO_GELU (a Phi(a), Phi the normal distribution's
+ *   function), DOMINO_RELU
+ * Gradient, from grad = dloss/dy: with dpre = grad act'(pre),
+ *   grad_x [B, R, K] = dpre weight, grad_weight [1, N, K] = dpre^T x, grad_bias [1, 1, N] = sum of dpre over the rows;
+ *   NULL: not wanted (not all three).  pre: NULL without an activation.  accumulate != 0: grad_weight and grad_bias
+ *   are added to what is there (grad_x is not).  relu's slope at 0 is 0.  The residual's gradient is grad itself.
+ * Operands are multiplied as they are: products of bfloat16 are exact, float32 operands go in three parts of 8 bits, so
+ * that two of them multiply to 2^-24 of the product; sums are float32, and each output is rounded once.  An infinity or
+ * NaN of an operand (float32 from 3.39e38 on among them) makes the elements that it takes part in infinite or NaN.
+ * Results do not change from call to call; the last places of an element may depend on the other sizes of the call.
+ * workspace >= domino_linear_workspace_size (x and weight: sizes alone) or domino_linear_backward_workspace_size (grad,
+ * x, weight, and which gradients are wanted: sizes alone) bytes, 16-byte aligned (where that is 0, NULL will do).
+ * y may be the residual (same data, and strides where a dimension is longer than 1).
+ * B R, N and K below 2^24 each.  B = 0: y has no rows; grad_weight and grad_bias are 0 (without accumulate).
+ * At most two launches forward and six backward, asynchronous on `stream`; no allocation, no synchronization.
+ */
+#define DOMINO_NO_ACT 0
+#define DOMINO_SILU 1
+#define DOMINO_GELU 2
+#define DOMINO_RELU 3
+
+int domino_linear_workspace_size(const domino_rows *x, const domino_rows *weight, size_t *bytes);
+int domino_linear(const domino_rows *x, const domino_rows *weight, const domino_rows *bias, int32_t activation,
+                  const domino_rows *residual, void *workspace, size_t workspace_bytes, const domino_rows *y,
+                  const domino_rows *pre, void *stream);
+int domino_linear_backward_workspace_size(const domino_rows *grad, const domino_rows *x, const domino_rows *weight,
+                                          int32_t activation, int32_t want_x, int32_t want_weight, int32_t want_bias,
+                                          size_t *bytes);
+int domino_linear_backward(const domino_rows *grad, const domino_rows *x, const domino_rows *weight,
+                           const domino_rows *pre, int32_t activation, int32_t accumulate, void *workspace,
+                           size_t workspace_bytes, const domino_rows *grad_x, const domino_rows *grad_weight,
+                           const domino_rows *grad_bias, void *stream);
+
+/*
  * Synchronizes the device (every stream, so drafts replayed from a captured
  * HIP graph on any stream are included), reads and clears the device flags
  * (DOMINO_FLAG_*) into *device_flags (may be NULL) and resets the handle's

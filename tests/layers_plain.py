@@ -1,5 +1,7 @@
 """Plain 64-bit forms of the layers on the host, written from the definitions in include/domino_head.h: what the GPU
 results are compared with."""
+import math
+
 import numpy as np
 
 
@@ -22,3 +24,32 @@ def embed_backward(grad, ids, V, scale):
             size[v] += abs(scale) * np.abs(g[i])
             count[v] += 1
     return total, size, count
+
+
+def _erfc(z):
+    return np.vectorize(math.erfc, otypes=[np.float64])(z) if z.size else z
+
+
+def act(a, name):
+    with np.errstate(over="ignore"):
+        if name == "silu":
+            return a / (1 + np.exp(-a))
+        if name == "gelu":
+            return 0.5 * a * _erfc(-a / math.sqrt(2))
+    return np.maximum(a, 0) if name == "relu" else a
+
+
+def slope(a, name):
+    with np.errstate(over="ignore"):
+        if name == "silu":
+            s = 1 / (1 + np.exp(-a))
+            return s * (1 + a / (1 + np.exp(a)))
+        if name == "gelu":
+            return 0.5 * _erfc(-a / math.sqrt(2)) + a * np.exp(-0.5 * a * a) / math.sqrt(2 * math.pi)
+    return (a > 0) * 1.0 if name == "relu" else np.ones_like(a)
+
+
+def product(a, b):
+    """a b^T, and the same of magnitudes."""
+    a, b = np.asarray(a, np.float64), np.asarray(b, np.float64)
+    return a @ b.T, np.abs(a) @ np.abs(b).T
