@@ -13,7 +13,7 @@ from .layers import (  # noqa: F401
     linear_workspace_size,
 )
 from .rows import (  # noqa: F401
-    beam_step, beam_step_workspace_size, distill, distill_backward, distill_workspace_size, top_logits,
-    top_logits_workspace_size,
+    beam_step, beam_step_workspace_size, distill, distill_backward, distill_workspace_size,
+    token_logprobs, token_logprobs_backward, token_logprobs_workspace_size, top_logits, top_logits_workspace_size,
 )
 from .tensors import device_tensor, head_weights_to_device  # noqa: F401

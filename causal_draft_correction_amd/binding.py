@@ -37,6 +37,7 @@ SYMBOLS = ("domino_head_workspace_size", "domino_head_create", "domino_head_draf
            "domino_verify_workspace_size", "domino_verify", "domino_verify_noalloc",
            "domino_top_logits_workspace_size", "domino_top_logits", "domino_beam_step_workspace_size",
            "domino_beam_step", "domino_distill_workspace_size", "domino_distill", "domino_distill_backward",
+           "domino_token_logprobs_workspace_size", "domino_token_logprobs", "domino_token_logprobs_backward",
            "domino_embed", "domino_embed_backward_workspace_size", "domino_embed_backward",
            "domino_linear_workspace_size", "domino_linear", "domino_linear_backward_workspace_size",
            "domino_linear_backward", "domino_head_check_error", "domino_head_exec_info",

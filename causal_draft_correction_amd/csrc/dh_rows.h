@@ -273,13 +273,24 @@ struct Expo {
     float ref, c;
     bool small;
     __device__ Expo(float r, const Scale &s) : ref(r), c(-r * s.near), small(fabsf(r * s.near) < 1024.f) {}
+    // the power of 2
+    template <bool SMALL>
+    __device__ float exponent(float z, const Scale &s) const
+    {
+        if constexpr (SMALL)
+            return fmaf(z, s.near, c);
+        const float d = z - ref;
+        return fmaf(d, s.hi, d * s.lo);
+    }
     template <bool SMALL>
     __device__ float at(float z, const Scale &s) const
     {
-        if constexpr (SMALL)
-            return __builtin_amdgcn_exp2f(fmaf(z, s.near, c));
-        const float d = z - ref;
-        return __builtin_amdgcn_exp2f(fmaf(d, s.hi, d * s.lo));
+        return __builtin_amdgcn_exp2f(exponent<SMALL>(z, s));
+    }
+    // by how much exponent() is too large everywhere
+    __device__ double off(const Scale &s) const
+    {
+        return small ? static_cast<double>(c) + static_cast<double>(ref) * s.near : 0.0;
     }
     // what a sum of at() has to be multiplied by
     __device__ double fix(const Scale &s) const

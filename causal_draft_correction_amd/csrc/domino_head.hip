@@ -32,6 +32,7 @@
 #include "dh_resident.h"
 #include "dh_batched.h"
 #include "dh_verify.h"
+#include "dh_token.h"
 #include "dh_top.h"
 #include "dh_distill.h"
 #include "dh_embed.h"
@@ -1557,6 +1558,106 @@ int domino_distill_backward(const domino_logits *lg, int32_t k, const int32_t *i
     HIP_TRY(dhdistill::backward(*lg, k, ids, stats, grad_loss, temperature, n_rows, *grad,
                                 static_cast<hipStream_t>(stream)),
             "launch distill_backward");
+    return DOMINO_OK;
+}
+
+static int token_args(const domino_logits *lg, int32_t k, double temperature)
+{
+    if (k < 0 || k > dhtop::MAX_K)
+        return fail(DOMINO_EINVAL, "k=%d outside [0, %d]", k, dhtop::MAX_K);
+    const int rc = k ? top_args(lg, k) : logits_args(lg, "logits");
+    return rc ? rc : temperature_arg(temperature);
+}
+
+static size_t token_workspace(const domino_logits *lg, int32_t k)
+{
+    return k ? dhtop::score_workspace_bytes(*lg, k) : dhtoken::workspace_bytes(*lg);
+}
+
+int domino_token_logprobs_workspace_size(const domino_logits *lg, int32_t k, size_t *bytes)
+{
+    const int rc = token_args(lg, k, 1.0);
+    if (rc)
+        return rc;
+    if (!bytes)
+        return fail(DOMINO_EINVAL, "bytes is NULL");
+    *bytes = lg->B ? token_workspace(lg, k) : 0;
+    return DOMINO_OK;
+}
+
+int domino_token_logprobs(const domino_logits *lg, const int32_t *tokens, int32_t k, double temperature,
+                          const int32_t *n_rows, void *workspace, size_t workspace_bytes, float *logprob, float *entropy,
+                          int32_t *ids, float *logprobs, float *stats, const float *grad_logprob,
+                          const float *grad_entropy, const domino_logits *grad, void *stream)
+{
+    int rc = token_args(lg, k, temperature);
+    if (rc)
+        return rc;
+    if (!grad != (!grad_logprob && !grad_entropy) || (grad && (stats || k)))
+        return fail(DOMINO_EINVAL, "grad goes with grad_logprob or grad_entropy, without stats and alternatives");
+    if (grad && (rc = grad_args(lg, grad)))
+        return rc;
+    if (lg->B == 0)
+        return DOMINO_OK;
+    if ((rc = logits_data(lg, "logits")))
+        return rc;
+    if (!k != !ids || !ids != !logprobs)
+        return fail(DOMINO_EINVAL, "ids and logprobs go with k");
+    if (!tokens || !logprob || !entropy)
+        return fail(DOMINO_EINVAL, "NULL pointer");
+    for (const void *p : {static_cast<const void *>(tokens), static_cast<const void *>(n_rows),
+                          static_cast<const void *>(logprob), static_cast<const void *>(entropy),
+                          static_cast<const void *>(ids), static_cast<const void *>(logprobs),
+                          static_cast<const void *>(stats), static_cast<const void *>(grad_logprob),
+                          static_cast<const void *>(grad_entropy)})
+        if (!aligned16(p))
+            return fail(DOMINO_EINVAL, "pointers must be 16-byte aligned");
+    const size_t need = token_workspace(lg, k);
+    if ((rc = workspace_arg(workspace, workspace_bytes, need)))
+        return rc;
+    const __int128 rows = static_cast<__int128>(lg->B) * lg->R;
+    if ((rc = alias_args(*lg, grad,
+                         {range(logprob, rows * 4), range(entropy, rows * 4), range(ids, rows * k * 4),
+                          range(logprobs, rows * k * 4), range(stats, rows * dhtoken::STATS * 4), range(workspace, need)},
+                         {range(tokens, rows * 4), range(n_rows, lg->B * 4ll), range(grad_logprob, rows * 4),
+                          range(grad_entropy, rows * 4)})))
+        return rc;
+    const dhtoken::Scores s = {tokens, logprob, entropy, stats};
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (grad)
+        HIP_TRY(dhtoken::both(*lg, s, temperature, n_rows, workspace, grad_logprob, grad_entropy, *grad, st),
+                "launch token_logprobs");
+    else if (k)
+        HIP_TRY(dhtop::scores(*lg, s, k, temperature, n_rows, workspace, ids, logprobs, st), "launch token_logprobs");
+    else
+        HIP_TRY(dhtoken::forward(*lg, s, temperature, n_rows, workspace, st), "launch token_logprobs");
+    return DOMINO_OK;
+}
+
+int domino_token_logprobs_backward(const domino_logits *lg, const int32_t *tokens, const float *stats,
+                                   const float *grad_logprob, const float *grad_entropy, double temperature,
+                                   const int32_t *n_rows, const domino_logits *grad, void *stream)
+{
+    int rc = token_args(lg, 0, temperature);
+    if (rc || (rc = grad_args(lg, grad)) || lg->B == 0)
+        return rc;
+    if ((rc = logits_data(lg, "logits")))
+        return rc;
+    if (!tokens || !stats || (!grad_logprob && !grad_entropy))
+        return fail(DOMINO_EINVAL, "NULL pointer");
+    for (const void *p : {static_cast<const void *>(tokens), static_cast<const void *>(stats),
+                          static_cast<const void *>(n_rows), static_cast<const void *>(grad_logprob),
+                          static_cast<const void *>(grad_entropy)})
+        if (!aligned16(p))
+            return fail(DOMINO_EINVAL, "pointers must be 16-byte aligned");
+    const __int128 rows = static_cast<__int128>(lg->B) * lg->R;
+    if ((rc = alias_args(*lg, grad, {},
+                         {range(tokens, rows * 4), range(stats, rows * dhtoken::STATS * 4),
+                          range(grad_logprob, rows * 4), range(grad_entropy, rows * 4), range(n_rows, lg->B * 4ll)})))
+        return rc;
+    HIP_TRY(dhtoken::backward(*lg, tokens, stats, grad_logprob, grad_entropy, temperature, n_rows, *grad,
+                              static_cast<hipStream_t>(stream)),
+            "launch token_logprobs_backward");
     return DOMINO_OK;
 }
 

@@ -27,10 +27,16 @@
 // 16 out of each, 4 KiB of state, one beam of each ended: 19.3 + 9.1 us (71 MB); its 2240 blocks with work are more than
 // the 2048 that the device holds (8 a compute unit, by 61 registers and 20 KB of LDS), so the last 192 run almost alone.
 // Four f32 beams of one request, 8 out: 5.2 + 8.2 us, latency.
+//
+// token log-probabilities with alternatives: the same launches (SCORE), which take the row's entropy with its sum and
+// give the k largest as log-probabilities (dh_score.h).
 #define DH_NT 256
 #define DH_NS dht
 #include "dh_rows.h"
+#include "dh_score.h"
 #include "dh_top.h"
+
+#include <type_traits>
 
 namespace DH_NS {
 
@@ -223,7 +229,7 @@ struct ChunkShared {
     uint32_t bound[NTB / 64];
     int place[NTB];
     float m[NTB / 64];
-    double s[NTB / 64];
+    double s[NTB / 64], t[NTB / 64];
     uint32_t count[2 * (NTB / 64)];
     int nvec, n;
 };
@@ -374,7 +380,33 @@ struct TopOut {
     Part *parts;       // [rows, nch]
     int32_t *ids;      // [rows, k]; NULL where keys and parts are wanted
     float *values, *lse;
+    ScorePart *score_parts;  // SCORE: in the place of parts; values are log-probabilities, lse is not there
+    Score score;
 };
+
+template <bool SCORE>
+__device__ inline bool row_wanted(const Rows &rows, const Live &live, const TopOut &o, const Place &at)
+{
+    if constexpr (SCORE)
+        return score_counts(rows, o.score, at);
+    return row_live(rows, live, at);
+}
+
+// The results of a row that is left out.
+template <bool SCORE, int NTB>
+__device__ inline void put_none(const TopOut &o, int row, int k)
+{
+    for (int i = threadIdx.x; i < k; i += NTB) {
+        o.ids[static_cast<int64_t>(row) * k + i] = -1;
+        o.values[static_cast<int64_t>(row) * k + i] = NEG_INF;
+    }
+    if (threadIdx.x == 0) {
+        if constexpr (SCORE)
+            no_score(o.score, row);
+        else
+            o.lse[row] = NEG_INF;
+    }
+}
 
 __device__ inline void put_result(const TopOut &o, int row, int k, int place, uint64_t key)
 {
@@ -382,8 +414,20 @@ __device__ inline void put_result(const TopOut &o, int row, int k, int place, ui
     o.values[static_cast<int64_t>(row) * k + place] = key_value(key);
 }
 
+__device__ inline void put_alternative(const TopOut &o, int row, int k, int place, uint64_t key, const ScorePart &all,
+                                       double log_s, double inv_tau)
+{
+    o.ids[static_cast<int64_t>(row) * k + place] = static_cast<int32_t>(key_index(key));
+    o.values[static_cast<int64_t>(row) * k + place] =
+        static_cast<float>(log_prob(key_value(key), all, log_s, inv_tau));
+}
+__device__ inline float *stats_of(const Score &score, int row)
+{
+    return score.stats ? score.stats + static_cast<int64_t>(row) * SCORE_STATS : nullptr;
+}
+
 // One chunk of a row: its k largest and its part of the row's sum, or the row's results where it is one chunk.
-template <typename T, int NTB, int NV>
+template <typename T, int NTB, int NV, bool SCORE>
 __global__ __launch_bounds__(NTB) void k_top_chunk(Rows rows, Live live, int k, Split sp, Scale sc,
                                                   double inv_tau, TopOut out)
 {
@@ -395,15 +439,9 @@ __global__ __launch_bounds__(NTB) void k_top_chunk(Rows rows, Live live, int k, 
     const int row = place.row;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const bool direct = nch == 1 && out.ids;
-    if (!row_live(rows, live, place)) {
-        if (direct) {
-            for (int i = threadIdx.x; i < k; i += NTB) {
-                out.ids[static_cast<int64_t>(row) * k + i] = -1;
-                out.values[static_cast<int64_t>(row) * k + i] = NEG_INF;
-            }
-            if (threadIdx.x == 0)
-                out.lse[row] = NEG_INF;
-        }
+    if (!row_wanted<SCORE>(rows, live, out, place)) {
+        if (direct)
+            put_none<SCORE, NTB>(out, row, k);
         return;
     }
     const T *z = row_at<T>(rows, place);
@@ -445,9 +483,21 @@ __global__ __launch_bounds__(NTB) void k_top_chunk(Rows rows, Live live, int k, 
         }
     const Expo ex(m > NEG_INF ? m : 0.f, sc);
     // (a thread's sum in float32, all others in 64 bits: continuations of different beams lie close to each other)
-    const double s = wave_sum_f64(ex.small ? sum_exps<T, true>(x, ex, sc) : sum_exps<T, false>(x, ex, sc));
-    if (lane == 0)
-        sh.s[wave] = s;
+    if constexpr (SCORE) {
+        float s, t;
+        set_apart<T, NV, NTB>(x, tm, m, sh.m);
+        if (ex.small)
+            sum_scores<T, true>(x, ex, sc, s, t);
+        else
+            sum_scores<T, false>(x, ex, sc, s, t);
+        const double ws = wave_sum_f64(s), wt = wave_sum_f64(t);
+        if (lane == 0)
+            sh.s[wave] = ws, sh.t[wave] = wt;
+    } else {
+        const double s = wave_sum_f64(ex.small ? sum_exps<T, true>(x, ex, sc) : sum_exps<T, false>(x, ex, sc));
+        if (lane == 0)
+            sh.s[wave] = s;
+    }
     __syncthreads();
     const int nvec = sh.nvec;
     bool nan = false;
@@ -467,8 +517,21 @@ __global__ __launch_bounds__(NTB) void k_top_chunk(Rows rows, Live live, int k, 
         }
     __syncthreads();
     const int64_t slot = static_cast<int64_t>(row) * nch + c;
-    auto emit = [&](int at, uint64_t key) {
+    ScorePart all = {};
+    double log_s = 0.0;
+    if constexpr (SCORE) {
+        double total = 0.0, two = 0.0;
+#pragma unroll
+        for (int w = 0; w < NTB / 64; ++w)
+            total += sh.s[w], two += sh.t[w];
+        all = score_part(m, total, two, ex, sc);
         if (direct)
+            log_s = log1p(all.s);
+    }
+    auto emit = [&](int at, uint64_t key) {
+        if (SCORE && direct)
+            put_alternative(out, row, k, at, key, all, log_s, inv_tau);
+        else if (direct)
             put_result(out, row, k, at, key);
         else
             out.keys[slot * k + at] = key;
@@ -491,6 +554,16 @@ __global__ __launch_bounds__(NTB) void k_top_chunk(Rows rows, Live live, int k, 
         const uint64_t hi = nan ? 1ull << 32 : static_cast<uint64_t>(key_word(m)) + 1;
         list_any(z, v0, v1, k, t_ord > ORD_NEG_INF ? t_ord : ORD_NEG_INF, hi, sh);
         emit_largest<NTB>(sh.list, sh.place, sh.n, k, emit);
+    }
+    if constexpr (SCORE) {
+        if (threadIdx.x == NTB - 1) {
+            if (direct)
+                put_score(out.score, row, VT::one(z + out.score.tokens[row]), all, log_s, inv_tau,
+                          stats_of(out.score, row));
+            else
+                out.score_parts[slot] = all;
+        }
+        return;
     }
     if (threadIdx.x == NTB - 1) {  // (of the wave with the least to rank)
         double total = 0.0;
@@ -593,23 +666,33 @@ __device__ inline int merge_list(const uint64_t *keys, int nch, int k, MergeShar
     return greater + have < k ? greater + have : greater > k ? greater : k;
 }
 
-// The k largest of a row from its chunks' lists, and its log-sum-exp.
-template <int PER>
+// The k largest of a row from its chunks' lists, and its log-sum-exp (TS: with the token's log-probability and the
+// entropy, of logits of this type).
+template <int PER, typename TS = void>
 __global__ __launch_bounds__(NT) void k_top_merge(Rows rows, Live live, int k, int nch, double inv_tau, TopOut out)
 {
+    constexpr bool SCORE = !std::is_void<TS>::value;
     __shared__ MergeShared sh;
     const Place place = rows.place(blockIdx.x);
     const int row = place.row;
-    if (!row_live(rows, live, place)) {
-        for (int i = threadIdx.x; i < k; i += NT) {
-            out.ids[static_cast<int64_t>(row) * k + i] = -1;
-            out.values[static_cast<int64_t>(row) * k + i] = NEG_INF;
-        }
-        if (threadIdx.x == 0)
-            out.lse[row] = NEG_INF;
+    if (!row_wanted<SCORE>(rows, live, out, place)) {
+        put_none<SCORE, NT>(out, row, k);
         return;
     }
     const int64_t slot = static_cast<int64_t>(row) * nch;
+    if constexpr (SCORE) {
+        const ScorePart *parts = out.score_parts + slot, first = first_part(parts, nch);
+        const float z = Vec<TS>::one(row_at<TS>(rows, place) + out.score.tokens[row]);
+        const int n = merge_list<PER>(out.keys + slot * k, nch, k, sh);
+        const ScorePart all = join_parts(first, parts, nch, inv_tau);
+        const double log_s = log1p(all.s);
+        emit_counted<NT>(sh.list, sh.place, n, k, [&](int at, uint64_t key) {
+            put_alternative(out, row, k, at, key, all, log_s, inv_tau);
+        });
+        if (threadIdx.x == NT - 1)
+            put_score(out.score, row, z, all, log_s, inv_tau, stats_of(out.score, row));
+        return;
+    }
     const Part part = first_part(out.parts + slot, nch);
     const int n = merge_list<PER>(out.keys + slot * k, nch, k, sh);
     emit_counted<NT>(sh.list, sh.place, n, k, [&](int at, uint64_t key) { put_result(out, row, k, at, key); });
@@ -1037,8 +1120,12 @@ template <typename T, int NTB, int NV>
 void launch_chunk(const Rows &rows, const Live &live, int k, const Split &sp, double tau, const TopOut &out,
                   unsigned grid, hipStream_t st)
 {
-    hipLaunchKernelGGL((k_top_chunk<T, NTB, NV>), dim3(grid), dim3(NTB), 0, st, rows, live, k, sp, scale_of(tau),
-                       1.0 / tau, out);
+    if (out.score.tokens)
+        hipLaunchKernelGGL((k_top_chunk<T, NTB, NV, true>), dim3(grid), dim3(NTB), 0, st, rows, live, k, sp,
+                           scale_of(tau), 1.0 / tau, out);
+    else
+        hipLaunchKernelGGL((k_top_chunk<T, NTB, NV, false>), dim3(grid), dim3(NTB), 0, st, rows, live, k, sp,
+                           scale_of(tau), 1.0 / tau, out);
 }
 
 template <typename T>
@@ -1063,19 +1150,19 @@ void pick_chunk(const Rows &rows, const Live &live, int k, const Split &sp, doub
 
 struct Scratch {
     uint64_t *keys;
-    Part *parts;
+    void *parts;
     size_t bytes;
 };
 
-Scratch scratch_of(const domino_logits &lg, int k, const Split &sp, void *ws)
+Scratch scratch_of(const domino_logits &lg, int k, const Split &sp, void *ws, size_t part = sizeof(Part))
 {
     const size_t rows = static_cast<size_t>(lg.B) * lg.R, slots = rows * sp.nch;
     char *p = static_cast<char *>(ws);
     Scratch s;
     s.keys = reinterpret_cast<uint64_t *>(p);
     const size_t at = round16(slots * k * sizeof(uint64_t));
-    s.parts = reinterpret_cast<Part *>(p + at);
-    s.bytes = at + round16(slots * sizeof(Part));
+    s.parts = p + at;
+    s.bytes = at + round16(slots * part);
     return s;
 }
 
@@ -1102,14 +1189,20 @@ size_t workspace_bytes(const domino_logits &lg, int k, bool for_beams)
     return sp.nch == 1 && !for_beams ? 0 : scratch_of(lg, k, sp, nullptr).bytes;
 }
 
-hipError_t top(const domino_logits &lg, int k, double tau, const int32_t *n_rows, void *ws, int32_t *ids,
-               float *values, float *lse, hipStream_t st)
+size_t score_workspace_bytes(const domino_logits &lg, int k)
 {
     const Split sp = split_of(lg, k, false);
+    return sp.nch == 1 ? 0 : scratch_of(lg, k, sp, nullptr, sizeof(ScorePart)).bytes;
+}
+
+namespace {
+
+// The launches of top() and scores().
+hipError_t largest(const domino_logits &lg, int k, double tau, const int32_t *n_rows, const TopOut &out, const Split &sp,
+                   hipStream_t st)
+{
     if (sp.nch > 1 && sp.nch > MERGE_LIST / k)  // (split_of makes no such split; the join would drop candidates)
         return hipErrorInvalidValue;
-    const Scratch s = scratch_of(lg, k, sp, ws);
-    const TopOut out = {s.keys, s.parts, ids, values, lse};
     const Rows rows = rows_of(lg, n_rows, n_rows != nullptr);
     const Live live = {nullptr, nullptr};
     chunks(lg, rows, live, k, tau, sp, out, st);
@@ -1118,11 +1211,40 @@ hipError_t top(const domino_logits &lg, int k, double tau, const int32_t *n_rows
         return e;
     const dim3 grid(static_cast<unsigned>(lg.B) * static_cast<unsigned>(lg.R));
     const double inv_tau = 1.0 / tau;
-    if (sp.nch * k <= NT * 4)
-        hipLaunchKernelGGL((k_top_merge<4>), grid, dim3(NT), 0, st, rows, live, k, sp.nch, inv_tau, out);
+    const auto merge = [&](auto few, auto many) {
+        if (sp.nch * k <= NT * 4)
+            hipLaunchKernelGGL(few, grid, dim3(NT), 0, st, rows, live, k, sp.nch, inv_tau, out);
+        else
+            hipLaunchKernelGGL(many, grid, dim3(NT), 0, st, rows, live, k, sp.nch, inv_tau, out);
+    };
+    if (!out.score.tokens)
+        merge(k_top_merge<4>, k_top_merge<MERGE_LIST / NT>);
+    else if (lg.dtype == DOMINO_F32)
+        merge(k_top_merge<4, float>, k_top_merge<MERGE_LIST / NT, float>);
     else
-        hipLaunchKernelGGL((k_top_merge<MERGE_LIST / NT>), grid, dim3(NT), 0, st, rows, live, k, sp.nch, inv_tau, out);
+        merge(k_top_merge<4, bf16s>, k_top_merge<MERGE_LIST / NT, bf16s>);
     return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t top(const domino_logits &lg, int k, double tau, const int32_t *n_rows, void *ws, int32_t *ids,
+               float *values, float *lse, hipStream_t st)
+{
+    const Split sp = split_of(lg, k, false);
+    const Scratch s = scratch_of(lg, k, sp, ws);
+    const TopOut out = {s.keys, static_cast<Part *>(s.parts), ids, values, lse, nullptr, Score{}};
+    return largest(lg, k, tau, n_rows, out, sp, st);
+}
+
+hipError_t scores(const domino_logits &lg, const dhtoken::Scores &want, int k, double tau, const int32_t *n_rows,
+                  void *ws, int32_t *ids, float *logprobs, hipStream_t st)
+{
+    const Split sp = split_of(lg, k, false);
+    const Scratch s = scratch_of(lg, k, sp, ws, sizeof(ScorePart));
+    const TopOut out = {s.keys, nullptr, ids, logprobs, nullptr, static_cast<ScorePart *>(s.parts),
+                        Score{want.tokens, want.logprob, want.entropy, want.stats}};
+    return largest(lg, k, tau, n_rows, out, sp, st);
 }
 
 hipError_t beam(const domino_logits &lg, const domino_beam &bm, void *ws, hipStream_t st)
@@ -1130,7 +1252,7 @@ hipError_t beam(const domino_logits &lg, const domino_beam &bm, void *ws, hipStr
     const int kc = bm.n_out < lg.V ? bm.n_out : lg.V;
     const Split sp = split_of(lg, kc, true);
     const Scratch s = scratch_of(lg, kc, sp, ws);
-    const TopOut out = {s.keys, s.parts, nullptr, nullptr, nullptr};
+    const TopOut out = {s.keys, static_cast<Part *>(s.parts), nullptr, nullptr, nullptr, nullptr, Score{}};
     chunks(lg, rows_of(lg, nullptr, true), Live{bm.scores, bm.finished}, kc, 1.f, sp, out, st);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess)
@@ -1139,7 +1261,7 @@ hipError_t beam(const domino_logits &lg, const domino_beam &bm, void *ws, hipStr
     a.W = lg.R, a.M = bm.n_out, a.V = lg.V, a.kc = kc, a.nch = sp.nch, a.eos = bm.eos, a.T = bm.T, a.step = bm.step;
     a.state_bytes = bm.state ? bm.state_bytes : 0;
     a.keys = s.keys;
-    a.parts = s.parts;
+    a.parts = static_cast<const Part *>(s.parts);
     a.scores = bm.scores;
     a.finished = bm.finished;
     a.state = static_cast<const char *>(bm.state);

@@ -1,4 +1,5 @@
-"""Operators over vocabulary rows: top logits, one step of beam search, distillation from top logits.
+"""Operators over vocabulary rows: top logits, one step of beam search, distillation from top logits, and the
+log-probabilities of given tokens.
 
 Argument marshalling only, as in binding.py: every computation runs in the HIP library, asynchronous on the
 current stream.  Logits are CUDA tensors [B, R, V] or [N, V], float32 or bfloat16, whose last dimension is
@@ -18,6 +19,8 @@ from .binding import DOMINO_BF16, DOMINO_F32, _check, load_library
 
 STAT_HEAD = 4  # floats of a row's statistics before those of its ids
 _TOP_OUT, _LOSS_ONLY, _LOSS_OUT, _GRAD_OUT = {"ids", "values", "lse"}, {"loss"}, {"loss", "stats"}, {"loss", "grad"}
+SCORE_STATS = 8  # floats of a row's statistics for token_logprobs_backward
+_SCORE_OUT, _SCORE_GRAD = ("logprob", "entropy"), {"logprob", "entropy", "grad"}
 _BEAM_OUT = {"scores", "parent", "token", "finished", "state", "history"}
 _DTYPES = {torch.float32: DOMINO_F32, torch.bfloat16: DOMINO_BF16}
 
@@ -55,6 +58,9 @@ def _lib():
         lib.domino_distill_workspace_size.argtypes = [P, I32, ctypes.POINTER(SZ)]
         lib.domino_distill.argtypes = [P, I32, P, P, P, F64, P, P, SZ, P, P, P, P, P]
         lib.domino_distill_backward.argtypes = [P, I32, P, P, P, F64, P, P, P]
+        lib.domino_token_logprobs_workspace_size.argtypes = [P, I32, ctypes.POINTER(SZ)]
+        lib.domino_token_logprobs.argtypes = [P, P, I32, F64, P, P, SZ, P, P, P, P, P, P, P, P, P]
+        lib.domino_token_logprobs_backward.argtypes = [P, P, P, P, P, F64, P, P, P]
         _declared = lib
     return lib
 
@@ -306,6 +312,92 @@ def distill_backward(logits: torch.Tensor, ids: torch.Tensor, stats: torch.Tenso
         out = torch.empty(logits.shape, dtype=logits.dtype, device="cuda")
     _check(lib.domino_distill_backward(lg, k, i_ids, i_stats, i_grad, temperature, rows, _grad("out", out, logits),
                                        _stream(gpu)))
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def token_logprobs_workspace_size(B: int, R: int, V: int, k: int = 0, dtype: torch.dtype = torch.float32) -> int:
+    """Bytes of device workspace `token_logprobs` needs (host only)."""
+    return _size_of(_lib().domino_token_logprobs_workspace_size, _shape_only(B, R, V, dtype), k)
+
+
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, k: int = 0, temperature: float = 1.0,
+                   n_rows: Optional[torch.Tensor] = None, grad_logprob: Optional[torch.Tensor] = None,
+                   grad_entropy: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   out: Optional[dict] = None, want_stats: bool = False) -> dict:
+    """Log-probabilities of given tokens at `temperature`, the entropies of their rows, and the k likeliest alternatives.
+
+    logits [B, R, V] (or [N, V]); tokens [B, R] int32 (outside [0, V): the row is left out, as -1 does); n_rows [B]
+    int32: rows r >= n_rows[b] are left out.  Returns logprob and entropy [B, R] float32 (0 in rows left out), with k
+    ids [B, R, k] int32 and logprobs [B, R, k] float32, likeliest first (-1 and -inf in rows left out), with want_stats
+    stats [B, R, 8] float32 for `token_logprobs_backward`.
+
+    With grad_logprob or grad_entropy [B, R] float32 (and no k, no stats) also grad, of the logits' shape and type:
+    grad_logprob * dlogprob/dlogits + grad_entropy * dentropy/dlogits.  ``out`` may supply these tensors (grad may be
+    the logits themselves, or any tensor of their shape and type with a contiguous last dimension), ``workspace``
+    (uint8) the scratch.
+
+    No graph is recorded: the gradient is the one this call or `token_logprobs_backward` returns, so logits that
+    require one are refused without either (under no_grad they are taken).
+    """
+    lib = _declared or _lib()
+    lg, B, R, V, gpu = _logits("logits", logits)
+    lead = logits.shape[:-1]
+    need = token_logprobs_workspace_size(B, R, V, k, logits.dtype)
+    i_tokens = _need("tokens", tokens, lead, torch.int32, gpu)
+    rows = None if n_rows is None else _need("n_rows", n_rows, (B,), torch.int32, gpu)
+    i_logprob = i_entropy = gd = ids = logprobs = stats = None
+    if grad_logprob is None and grad_entropy is None:
+        if logits.requires_grad and torch.is_grad_enabled():
+            raise ValueError("logits require a gradient, of which the log-probabilities record nothing: give "
+                             "grad_logprob, or logits.detach() and call token_logprobs_backward")
+        out = _known(out, set(_SCORE_OUT + (("ids", "logprobs") if k else ()) + (("stats",) if want_stats else ())))
+        if k:
+            ids = _output(out, "ids", lead + (k,), torch.int32, gpu)
+            logprobs = _output(out, "logprobs", lead + (k,), torch.float32, gpu)
+        if want_stats:
+            stats = _output(out, "stats", lead + (SCORE_STATS,), torch.float32, gpu)
+    else:
+        if k or want_stats:
+            raise ValueError("a call that gives the gradient gives no alternatives and no stats")
+        i_logprob = None if grad_logprob is None else _need("grad_logprob", grad_logprob, lead, torch.float32, gpu)
+        i_entropy = None if grad_entropy is None else _need("grad_entropy", grad_entropy, lead, torch.float32, gpu)
+        out = _known(out, _SCORE_GRAD)
+        if out.get("grad") is None:
+            out["grad"] = torch.empty(logits.shape, dtype=logits.dtype, device="cuda")
+        gd = _grad("out['grad']", out["grad"], logits)
+    logprob = _output(out, "logprob", lead, torch.float32, gpu)
+    entropy = _output(out, "entropy", lead, torch.float32, gpu)
+    _ws, ws, ws_bytes = _scratch(workspace, need, gpu)
+    _check(lib.domino_token_logprobs(lg, i_tokens, k, temperature, rows, ws, ws_bytes, logprob, entropy, ids, logprobs,
+                                     stats, i_logprob, i_entropy, gd, _stream(gpu)))
+    return out
+
+
+def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, stats: torch.Tensor,
+                            grad_logprob: Optional[torch.Tensor] = None, grad_entropy: Optional[torch.Tensor] = None,
+                            temperature: float = 1.0, n_rows: Optional[torch.Tensor] = None,
+                            out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """grad_logprob * dlogprob/dlogits + grad_entropy * dentropy/dlogits of an earlier `token_logprobs` call, from its
+    logits, tokens and stats.
+
+    grad_logprob and grad_entropy [B, R] float32 (None: 0, not both); temperature and n_rows as in that call.  ``out``
+    may be the logits themselves, or any tensor of their shape and type with a contiguous last dimension.
+    """
+    lib = _declared or _lib()
+    lg, B, _, _, gpu = _logits("logits", logits)
+    lead = logits.shape[:-1]
+    i_tokens = _need("tokens", tokens, lead, torch.int32, gpu)
+    i_stats = _need("stats", stats, lead + (SCORE_STATS,), torch.float32, gpu)
+    i_logprob = None if grad_logprob is None else _need("grad_logprob", grad_logprob, lead, torch.float32, gpu)
+    i_entropy = None if grad_entropy is None else _need("grad_entropy", grad_entropy, lead, torch.float32, gpu)
+    if i_logprob is None and i_entropy is None:
+        raise ValueError("grad_logprob or grad_entropy has to be given")
+    rows = None if n_rows is None else _need("n_rows", n_rows, (B,), torch.int32, gpu)
+    if out is None:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device="cuda")
+    _check(lib.domino_token_logprobs_backward(lg, i_tokens, i_stats, i_logprob, i_entropy, temperature, rows,
+                                              _grad("out", out, logits), _stream(gpu)))
     return out
 
 

@@ -367,6 +367,42 @@ int domino_distill_backward(const domino_logits *logits, int32_t k, const int32_
                             const domino_logits *grad, void *stream);
 
 /*
+ * Log-probabilities of given tokens, the entropies of their rows, and the likeliest alternatives.  With y = z /
+ * temperature, p = softmax(y), w the row's token:
+ *     logprob = log p_w       entropy = - sum_v p_v log p_v (0 log 0 = 0)
+ *     alternatives: the k largest logits' ids, in the order of domino_top_logits, and log p of each
+ *     dlogprob/dz_v = (1[v = w] - p_v) / temperature       dentropy/dz_v = - p_v (log p_v + entropy) / temperature
+ * Rows r >= n_rows[b], and rows whose token lies outside [0, V) (-1 ignores a row), are left out: not read, logprob,
+ * entropy and gradient 0, ids -1, their log-probabilities -inf.  A logit of -inf has probability 0; a row of nothing but
+ * -inf has logprob -inf, entropy 0, alternatives of -inf and gradient 0.  A NaN or +inf among a row's logits makes its
+ * logprob, entropy, alternatives' log-probabilities and gradient NaN (the ids stay those of domino_top_logits).  A
+ * log-probability below float32's range (logits at the type's lowest value, temperatures below 1) is -inf.
+ *   tokens        [B, R] int32
+ *   k             alternatives, 0 for none; ids [B, R, k] int32 and logprobs [B, R, k] float32, NULL with k = 0
+ *   n_rows        [B] int32 or NULL (all R)
+ *   workspace     >= domino_token_logprobs_workspace_size bytes; scratch of this call (where that is 0, NULL will do)
+ *   logprob, entropy  [B, R] float32
+ *   stats         [B, R, 8] float32: what the backward pass needs of the forward pass; NULL = not stored
+ *   grad_logprob, grad_entropy  [B, R] float32 or NULL (0).  One given, the call also writes grad_logprob dlogprob/dz +
+ *                 grad_entropy dentropy/dz to `grad` (then not NULL); stats must be NULL and k 0
+ *   grad          as for domino_distill: the logits' own rows, or apart from them
+ * domino_token_logprobs_backward writes the gradient from the forward pass' stats, with the same logits, tokens,
+ * temperature and n_rows.  0 <= B, 1 <= R, 1 <= V, 0 <= k <= 128, 1e-4 <= temperature <= 1e4; with alternatives k <= V <=
+ * 524288.  B = 0 is a no-op.  A thread's sums are float32, all others 64 bits; the largest element of a row is taken
+ * apart from its sums, so that rows that are nearly certain keep their digits.  Results do not change from call to
+ * call.  At most two launches forward and one backward, asynchronous on `stream`; no allocation, no synchronization.
+ * Pointers other than the logits' and the gradient's data 16-byte aligned; outputs may not alias inputs or the workspace.
+ */
+int domino_token_logprobs_workspace_size(const domino_logits *logits, int32_t k, size_t *bytes);
+int domino_token_logprobs(const domino_logits *logits, const int32_t *tokens, int32_t k, double temperature,
+                          const int32_t *n_rows, void *workspace, size_t workspace_bytes, float *logprob, float *entropy,
+                          int32_t *ids, float *logprobs, float *stats, const float *grad_logprob,
+                          const float *grad_entropy, const domino_logits *grad, void *stream);
+int domino_token_logprobs_backward(const domino_logits *logits, const int32_t *tokens, const float *stats,
+                                   const float *grad_logprob, const float *grad_entropy, double temperature,
+                                   const int32_t *n_rows, const domino_logits *grad, void *stream);
+
+/*
  * ---- layers: embedding, linear, and their gradients ----
  *
  * Operands are rows of V elements, [B, R, V] as for logits: any element alignment and strides, float32 or bfloat16 each
