@@ -1,4 +1,4 @@
-"""Beam drafts and distillation of a Domino head: the row operators used together.
+"""Beam drafts, distillation and training on tokens of a Domino head: the row operators and layers used together.
 
 `beam_draft` drafts the W best blocks of a head instead of the greedy one: position after position the head's
 corrected logits of every beam go through `beam_step`, which also puts the recurrent states in the new order.
@@ -7,10 +7,15 @@ corrected logits of every beam go through `beam_step`, which also puts the recur
 block, `verify`, the target's `top_logits` on the accepted prefix, `distill` of the head's logits against them, and
 the gradient of W2, whose correction W2 u is what the loss reaches directly (dL/dW2 = (dL/dL_final)^T u).
 
+`token_step` is one step of training a Markov head on given tokens (the target's own, as a rule): its state is a row
+of a per-token table (`markov_table`), so its forward pass is `embed`, `linear` with SiLU and `linear` onto the base
+logits, its loss the tokens' `token_logprobs`, and their backward calls give the gradients of W1, W2 and the table.
+
     python -m causal_draft_correction_amd.adapt            # the 1024-token synthetic head
     python -m causal_draft_correction_amd.adapt qwen3_8b_b1
 
-runs both on synthetic inputs: the target is the same head with another W2, forced on the drafted tokens.
+runs them on synthetic inputs: the target is the same head with another W2, forced on the drafted tokens; the tokens are
+that target's choices.
 """
 from __future__ import annotations
 
@@ -20,7 +25,8 @@ from typing import Callable, Optional
 import torch
 
 from .binding import DominoHead, verify
-from .rows import beam_step, distill, top_logits
+from .layers import embed, embed_backward, linear, linear_backward
+from .rows import beam_step, distill, token_logprobs, top_logits
 
 
 def beam_draft(head: DominoHead, H: torch.Tensor, L_base: torch.Tensor, last_tok: torch.Tensor, beams: int,
@@ -82,6 +88,47 @@ def distill_step(weights: dict, W2: torch.Tensor, H: torch.Tensor, L_base: torch
     return {"loss": (got["loss"] * weight).sum(), "accept": checked["accept"].float().mean(), "tokens": out["tokens"]}
 
 
+def markov_table(weights: dict) -> torch.Tensor:
+    """A Markov head's states [V, h] float32: the GRU step on each token's embedding from the zero state."""
+    E, W_ih, W_hh = (weights[name] for name in ("E", "W_ih", "W_hh"))
+    g = linear(E, W_ih, bias=weights.get("b_ih"), dtype=torch.float32)["y"]
+    q = torch.zeros(W_ih.shape[0], device=E.device) if weights.get("b_hh") is None else weights["b_hh"].float()
+    (gr, gz, gn), (qr, qz, qn) = g.chunk(3, 1), q.chunk(3)
+    return (1 - torch.sigmoid(gz + qz)) * torch.tanh(gn + torch.sigmoid(gr + qr) * qn)
+
+
+@torch.no_grad()
+def token_step(W1: torch.Tensor, W2: torch.Tensor, table: torch.Tensor, H: torch.Tensor, L_base: torch.Tensor,
+               last_tok: torch.Tensor, tokens: torch.Tensor, n_rows: Optional[torch.Tensor] = None,
+               entropy: float = 0.0) -> dict:
+    """Loss of a Markov head on given tokens, and its gradient in W1.grad, W2.grad and table.grad.
+
+    W1 [r, d + h], W2 [V, r] and table [V, h] float32; H [B, K, d], L_base [B, K, V] and last_tok [B] as
+    `DominoHead.draft` takes them; tokens [B, K] int32 (-1: a position that does not count), n_rows [B] int32 the
+    positions of each row that do.  The loss is the mean of -log p over these, less `entropy` times their mean
+    entropy.  Returns loss, logprob and entropy [B, K] (0 where a position does not count).
+    """
+    B, K, V = L_base.shape
+    d = H.shape[2]
+    prev = torch.cat([last_tok[:, None], tokens[:, :-1]], 1).contiguous()
+    x = torch.cat([H.float(), embed(table, prev)], -1)
+    low = linear(x, W1, activation="silu", want_pre=True)
+    logits = linear(low["y"], W2, residual=L_base, dtype=torch.float32)["y"]
+    counts = (tokens >= 0) & (tokens < V)
+    if n_rows is not None:
+        counts &= torch.arange(K, device=tokens.device) < n_rows[:, None]
+    weight = (counts / counts.sum().clamp(min=1)).float().contiguous()
+    # the gradient takes the place of the logits
+    got = token_logprobs(logits, tokens, n_rows=n_rows, grad_logprob=-weight,
+                         grad_entropy=-entropy * weight if entropy else None, out={"grad": logits})
+    up = linear_backward(got["grad"], low["y"], W2)
+    down = linear_backward(up["x"], x, W1, pre=low["pre"], activation="silu")
+    W1.grad, W2.grad = down["weight"], up["weight"]
+    table.grad = embed_backward(down["x"][..., d:], prev, V)
+    loss = -((got["logprob"] + entropy * got["entropy"]) * weight).sum()
+    return {"loss": loss, "logprob": got["logprob"], "entropy": got["entropy"]}
+
+
 def synthetic_target(weights: dict, W2: torch.Tensor, H: torch.Tensor, L_base: torch.Tensor,
                      last_tok: torch.Tensor) -> Callable[[torch.Tensor], torch.Tensor]:
     """A target that is the head itself with another W2, forced on the drafted tokens; its last row, which follows
@@ -122,7 +169,16 @@ def main(workload: Optional[str] = None, steps: int = 8, beams: int = 4) -> dict
     greedy = beam_draft(one, H, L_base, last_tok, 1)
     print("log-probability of the best of %d beams' drafts %.3f, of the greedy ones %.3f (means over %d rows)" %
           (beams, float(best["scores"][:, 0].mean()), float(greedy["scores"][:, 0].mean()), B))
-    return {"losses": losses, "best": best, "greedy": greedy}
+    # a Markov head on the target's choices after the greedy drafts
+    tokens = target(greedy["tokens"][:, 0].contiguous())[:, :K].argmax(-1).int()
+    params = [torch.nn.Parameter(t) for t in (weights["W1"].float(), weights["W2"].float(), markov_table(weights))]
+    optimizer, token_losses = torch.optim.AdamW(params, lr=0.1 * spread), []
+    for step in range(steps):
+        got = token_step(*params, H, L_base, last_tok, tokens)
+        optimizer.step()
+        token_losses.append(float(got["loss"]))
+        print("step %d on tokens: mean log-probability %.4f" % (step, -token_losses[-1]))
+    return {"losses": losses, "best": best, "greedy": greedy, "token_losses": token_losses}
 
 
 if __name__ == "__main__":
