@@ -24,7 +24,7 @@ struct Mat {
     const void *data;
     int64_t bs, rs;
     Divisor by;  // R
-    bool flat, f32;
+    bool flat, near, f32;
     __device__ int64_t row(int i) const
     {
         if (flat)
@@ -42,18 +42,25 @@ inline Mat mat_of(const domino_rows &m)
     t.by = divisor(static_cast<uint32_t>(m.R));
     t.flat = m.R == 1 || m.B <= 1 || m.batch_stride == m.R * m.row_stride;
     t.f32 = m.dtype == DOMINO_F32;
+    t.near = t.flat && t.rs < (1 << 21);  // (a tile's 128 rows within 31 bits)
     return t;
 }
 
 // ---- epilogue ----
 
-__device__ inline float act_of(float a, int act)
+// Activations of a few instructions, which a product's epilogue has in every element's place; gelu's erfc has some
+// hundreds, and is left to the kernel that joins partial sums.
+__device__ inline float light_act(float a, int act)
 {
     if (act == DOMINO_SILU)
-        return a / (1.f + expf(-a));
+        return a * sigmoidf_(a);
+    return act == DOMINO_RELU ? (a > 0.f || a != a ? a : 0.f) : a;
+}
+__device__ inline float act_of(float a, int act)
+{
     if (act == DOMINO_GELU)
         return 0.5f * a * erfcf(-0.70710678f * a);
-    return act == DOMINO_RELU ? (a > 0.f || a != a ? a : 0.f) : a;
+    return light_act(a, act);
 }
 __device__ inline float slope_of(float a, int act)
 {
@@ -68,7 +75,8 @@ __device__ inline float slope_of(float a, int act)
 }
 
 // n (at most 4) elements from o of a row.
-__device__ inline void get4(const void *data, bool f32, int64_t o, int n, float (&f)[4])
+template <typename F>
+__device__ inline void get4(const void *data, bool f32, int64_t o, int n, F &f)
 {
     if (f32) {
         const float *p = static_cast<const float *>(data) + o;
@@ -97,7 +105,8 @@ __device__ inline void get4(const void *data, bool f32, int64_t o, int n, float 
         }
     }
 }
-__device__ inline void put4(const void *data, bool f32, int64_t o, int n, const float (&f)[4])
+template <typename F>
+__device__ inline void put4(const void *data, bool f32, int64_t o, int n, const F &f)
 {
     if (f32) {
         float *p = static_cast<float *>(const_cast<void *>(data)) + o;
@@ -132,8 +141,9 @@ struct Epilogue {
     int act;
 };
 
-// Elements i .. i + 3 (those below I) of row j.
-__device__ inline void emit(const Epilogue &e, int i, int I, int64_t o_out, int64_t o_pre, int64_t o_res, float (&v)[4])
+// Elements i .. i + 3 (those below I) of row j.  ANY: with any activation.
+template <bool ANY>
+__device__ inline void emit(const Epilogue &e, int i, int I, int64_t o_out, int64_t o_pre, int64_t o_res, f32x4 v)
 {
     const int n = I - i;
     float f[4];
@@ -148,7 +158,7 @@ __device__ inline void emit(const Epilogue &e, int i, int I, int64_t o_out, int6
     if (e.act != DOMINO_NO_ACT)
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-            v[u] = act_of(v[u], e.act);
+            v[u] = ANY ? act_of(v[u], e.act) : light_act(v[u], e.act);
     if (e.residual.data) {
         get4(e.residual.data, e.residual.f32, o_res + i, n, f);
 #pragma unroll
@@ -156,6 +166,74 @@ __device__ inline void emit(const Epilogue &e, int i, int I, int64_t o_out, int6
             v[u] += f[u];
     }
     put4(e.out.data, e.out.f32, o_out + i, n, v);
+}
+
+// The same for all of a wave's elements inside the matrix: i0 + 16 a + 4 (lane / 16) of row j0 + 16 b + lane % 16 (rows
+// from J on are not there), with a light activation.  Each step is taken for two of b at once, so that its loads are in
+// flight together.
+template <int FI, int FJ>
+__device__ inline void emit_all(const Epilogue &e, int i0, int j0, int J, f32x4 (&acc)[FI][FJ])
+{
+    constexpr int AT_ONCE = FJ < 2 ? FJ : 2;
+    const int lane = threadIdx.x & 63, i = i0 + 4 * (lane >> 4);
+    f32x4 bias[FI];
+    if (e.bias) {
+#pragma unroll
+        for (int a = 0; a < FI; ++a)
+            get4(e.bias, e.bias_f32, i + 16 * a, 4, bias[a]);
+    }
+#pragma unroll
+    for (int b0 = 0; b0 < FJ; b0 += AT_ONCE) {
+        const int j = j0 + 16 * b0 + (lane & 15);
+        f32x4 res[FI][AT_ONCE];
+        const auto all = [&](auto f) {
+#pragma unroll
+            for (int b = 0; b < AT_ONCE; ++b)
+#pragma unroll
+                for (int a = 0; a < FI; ++a)
+                    f(a, b);
+        };
+        const auto rows = [&](const Mat &m, int64_t(&o)[AT_ONCE]) {
+#pragma unroll
+            for (int b = 0; b < AT_ONCE; ++b)
+                o[b] = m.row(j + 16 * b < J ? j + 16 * b : J - 1) + i;
+        };
+        const auto put = [&](const Mat &m) {
+            int64_t o[AT_ONCE];
+            rows(m, o);
+            if (m.f32)
+                all([&](int a, int b) {
+                    if (j + 16 * b < J)
+                        put4(m.data, true, o[b] + 16 * a, 4, acc[a][b0 + b]);
+                });
+            else
+                all([&](int a, int b) {
+                    if (j + 16 * b < J)
+                        put4(m.data, false, o[b] + 16 * a, 4, acc[a][b0 + b]);
+                });
+        };
+        if (e.residual.data) {
+            int64_t o[AT_ONCE];
+            rows(e.residual, o);
+            if (e.residual.f32)
+                all([&](int a, int b) { get4(e.residual.data, true, o[b] + 16 * a, 4, res[a][b]); });
+            else
+                all([&](int a, int b) { get4(e.residual.data, false, o[b] + 16 * a, 4, res[a][b]); });
+        }
+        if (e.bias)
+            all([&](int a, int b) { acc[a][b0 + b] += bias[a]; });
+        if (e.pre.data)
+            put(e.pre);
+        if (e.act != DOMINO_NO_ACT)
+            all([&](int a, int b) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    acc[a][b0 + b][u] = light_act(acc[a][b0 + b][u], e.act);
+            });
+        if (e.residual.data)
+            all([&](int a, int b) { acc[a][b0 + b] += res[a][b]; });
+        put(e.out);
+    }
 }
 
 // ---- operands ----
@@ -185,87 +263,121 @@ __device__ inline void cut(const float (&f)[8], uint4 (&plane)[3])
 
 template <typename T>
 constexpr int PLANES = sizeof(T) == 4 ? 3 : 1;
-constexpr int LDS_PAD = 4;  // rows between the chunks of 8 of k: 16 lanes that store 4 rows of 4 chunks hit all banks
+constexpr int LDS_PAD = 2;  // rows between the chunks of 8 of k, so that 8 lanes that store a row's chunks hit all banks
 
-// The X rows' (or columns') share of one step: BX of them by BK of k, in units of 8 of k of one row (along k), or of two
-// columns (across k).
+// The X rows' (or columns') share of one step: BX of them by BK of k, in units of 8 of k of one row (along k), or of 8 of
+// k of the columns that 8 bytes hold (across k).  near: the addresses of a tile are a common one and 32 bits.
 template <typename T, bool ACROSS, int BX, int BK, int NTB>
 struct Stage {
-    static constexpr int CH = BK / 8, PITCH = BX + LDS_PAD;
-    static constexpr int UNITS = ACROSS ? BX / 2 * CH : BX * CH;
+    static constexpr int CH = BK / 8, PITCH = BX + LDS_PAD, SIZE = sizeof(T);
+    static constexpr int COLS = 8 / SIZE;
+    static constexpr int UNITS = ACROSS ? BX / COLS * CH : BX * CH;
     static constexpr int U = (UNITS + NTB - 1) / NTB;
     static constexpr int LDS = PLANES<T> * CH * PITCH;  // vectors of 16 bytes
+    static constexpr int PARTS = 8 / Vec<T>::N;
     typedef typename Vec<T>::raw raw;
     typedef typename Vec<T>::mem mem;
-    static constexpr int PARTS = 8 / Vec<T>::N;
+    typedef uint32_t two __attribute__((ext_vector_type(2)));
+    typedef uint32_t two_mem __attribute__((ext_vector_type(2), aligned(2)));
 
-    raw x[U][ACROSS ? 1 : PARTS];       // along k
-    uint32_t y[U][ACROSS ? 8 : 1][ACROSS ? PARTS : 1];  // across k: two columns in a word, or in two
-    const T *row[U];
+    raw x[ACROSS ? 1 : U][PARTS];
+    two y[ACROSS ? U : 1][8];
+    uint32_t off[U];
+    const char *base;  // of the tile's first row and k = 0
+    int64_t step;      // bytes from a k to the next
     int x0, X;
+    bool fast;
 
     __device__ static int unit(int u) { return u * NTB + static_cast<int>(threadIdx.x); }
     __device__ static bool any(int u) { return UNITS % NTB == 0 || unit(u) < UNITS; }
+    __device__ static int column(int u) { return unit(u) % (BX / COLS) * COLS; }
+    __device__ static int place(int i) { return ACROSS ? i ^ ((i >> 4) & 3) : i; }  // (4 columns a lane: all banks again)
 
     __device__ void begin(const Mat &m, int at, int n)
     {
         x0 = at, X = n;
+        const char *data = static_cast<const char *>(m.data);
+        // (rows past the last are that one again, columns the last whole unit's: their products go nowhere)
+        fast = m.near && !(ACROSS && x0 + BX > X && X % COLS);
+        if constexpr (ACROSS) {
+            base = data + static_cast<int64_t>(x0) * SIZE;
+            step = m.rs * SIZE;
+        } else {
+            base = data + static_cast<int64_t>(x0) * m.rs * SIZE;
+            step = SIZE;
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if constexpr (ACROSS) {
-                row[u] = static_cast<const T *>(m.data);
+                const int i = x0 + column(u) + COLS <= X ? column(u) : X - COLS - x0;
+                off[u] = static_cast<uint32_t>(unit(u) / (BX / COLS) * 8 * static_cast<uint32_t>(step) + i * SIZE);
             } else {
-                // (rows past the last are that one again: their products go nowhere)
-                const int i = x0 + unit(u) / CH;
-                row[u] = static_cast<const T *>(m.data) + m.row(i < X ? i : X - 1);
+                const int i = unit(u) / CH, last = X - 1 - x0;
+                off[u] = static_cast<uint32_t>(static_cast<uint32_t>(i < last ? i : last) *
+                                                   static_cast<uint32_t>(m.rs * SIZE) + unit(u) % CH * 8 * SIZE);
             }
         }
     }
     // k from k0 on; past k1 zeros
     __device__ void load(const Mat &m, int k0, int k1)
     {
+        if (fast && k0 + BK <= k1) {
+            const char *from = base + k0 * step;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (!any(u))
+                    continue;
+                if constexpr (ACROSS) {
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        y[u][r] = *reinterpret_cast<const two_mem *>(
+                            from + static_cast<uint32_t>(off[u] + r * static_cast<uint32_t>(step)));
+                } else {
+#pragma unroll
+                    for (int v = 0; v < PARTS; ++v)
+                        x[u][v] = *reinterpret_cast<const mem *>(from + off[u] + 16 * v);
+                }
+            }
+        } else {
+            slow(m, k0, k1);
+        }
+    }
+    // Any strides, edges and ends: element by element.
+    __device__ void slow(const Mat &m, int k0, int k1)
+    {
+        const T *data = static_cast<const T *>(m.data);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (!any(u))
                 continue;
             if constexpr (ACROSS) {
-                const int i = x0 + unit(u) % (BX / 2) * 2, k = k0 + unit(u) / (BX / 2) * 8;
+                const int i = x0 + column(u), k = k0 + unit(u) / (BX / COLS) * 8;
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
-                    if constexpr (PARTS == 2)
-                        y[u][r][0] = y[u][r][1] = 0;
-                    else
-                        y[u][r][0] = 0;
-                    if (k + r < k1 && i < X) {
-                        const T *p = row[u] + m.row(k + r) + i;
-                        if (i + 1 < X) {
-                            if constexpr (PARTS == 2) {
-                                typedef uint32_t two __attribute__((ext_vector_type(2), aligned(4)));
-                                const two w = *reinterpret_cast<const two *>(p);
-                                y[u][r][0] = w[0], y[u][r][1] = w[1];
-                            } else {
-                                typedef uint32_t one __attribute__((aligned(2)));
-                                y[u][r][0] = *reinterpret_cast<const one *>(p);
+                    y[u][r] = two{0, 0};
+                    if (k + r < k1) {
+                        const T *p = data + m.row(k + r) + i;
+#pragma unroll
+                        for (int c = 0; c < COLS; ++c)
+                            if (i + c < X) {
+                                const uint32_t w = SIZE == 4 ? __float_as_uint(Vec<T>::one(p + c))
+                                                             : __float_as_uint(Vec<T>::one(p + c)) >> 16;
+                                if constexpr (SIZE == 4)
+                                    y[u][r][c] = w;
+                                else
+                                    y[u][r][c >> 1] |= w << (c & 1) * 16;
                             }
-                        } else {
-                            if constexpr (PARTS == 2)
-                                y[u][r][0] = __float_as_uint(Vec<T>::one(p));
-                            else
-                                y[u][r][0] = __float_as_uint(Vec<T>::one(p)) >> 16;
-                        }
                     }
                 }
             } else {
-                const int k = k0 + unit(u) % CH * 8;
-                const T *p = row[u] + k;
-                if (k + 8 <= k1) {
+                const int i = x0 + unit(u) / CH, k = k0 + unit(u) % CH * 8;
+                const T *p = data + m.row(i < X ? i : X - 1) + k;
 #pragma unroll
-                    for (int v = 0; v < PARTS; ++v)
+                for (int v = 0; v < PARTS; ++v) {
+                    x[u][v] = raw{0, 0, 0, 0};
+                    if (k + 8 <= k1) {
                         x[u][v] = *reinterpret_cast<const mem *>(p + v * Vec<T>::N);
-                } else {
-#pragma unroll
-                    for (int v = 0; v < PARTS; ++v) {
-                        x[u][v] = raw{0, 0, 0, 0};
+                    } else {
 #pragma unroll
                         for (int e = 0; e < Vec<T>::N; ++e)
                             if (k + v * Vec<T>::N + e < k1)
@@ -281,7 +393,7 @@ struct Stage {
         cut(f, plane);
 #pragma unroll
         for (int p = 0; p < 3; ++p)
-            lds[(p * CH + chunk) * PITCH + i] = plane[p];
+            lds[(p * CH + chunk) * PITCH + place(i)] = plane[p];
     }
     __device__ void store(uint4 *lds) const
     {
@@ -290,26 +402,24 @@ struct Stage {
             if (!any(u))
                 continue;
             if constexpr (ACROSS) {
-                const int i = unit(u) % (BX / 2) * 2, chunk = unit(u) / (BX / 2);
-                if constexpr (PARTS == 2) {
+                const int i = column(u), chunk = unit(u) / (BX / COLS);
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
+                for (int c = 0; c < COLS; ++c) {
+                    if constexpr (SIZE == 4) {
                         float f[8];
 #pragma unroll
                         for (int r = 0; r < 8; ++r)
-                            f[r] = __uint_as_float(y[u][r][s]);
-                        put(lds, chunk, i + s, f);
-                    }
-                } else {
-                    uint4 a, b;
-                    uint32_t *pa = reinterpret_cast<uint32_t *>(&a), *pb = reinterpret_cast<uint32_t *>(&b);
+                            f[r] = __uint_as_float(y[u][r][c]);
+                        put(lds, chunk, i + c, f);
+                    } else {
+                        uint4 w;
+                        uint32_t *pw = reinterpret_cast<uint32_t *>(&w);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        pa[r] = __builtin_amdgcn_perm(y[u][2 * r + 1][0], y[u][2 * r][0], 0x05040100u);
-                        pb[r] = __builtin_amdgcn_perm(y[u][2 * r + 1][0], y[u][2 * r][0], 0x07060302u);
+                        for (int r = 0; r < 4; ++r)
+                            pw[r] = __builtin_amdgcn_perm(y[u][2 * r + 1][c >> 1], y[u][2 * r][c >> 1],
+                                                          c & 1 ? 0x07060302u : 0x05040100u);
+                        lds[chunk * PITCH + place(i + c)] = w;
                     }
-                    lds[chunk * PITCH + i] = a;
-                    lds[chunk * PITCH + i + 1] = b;
                 }
             } else {
                 const int chunk = unit(u) % CH, i = unit(u) / CH;
@@ -325,11 +435,11 @@ struct Stage {
             }
         }
     }
-    // The lane's 8 of k (step kk of 32) of row i of a plane.
+    // The lane's 8 of k (step kk of 32) of row i + lane % 16 of a plane; i a multiple of 16.
     __device__ static bf16x8 fragment(const uint4 *lds, int plane, int kk, int i)
     {
         const int lane = threadIdx.x & 63;
-        return __builtin_bit_cast(bf16x8, lds[(plane * CH + kk * 4 + (lane >> 4)) * PITCH + i + (lane & 15)]);
+        return __builtin_bit_cast(bf16x8, lds[(plane * CH + kk * 4 + (lane >> 4)) * PITCH + place(i + (lane & 15))]);
     }
 };
 
@@ -338,7 +448,7 @@ struct Gemm {
     int I, J, K;
     int ti, tj, splits, k_split;  // tiles, parts of k of k_split each
     bool i_inner;                 // tiles that share a j come one after the other (else those that share an i)
-    float *partial;               // [splits, J, pitch], where splits > 1
+    float *partial;               // [splits, J, pitch], or NULL: the results go out (splits = 1)
     int pitch;
     Epilogue e;
 };
@@ -352,13 +462,14 @@ __device__ inline int tile_id(int n)
 }
 
 template <typename TA, typename TB, bool A_ACROSS, bool B_ACROSS, int BI, int BJ, int WI, int WJ, int BK>
-__global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64) void k_gemm(Gemm g)
+__global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64, 2) void k_gemm(Gemm g)
 {
     constexpr int NTB = BI / WI * (BJ / WJ) * 64;
     typedef Stage<TA, A_ACROSS, BI, BK, NTB> SA;
     typedef Stage<TB, B_ACROSS, BJ, BK, NTB> SB;
     constexpr int FI = WI / 16, FJ = WJ / 16, PA = PLANES<TA>, PB = PLANES<TB>;
-    __shared__ uint4 lds[SA::LDS + SB::LDS];
+    constexpr int LDS = SA::LDS + SB::LDS, BUF = LDS * 32 <= 80 << 10 ? 2 : 1;
+    __shared__ uint4 lds[BUF * LDS];
     const int tiles = g.ti * g.tj, id = tile_id(tiles * g.splits);
     const int split = id / tiles, tile = id - split * tiles;
     const int outer = g.i_inner ? tile / g.ti : tile / g.tj, inner = tile - outer * (g.i_inner ? g.ti : g.tj);
@@ -380,10 +491,13 @@ __global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64) void k_gemm(Gemm g)
         sa.load(g.a, k0, k1);
         sb.load(g.b, k0, k1);
     }
+    uint4 *at = lds;
     for (int k = k0; k < k1; k += BK) {
-        __syncthreads();
-        sa.store(lds);
-        sb.store(lds + SA::LDS);
+        // (of two buffers, the one of the last step but one: all waves are past it once they have met in the last step)
+        if constexpr (BUF == 1)
+            __syncthreads();
+        sa.store(at);
+        sb.store(at + SA::LDS);
         __syncthreads();
         if (k + BK < k1) {
             sa.load(g.a, k + BK, k1);
@@ -396,13 +510,13 @@ __global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64) void k_gemm(Gemm g)
             for (int p = 0; p < PB; ++p)
 #pragma unroll
                 for (int b = 0; b < FJ; ++b)
-                    fb[p][b] = SB::fragment(lds + SA::LDS, p, kk, wj + 16 * b);
+                    fb[p][b] = SB::fragment(at + SA::LDS, p, kk, wj + 16 * b);
 #pragma unroll
             for (int a = 0; a < FI; ++a) {
                 bf16x8 fa[PA];
 #pragma unroll
                 for (int p = 0; p < PA; ++p)
-                    fa[p] = SA::fragment(lds, p, kk, wi + 16 * a);
+                    fa[p] = SA::fragment(at, p, kk, wi + 16 * a);
 #pragma unroll
                 for (int s = 2; s >= 0; --s)  // (small products first)
 #pragma unroll
@@ -414,34 +528,30 @@ __global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64) void k_gemm(Gemm g)
                                                                                    acc[a][b], 0, 0, 0);
             }
         }
+        if constexpr (BUF == 2)
+            at = at == lds ? lds + LDS : lds;
     }
     // a lane has four neighbouring i of one j
+    if (!g.partial && i0 + BI <= g.I) {
+        emit_all<FI, FJ>(g.e, i0 + wi, j0 + wj, g.J, acc);
+        return;
+    }
 #pragma unroll
     for (int b = 0; b < FJ; ++b) {
         const int j = j0 + wj + 16 * b + (lane & 15);
         if (j >= g.J)
             continue;
-        int64_t o_out = 0, o_pre = 0, o_res = 0;
-        if (g.splits > 1) {
-            o_out = (static_cast<int64_t>(split) * g.J + j) * g.pitch;
-        } else {
-            o_out = g.e.out.row(j);
-            if (g.e.pre.data)
-                o_pre = g.e.pre.row(j);
-            if (g.e.residual.data)
-                o_res = g.e.residual.row(j);
-        }
+        const int64_t o_part = (static_cast<int64_t>(split) * g.J + j) * g.pitch;
 #pragma unroll
         for (int a = 0; a < FI; ++a) {
             const int i = i0 + wi + 16 * a + 4 * (lane >> 4);
             if (i >= g.I)
                 continue;
-            if (g.splits > 1) {
-                *reinterpret_cast<f32x4 *>(g.partial + o_out + i) = acc[a][b];
-            } else {
-                float v[4] = {acc[a][b][0], acc[a][b][1], acc[a][b][2], acc[a][b][3]};
-                emit(g.e, i, g.I, o_out, o_pre, o_res, v);
-            }
+            if (g.partial)
+                *reinterpret_cast<f32x4 *>(g.partial + o_part + i) = acc[a][b];
+            else
+                emit<false>(g.e, i, g.I, g.e.out.row(j), g.e.pre.data ? g.e.pre.row(j) : 0,
+                            g.e.residual.data ? g.e.residual.row(j) : 0, acc[a][b]);
         }
     }
 }

@@ -1818,15 +1818,15 @@ static bool same_rows(const domino_rows *a, const domino_rows *b)
            (a->B == 1 || a->batch_stride == b->batch_stride) && (a->R == 1 || a->row_stride == b->row_stride);
 }
 
-int domino_linear_workspace_size(const domino_rows *x, const domino_rows *weight, size_t *bytes)
+int domino_linear_workspace_size(const domino_rows *x, const domino_rows *weight, int32_t activation, size_t *bytes)
 {
-    const int rc = linear_args(x, weight);
-    if (rc)
+    int rc = linear_args(x, weight);
+    if (rc || (rc = activation_arg(activation)))
         return rc;
     if (!bytes)
         return fail(DOMINO_EINVAL, "bytes is NULL");
     dhlinear::Forward f = {};
-    f.x = x, f.weight = weight;
+    f.x = x, f.weight = weight, f.act = activation;
     *bytes = x->B ? dhlinear::workspace_bytes(f) : 0;
     return DOMINO_OK;
 }

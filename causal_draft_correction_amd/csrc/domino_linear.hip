@@ -28,45 +28,55 @@ __global__ __launch_bounds__(NT) void k_gemm_join(Gemm g, Divisor per)
 #pragma unroll 8
     for (int s = 1; s < g.splits; ++s)
         sum += *reinterpret_cast<const f32x4 *>(p + s * step);
-    float v[4] = {sum[0], sum[1], sum[2], sum[3]};
-    emit(g.e, i, g.I, g.e.out.row(j), g.e.pre.data ? g.e.pre.row(j) : 0, g.e.residual.data ? g.e.residual.row(j) : 0, v);
+    emit<true>(g.e, i, g.I, g.e.out.row(j), g.e.pre.data ? g.e.pre.row(j) : 0,
+               g.e.residual.data ? g.e.residual.row(j) : 0, sum);
 }
 
-constexpr int SUM_COLS = 256;  // columns of a block of k_dpre
+constexpr int SUM_COLS = 256, SUM_ROWS = 4 * NWAVE;  // columns of a block of k_dpre, rows that it has in flight
 
 struct Dpre {
-    Mat grad, pre;       // pre: data NULL without an activation
+    Mat grad, pre;        // pre: data NULL without an activation
     int M, N, act, rows;  // rows of a block
-    float *dpre;         // [M, pitch]; NULL: not wanted
+    float *dpre;          // [M, pitch]; NULL: not wanted
     int pitch;
-    float *sums;         // [blocks of rows, N4]; NULL: not wanted
+    float *sums;          // [blocks of rows, N4]; NULL: not wanted
     int N4;
 };
 
 // dpre of a block's rows and columns, and their sums over the rows: 4 waves take every 4th row, 4 columns a lane.
+template <bool GF32, bool PF32>
 __global__ __launch_bounds__(NT) void k_dpre(Dpre d)
 {
     __shared__ float part[NWAVE][SUM_COLS];
     const int wave = threadIdx.x >> 6, c = static_cast<int>(blockIdx.x) * SUM_COLS + 4 * (threadIdx.x & 63);
     const int m0 = static_cast<int>(blockIdx.y) * d.rows, m1 = m0 + d.rows < d.M ? m0 + d.rows : d.M, n = d.N - c;
+    const bool act = d.pre.data;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     if (n > 0) {
-#pragma unroll 4
-        for (int m = m0 + wave; m < m1; m += NWAVE) {
-            float g[4], p[4];
-            get4(d.grad.data, d.grad.f32, d.grad.row(m) + c, n, g);
-            if (d.pre.data) {
-                get4(d.pre.data, d.pre.f32, d.pre.row(m) + c, n, p);
+        for (int m = m0 + wave; m < m1; m += SUM_ROWS) {
+            float g[4][4], p[4][4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int at = m + u * NWAVE < m1 ? m + u * NWAVE : m1 - 1;
+                get4(d.grad.data, GF32, d.grad.row(at) + c, n, g[u]);
+                if (act)
+                    get4(d.pre.data, PF32, d.pre.row(at) + c, n, p[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (m + u * NWAVE >= m1)
+                    break;
+                if (act)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        g[u][e] *= slope_of(p[u][e], d.act);
+                if (d.dpre)
+                    *reinterpret_cast<f32x4 *>(d.dpre + static_cast<int64_t>(m + u * NWAVE) * d.pitch + c) =
+                        f32x4{g[u][0], g[u][1], g[u][2], g[u][3]};
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    g[e] *= slope_of(p[e], d.act);
+                    sum[e] += g[u][e];
             }
-            if (d.dpre)
-                *reinterpret_cast<f32x4 *>(d.dpre + static_cast<int64_t>(m) * d.pitch + c) =
-                    f32x4{g[0], g[1], g[2], g[3]};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                sum[e] += g[e];
         }
     }
     if (!d.sums)
@@ -112,12 +122,13 @@ size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
 
 struct Cut {
     int shape, ti, tj, splits, k_split, pitch;
+    bool joined;   // the sums go out through k_gemm_join
     size_t bytes;  // of the parts
 };
 
 // Tiles of 128 x 128 where both sides fill them, of 64 x 16 for up to 16 rows.  Few tiles share out their sums until
 // there are two blocks a compute unit, in parts of 256 of k at least.
-Cut cut_of(int64_t I, int64_t J, int64_t K)
+Cut cut_of(int64_t I, int64_t J, int64_t K, int act = DOMINO_NO_ACT)
 {
     Cut c;
     c.shape = J <= 16 ? FEW : I >= 128 && J >= 128 ? LARGE : MEDIUM;
@@ -130,7 +141,8 @@ Cut cut_of(int64_t I, int64_t J, int64_t K)
     c.k_split = up(up(K, n), 64) * 64;
     c.splits = K ? up(K, c.k_split) : 1;
     c.pitch = up(I, 4) * 4;
-    c.bytes = c.splits > 1 ? static_cast<size_t>(c.splits) * J * c.pitch * sizeof(float) : 0;
+    c.joined = c.splits > 1 || act == DOMINO_GELU;
+    c.bytes = c.joined ? static_cast<size_t>(c.splits) * J * c.pitch * sizeof(float) : 0;
     return c;
 }
 
@@ -141,7 +153,7 @@ Gemm gemm_of(const Cut &c, const Mat &a, const Mat &b, int64_t I, int64_t J, int
     g.I = static_cast<int>(I), g.J = static_cast<int>(J), g.K = static_cast<int>(K);
     g.ti = c.ti, g.tj = c.tj, g.splits = c.splits, g.k_split = c.k_split;
     g.i_inner = c.ti <= c.tj;
-    g.partial = static_cast<float *>(ws);
+    g.partial = c.joined ? static_cast<float *>(ws) : nullptr;
     g.pitch = c.pitch;
     return g;
 }
@@ -150,7 +162,7 @@ template <typename F>
 hipError_t run(const Gemm &g, const Cut &c, F product, hipStream_t st)
 {
     hipError_t e = product(g, c.shape, st);
-    if (e != hipSuccess || g.splits == 1)
+    if (e != hipSuccess || !c.joined)
         return e;
     const int per = g.pitch / 4;
     hipLaunchKernelGGL(k_gemm_join, dim3(up(static_cast<int64_t>(g.J) * per, NT)), dim3(NT), 0, st, g,
@@ -162,12 +174,12 @@ int64_t rows(const domino_rows &m) { return static_cast<int64_t>(m.B) * m.R; }
 
 }  // namespace
 
-size_t workspace_bytes(const Forward &f) { return cut_of(f.weight->R, rows(*f.x), f.x->V).bytes; }
+size_t workspace_bytes(const Forward &f) { return cut_of(f.weight->R, rows(*f.x), f.x->V, f.act).bytes; }
 
 hipError_t forward(const Forward &f, void *ws, hipStream_t st)
 {
     const int64_t M = rows(*f.x), N = f.weight->R, K = f.x->V;
-    const Cut c = cut_of(N, M, K);
+    const Cut c = cut_of(N, M, K, f.act);
     Gemm g = gemm_of(c, mat_of(*f.weight), mat_of(*f.x), N, M, K, ws);
     g.e.out = mat_of(*f.y);
     if (f.pre)
@@ -197,8 +209,8 @@ Layout layout_of(const Backward &b)
     l.dpre = at;
     if (b.act != DOMINO_NO_ACT)
         at += static_cast<size_t>(M) * l.pitch * sizeof(float);
-    // blocks of 64 rows, and more where that would be more than 64 blocks
-    l.sum_rows = M > 64 * 64 ? up(M, 64) : 64;
+    // blocks of 16 rows, and more where that would be more than 64 blocks
+    l.sum_rows = M > 64 * SUM_ROWS ? up(M, 64 * SUM_ROWS) * SUM_ROWS : SUM_ROWS;
     l.sum_blocks = up(M, l.sum_rows);
     l.sums = at;
     if (b.grad_bias)
@@ -238,7 +250,10 @@ hipError_t backward(const Backward &b, void *ws, hipStream_t st)
         d.M = static_cast<int>(M), d.N = static_cast<int>(N), d.act = b.act, d.rows = l.sum_rows;
         d.pitch = l.pitch, d.N4 = l.N4;
         d.sums = b.grad_bias ? reinterpret_cast<float *>(base + l.sums) : nullptr;
-        hipLaunchKernelGGL(k_dpre, dim3(up(N, SUM_COLS), l.sum_blocks), dim3(NT), 0, st, d);
+        const bool pf32 = !act || d.pre.f32;
+        const auto kernel = grad.f32 ? (pf32 ? k_dpre<true, true> : k_dpre<true, false>)
+                                     : (pf32 ? k_dpre<false, true> : k_dpre<false, false>);
+        hipLaunchKernelGGL(kernel, dim3(up(N, SUM_COLS), l.sum_blocks), dim3(NT), 0, st, d);
         if ((e = hipGetLastError()) != hipSuccess)
             return e;
     }
@@ -247,6 +262,7 @@ hipError_t backward(const Backward &b, void *ws, hipStream_t st)
         grad.data = base + l.dpre;
         grad.rs = l.pitch;
         grad.flat = grad.f32 = true;
+        grad.near = grad.rs < (1 << 21);
     }
     if (b.grad_bias) {
         hipLaunchKernelGGL(k_bias_join, dim3(up(N, NT)), dim3(NT), 0, st, reinterpret_cast<float *>(base + l.sums),

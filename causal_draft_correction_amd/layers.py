@@ -30,7 +30,7 @@ def _lib():
         lib.domino_embed.argtypes = [P, P, F64, P, P]
         lib.domino_embed_backward_workspace_size.argtypes = [P, ctypes.POINTER(SZ)]
         lib.domino_embed_backward.argtypes = [P, P, F64, I32, P, SZ, P, P]
-        lib.domino_linear_workspace_size.argtypes = [P, P, ctypes.POINTER(SZ)]
+        lib.domino_linear_workspace_size.argtypes = [P, P, I32, ctypes.POINTER(SZ)]
         lib.domino_linear.argtypes = [P, P, P, I32, P, P, SZ, P, P, P]
         lib.domino_linear_backward_workspace_size.argtypes = [P, P, P, I32, I32, I32, I32, ctypes.POINTER(SZ)]
         lib.domino_linear_backward.argtypes = [P, P, P, P, I32, I32, P, SZ, P, P, P, P]
@@ -139,10 +139,11 @@ def _vector(name: str, t, n: int, gpu: int) -> bytes:
 
 
 @functools.lru_cache(maxsize=1024)
-def linear_workspace_size(B: int, R: int, K: int, N: int) -> int:
+def linear_workspace_size(B: int, R: int, K: int, N: int, activation: Optional[str] = None) -> int:
     """Bytes of device workspace `linear` needs for x [B, R, K] and weight [N, K] (host only)."""
     w = _shape_only(1, N, K, torch.float32)
-    return _size_of(_lib().domino_linear_workspace_size, _shape_only(B, R, K, torch.float32), ctypes.byref(w))
+    return _size_of(_lib().domino_linear_workspace_size, _shape_only(B, R, K, torch.float32), ctypes.byref(w),
+                    _act(activation))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -184,7 +185,7 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
     rd = None if residual is None else _rows_like("residual", residual, shape)
     bd = None if bias is None else _vector("bias", bias, n, gpu)
     if B * R:
-        _ws, ws, ws_bytes = _scratch(workspace, linear_workspace_size(B, R, K, n), gpu)
+        _ws, ws, ws_bytes = _scratch(workspace, linear_workspace_size(B, R, K, n, activation), gpu)
         _check(lib.domino_linear(xd, wd, bd, act, rd, ws, ws_bytes, yd, pd, _stream(gpu)))
     return out
 

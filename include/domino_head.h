@@ -440,8 +440,8 @@ int domino_embed_backward(const domino_rows *grad, const int32_t *ids, double sc
  * that two of them multiply to 2^-24 of the product; sums are float32, and each output is rounded once.  An infinity or
  * NaN of an operand (float32 from 3.39e38 on among them) makes the elements that it takes part in infinite or NaN.
  * Results do not change from call to call; the last places of an element may depend on the other sizes of the call.
- * workspace >= domino_linear_workspace_size (x and weight: sizes alone) or domino_linear_backward_workspace_size (grad,
- * x, weight, and which gradients are wanted: sizes alone) bytes, 16-byte aligned (where that is 0, NULL will do).
+ * workspace >= domino_linear_workspace_size (x and weight: sizes and types alone) or domino_linear_backward_workspace_size (grad,
+ * x, weight, and which gradients are wanted: likewise) bytes, 16-byte aligned (where that is 0, NULL will do).
  * y may be the residual (same data, and strides where a dimension is longer than 1).
  * B R, N and K below 2^24 each.  B = 0: y has no rows; grad_weight and grad_bias are 0 (without accumulate).
  * At most two launches forward and six backward, asynchronous on `stream`; no allocation, no synchronization.
@@ -451,7 +451,7 @@ int domino_embed_backward(const domino_rows *grad, const int32_t *ids, double sc
 #define DOMINO_GELU 2
 #define DOMINO_RELU 3
 
-int domino_linear_workspace_size(const domino_rows *x, const domino_rows *weight, size_t *bytes);
+int domino_linear_workspace_size(const domino_rows *x, const domino_rows *weight, int32_t activation, size_t *bytes);
 int domino_linear(const domino_rows *x, const domino_rows *weight, const domino_rows *bias, int32_t activation,
                   const domino_rows *residual, void *workspace, size_t workspace_bytes, const domino_rows *y,
                   const domino_rows *pre, void *stream);

@@ -298,7 +298,7 @@ def test_captured_twice_on_one_workspace_and_another_stream():
     pre = dca.linear(x, w, want_pre=True)["pre"]
     kw = dict(pre=pre, activation="silu", want=("x", "weight", "bias"))
     want_y, want = dca.linear(x, w, activation="silu")["y"], dca.linear_backward(g, x, w, **kw)
-    need = max(dca.linear_workspace_size(M, 1, K, N), dca.linear_backward_workspace_size(M, 1, K, N, "silu", kw["want"]))
+    need = max(dca.linear_workspace_size(M, 1, K, N, "silu"), dca.linear_backward_workspace_size(M, 1, K, N, "silu", kw["want"]))
     assert dca.linear_workspace_size(M, 1, K, N) > 0  # (its sums are shared out)
     ws = torch.empty(need, dtype=torch.uint8, device="cuda")
     stream = torch.cuda.Stream()

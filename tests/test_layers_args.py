@@ -172,7 +172,7 @@ def test_other_arguments_of_a_linear_layer():
     pre = y(data=1 << 26)
     assert need > 0 and linear_back(y(), rows(), w(), pre=pre, act=1, dx=DX, nbytes=need - 1) == EWORKSPACE
     assert linear(rows(B=0, data=None), w(), y(B=0, data=None), ws=None) == 0
-    assert _lib().domino_linear_workspace_size(ref(rows()), ref(w()), None) == EINVAL
+    assert _lib().domino_linear_workspace_size(ref(rows()), ref(w()), 0, None) == EINVAL
     assert _lib().domino_linear_backward_workspace_size(ref(y()), ref(rows()), ref(w()), 0, 1, 1, 1, None) == EINVAL
 
 
