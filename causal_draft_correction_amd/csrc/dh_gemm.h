@@ -14,6 +14,8 @@
 #include "dh_linear.h"
 #include "dh_rows.h"
 
+#include <type_traits>
+
 namespace DH_NS {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -75,13 +77,14 @@ __device__ inline float slope_of(float a, int act)
 }
 
 // n (at most 4) elements from o of a row.
-template <typename F>
+template <bool STREAM = false, typename F>
 __device__ inline void get4(const void *data, bool f32, int64_t o, int n, F &f)
 {
     if (f32) {
         const float *p = static_cast<const float *>(data) + o;
         if (n >= 4) {
-            const Vec<float>::raw x = *reinterpret_cast<const Vec<float>::mem *>(p);
+            const auto *v = reinterpret_cast<const Vec<float>::mem *>(p);
+            const Vec<float>::raw x = STREAM ? __builtin_nontemporal_load(v) : *v;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 f[e] = x[e];
@@ -94,7 +97,8 @@ __device__ inline void get4(const void *data, bool f32, int64_t o, int n, F &f)
         typedef uint32_t two __attribute__((ext_vector_type(2), aligned(2)));
         const bf16s *p = static_cast<const bf16s *>(data) + o;
         if (n >= 4) {
-            const two x = *reinterpret_cast<const two *>(p);
+            const auto *v = reinterpret_cast<const two *>(p);
+            const two x = STREAM ? __builtin_nontemporal_load(v) : *v;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 f[e] = __uint_as_float(e & 1 ? x[e >> 1] & 0xFFFF0000u : x[e >> 1] << 16);
@@ -105,13 +109,17 @@ __device__ inline void get4(const void *data, bool f32, int64_t o, int n, F &f)
         }
     }
 }
-template <typename F>
+template <bool STREAM = false, typename F>
 __device__ inline void put4(const void *data, bool f32, int64_t o, int n, const F &f)
 {
     if (f32) {
         float *p = static_cast<float *>(const_cast<void *>(data)) + o;
         if (n >= 4) {
-            *reinterpret_cast<Vec<float>::mem *>(p) = Vec<float>::raw{f[0], f[1], f[2], f[3]};
+            const Vec<float>::raw x = {f[0], f[1], f[2], f[3]};
+            if (STREAM)
+                __builtin_nontemporal_store(x, reinterpret_cast<Vec<float>::mem *>(p));
+            else
+                *reinterpret_cast<Vec<float>::mem *>(p) = x;
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -122,8 +130,12 @@ __device__ inline void put4(const void *data, bool f32, int64_t o, int n, const 
         typedef uint32_t two __attribute__((ext_vector_type(2), aligned(2)));
         bf16s *p = static_cast<bf16s *>(const_cast<void *>(data)) + o;
         if (n >= 4) {
-            *reinterpret_cast<two *>(p) = two{Vec<bf16s>::bits(f[0]) | (Vec<bf16s>::bits(f[1]) << 16),
-                                              Vec<bf16s>::bits(f[2]) | (Vec<bf16s>::bits(f[3]) << 16)};
+            const two x = {Vec<bf16s>::bits(f[0]) | (Vec<bf16s>::bits(f[1]) << 16),
+                           Vec<bf16s>::bits(f[2]) | (Vec<bf16s>::bits(f[3]) << 16)};
+            if (STREAM)
+                __builtin_nontemporal_store(x, reinterpret_cast<two *>(p));
+            else
+                *reinterpret_cast<two *>(p) = x;
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -137,12 +149,11 @@ __device__ inline void put4(const void *data, bool f32, int64_t o, int n, const 
 struct Epilogue {
     Mat out, pre, residual;  // data NULL: none
     const void *bias;
-    bool bias_f32;
+    bool bias_f32, stream;   // stream: out and residual are too large for the caches
     int act;
 };
 
-// Elements i .. i + 3 (those below I) of row j.  ANY: with any activation.
-template <bool ANY>
+// Elements i .. i + 3 (those below I) of row j.
 __device__ inline void emit(const Epilogue &e, int i, int I, int64_t o_out, int64_t o_pre, int64_t o_res, f32x4 v)
 {
     const int n = I - i;
@@ -158,7 +169,7 @@ __device__ inline void emit(const Epilogue &e, int i, int I, int64_t o_out, int6
     if (e.act != DOMINO_NO_ACT)
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-            v[u] = ANY ? act_of(v[u], e.act) : light_act(v[u], e.act);
+            v[u] = act_of(v[u], e.act);
     if (e.residual.data) {
         get4(e.residual.data, e.residual.f32, o_res + i, n, f);
 #pragma unroll
@@ -168,73 +179,105 @@ __device__ inline void emit(const Epilogue &e, int i, int I, int64_t o_out, int6
     put4(e.out.data, e.out.f32, o_out + i, n, v);
 }
 
-// The same for all of a wave's elements inside the matrix: i0 + 16 a + 4 (lane / 16) of row j0 + 16 b + lane % 16 (rows
-// from J on are not there), with a light activation.  Each step is taken for two of b at once, so that its loads are in
-// flight together.
-template <int FI, int FJ>
-__device__ inline void emit_all(const Epilogue &e, int i0, int j0, int J, f32x4 (&acc)[FI][FJ])
-{
-    constexpr int AT_ONCE = FJ < 2 ? FJ : 2;
-    const int lane = threadIdx.x & 63, i = i0 + 4 * (lane >> 4);
-    f32x4 bias[FI];
-    if (e.bias) {
+// The same for a block's tile of BI x BJ from (i0, j0), with a light activation, by way of LDS (`tile`, free after a
+// barrier), PART rows at a time: a thread has the elements i .. i + 3 of every STEP-th row, so that a row's neighbours are
+// loaded and stored together.  The residual is on its way before the sums are exchanged.
+template <int BI, int BJ, int NTB>
+struct EmitTile {
+    static constexpr int PART = BJ < 64 ? BJ : 64;
+    static constexpr int LANES = BI / 4, STEP = NTB / LANES, N = PART / STEP, PITCH = BI + 4;
+    static constexpr int LDS = PART * PITCH / 4;  // vectors of 16 bytes
+    static constexpr int G = N < 8 ? N : 8;       // rows in registers at once
+    static_assert(PART % STEP == 0 && N % G == 0 && BJ % PART == 0, "");
+
+    template <bool F32, bool STREAM>
+    __device__ static void get(const Mat &m, int i, int j0, int J, f32x4 (&v)[G])
+    {
 #pragma unroll
-        for (int a = 0; a < FI; ++a)
-            get4(e.bias, e.bias_f32, i + 16 * a, 4, bias[a]);
-    }
-#pragma unroll
-    for (int b0 = 0; b0 < FJ; b0 += AT_ONCE) {
-        const int j = j0 + 16 * b0 + (lane & 15);
-        f32x4 res[FI][AT_ONCE];
-        const auto all = [&](auto f) {
-#pragma unroll
-            for (int b = 0; b < AT_ONCE; ++b)
-#pragma unroll
-                for (int a = 0; a < FI; ++a)
-                    f(a, b);
-        };
-        const auto rows = [&](const Mat &m, int64_t(&o)[AT_ONCE]) {
-#pragma unroll
-            for (int b = 0; b < AT_ONCE; ++b)
-                o[b] = m.row(j + 16 * b < J ? j + 16 * b : J - 1) + i;
-        };
-        const auto put = [&](const Mat &m) {
-            int64_t o[AT_ONCE];
-            rows(m, o);
-            if (m.f32)
-                all([&](int a, int b) {
-                    if (j + 16 * b < J)
-                        put4(m.data, true, o[b] + 16 * a, 4, acc[a][b0 + b]);
-                });
-            else
-                all([&](int a, int b) {
-                    if (j + 16 * b < J)
-                        put4(m.data, false, o[b] + 16 * a, 4, acc[a][b0 + b]);
-                });
-        };
-        if (e.residual.data) {
-            int64_t o[AT_ONCE];
-            rows(e.residual, o);
-            if (e.residual.f32)
-                all([&](int a, int b) { get4(e.residual.data, true, o[b] + 16 * a, 4, res[a][b]); });
-            else
-                all([&](int a, int b) { get4(e.residual.data, false, o[b] + 16 * a, 4, res[a][b]); });
+        for (int u = 0; u < G; ++u) {
+            const int j = j0 + u * STEP;
+            get4<STREAM>(m.data, F32, m.row(j < J ? j : J - 1) + i, 4, v[u]);
         }
-        if (e.bias)
-            all([&](int a, int b) { acc[a][b0 + b] += bias[a]; });
-        if (e.pre.data)
-            put(e.pre);
-        if (e.act != DOMINO_NO_ACT)
-            all([&](int a, int b) {
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    acc[a][b0 + b][u] = light_act(acc[a][b0 + b][u], e.act);
-            });
-        if (e.residual.data)
-            all([&](int a, int b) { acc[a][b0 + b] += res[a][b]; });
-        put(e.out);
     }
-}
+    template <bool F32, bool STREAM>
+    __device__ static void put(const Mat &m, int i, int j0, int J, const f32x4 (&v)[G])
+    {
+#pragma unroll
+        for (int u = 0; u < G; ++u) {
+            const int j = j0 + u * STEP;
+            if (j < J)
+                put4<STREAM>(m.data, F32, m.row(j) + i, 4, v[u]);
+        }
+    }
+
+    // store(tile): the waves that hold the rows from j0 on write them to rows of PITCH floats.
+    template <typename STORE>
+    __device__ static void part(const Epilogue &e, int i0, int I, int j0, int J, float *tile, STORE store)
+    {
+        const int c = 4 * (static_cast<int>(threadIdx.x) % LANES), r = static_cast<int>(threadIdx.x) / LANES, i = i0 + c;
+        const bool whole = i + 4 <= I;
+        const float *mine = tile + r * PITCH + c;
+        f32x4 bias = {0.f, 0.f, 0.f, 0.f}, res[G];
+        j0 += r;
+        const auto residual = [&](int j) {
+            if (e.residual.f32)
+                e.stream ? get<true, true>(e.residual, i, j, J, res) : get<true, false>(e.residual, i, j, J, res);
+            else
+                e.stream ? get<false, true>(e.residual, i, j, J, res) : get<false, false>(e.residual, i, j, J, res);
+        };
+        if (whole && e.residual.data)
+            residual(j0);
+        if (whole && e.bias)
+            get4(e.bias, e.bias_f32, i, 4, bias);
+        __syncthreads();
+        store(tile);
+        __syncthreads();
+        if (!whole) {
+#pragma unroll 1
+            for (int u = 0; i < I && u < N && j0 + u * STEP < J; ++u) {
+                const int j = j0 + u * STEP;
+                emit(e, i, I, e.out.row(j), e.pre.data ? e.pre.row(j) : 0, e.residual.data ? e.residual.row(j) : 0,
+                     *reinterpret_cast<const f32x4 *>(mine + u * STEP * PITCH));
+            }
+            return;
+        }
+#pragma unroll 1
+        for (int u0 = 0; u0 < N; u0 += G, j0 += G * STEP, mine += G * STEP * PITCH) {
+            f32x4 v[G];
+            if (u0 && e.residual.data)
+                residual(j0);
+#pragma unroll
+            for (int u = 0; u < G; ++u)
+                v[u] = *reinterpret_cast<const f32x4 *>(mine + u * STEP * PITCH) + bias;
+            if (e.pre.data) {
+                if (e.pre.f32)
+                    put<true, false>(e.pre, i, j0, J, v);
+                else
+                    put<false, false>(e.pre, i, j0, J, v);
+            }
+            const auto activate = [&](int act) {
+#pragma unroll
+                for (int u = 0; u < G; ++u)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        v[u][k] = light_act(v[u][k], act);
+            };
+            if (e.act == DOMINO_SILU)
+                activate(DOMINO_SILU);
+            else if (e.act == DOMINO_RELU)
+                activate(DOMINO_RELU);
+            if (e.residual.data) {
+#pragma unroll
+                for (int u = 0; u < G; ++u)
+                    v[u] += res[u];
+            }
+            if (e.out.f32)
+                e.stream ? put<true, true>(e.out, i, j0, J, v) : put<true, false>(e.out, i, j0, J, v);
+            else
+                e.stream ? put<false, true>(e.out, i, j0, J, v) : put<false, false>(e.out, i, j0, J, v);
+        }
+    }
+};
 
 // ---- operands ----
 
@@ -267,7 +310,8 @@ constexpr int LDS_PAD = 2;  // rows between the chunks of 8 of k, so that 8 lane
 
 // The X rows' (or columns') share of one step: BX of them by BK of k, in units of 8 of k of one row (along k), or of 8 of
 // k of the columns that 8 bytes hold (across k).  near: the addresses of a tile are a common one and 32 bits.
-template <typename T, bool ACROSS, int BX, int BK, int NTB>
+// D: steps that are in registers at once.
+template <typename T, bool ACROSS, int BX, int BK, int NTB, int D>
 struct Stage {
     static constexpr int CH = BK / 8, PITCH = BX + LDS_PAD, SIZE = sizeof(T);
     static constexpr int COLS = 8 / SIZE;
@@ -280,8 +324,8 @@ struct Stage {
     typedef uint32_t two __attribute__((ext_vector_type(2)));
     typedef uint32_t two_mem __attribute__((ext_vector_type(2), aligned(2)));
 
-    raw x[ACROSS ? 1 : U][PARTS];
-    two y[ACROSS ? U : 1][8];
+    raw x[D][ACROSS ? 1 : U][PARTS];
+    two y[D][ACROSS ? U : 1][8];
     uint32_t off[U];
     const char *base;  // of the tile's first row and k = 0
     int64_t step;      // bytes from a k to the next
@@ -318,72 +362,83 @@ struct Stage {
             }
         }
     }
-    // k from k0 on; past k1 zeros
-    __device__ void load(const Mat &m, int k0, int k1)
+    // A whole step's share, k from k0 on, into registers: the short way.
+    template <int S>
+    __device__ void load(int k0)
     {
-        if (fast && k0 + BK <= k1) {
-            const char *from = base + k0 * step;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (!any(u))
-                    continue;
-                if constexpr (ACROSS) {
-#pragma unroll
-                    for (int r = 0; r < 8; ++r)
-                        y[u][r] = *reinterpret_cast<const two_mem *>(
-                            from + static_cast<uint32_t>(off[u] + r * static_cast<uint32_t>(step)));
-                } else {
-#pragma unroll
-                    for (int v = 0; v < PARTS; ++v)
-                        x[u][v] = *reinterpret_cast<const mem *>(from + off[u] + 16 * v);
-                }
-            }
-        } else {
-            slow(m, k0, k1);
-        }
-    }
-    // Any strides, edges and ends: element by element.
-    __device__ void slow(const Mat &m, int k0, int k1)
-    {
-        const T *data = static_cast<const T *>(m.data);
+        const char *from = base + k0 * step;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (!any(u))
                 continue;
             if constexpr (ACROSS) {
-                const int i = x0 + column(u), k = k0 + unit(u) / (BX / COLS) * 8;
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    y[u][r] = two{0, 0};
-                    if (k + r < k1) {
-                        const T *p = data + m.row(k + r) + i;
-#pragma unroll
-                        for (int c = 0; c < COLS; ++c)
-                            if (i + c < X) {
-                                const uint32_t w = SIZE == 4 ? __float_as_uint(Vec<T>::one(p + c))
-                                                             : __float_as_uint(Vec<T>::one(p + c)) >> 16;
-                                if constexpr (SIZE == 4)
-                                    y[u][r][c] = w;
-                                else
-                                    y[u][r][c >> 1] |= w << (c & 1) * 16;
-                            }
-                    }
-                }
+                for (int r = 0; r < 8; ++r)
+                    y[S][u][r] = *reinterpret_cast<const two_mem *>(
+                        from + static_cast<uint32_t>(off[u] + r * static_cast<uint32_t>(step)));
             } else {
-                const int i = x0 + unit(u) / CH, k = k0 + unit(u) % CH * 8;
-                const T *p = data + m.row(i < X ? i : X - 1) + k;
 #pragma unroll
-                for (int v = 0; v < PARTS; ++v) {
-                    x[u][v] = raw{0, 0, 0, 0};
-                    if (k + 8 <= k1) {
-                        x[u][v] = *reinterpret_cast<const mem *>(p + v * Vec<T>::N);
-                    } else {
+                for (int v = 0; v < PARTS; ++v)
+                    x[S][u][v] = *reinterpret_cast<const mem *>(from + off[u] + 16 * v);
+            }
+        }
+    }
+    // The last of k, fewer than a step's: rows past it are that row again, and become zeros.
+    __device__ void load_last(int k0, int k1)
+    {
+        const char *from = base + k0 * step;
+        const int left = k1 - 1 - k0;
 #pragma unroll
-                        for (int e = 0; e < Vec<T>::N; ++e)
-                            if (k + v * Vec<T>::N + e < k1)
-                                Vec<T>::set(x[u][v], e, Vec<T>::one(p + v * Vec<T>::N + e));
-                    }
-                }
+        for (int u = 0; u < U; ++u) {
+            const int k = unit(u) / (BX / COLS) * 8, column_off = static_cast<int>(off[u] - k * static_cast<uint32_t>(step));
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const int at = k + r < left ? k + r : left;
+                y[0][u][r] = two{0, 0};
+                if (any(u))
+                    y[0][u][r] = *reinterpret_cast<const two_mem *>(
+                        from + static_cast<uint32_t>(column_off + at * static_cast<uint32_t>(step)));
+            }
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                y[0][u][r] = k + r <= left ? y[0][u][r] : two{0, 0};
+        }
+    }
+    // Any strides, edges and ends: k from k0 on, past k1 zeros, to LDS.
+    __device__ void slow(const Mat &m, int k0, int k1, uint4 *lds)
+    {
+        if constexpr (ACROSS)
+            if (fast) {
+                load_last(k0, k1);
+                store<0>(lds);
+                return;
+            }
+        const T *data = static_cast<const T *>(m.data);
+#pragma unroll 1
+        for (int q = threadIdx.x; q < BX * CH; q += NTB) {
+            const int row = ACROSS ? q % BX : q / CH, chunk = ACROSS ? q / BX : q % CH, k = k0 + 8 * chunk;
+            const int i = x0 + row < X ? x0 + row : X - 1;
+            const T *p = ACROSS ? data + i : data + m.row(i);
+            float f[8];
+            // (loads without conditions are in flight together; past the end, the last one again)
+            const int last = k1 - 1 - k;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const int at = k + (r < last ? r : last);
+                f[r] = Vec<T>::one(ACROSS ? p + m.row(at) : p + at);
+            }
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                f[r] = r <= last ? f[r] : 0.f;
+            if constexpr (SIZE == 4) {
+                put(lds, chunk, row, f);
+            } else {
+                uint4 w;
+                uint32_t *pw = reinterpret_cast<uint32_t *>(&w);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    pw[r] = (__float_as_uint(f[2 * r]) >> 16) | (__float_as_uint(f[2 * r + 1]) & 0xFFFF0000u);
+                lds[chunk * PITCH + place(row)] = w;
             }
         }
     }
@@ -395,6 +450,8 @@ struct Stage {
         for (int p = 0; p < 3; ++p)
             lds[(p * CH + chunk) * PITCH + place(i)] = plane[p];
     }
+    // What load() took, to LDS.
+    template <int S>
     __device__ void store(uint4 *lds) const
     {
 #pragma unroll
@@ -409,14 +466,14 @@ struct Stage {
                         float f[8];
 #pragma unroll
                         for (int r = 0; r < 8; ++r)
-                            f[r] = __uint_as_float(y[u][r][c]);
+                            f[r] = __uint_as_float(y[S][u][r][c]);
                         put(lds, chunk, i + c, f);
                     } else {
                         uint4 w;
                         uint32_t *pw = reinterpret_cast<uint32_t *>(&w);
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
-                            pw[r] = __builtin_amdgcn_perm(y[u][2 * r + 1][c >> 1], y[u][2 * r][c >> 1],
+                            pw[r] = __builtin_amdgcn_perm(y[S][u][2 * r + 1][c >> 1], y[S][u][2 * r][c >> 1],
                                                           c & 1 ? 0x07060302u : 0x05040100u);
                         lds[chunk * PITCH + place(i + c)] = w;
                     }
@@ -427,10 +484,10 @@ struct Stage {
                     float f[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        f[e] = x[u][e / 4][e % 4];
+                        f[e] = x[S][u][e / 4][e % 4];
                     put(lds, chunk, i, f);
                 } else {
-                    lds[chunk * PITCH + i] = __builtin_bit_cast(uint4, x[u][0]);
+                    lds[chunk * PITCH + i] = __builtin_bit_cast(uint4, x[S][u][0]);
                 }
             }
         }
@@ -446,12 +503,16 @@ struct Stage {
 struct Gemm {
     Mat a, b;
     int I, J, K;
-    int ti, tj, splits, k_split;  // tiles, parts of k of k_split each
+    int ti, tj, splits;           // tiles; parts of k: part p takes the steps p, p + splits, p + 2 splits, ...
     bool i_inner;                 // tiles that share a j come one after the other (else those that share an i)
     float *partial;               // [splits, J, pitch], or NULL: the results go out (splits = 1)
     int pitch;
     Epilogue e;
 };
+
+// Waves a SIMD that a kernel's registers allow.
+template <typename TA, typename TB, int ACROSS, int TILE>
+constexpr int WAVES = TILE >= 128 * 128 || ACROSS == 2 ? 2 : sizeof(TA) == 2 && sizeof(TB) == 2 && !ACROSS ? 4 : 3;
 
 // A launch's blocks go to the 8 dies in turn; the die's own blocks take neighbouring tiles, whose shared operand its
 // cache then holds.
@@ -462,19 +523,21 @@ __device__ inline int tile_id(int n)
 }
 
 template <typename TA, typename TB, bool A_ACROSS, bool B_ACROSS, int BI, int BJ, int WI, int WJ, int BK>
-__global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64, 2) void k_gemm(Gemm g)
+__global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64, (WAVES<TA, TB, A_ACROSS + B_ACROSS, BI * BJ>)) void k_gemm(Gemm g)
 {
     constexpr int NTB = BI / WI * (BJ / WJ) * 64;
-    typedef Stage<TA, A_ACROSS, BI, BK, NTB> SA;
-    typedef Stage<TB, B_ACROSS, BJ, BK, NTB> SB;
+    // (two steps ahead of the one that is multiplied, where the registers allow it)
+    constexpr int D = sizeof(TA) == 2 && sizeof(TB) == 2 && BI * BJ <= 128 * 128 ? 2 : 1;
+    typedef Stage<TA, A_ACROSS, BI, BK, NTB, D> SA;
+    typedef Stage<TB, B_ACROSS, BJ, BK, NTB, D> SB;
     constexpr int FI = WI / 16, FJ = WJ / 16, PA = PLANES<TA>, PB = PLANES<TB>;
-    constexpr int LDS = SA::LDS + SB::LDS, BUF = LDS * 32 <= 80 << 10 ? 2 : 1;
-    __shared__ uint4 lds[BUF * LDS];
+    constexpr int LDS = SA::LDS + SB::LDS, BUF = LDS * 32 <= (NTB == 256 ? 80 << 10 : 160 << 10) ? 2 : 1;
+    typedef EmitTile<BI, BJ, NTB> Emit;
+    __shared__ uint4 lds[BUF * LDS > Emit::LDS ? BUF * LDS : Emit::LDS];
     const int tiles = g.ti * g.tj, id = tile_id(tiles * g.splits);
     const int split = id / tiles, tile = id - split * tiles;
     const int outer = g.i_inner ? tile / g.ti : tile / g.tj, inner = tile - outer * (g.i_inner ? g.ti : g.tj);
     const int i0 = (g.i_inner ? inner : outer) * BI, j0 = (g.i_inner ? outer : inner) * BJ;
-    const int k0 = split * g.k_split, k1 = k0 + g.k_split < g.K ? k0 + g.k_split : g.K;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int wi = wave % (BI / WI) * WI, wj = wave / (BI / WI) * WJ;
     SA sa;
@@ -487,22 +550,8 @@ __global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64, 2) void k_gemm(Gemm g)
 #pragma unroll
         for (int b = 0; b < FJ; ++b)
             acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (k0 < k1) {
-        sa.load(g.a, k0, k1);
-        sb.load(g.b, k0, k1);
-    }
     uint4 *at = lds;
-    for (int k = k0; k < k1; k += BK) {
-        // (of two buffers, the one of the last step but one: all waves are past it once they have met in the last step)
-        if constexpr (BUF == 1)
-            __syncthreads();
-        sa.store(at);
-        sb.store(at + SA::LDS);
-        __syncthreads();
-        if (k + BK < k1) {
-            sa.load(g.a, k + BK, k1);
-            sb.load(g.b, k + BK, k1);
-        }
+    const auto multiply = [&]() {
 #pragma unroll
         for (int kk = 0; kk < BK / 32; ++kk) {
             bf16x8 fb[PB][FJ];
@@ -530,29 +579,80 @@ __global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64, 2) void k_gemm(Gemm g)
         }
         if constexpr (BUF == 2)
             at = at == lds ? lds + LDS : lds;
+    };
+    // whole steps, without a condition between the loads and their use: the wait for a step's loads leaves those of the
+    // next step in flight
+    const int steps = sa.fast && sb.fast ? g.K / BK : 0, every = (g.K + BK - 1) / BK;
+    const int last = steps - 1;
+    const auto load = [&](auto slot, int t) {
+        constexpr int S = decltype(slot)::value;
+        t = t < last ? t : last;  // (past the last one: that one, for nothing)
+        sa.template load<S>(t * BK);
+        sb.template load<S>(t * BK);
+        __builtin_amdgcn_sched_barrier(0);  // (they go out now, not where they are used)
+    };
+    const auto step = [&](auto slot, int t) {
+        constexpr int S = decltype(slot)::value;
+        // (of two buffers, the one of the last step but one: all waves are past it once they have met in the last step)
+        if constexpr (BUF == 1)
+            __syncthreads();
+        sa.template store<S>(at);
+        sb.template store<S>(at + SA::LDS);
+        __syncthreads();
+        load(slot, t + D * g.splits);
+        multiply();
+    };
+    typedef std::integral_constant<int, 0> First;
+    typedef std::integral_constant<int, D - 1> Second;
+    int t = split;
+    if (t < steps) {
+        load(First{}, t);
+        if constexpr (D == 2) {
+            load(Second{}, t + g.splits);
+            for (; t + g.splits < steps; t += 2 * g.splits) {
+                step(First{}, t);
+                step(Second{}, t + g.splits);
+            }
+        }
+        for (; t < steps; t += g.splits)  // (with two in registers: one at the most)
+            step(First{}, t);
+    }
+    for (; t < every; t += g.splits) {
+        if constexpr (BUF == 1)
+            __syncthreads();
+        sa.slow(g.a, t * BK, g.K, at);
+        sb.slow(g.b, t * BK, g.K, at + SA::LDS);
+        __syncthreads();
+        multiply();
     }
     // a lane has four neighbouring i of one j
-    if (!g.partial && i0 + BI <= g.I) {
-        emit_all<FI, FJ>(g.e, i0 + wi, j0 + wj, g.J, acc);
+    if (!g.partial) {
+        static_assert(Emit::PART % WJ == 0, "a wave's rows are in one part");
+#pragma unroll 1
+        for (int p = 0; p < BJ; p += Emit::PART)
+            Emit::part(g.e, i0, g.I, j0 + p, g.J, reinterpret_cast<float *>(lds), [&](float *tile) {
+                if (wj < p || wj >= p + Emit::PART)
+                    return;
+#pragma unroll
+                for (int b = 0; b < FJ; ++b)
+#pragma unroll
+                    for (int a = 0; a < FI; ++a)
+                        *reinterpret_cast<f32x4 *>(tile + (wj - p + 16 * b + (lane & 15)) * Emit::PITCH + wi + 16 * a +
+                                                   4 * (lane >> 4)) = acc[a][b];
+            });
         return;
     }
 #pragma unroll
     for (int b = 0; b < FJ; ++b) {
         const int j = j0 + wj + 16 * b + (lane & 15);
-        if (j >= g.J)
-            continue;
-        const int64_t o_part = (static_cast<int64_t>(split) * g.J + j) * g.pitch;
+        float *part = g.partial + (static_cast<int64_t>(split) * g.J + j) * g.pitch;
+        if (j < g.J)
 #pragma unroll
-        for (int a = 0; a < FI; ++a) {
-            const int i = i0 + wi + 16 * a + 4 * (lane >> 4);
-            if (i >= g.I)
-                continue;
-            if (g.partial)
-                *reinterpret_cast<f32x4 *>(g.partial + o_part + i) = acc[a][b];
-            else
-                emit<false>(g.e, i, g.I, g.e.out.row(j), g.e.pre.data ? g.e.pre.row(j) : 0,
-                            g.e.residual.data ? g.e.residual.row(j) : 0, acc[a][b]);
-        }
+            for (int a = 0; a < FI; ++a) {
+                const int i = i0 + wi + 16 * a + 4 * (lane >> 4);
+                if (i < g.I)
+                    *reinterpret_cast<f32x4 *>(part + i) = acc[a][b];
+            }
     }
 }
 
@@ -562,6 +662,11 @@ inline hipError_t launch_types(const Gemm &g, int shape, hipStream_t st)
 {
     constexpr int BK = sizeof(TA) == 2 && sizeof(TB) == 2 ? 64 : 32;
     const dim3 grid(static_cast<unsigned>(g.ti) * g.tj * g.splits);
+    if constexpr (BK == 64)
+        if (shape == dhlinear::HUGE) {
+            hipLaunchKernelGGL((k_gemm<TA, TB, A_ACROSS, B_ACROSS, 256, 256, 128, 64, BK>), grid, dim3(512), 0, st, g);
+            return hipGetLastError();
+        }
     if (shape == dhlinear::LARGE)
         hipLaunchKernelGGL((k_gemm<TA, TB, A_ACROSS, B_ACROSS, 128, 128, 64, 64, BK>), grid, dim3(256), 0, st, g);
     else if (shape == dhlinear::MEDIUM)

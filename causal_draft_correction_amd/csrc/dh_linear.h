@@ -9,8 +9,8 @@
 
 namespace dhlinear {
 
-// Tiles of a product: 128 x 128, 64 x 64, 64 x 16.
-enum Shape { LARGE, MEDIUM, FEW };
+// Tiles of a product: 128 x 128, 64 x 64, 64 x 16, 256 x 256 (two bfloat16 operands).
+enum Shape { LARGE, MEDIUM, FEW, HUGE };
 
 struct Forward {
     const domino_rows *x, *weight, *bias, *residual, *y, *pre;  // bias, residual, pre: NULL for none

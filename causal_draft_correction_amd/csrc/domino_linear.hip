@@ -28,8 +28,8 @@ __global__ __launch_bounds__(NT) void k_gemm_join(Gemm g, Divisor per)
 #pragma unroll 8
     for (int s = 1; s < g.splits; ++s)
         sum += *reinterpret_cast<const f32x4 *>(p + s * step);
-    emit<true>(g.e, i, g.I, g.e.out.row(j), g.e.pre.data ? g.e.pre.row(j) : 0,
-               g.e.residual.data ? g.e.residual.row(j) : 0, sum);
+    emit(g.e, i, g.I, g.e.out.row(j), g.e.pre.data ? g.e.pre.row(j) : 0,
+         g.e.residual.data ? g.e.residual.row(j) : 0, sum);
 }
 
 constexpr int SUM_COLS = 256, SUM_ROWS = 4 * NWAVE;  // columns of a block of k_dpre, rows that it has in flight
@@ -121,25 +121,35 @@ int up(int64_t n, int64_t d) { return static_cast<int>((n + d - 1) / d); }
 size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
 
 struct Cut {
-    int shape, ti, tj, splits, k_split, pitch;
+    int shape, ti, tj, splits, pitch;
     bool joined;   // the sums go out through k_gemm_join
     size_t bytes;  // of the parts
 };
 
-// Tiles of 128 x 128 where both sides fill them, of 64 x 16 for up to 16 rows.  Few tiles share out their sums until
-// there are two blocks a compute unit, in parts of 256 of k at least.
-Cut cut_of(int64_t I, int64_t J, int64_t K, int act = DOMINO_NO_ACT)
+// Tiles.  bf: both operands are bfloat16.
+Cut cut_of(int64_t I, int64_t J, int64_t K, bool bf, int act = DOMINO_NO_ACT)
 {
+    static const int BI[] = {128, 64, 64, 256}, BJ[] = {128, 64, 16, 256};
     Cut c;
-    c.shape = J <= 16 ? FEW : I >= 128 && J >= 128 ? LARGE : MEDIUM;
-    const int bi = c.shape == LARGE ? 128 : 64, bj = c.shape == LARGE ? 128 : c.shape == MEDIUM ? 64 : 16;
-    c.ti = up(I, bi), c.tj = up(J, bj);
-    const int64_t tiles = static_cast<int64_t>(c.ti) * c.tj;
-    int64_t n = tiles ? 512 / tiles : 1;
-    n = n < K / 256 ? n : K / 256;
-    n = n < 1 ? 1 : n;
-    c.k_split = up(up(K, n), 64) * 64;
-    c.splits = K ? up(K, c.k_split) : 1;
+    const auto tiles = [&](int shape) { return static_cast<int64_t>(up(I, BI[shape])) * up(J, BJ[shape]); };
+    const int64_t steps = up(K, 64);
+    c.shape = J <= 16 ? FEW
+              : bf && tiles(HUGE) >= 256 && K >= 512 ? HUGE
+              : I >= 128 && J >= 128 && tiles(LARGE) * steps >= 2048 ? LARGE : MEDIUM;
+    c.ti = up(I, BI[c.shape]), c.tj = up(J, BJ[c.shape]);
+    // Few tiles share out their sums.  A part costs the join as I J does and saves steps as K does: 50 sqrt(K / (I J))
+    // parts are best, or what makes one or two blocks a compute unit of them (512 x 256 results over K = 5120: 1, 4, 10,
+    // 20, 40 parts 68, 22, 13.3, 15.6, 21 us; over 151936: 32, 64, 96 parts 82, 77, 84 us).  A short sum is not worth
+    // the second launch (256 x 1024 over 1024, bfloat16: 9.2 us in one part, 13.3 in four; 203 x 1091 over 331, float32:
+    // 20.9 and 15.2 us).
+    const int64_t count = tiles(c.shape);
+    int64_t n = count ? static_cast<int64_t>(std::ceil(50 * std::sqrt(static_cast<double>(K) /
+                                                                     (static_cast<double>(I) * J)))) : 1;
+    for (int blocks = 256; count && blocks <= 512; blocks += 256)
+        if (10 * n >= 7 * (blocks / count))
+            n = blocks == 512 || 10 * n < 7 * (512 / count) ? blocks / count : n;
+    n = n < K / 64 ? n : K / 64;
+    c.splits = n < 1 || K < (bf ? 1536 : 320) || c.shape == HUGE ? 1 : static_cast<int>(n);
     c.pitch = up(I, 4) * 4;
     c.joined = c.splits > 1 || act == DOMINO_GELU;
     c.bytes = c.joined ? static_cast<size_t>(c.splits) * J * c.pitch * sizeof(float) : 0;
@@ -151,7 +161,7 @@ Gemm gemm_of(const Cut &c, const Mat &a, const Mat &b, int64_t I, int64_t J, int
     Gemm g = {};
     g.a = a, g.b = b;
     g.I = static_cast<int>(I), g.J = static_cast<int>(J), g.K = static_cast<int>(K);
-    g.ti = c.ti, g.tj = c.tj, g.splits = c.splits, g.k_split = c.k_split;
+    g.ti = c.ti, g.tj = c.tj, g.splits = c.splits;
     g.i_inner = c.ti <= c.tj;
     g.partial = c.joined ? static_cast<float *>(ws) : nullptr;
     g.pitch = c.pitch;
@@ -159,8 +169,12 @@ Gemm gemm_of(const Cut &c, const Mat &a, const Mat &b, int64_t I, int64_t J, int
 }
 
 template <typename F>
-hipError_t run(const Gemm &g, const Cut &c, F product, hipStream_t st)
+hipError_t run(Gemm &g, const Cut &c, F product, hipStream_t st)
 {
+    // large results, and a residual with them, go past the dies' caches: float32 logits of 151936 with a residual, 512
+    // rows: 150 us, through the caches 166; 16 rows: 20.8 and 24.6 us
+    const int64_t size = (g.e.out.f32 ? 4 : 2) + (g.e.residual.data ? g.e.residual.f32 ? 4 : 2 : 0);
+    g.e.stream = size * g.I * g.J > 4 << 20;
     hipError_t e = product(g, c.shape, st);
     if (e != hipSuccess || !c.joined)
         return e;
@@ -171,15 +185,16 @@ hipError_t run(const Gemm &g, const Cut &c, F product, hipStream_t st)
 }
 
 int64_t rows(const domino_rows &m) { return static_cast<int64_t>(m.B) * m.R; }
+bool bfloat(const domino_rows &a, const domino_rows &b) { return a.dtype == DOMINO_BF16 && b.dtype == DOMINO_BF16; }
 
 }  // namespace
 
-size_t workspace_bytes(const Forward &f) { return cut_of(f.weight->R, rows(*f.x), f.x->V, f.act).bytes; }
+size_t workspace_bytes(const Forward &f) { return cut_of(f.weight->R, rows(*f.x), f.x->V, bfloat(*f.x, *f.weight), f.act).bytes; }
 
 hipError_t forward(const Forward &f, void *ws, hipStream_t st)
 {
     const int64_t M = rows(*f.x), N = f.weight->R, K = f.x->V;
-    const Cut c = cut_of(N, M, K, f.act);
+    const Cut c = cut_of(N, M, K, bfloat(*f.x, *f.weight), f.act);
     Gemm g = gemm_of(c, mat_of(*f.weight), mat_of(*f.x), N, M, K, ws);
     g.e.out = mat_of(*f.y);
     if (f.pre)
@@ -204,10 +219,11 @@ Layout layout_of(const Backward &b)
 {
     Layout l = {};
     const int64_t M = rows(*b.grad), N = b.weight->R, K = b.x->V;
+    const bool act = b.act != DOMINO_NO_ACT;
     size_t at = 0, parts = 0;
     l.pitch = l.N4 = up(N, 4) * 4;
     l.dpre = at;
-    if (b.act != DOMINO_NO_ACT)
+    if (act)
         at += static_cast<size_t>(M) * l.pitch * sizeof(float);
     // blocks of 16 rows, and more where that would be more than 64 blocks
     l.sum_rows = M > 64 * SUM_ROWS ? up(M, 64 * SUM_ROWS) * SUM_ROWS : SUM_ROWS;
@@ -216,11 +232,11 @@ Layout layout_of(const Backward &b)
     if (b.grad_bias)
         at += round16(static_cast<size_t>(l.sum_blocks) * l.N4 * sizeof(float));
     if (b.grad_x && M) {
-        l.x = cut_of(K, M, N);
+        l.x = cut_of(K, M, N, !act && bfloat(*b.grad, *b.weight));
         parts = l.x.bytes;
     }
     if (b.grad_weight) {
-        l.w = cut_of(K, N, M);
+        l.w = cut_of(K, N, M, !act && bfloat(*b.grad, *b.x));
         parts = parts > l.w.bytes ? parts : l.w.bytes;
     }
     l.parts = at;

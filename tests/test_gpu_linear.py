@@ -115,10 +115,43 @@ def test_linear(M, K, N, xt, wt):
         assert y.kept() and pre.kept()
 
 
+# Sizes of each kind of tile, with edges that fill none: 512 x 256 results over a long sum; 256 tiles of 256 x 256 and
+# more (bfloat16), and the same sizes with a float32 operand.
+LONG = [("y", 300, 263, 20003), ("x", 300, 261, 20003), ("weight", 517, 262, 20003), ("y", 261, 20003, 300),
+        ("y", 4100, 523, 4098), ("x", 4100, 4098, 523), ("weight", 523, 4098, 4100)]
+
+
+@pytest.mark.parametrize("at,bt", TYPES)
+@pytest.mark.parametrize("kind,M,K,N", LONG)
+def test_long_products(kind, M, K, N, at, bt):
+    """Against float64 products on the device (numpy's would take a minute)."""
+    if kind == "y":
+        a, b = matrix(M, K, at, 1, 1, 1), matrix(N, K, bt, 2)
+        want, n = lambda x, y: x @ y.t(), K  # noqa: E731
+        residual, bias = matrix(M, N, F32, 3), matrix(1, N, F32, 4)[0]
+        got = dca.linear(a, b, bias=bias, activation="relu", residual=residual, want_pre=True)
+        pre = want(a.double(), b.double()) + bias.double()
+        size = want(a.double().abs(), b.double().abs()) + bias.abs()
+        bound = (parts(at, bt) * n + 600) * 2 * H * size + H / 4 * size + pre.abs() * H + TINY
+        assert ((got["pre"].double() - pre).abs() <= bound).all()
+        y = pre.clamp(min=0) + residual.double()
+        assert ((got["y"].double() - y).abs() <= bound + (y.abs() + residual.abs()) * 2 * H).all()
+        return
+    g = matrix(M, N, at, 1, 0, 1)
+    other = matrix(N, K, bt, 2) if kind == "x" else matrix(M, K, bt, 2)
+    x, w = (matrix(M, K, bt, 5), other) if kind == "x" else (other, matrix(N, K, bt, 5))
+    want, n = ((lambda p, q: p @ q), N) if kind == "x" else ((lambda p, q: p.t() @ q), M)
+    out = matrix(M, K, F32, 9, 3, 1) if kind == "x" else matrix(N, K, F32, 9, 3, 1)
+    dca.linear_backward(g, x, w, want=(kind,), out={kind: out})
+    size = want(g.double().abs(), other.double().abs())
+    bound = (parts(at, bt) * n + 600) * 2 * H * size + H / 4 * size + TINY
+    assert ((out.double() - want(g.double(), other.double())).abs() <= bound).all()
+
+
 def test_linear_without_rounding():
     """Operands whose products and sums float32 holds: every bit of the result."""
     g = torch.Generator().manual_seed(3)
-    for M, K, N in ((5, 37, 70), (130, 64, 140), (40, 700, 65)):
+    for M, K, N in ((5, 37, 70), (130, 64, 140), (40, 700, 65), (300, 200, 20003), (2100, 515, 8200)):
         x = torch.randint(-2 ** 5, 2 ** 5, (M, K), generator=g)
         w = torch.randint(-2 ** 5, 2 ** 5, (N, K), generator=g)
         want = (x.double() @ w.double().t()).float()
