@@ -169,7 +169,9 @@ __device__ inline void clear_rows(const Rows &table, int64_t block, int64_t bloc
         const int64_t head = skew < n ? skew : n, vecs = (n - head) / Vec<T>::N;
         typedef typename Vec<bf16s>::raw words;
         words *v = reinterpret_cast<words *>(data + head);
-        for (int64_t i = first; i < vecs; i += step)
+        // (a block's share in one piece: 622 MB in pieces of 16 KiB 95 us, strided over 512 blocks 122 us)
+        const int64_t each = (vecs + blocks - 1) / blocks, from = block * each;
+        for (int64_t i = from + threadIdx.x; i < from + each && i < vecs; i += threads)
             __builtin_nontemporal_store(words{0, 0, 0, 0}, v + i);
         const int64_t tail = head + vecs * Vec<T>::N;
         if (first < head)
@@ -433,16 +435,13 @@ __global__ __launch_bounds__(NT) void k_embed_join(Sums s, int tiles, Rows table
     const int64_t begin = end - s.tile;
     if (begin && s.sorted[begin - 1].x == token)
         return;  // (it began before)
-    // the first pair that is not the token's
-    int64_t lo = end + 1, hi = s.n;
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) / 2;
-        if (s.sorted[mid].x == token)
-            lo = mid + 1;
-        else
-            hi = mid;
+    // the tiles that begin with the token follow one another
+    int last = static_cast<int>(blockIdx.x);
+    for (int more = NT; more == NT;) {
+        const int64_t at = (static_cast<int64_t>(last) + 1 + threadIdx.x) * s.tile;
+        more = __syncthreads_count(at < s.n && s.sorted[at].x == token);
+        last += more;
     }
-    const int last = static_cast<int>((lo - 1) / s.tile);
     const int group = threadIdx.x >> 4, c = static_cast<int>(blockIdx.y) * 64 + 4 * (static_cast<int>(threadIdx.x) & 15);
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     if (c < s.pitch)
@@ -465,6 +464,87 @@ __global__ __launch_bounds__(NT) void k_embed_join(Sums s, int tiles, Rows table
         for (int e = 0; e < 4; ++e)
             sum[e] += part[g][4 * (threadIdx.x & 15) + e];
     put_sum<TT>(table, token, c, s.scale, s.accumulate, sum);
+}
+
+// ---- few tokens ----
+
+// The places of the block's hits in their order (thread after thread); returns how many there are.  Two barriers.
+__device__ inline int ordered_places(bool hit, uint32_t *count, int &place)
+{
+    const int wave = threadIdx.x >> 6;
+    const uint64_t mask = __ballot(hit);
+    if ((threadIdx.x & 63) == 0)
+        count[wave] = __popcll(mask);
+    __syncthreads();
+    place = __popcll(mask & ((1ull << (threadIdx.x & 63)) - 1));
+    int all = 0;
+#pragma unroll
+    for (int w = 0; w < NWAVE; ++w) {
+        place += w < wave ? static_cast<int>(count[w]) : 0;
+        all += static_cast<int>(count[w]);
+    }
+    __syncthreads();
+    return all;
+}
+
+// At most NT tokens, one a thread: a block writes `per` rows of the table, those of its tokens and zeros for the others.
+template <typename TG, typename TT>
+__global__ __launch_bounds__(NT) void k_embed_few(const int32_t *ids, int n, float scale, bool accumulate, int per,
+                                                  Rows grad, Rows table)
+{
+    __shared__ int token[NT], at[NT], mine[NT];
+    __shared__ uint32_t count[NWAVE];
+    __shared__ uint8_t named[NT];
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * per, row1 = row0 + per < table.R ? row0 + per : table.R;
+    const int t = threadIdx.x, id = t < n ? ids[t] : -1;
+    const bool hit = id >= row0 && id < row1;
+    int place;
+    named[t] = 0;
+    const int hits = ordered_places(hit, count, place);
+    if (hit) {
+        token[place] = id;
+        at[place] = t;
+        named[id - row0] = 1;
+    }
+    __syncthreads();
+    const int d = table.V, quads = (d + 3) / 4, rows = static_cast<int>(row1 - row0);
+    TT *out = static_cast<TT *>(const_cast<void *>(table.data)) + row0 * table.rs;
+    if (!accumulate)
+        for (int i = t; i < rows * quads; i += NT) {
+            const int r = i / quads, c = 4 * (i - r * quads);
+            const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+            if (!named[r])
+                store4(out + r * table.rs + c, d - c, zero);
+        }
+    for (int h = 0; h < hits; ++h) {
+        const int now = token[h];
+        if (!named[now - row0])
+            continue;  // (an earlier place took them all)
+        const bool same = t < hits && token[t] == now;
+        const int all = ordered_places(same, count, place);
+        if (same)
+            mine[place] = at[t];
+        if (t == 0)
+            named[now - row0] = 0;
+        __syncthreads();
+        for (int c = 4 * t; c < d; c += 4 * NT) {
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            constexpr int AHEAD = 8;
+            for (int i = 0; i < all; i += AHEAD) {
+                float f[AHEAD][4];
+#pragma unroll
+                for (int u = 0; u < AHEAD; ++u)
+                    load4(row_at<TG>(grad, grad.place(mine[i + u < all ? i + u : all - 1])) + c, d - c, f[u]);
+#pragma unroll
+                for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        sum[e] += i + u < all ? f[u][e] : 0.f;
+            }
+            put_sum<TT>(table, now, c, scale, accumulate, sum);
+        }
+        __syncthreads();
+    }
 }
 
 }  // namespace DH_NS
@@ -527,11 +607,33 @@ hipError_t forward(const domino_rows &table, const int32_t *ids, float scale, co
     return hipGetLastError();
 }
 
-size_t workspace_bytes(const domino_rows &grad) { return layout_of(grad).bytes; }
+// Tokens that one launch takes, each block with its own rows of the table: no more than that many gradients are added in
+// turn, and every block reads them all.
+constexpr int FEW = NT;
+
+size_t workspace_bytes(const domino_rows &grad)
+{
+    return static_cast<int64_t>(grad.B) * grad.R <= FEW ? 0 : layout_of(grad).bytes;
+}
 
 hipError_t backward(const domino_rows &grad, const int32_t *ids, float scale, bool accumulate, void *ws,
                     const domino_rows &table, hipStream_t st)
 {
+    if (static_cast<int64_t>(grad.B) * grad.R <= FEW) {
+        // 16 KiB of the table a block, and no more than makes 512 blocks: a block takes its tokens one after the other
+        const int64_t row = static_cast<int64_t>(table.V) * (table.dtype == DOMINO_F32 ? 4 : 2);
+        int64_t per = 16384 / row < table.R / 512 ? 16384 / row : table.R / 512;
+        per = per < 1 ? 1 : per > NT ? NT : per;
+        const Rows g = rows_of(grad, nullptr, false), t = rows_of(table, nullptr, false);
+        by_type(table.dtype, [&](auto to) {
+            by_type(grad.dtype, [&](auto from) {
+                hipLaunchKernelGGL((k_embed_few<decltype(from), decltype(to)>),
+                                   dim3(static_cast<unsigned>((table.R + per - 1) / per)), dim3(NT), 0, st, ids,
+                                   grad.B * grad.R, scale, accumulate, static_cast<int>(per), g, t);
+            });
+        });
+        return hipGetLastError();
+    }
     const Layout l = layout_of(grad);
     char *base = static_cast<char *>(ws);
     Pair *sorted = reinterpret_cast<Pair *>(base + l.sorted), *other = reinterpret_cast<Pair *>(base + l.other);
@@ -541,10 +643,10 @@ hipError_t backward(const domino_rows &grad, const int32_t *ids, float scale, bo
     int bits = 1;
     while (bits < 31 && (V >> bits))
         ++bits;  // V itself stands for no row
-    // blocks that clear the table: 64 KiB each, up to two a compute unit
+    // blocks that clear the table: one store a thread
     const int64_t size = static_cast<int64_t>(table.R) * table.V * (table.dtype == DOMINO_F32 ? 4 : 2);
-    const int64_t want = (size + 65535) / 65536;
-    const unsigned clears = accumulate ? 0 : static_cast<unsigned>(want < 512 ? want : 512);
+    const int64_t want = (size + 16 * SORT_NT - 1) / (16 * SORT_NT);
+    const unsigned clears = accumulate ? 0 : static_cast<unsigned>(want < 1 << 20 ? want : 1 << 20);
     hipError_t e;
     if (!l.sort_tiles) {
         const int n = static_cast<int>(l.n);
@@ -558,7 +660,7 @@ hipError_t backward(const domino_rows &grad, const int32_t *ids, float scale, bo
             else
                 hipLaunchKernelGGL((k_embed_sort<T, 8>), grid, block, 0, st, ids, n, V, bits, sorted, t);
         });
-        if ((e = hipGetLastError()) != hipSuccess || !n)
+        if ((e = hipGetLastError()) != hipSuccess)
             return e;
     } else {
         const int passes = (bits + DIGIT - 1) / DIGIT;

@@ -414,10 +414,11 @@ int domino_token_logprobs_backward(const domino_logits *logits, const int32_t *t
  *
  * domino_embed_backward: table[v] = scale * sum of grad_i over the i with ids_i = v, for every row v; with accumulate
  * != 0 that is added to the rows that ids name, and the others stay as they are.  Ids outside the table are passed
- * over.  The tokens are sorted, and each one's rows added in float32: the tile of up to 64 tokens in the order of their
- * places, tiles in theirs; the result does not change from call to call.  `table` is the gradient, of type and shape of
- * its own ([1, rows, V]).  workspace >= domino_embed_backward_workspace_size bytes, 16-byte aligned.  At most three
- * launches for 8192 tokens, above that 3 for each 6 bits of the table's rows besides.
+ * over.  Each token's rows are added in float32: up to 256 tokens in the order of their places; more are sorted, and a
+ * token's are added in that order within tiles of up to 64, whose sums are added in theirs.  The result does not change
+ * from call to call.  `table` is the gradient, of type and shape of its own ([1, rows, V]).  workspace >=
+ * domino_embed_backward_workspace_size bytes, 16-byte aligned (where that is 0, NULL will do).  One launch for up to 256
+ * tokens, three for up to 8192, above that three for each 6 bits of the table's rows besides.
  * V <= 2^20, scale finite in float32.  B = 0: nothing to look up; the gradient is 0 (without accumulate).
  * Asynchronous on `stream`; no allocation, no synchronization.
  */

@@ -1,9 +1,9 @@
 """GPU results of the embedding and its gradient against their plain 64-bit forms (layers_plain.py).
 
 Bounds, in halves of a float32 step (H = 2^-24).  A looked-up element is one product, rounded to float32 (H) and to the
-output's type.  A token's gradient adds its n rows in tiles of at most 64, the tiles' sums in 16 strands and these in
-turn: of n float32 additions an addend passes through at most 64 + n / 1024 + 17 (and no more than n), each of which
-rounds a value no larger than the sum of magnitudes; the scale and the addition to an earlier gradient round once more
+output's type.  A token's gradient adds its n rows in turn (up to 256 tokens), or in tiles of at most 64, the tiles' sums in 16
+strands and these in turn: of n float32 additions an addend passes through at most max(256, 64 + n / 256 + 17) (and no
+more than n), each of which rounds a value no larger than the sum of magnitudes; the scale and the addition to an earlier gradient round once more
 each; then the output's type."""
 import numpy as np
 import pytest
@@ -85,7 +85,7 @@ def check_backward(grad, ids, V, scale, otype, accumulate=False, pad=0, shift=0,
     dca.embed_backward(grad, ids, V, scale=scale, accumulate=accumulate, out=again)
     torch.cuda.synchronize()
     total, size, count = plain.embed_backward(host(grad), ids.cpu().numpy(), V, float(np.float32(scale)))
-    steps = np.minimum(count, 64 + count // 1024 + 17)[:, None]
+    steps = np.minimum(count, np.maximum(256, 64 + count // 256 + 17))[:, None]
     bound = size * (steps + 2) * H * 1.01
     if accumulate:
         bound = bound + np.where(count[:, None] > 0, np.abs(was) + size, 0.0) * H
@@ -103,7 +103,8 @@ def check_backward(grad, ids, V, scale, otype, accumulate=False, pad=0, shift=0,
 
 @pytest.mark.parametrize("gtype,otype", [(F32, F32), (F32, BF16), (BF16, F32), (BF16, BF16)])
 @pytest.mark.parametrize("n,V,d,pad,shift", [
-    (1, 1, 1, 0, 0), (2, 5, 3, 1, 1), (16, 64, 64, 0, 0), (33, 1000, 130, 0, 3), (1025, 77, 5, 3, 1),
+    (1, 1, 1, 0, 0), (2, 5, 3, 1, 1), (16, 64, 64, 0, 0), (33, 1000, 130, 0, 3), (256, 70, 1030, 1, 1),
+    (257, 70, 20, 1, 1), (200, 3000, 2, 0, 0), (50, 7, 9001, 0, 0), (1025, 77, 5, 3, 1),
     (700, 3001, 1029, 0, 1), (4097, 40000, 12, 0, 0)])
 def test_embed_backward(n, V, d, pad, shift, gtype, otype):
     for kind in ("even", "one", "few", "outside", "none", "zipf"):
@@ -214,7 +215,8 @@ def test_refusals_on_the_device():
     with pytest.raises(dca.DominoError, match="overlap"):
         dca.embed_backward(table[:3], ids, 5, out=torch.zeros((1, 4), device="cuda").expand(5, 4))
     with pytest.raises(dca.DominoError, match="EWORKSPACE"):
-        dca.embed_backward(table[:3], ids, 5, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        dca.embed_backward(matrix(300, 4, F32, 1), tokens(300, 5, "even", 1), 5,
+                           workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(dca.DominoError):
         dca.embed(table, ids, scale=float("nan"))
     with pytest.raises(ValueError):

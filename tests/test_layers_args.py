@@ -64,10 +64,10 @@ def test_other_arguments_of_an_embedding():
     assert backward(rows(), table(rs=99)) == EINVAL
     wide = 2 ** 20 + 1
     assert embed(table(V=wide, rs=wide), rows(V=wide, rs=wide, bs=3 * wide)) == EUNSUPPORTED
-    need = dca.embed_backward_workspace_size(2, 3, 100)
-    assert need > 0 and need % 16 == 0
-    assert backward(rows(), table(), nbytes=need - 1) == EWORKSPACE
-    assert backward(rows(), table(), ws=None) == backward(rows(), table(), ws=24) == EINVAL
+    need, many = dca.embed_backward_workspace_size(200, 3, 100), rows(B=200)
+    assert dca.embed_backward_workspace_size(2, 3, 100) == 0 and need > 0 and need % 16 == 0
+    assert backward(many, table(), nbytes=need - 1) == EWORKSPACE
+    assert backward(many, table(), ws=None) == backward(many, table(), ws=24) == EINVAL
     assert embed(table(), rows(B=0, data=None), ids=None) == 0
     assert backward(rows(B=0, data=None), table(data=None), ids=None, accumulate=1, ws=None) == 0
     assert _lib().domino_embed_backward_workspace_size(ref(rows()), None) == EINVAL
@@ -83,8 +83,11 @@ def test_memory_shared_by_an_embeddings_arguments():
     for out in (rows(data=t), rows(data=t - 2396), rows(data=t + 9996)):
         assert refused(embed(table(), out)) and refused(backward(out, table(), ids=64, ws=256))
     assert refused(embed(table(), rows(), ids=at + 2396)) and refused(embed(table(), rows(), ids=at - 20))
-    assert refused(backward(rows(), table(), ids=t)) and refused(backward(rows(), table(), ws=t))
-    assert refused(backward(rows(), table(), ids=256, ws=256)) and refused(backward(rows(), table(), ws=at + 16))
+    many = dict(B=200)
+    assert refused(backward(rows(), table(), ids=t)) and refused(backward(rows(**many), table(), ws=t))
+    assert refused(backward(rows(**many), table(), ids=256, ws=256))
+    assert refused(backward(rows(**many), table(), ids=1 << 27, ws=at + 16))
+    assert backward(rows(**many), table(), ids=1 << 27, ws=1 << 28) == backward(rows(), table(), ws=None) == EHIP
     # beside each other
     assert embed(table(), rows(), ids=at + 2400) == embed(table(), rows(data=t - 2400)) == EHIP
     assert embed(table(), rows(data=t + 10000)) == EHIP
