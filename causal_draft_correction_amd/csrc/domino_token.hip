@@ -17,9 +17,10 @@ namespace DH_NS {
 
 static_assert(SCORE_STATS == dhtoken::STATS, "");
 
-// The block's part, in every thread.  BACK: the elements are as they were, after it.
-template <typename T, int NV, int NTB, bool BACK = false>
-__device__ inline ScorePart chunk_score(typename Vec<T>::raw (&x)[NV], const Scale &sc, float *red_m, double (*red)[2])
+// The block's part, in every thread.
+template <typename T, int NV, int NTB>
+__device__ inline ScorePart chunk_score(typename Vec<T>::raw (&x)[NV], const T *row, int V, int c, int cvec,
+                                        const Scale &sc, float *red_m, double (*red)[2])
 {
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     float mine = NEG_INF;
@@ -35,23 +36,8 @@ __device__ inline ScorePart chunk_score(typename Vec<T>::raw (&x)[NV], const Sca
     for (int w = 1; w < NTB / 64; ++w)
         m = fmaxf(m, red_m[w]);
     const Expo ex(m > NEG_INF ? m : 0.f, sc);
-    const int at = set_apart<T, NV, NTB>(x, mine, m, red_m);
-    float s, t;
-    if (ex.small)
-        sum_scores<T, true>(x, ex, sc, s, t);
-    else
-        sum_scores<T, false>(x, ex, sc, s, t);
-    if constexpr (BACK)
-        put_back<T, NV>(x, at, m);
-    const double ws = wave_sum_f64(s), wt = wave_sum_f64(t);
-    if (lane == 0)
-        red[wave][0] = ws, red[wave][1] = wt;
-    __syncthreads();
-    double sum = 0.0, two = 0.0;
-#pragma unroll
-    for (int w = 0; w < NTB / 64; ++w)
-        sum += red[w][0], two += red[w][1];
-    return score_part(m, sum, two, ex, sc);
+    bool odd;
+    return block_score<T, NV, NTB>(x, row, V, c, cvec, mine, m, red_m, red, ex, sc, odd);
 }
 
 // The chunk's elements of the gradient; not live: zeros.
@@ -118,7 +104,7 @@ __global__ __launch_bounds__(NT) void k_token_part(Rows rows, Score score, Split
         load_chunk<T, NV, NT, true>(x, z, rows.V, c, sp.cvec);
     else
         load_chunk<T, NV>(x, z, rows.V, c, sp.cvec);
-    const ScorePart part = chunk_score<T, NV, NT>(x, sc, red_m, red);
+    const ScorePart part = chunk_score<T, NV, NT>(x, z, rows.V, c, sp.cvec, sc, red_m, red);
     if (threadIdx.x == 0)
         parts[static_cast<int64_t>(place.row) * sp.nch + c] = part;
 }
@@ -199,7 +185,7 @@ __global__ __launch_bounds__(NTB) void k_token_row(Rows rows, Score score, doubl
     if (counts) {
         const T *z = row_at<T>(rows, place);
         load_chunk<T, NV, NTB>(x, z, rows.V, 0, NV * NTB);
-        const ScorePart part = chunk_score<T, NV, NTB, GRAD>(x, sc, red_m, red);
+        const ScorePart part = chunk_score<T, NV, NTB>(x, z, rows.V, 0, NV * NTB, sc, red_m, red);
         if (threadIdx.x == 0)
             put_score(score, row, VT::one(z + score.tokens[row]), part, log1p(part.s), inv_tau,
                       GRAD ? s_stat
@@ -221,6 +207,7 @@ __global__ __launch_bounds__(NTB) void k_token_row(Rows rows, Score score, doubl
         const Expo ex(st[0], sc);
         const Coef coef = coef_of(st, ex, sc, grad_at(g_logprob, row), grad_at(g_entropy, row),
                                   static_cast<float>(inv_tau));
+        forget(x);
         chunk_grad<T, NV>(x, live, ex, sc, coef);
         store_chunk<T, NV, NTB>(x, out, 0, rows.V);
         if (live) {
@@ -241,7 +228,7 @@ using namespace dhk;
 namespace {
 
 constexpr int TARGET_BLOCKS = 1024;
-constexpr int PART_NV = 8, GRAD_NV = 4;  // vectors a thread takes at most: forward, backward
+constexpr int PART_NV = 4, GRAD_NV = 4;  // vectors a thread takes at most: forward, backward
 
 int vectors(const domino_logits &lg)
 {
@@ -329,10 +316,8 @@ hipError_t in_parts(const domino_logits &lg, const Scores &s, float *stats, doub
         const dim3 grid(n * sp.nch);
         if (sp.nv <= 2)
             hipLaunchKernelGGL((k_token_part<T, 2>), grid, dim3(NT), 0, st, rows, score, sp, keep, sc, parts);
-        else if (sp.nv <= 4)
-            hipLaunchKernelGGL((k_token_part<T, 4>), grid, dim3(NT), 0, st, rows, score, sp, keep, sc, parts);
         else
-            hipLaunchKernelGGL((k_token_part<T, 8>), grid, dim3(NT), 0, st, rows, score, sp, keep, sc, parts);
+            hipLaunchKernelGGL((k_token_part<T, PART_NV>), grid, dim3(NT), 0, st, rows, score, sp, keep, sc, parts);
     });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess)

@@ -229,7 +229,7 @@ struct ChunkShared {
     uint32_t bound[NTB / 64];
     int place[NTB];
     float m[NTB / 64];
-    double s[NTB / 64], t[NTB / 64];
+    double s[NTB / 64], score[NTB / 64][2];
     uint32_t count[2 * (NTB / 64)];
     int nvec, n;
 };
@@ -483,27 +483,20 @@ __global__ __launch_bounds__(NTB) void k_top_chunk(Rows rows, Live live, int k, 
         }
     const Expo ex(m > NEG_INF ? m : 0.f, sc);
     // (a thread's sum in float32, all others in 64 bits: continuations of different beams lie close to each other)
+    ScorePart all = {};
+    bool nan = false;
     if constexpr (SCORE) {
-        float s, t;
-        set_apart<T, NV, NTB>(x, tm, m, sh.m);
-        if (ex.small)
-            sum_scores<T, true>(x, ex, sc, s, t);
-        else
-            sum_scores<T, false>(x, ex, sc, s, t);
-        const double ws = wave_sum_f64(s), wt = wave_sum_f64(t);
-        if (lane == 0)
-            sh.s[wave] = ws, sh.t[wave] = wt;
+        all = block_score<T, NV, NTB>(x, z, rows.V, c, cvec, tm, m, sh.m, sh.score, ex, sc, nan);
     } else {
         const double s = wave_sum_f64(ex.small ? sum_exps<T, true>(x, ex, sc) : sum_exps<T, false>(x, ex, sc));
         if (lane == 0)
             sh.s[wave] = s;
-    }
-    __syncthreads();
-    const int nvec = sh.nvec;
-    bool nan = false;
+        __syncthreads();
 #pragma unroll
-    for (int w = 0; w < NTB / 64; ++w)
-        nan |= sh.s[w] != sh.s[w];
+        for (int w = 0; w < NTB / 64; ++w)
+            nan |= sh.s[w] != sh.s[w];
+    }
+    const int nvec = sh.nvec;
     // one element a thread
     if (nvec <= VECS)
         for (int i = threadIdx.x; i < (nvec * VT::N + 63) / 64 * 64; i += NTB) {
@@ -517,17 +510,7 @@ __global__ __launch_bounds__(NTB) void k_top_chunk(Rows rows, Live live, int k, 
         }
     __syncthreads();
     const int64_t slot = static_cast<int64_t>(row) * nch + c;
-    ScorePart all = {};
-    double log_s = 0.0;
-    if constexpr (SCORE) {
-        double total = 0.0, two = 0.0;
-#pragma unroll
-        for (int w = 0; w < NTB / 64; ++w)
-            total += sh.s[w], two += sh.t[w];
-        all = score_part(m, total, two, ex, sc);
-        if (direct)
-            log_s = log1p(all.s);
-    }
+    const double log_s = SCORE && direct ? log1p(all.s) : 0.0;
     auto emit = [&](int at, uint64_t key) {
         if (SCORE && direct)
             put_alternative(out, row, k, at, key, all, log_s, inv_tau);

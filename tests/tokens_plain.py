@@ -4,7 +4,8 @@ GPU results are compared with, with bounds of their errors.  Written from the de
 Bounds, in halves of a float32 step (H = 2^-24).  An exponential exp(-d) has one step of its own (2 H), and its argument
 is rounded twice, the factor and the product: 2 d H.  A thread adds at most 128 of them, vector by vector (22 additions
 deep at most), all others in 64 bits.  So a sum of exponentials is known to 26 H and 2 d H of each term; a sum of
-exponentials times exponents to 28 H and 4 d H of each term's magnitude.  What follows is in 64 bits, but for the
+exponentials times exponents to 28 H and 4 d H of each term's magnitude.  Where the others than the largest come to 1/8
+at least, that one was among them in these additions, which rounded its 1 as well: 22 H.  What follows is in 64 bits, but for the
 statistics and the gradient: 12 float32 operations at most on an element of it, and the exponential's own errors again.
 (The hardware's exponential gives 0 below 2^-126: such an element of the gradient may be off by all of itself.)
 """
@@ -35,6 +36,8 @@ def row(z, token, tau):
         s_err = (e * 26 + 2 * ed).sum() * H
         t_err = np.where(e > 0, ed * (28 + 4 * d), 0.0).sum() * H
     s, t = e.sum(), ed.sum()
+    # (a row of several chunks: each has a largest one of its own, whose weight in the row is among the terms above)
+    s_err += 22 * H if s >= 0.124 else 0.0
     logp = -d - np.log1p(s)
     entropy = np.log1p(s) + t / (1 + s)
     logprob_err = s_err / (1 + s)
