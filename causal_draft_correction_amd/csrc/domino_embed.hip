@@ -56,16 +56,15 @@ __device__ inline void store8(T *p, const float (&f)[8])
 
 // Part of a row: eight columns a thread, `per` threads a row.
 template <typename TI, typename TO>
-__global__ __launch_bounds__(NT) void k_embed(Rows table, const int32_t *ids, float scale, Rows out, int64_t n,
+__global__ __launch_bounds__(NT) void k_embed(Rows table, const int32_t *ids, float scale, Rows out, uint32_t n,
                                               Divisor per)
 {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * NT + threadIdx.x;
+    const uint32_t i = blockIdx.x * NT + threadIdx.x;  // (below 2^31: B R (V / 1024 + 1) is below 2^24)
     if (i >= n)
         return;
-    // (n may pass 32 bits, the threads of a block's first row do not)
-    const int64_t row = n <= 0x7FFFFFFF ? per.quotient(static_cast<uint32_t>(i)) : i / per.d;
+    const uint32_t row = per.quotient(i);
     const int c = static_cast<int>(i - row * per.d) * 8, d = table.V;
-    const Place at = out.place(static_cast<uint32_t>(row));
+    const Place at = out.place(row);
     TO *o = const_cast<TO *>(row_at<TO>(out, at)) + c;
     const int id = ids[row];
     const bool in = id >= 0 && id < table.R;
@@ -600,8 +599,8 @@ hipError_t forward(const domino_rows &table, const int32_t *ids, float scale, co
     const dim3 grid(static_cast<unsigned>((n + NT - 1) / NT));
     by_type(table.dtype, [&](auto in) {
         by_type(out.dtype, [&](auto to) {
-            hipLaunchKernelGGL((k_embed<decltype(in), decltype(to)>), grid, dim3(NT), 0, st, t, ids, scale, o, n,
-                               divisor(static_cast<uint32_t>(per)));
+            hipLaunchKernelGGL((k_embed<decltype(in), decltype(to)>), grid, dim3(NT), 0, st, t, ids, scale, o,
+                               static_cast<uint32_t>(n), divisor(static_cast<uint32_t>(per)));
         });
     });
     return hipGetLastError();

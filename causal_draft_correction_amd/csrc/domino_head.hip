@@ -1843,6 +1843,8 @@ int domino_linear(const domino_rows *x, const domino_rows *weight, const domino_
         (pre && (rc = like_rows(pre, "pre", B, R, N, true))) ||
         (bias && (rc = like_rows(bias, "bias", 1, 1, N, false))) || B == 0)
         return rc;
+    if (activation == DOMINO_GELU && static_cast<int64_t>(B) * R * ((N + 3ll) / 4) > 0x7FFFFFFFll)
+        return fail(DOMINO_EUNSUPPORTED, "gelu of %lld rows of %d: less than 2^33 elements", static_cast<long long>(B) * R, N);
     if ((rc = logits_data(x, "x")) || (rc = logits_data(weight, "weight")))
         return rc;
     const dhlinear::Forward f = {x, weight, bias, residual, y, pre, activation};

@@ -139,19 +139,22 @@ def _vector(name: str, t, n: int, gpu: int) -> bytes:
 
 
 @functools.lru_cache(maxsize=1024)
-def linear_workspace_size(B: int, R: int, K: int, N: int, activation: Optional[str] = None) -> int:
-    """Bytes of device workspace `linear` needs for x [B, R, K] and weight [N, K] (host only)."""
-    w = _shape_only(1, N, K, torch.float32)
-    return _size_of(_lib().domino_linear_workspace_size, _shape_only(B, R, K, torch.float32), ctypes.byref(w),
+def linear_workspace_size(B: int, R: int, K: int, N: int, activation: Optional[str] = None,
+                          dtypes: tuple = (torch.float32, torch.float32)) -> int:
+    """Bytes of device workspace `linear` needs for x [B, R, K] and weight [N, K] of these types (host only)."""
+    w = _shape_only(1, N, K, dtypes[1])
+    return _size_of(_lib().domino_linear_workspace_size, _shape_only(B, R, K, dtypes[0]), ctypes.byref(w),
                     _act(activation))
 
 
 @functools.lru_cache(maxsize=1024)
 def linear_backward_workspace_size(B: int, R: int, K: int, N: int, activation: Optional[str] = None,
-                                   want: tuple = ("x", "weight")) -> int:
-    """Bytes of device workspace `linear_backward` needs for x [B, R, K] and weight [N, K] (host only)."""
-    x, w = _shape_only(B, R, K, torch.float32), _shape_only(1, N, K, torch.float32)
-    return _size_of(_lib().domino_linear_backward_workspace_size, _shape_only(B, R, N, torch.float32), ctypes.byref(x),
+                                   want: tuple = ("x", "weight"),
+                                   dtypes: tuple = (torch.float32, torch.float32, torch.float32)) -> int:
+    """Bytes of device workspace `linear_backward` needs for grad [B, R, N], x [B, R, K] and weight [N, K] of these
+    types (host only)."""
+    x, w = _shape_only(B, R, K, dtypes[1]), _shape_only(1, N, K, dtypes[2])
+    return _size_of(_lib().domino_linear_backward_workspace_size, _shape_only(B, R, N, dtypes[0]), ctypes.byref(x),
                     ctypes.byref(w), _act(activation), *(name in want for name in _LINEAR_GRADS))
 
 
@@ -185,7 +188,8 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
     rd = None if residual is None else _rows_like("residual", residual, shape)
     bd = None if bias is None else _vector("bias", bias, n, gpu)
     if B * R:
-        _ws, ws, ws_bytes = _scratch(workspace, linear_workspace_size(B, R, K, n, activation), gpu)
+        _ws, ws, ws_bytes = _scratch(workspace, linear_workspace_size(B, R, K, n, activation, (x.dtype, weight.dtype)),
+                                     gpu)
         _check(lib.domino_linear(xd, wd, bd, act, rd, ws, ws_bytes, yd, pd, _stream(gpu)))
     return out
 
@@ -233,6 +237,7 @@ def linear_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, p
     if not B * R:  # (a tensor without rows may have R = 0)
         none = [_LOGITS(0, 0, 0, 0, 1, v, 0) for v in (n, K)]
         gd, xd, dx, pd, B, R = none[0], none[1], None if dx is None else none[1], None if pd is None else none[0], 0, 1
-    _ws, ws, ws_bytes = _scratch(workspace, linear_backward_workspace_size(B, R, K, n, activation, want), gpu)
+    need = linear_backward_workspace_size(B, R, K, n, activation, want, (grad.dtype, x.dtype, weight.dtype))
+    _ws, ws, ws_bytes = _scratch(workspace, need, gpu)
     _check(lib.domino_linear_backward(gd, xd, wd, pd, act, bool(accumulate), ws, ws_bytes, dx, dw, db, _stream(gpu)))
     return out

@@ -438,13 +438,14 @@ int domino_embed_backward(const domino_rows *grad, const int32_t *ids, double sc
  *   NULL: not wanted (not all three).  pre: NULL without an activation.  accumulate != 0: grad_weight and grad_bias
  *   are added to what is there (grad_x is not).  relu's slope at 0 is 0.  The residual's gradient is grad itself.
  * Operands are multiplied as they are: products of bfloat16 are exact, float32 operands go in three parts of 8 bits, so
- * that two of them multiply to 2^-24 of the product; sums are float32, and each output is rounded once.  An infinity or
- * NaN of an operand (float32 from 3.39e38 on among them) makes the elements that it takes part in infinite or NaN.
+ * that two of them multiply to 2^-24 of the product (below 2^-100 a part may fall under the type's range); sums are
+ * float32, and each output is rounded once.  An infinity or NaN of an operand (float32 from 3.39e38 on among them)
+ * makes the elements that it takes part in infinite or NaN.  silu and gelu of -inf are NaN, as their formulas give.
  * Results do not change from call to call; the last places of an element may depend on the other sizes of the call.
  * workspace >= domino_linear_workspace_size (x and weight: sizes and types alone) or domino_linear_backward_workspace_size (grad,
  * x, weight, and which gradients are wanted: likewise) bytes, 16-byte aligned (where that is 0, NULL will do).
  * y may be the residual (same data, and strides where a dimension is longer than 1).
- * B R, N and K below 2^24 each.  B = 0: y has no rows; grad_weight and grad_bias are 0 (without accumulate).
+ * B R, N and K below 2^24 each, with gelu B R N below 2^33.  B = 0: y has no rows; grad_weight and grad_bias are 0 (without accumulate).
  * At most two launches forward and six backward, asynchronous on `stream`; no allocation, no synchronization.
  */
 #define DOMINO_NO_ACT 0

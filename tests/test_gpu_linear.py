@@ -331,8 +331,9 @@ def test_captured_twice_on_one_workspace_and_another_stream():
     pre = dca.linear(x, w, want_pre=True)["pre"]
     kw = dict(pre=pre, activation="silu", want=("x", "weight", "bias"))
     want_y, want = dca.linear(x, w, activation="silu")["y"], dca.linear_backward(g, x, w, **kw)
-    need = max(dca.linear_workspace_size(M, 1, K, N, "silu"), dca.linear_backward_workspace_size(M, 1, K, N, "silu", kw["want"]))
-    assert dca.linear_workspace_size(M, 1, K, N) > 0  # (its sums are shared out)
+    need = max(dca.linear_workspace_size(M, 1, K, N, "silu", (F32, BF16)),
+               dca.linear_backward_workspace_size(M, 1, K, N, "silu", kw["want"], (F32, F32, BF16)))
+    assert dca.linear_workspace_size(M, 1, K, N, None, (F32, BF16)) > 0  # (its sums are shared out)
     ws = torch.empty(need, dtype=torch.uint8, device="cuda")
     stream = torch.cuda.Stream()
     stream.wait_stream(torch.cuda.current_stream())
@@ -376,6 +377,12 @@ def test_refusals_on_the_device():
                  lambda: dca.linear(x, w, out={"y": torch.zeros((1, 6), device="cuda").expand(4, 6)})):
         with pytest.raises(dca.DominoError):
             call()
+    need = dca.linear_workspace_size(4, 1, 5000, 6, None, (BF16, BF16))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")  # as much as it says is enough, and no less
+    exact = matrix(4, 5000, BF16, 1), matrix(6, 5000, BF16, 2)
+    dca.linear(*exact, workspace=ws)
+    with pytest.raises(dca.DominoError, match="EWORKSPACE"):
+        dca.linear(*exact, workspace=ws[:-1])
     wide = matrix(4, 5000, F32, 1), matrix(6, 5000, F32, 2)
     with pytest.raises(dca.DominoError, match="EWORKSPACE"):
         dca.linear(*wide, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))

@@ -165,6 +165,10 @@ def test_other_arguments_of_a_linear_layer():
     assert linear_back(y(), rows(), w(), pre=y(data=1 << 26), dx=DX) == EINVAL
     for bias in (Rows(64, 0, 0, 1, 1, 49, 0), Rows(64, 0, 0, 1, 2, 50, 0), Rows(None, 0, 0, 1, 1, 50, 0)):
         assert linear(rows(), w(), y(), bias=bias) == linear_back(y(), rows(), w(), db=bias) == EINVAL
+    far, many = 1 << 40, 1 << 17  # 2^17 rows of 2^16: too many for gelu alone
+    huge = [rows(B=many, R=1, V=8, bs=8, rs=8), Rows(far, 0, 8, 1, 1 << 16, 8, 0), y(data=1 << 41, B=many, R=1, V=1 << 16,
+                                                                                   bs=1 << 16)]
+    assert linear(*huge, act=2) == EUNSUPPORTED
     long = 1 << 24
     assert linear(rows(V=long, rs=long, bs=3 * long, B=1, R=1), w(K=long, rs=long, N=1), y(B=1, R=1, V=1)) == EUNSUPPORTED
     need = dca.linear_workspace_size(2, 3, 5000, 50)
