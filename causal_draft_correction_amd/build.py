@@ -13,7 +13,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 SRC_DIR = os.path.join(HERE, "csrc")
 UNITS = ["domino_head.hip", "domino_head_res.hip", "domino_head_bat.hip", "domino_head_rb.hip", "domino_verify.hip",
          "domino_top.hip", "domino_distill.hip", "domino_token.hip", "domino_embed.hip",
-         "domino_linear.hip", "domino_linear_y.hip", "domino_linear_dx.hip", "domino_linear_dw.hip"]
+         "domino_linear.hip", "domino_linear_y.hip", "domino_linear_dx.hip", "domino_linear_dw.hip",
+         "domino_linear_pair.hip"]
 LIB = os.path.join(HERE, "libdomino_head.so")
 # the instrumented library: these units replace domino_head_res.hip and domino_head_rb.hip
 TRACE_UNITS = ["trace/trace_res.hip", "trace/trace_rb.hip"]

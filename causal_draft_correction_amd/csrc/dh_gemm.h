@@ -516,25 +516,33 @@ constexpr int WAVES = TILE >= 128 * 128 || ACROSS == 2 ? 2 : sizeof(TA) == 2 && 
 
 // A launch's blocks go to the 8 dies in turn; the die's own blocks take neighbouring tiles, whose shared operand its
 // cache then holds.
-__device__ inline int tile_id(int n)
+__device__ inline int tile_id(int block, int n)
 {
-    const int die = blockIdx.x & 7, at = blockIdx.x >> 3, per = n >> 3, more = n & 7;
+    const int die = block & 7, at = block >> 3, per = n >> 3, more = n & 7;
     return die * per + (die < more ? die : more) + at;
 }
 
+// One of a product's tiles, by a block.
 template <typename TA, typename TB, bool A_ACROSS, bool B_ACROSS, int BI, int BJ, int WI, int WJ, int BK>
-__global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64, (WAVES<TA, TB, A_ACROSS + B_ACROSS, BI * BJ>)) void k_gemm(Gemm g)
-{
-    constexpr int NTB = BI / WI * (BJ / WJ) * 64;
+struct Tile {
+    static constexpr int NTB = BI / WI * (BJ / WJ) * 64;
     // (two steps ahead of the one that is multiplied, where the registers allow it)
-    constexpr int D = sizeof(TA) == 2 && sizeof(TB) == 2 && BI * BJ <= 128 * 128 ? 2 : 1;
+    static constexpr int D = sizeof(TA) == 2 && sizeof(TB) == 2 && BI * BJ <= 128 * 128 ? 2 : 1;
     typedef Stage<TA, A_ACROSS, BI, BK, NTB, D> SA;
     typedef Stage<TB, B_ACROSS, BJ, BK, NTB, D> SB;
-    constexpr int FI = WI / 16, FJ = WJ / 16, PA = PLANES<TA>, PB = PLANES<TB>;
-    constexpr int LDS = SA::LDS + SB::LDS, BUF = LDS * 32 <= (NTB == 256 ? 80 << 10 : 160 << 10) ? 2 : 1;
     typedef EmitTile<BI, BJ, NTB> Emit;
-    __shared__ uint4 lds[BUF * LDS > Emit::LDS ? BUF * LDS : Emit::LDS];
-    const int tiles = g.ti * g.tj, id = tile_id(tiles * g.splits);
+    static constexpr int LDS = SA::LDS + SB::LDS, BUF = LDS * 32 <= (NTB == 256 ? 80 << 10 : 160 << 10) ? 2 : 1;
+    static constexpr int LDS_ALL = BUF * LDS > Emit::LDS ? BUF * LDS : Emit::LDS;  // vectors of 16 bytes
+
+    __device__ static void run(const Gemm &g, int block, uint4 *lds);
+};
+
+template <typename TA, typename TB, bool A_ACROSS, bool B_ACROSS, int BI, int BJ, int WI, int WJ, int BK>
+__device__ __forceinline__ void Tile<TA, TB, A_ACROSS, B_ACROSS, BI, BJ, WI, WJ, BK>::run(const Gemm &g, int block,
+                                                                                        uint4 *lds)
+{
+    constexpr int FI = WI / 16, FJ = WJ / 16, PA = PLANES<TA>, PB = PLANES<TB>;
+    const int tiles = g.ti * g.tj, id = tile_id(block, tiles * g.splits);
     const int split = id / tiles, tile = id - split * tiles;
     const int outer = g.i_inner ? tile / g.ti : tile / g.tj, inner = tile - outer * (g.i_inner ? g.ti : g.tj);
     const int i0 = (g.i_inner ? inner : outer) * BI, j0 = (g.i_inner ? outer : inner) * BJ;
@@ -656,11 +664,22 @@ __global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64, (WAVES<TA, TB, A_ACROSS +
     }
 }
 
+template <typename TA, typename TB, bool A_ACROSS, bool B_ACROSS, int BI, int BJ, int WI, int WJ, int BK>
+__global__ __launch_bounds__(BI / WI * (BJ / WJ) * 64, (WAVES<TA, TB, A_ACROSS + B_ACROSS, BI * BJ>)) void k_gemm(Gemm g)
+{
+    typedef Tile<TA, TB, A_ACROSS, B_ACROSS, BI, BJ, WI, WJ, BK> T;
+    __shared__ uint4 lds[T::LDS_ALL];
+    T::run(g, static_cast<int>(blockIdx.x), lds);
+}
+
+template <typename TA, typename TB>
+constexpr int STEP_K = sizeof(TA) == 2 && sizeof(TB) == 2 ? 64 : 32;
+
 // Launches of one arrangement of the operands: the tile sizes of `shape` (dhlinear::Shape).
 template <typename TA, typename TB, bool A_ACROSS, bool B_ACROSS>
 inline hipError_t launch_types(const Gemm &g, int shape, hipStream_t st)
 {
-    constexpr int BK = sizeof(TA) == 2 && sizeof(TB) == 2 ? 64 : 32;
+    constexpr int BK = STEP_K<TA, TB>;
     const dim3 grid(static_cast<unsigned>(g.ti) * g.tj * g.splits);
     if constexpr (BK == 64)
         if (shape == dhlinear::HUGE) {
@@ -671,7 +690,7 @@ inline hipError_t launch_types(const Gemm &g, int shape, hipStream_t st)
         hipLaunchKernelGGL((k_gemm<TA, TB, A_ACROSS, B_ACROSS, 128, 128, 64, 64, BK>), grid, dim3(256), 0, st, g);
     else if (shape == dhlinear::MEDIUM)
         hipLaunchKernelGGL((k_gemm<TA, TB, A_ACROSS, B_ACROSS, 64, 64, 32, 32, BK>), grid, dim3(256), 0, st, g);
-    else
+    else if constexpr (!A_ACROSS)  // (forward)
         hipLaunchKernelGGL((k_gemm<TA, TB, A_ACROSS, B_ACROSS, 64, 16, 16, 16, BK>), grid, dim3(256), 0, st, g);
     return hipGetLastError();
 }

@@ -9,7 +9,7 @@
 
 namespace dhlinear {
 
-// Tiles of a product: 128 x 128, 64 x 64, 64 x 16, 256 x 256 (two bfloat16 operands).
+// Tiles of a product: 128 x 128, 64 x 64, 64 x 16 (forward), 256 x 256 (two bfloat16 operands).
 enum Shape { LARGE, MEDIUM, FEW, HUGE };
 
 struct Forward {

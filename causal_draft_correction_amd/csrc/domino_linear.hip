@@ -14,11 +14,12 @@ namespace DH_NS {
 hipError_t product_y(const Gemm &g, int shape, hipStream_t st);
 hipError_t product_dx(const Gemm &g, int shape, hipStream_t st);
 hipError_t product_dw(const Gemm &g, int shape, hipStream_t st);
+hipError_t product_pair(const Gemm &x, const Gemm &w, hipStream_t st);
 
 // The parts of a product's sums, in order, and the epilogue.  Four elements a thread.
-__global__ __launch_bounds__(NT) void k_gemm_join(Gemm g, Divisor per)
+__device__ inline void join_block(const Gemm &g, const Divisor &per, uint32_t block)
 {
-    const uint32_t at = blockIdx.x * NT + threadIdx.x;
+    const uint32_t at = block * NT + threadIdx.x;
     const int j = static_cast<int>(per.quotient(at)), i = 4 * static_cast<int>(at - j * per.d);
     if (j >= g.J)
         return;
@@ -28,8 +29,45 @@ __global__ __launch_bounds__(NT) void k_gemm_join(Gemm g, Divisor per)
 #pragma unroll 8
     for (int s = 1; s < g.splits; ++s)
         sum += *reinterpret_cast<const f32x4 *>(p + s * step);
-    emit(g.e, i, g.I, g.e.out.row(j), g.e.pre.data ? g.e.pre.row(j) : 0,
-         g.e.residual.data ? g.e.residual.row(j) : 0, sum);
+    emit(g.e, i, g.I, g.e.out.row(j), g.e.pre.data ? g.e.pre.row(j) : 0, g.e.residual.data ? g.e.residual.row(j) : 0,
+         sum);
+}
+__global__ __launch_bounds__(NT) void k_gemm_join(Gemm g, Divisor per) { join_block(g, per, blockIdx.x); }
+
+// The sums of k_dpre's blocks of rows, in order.
+struct Bias {
+    const float *sums;  // NULL: not wanted
+    int blocks, N, N4;
+    Mat out;
+    bool accumulate;
+};
+__device__ inline void bias_block(const Bias &b, int block)
+{
+    const int c = block * NT + static_cast<int>(threadIdx.x);
+    if (c >= b.N)
+        return;
+    float sum = 0.f;
+#pragma unroll 8
+    for (int r = 0; r < b.blocks; ++r)
+        sum += b.sums[static_cast<int64_t>(r) * b.N4 + c];
+    if (b.out.f32) {
+        float *p = static_cast<float *>(const_cast<void *>(b.out.data)) + c;
+        *p = b.accumulate ? *p + sum : sum;
+    } else {
+        bf16s *p = static_cast<bf16s *>(const_cast<void *>(b.out.data)) + c;
+        Vec<bf16s>::put(p, b.accumulate ? Vec<bf16s>::one(p) + sum : sum);
+    }
+}
+
+// What is to be joined of a backward pass: nx and nw blocks for the products, the others for the bias.
+__global__ __launch_bounds__(NT) void k_join(Gemm x, Divisor px, uint32_t nx, Gemm w, Divisor pw, uint32_t nw, Bias b)
+{
+    if (blockIdx.x < nx)
+        join_block(x, px, blockIdx.x);
+    else if (blockIdx.x < nx + nw)
+        join_block(w, pw, blockIdx.x - nx);
+    else
+        bias_block(b, static_cast<int>(blockIdx.x - nx - nw));
 }
 
 constexpr int SUM_COLS = 256, SUM_ROWS = 4 * NWAVE;  // columns of a block of k_dpre, rows that it has in flight
@@ -91,24 +129,6 @@ __global__ __launch_bounds__(NT) void k_dpre(Dpre d)
             (part[0][threadIdx.x] + part[1][threadIdx.x]) + (part[2][threadIdx.x] + part[3][threadIdx.x]);
 }
 
-__global__ __launch_bounds__(NT) void k_bias_join(const float *sums, int blocks, int N, int N4, Mat out, bool accumulate)
-{
-    const int c = static_cast<int>(blockIdx.x) * NT + static_cast<int>(threadIdx.x);
-    if (c >= N)
-        return;
-    float sum = 0.f;
-#pragma unroll 8
-    for (int b = 0; b < blocks; ++b)
-        sum += sums[static_cast<int64_t>(b) * N4 + c];
-    if (out.f32) {
-        float *p = static_cast<float *>(const_cast<void *>(out.data)) + c;
-        *p = accumulate ? *p + sum : sum;
-    } else {
-        bf16s *p = static_cast<bf16s *>(const_cast<void *>(out.data)) + c;
-        Vec<bf16s>::put(p, accumulate ? Vec<bf16s>::one(p) + sum : sum);
-    }
-}
-
 }  // namespace DH_NS
 
 namespace dhlinear {
@@ -126,14 +146,15 @@ struct Cut {
     size_t bytes;  // of the parts
 };
 
-// Tiles.  bf: both operands are bfloat16.
-Cut cut_of(int64_t I, int64_t J, int64_t K, bool bf, int act = DOMINO_NO_ACT)
+// Tiles.  bf: both operands are bfloat16; few: there are tiles for up to 16 rows (forward: 16 float32 rows of 256 by
+// 151936 x 256 bfloat16 weights 21 us, in tiles of 64 rows 31; backward, 25 us either way).
+Cut cut_of(int64_t I, int64_t J, int64_t K, bool bf, bool few, int act = DOMINO_NO_ACT)
 {
     static const int BI[] = {128, 64, 64, 256}, BJ[] = {128, 64, 16, 256};
     Cut c;
     const auto tiles = [&](int shape) { return static_cast<int64_t>(up(I, BI[shape])) * up(J, BJ[shape]); };
     const int64_t steps = up(K, 64);
-    c.shape = J <= 16 ? FEW
+    c.shape = few && J <= 16 ? FEW
               : bf && tiles(HUGE) >= 256 && K >= 512 ? HUGE
               : I >= 128 && J >= 128 && tiles(LARGE) * steps >= 2048 ? LARGE : MEDIUM;
     c.ti = up(I, BI[c.shape]), c.tj = up(J, BJ[c.shape]);
@@ -168,19 +189,24 @@ Gemm gemm_of(const Cut &c, const Mat &a, const Mat &b, int64_t I, int64_t J, int
     return g;
 }
 
-template <typename F>
-hipError_t run(Gemm &g, const Cut &c, F product, hipStream_t st)
+void stream_of(Gemm &g)
 {
     // large results, and a residual with them, go past the dies' caches: float32 logits of 151936 with a residual, 512
     // rows: 150 us, through the caches 166; 16 rows: 20.8 and 24.6 us
     const int64_t size = (g.e.out.f32 ? 4 : 2) + (g.e.residual.data ? g.e.residual.f32 ? 4 : 2 : 0);
     g.e.stream = size * g.I * g.J > 4 << 20;
-    hipError_t e = product(g, c.shape, st);
+}
+
+unsigned join_blocks(const Gemm &g) { return up(static_cast<int64_t>(g.J) * (g.pitch / 4), NT); }
+Divisor join_divisor(const Gemm &g) { return divisor(static_cast<uint32_t>(g.pitch / 4)); }
+
+template <typename F>
+hipError_t run(const Gemm &g, const Cut &c, F product, hipStream_t st)
+{
+    const hipError_t e = product(g, c.shape, st);
     if (e != hipSuccess || !c.joined)
         return e;
-    const int per = g.pitch / 4;
-    hipLaunchKernelGGL(k_gemm_join, dim3(up(static_cast<int64_t>(g.J) * per, NT)), dim3(NT), 0, st, g,
-                       divisor(static_cast<uint32_t>(per)));
+    hipLaunchKernelGGL(k_gemm_join, dim3(join_blocks(g)), dim3(NT), 0, st, g, join_divisor(g));
     return hipGetLastError();
 }
 
@@ -189,12 +215,12 @@ bool bfloat(const domino_rows &a, const domino_rows &b) { return a.dtype == DOMI
 
 }  // namespace
 
-size_t workspace_bytes(const Forward &f) { return cut_of(f.weight->R, rows(*f.x), f.x->V, bfloat(*f.x, *f.weight), f.act).bytes; }
+size_t workspace_bytes(const Forward &f) { return cut_of(f.weight->R, rows(*f.x), f.x->V, bfloat(*f.x, *f.weight), true, f.act).bytes; }
 
 hipError_t forward(const Forward &f, void *ws, hipStream_t st)
 {
     const int64_t M = rows(*f.x), N = f.weight->R, K = f.x->V;
-    const Cut c = cut_of(N, M, K, bfloat(*f.x, *f.weight), f.act);
+    const Cut c = cut_of(N, M, K, bfloat(*f.x, *f.weight), true, f.act);
     Gemm g = gemm_of(c, mat_of(*f.weight), mat_of(*f.x), N, M, K, ws);
     g.e.out = mat_of(*f.y);
     if (f.pre)
@@ -204,6 +230,7 @@ hipError_t forward(const Forward &f, void *ws, hipStream_t st)
     if (f.bias)
         g.e.bias = f.bias->data, g.e.bias_f32 = f.bias->dtype == DOMINO_F32;
     g.e.act = f.act;
+    stream_of(g);
     return run(g, c, product_y, st);
 }
 
@@ -211,8 +238,9 @@ namespace {
 
 struct Layout {
     Cut x, w;
+    bool pair;  // both products in one launch
     int pitch, sum_rows, sum_blocks, N4;
-    size_t dpre, sums, parts, bytes;
+    size_t dpre, sums, parts_x, parts_w, bytes;
 };
 
 Layout layout_of(const Backward &b)
@@ -220,7 +248,7 @@ Layout layout_of(const Backward &b)
     Layout l = {};
     const int64_t M = rows(*b.grad), N = b.weight->R, K = b.x->V;
     const bool act = b.act != DOMINO_NO_ACT;
-    size_t at = 0, parts = 0;
+    size_t at = 0;
     l.pitch = l.N4 = up(N, 4) * 4;
     l.dpre = at;
     if (act)
@@ -231,16 +259,16 @@ Layout layout_of(const Backward &b)
     l.sums = at;
     if (b.grad_bias)
         at += round16(static_cast<size_t>(l.sum_blocks) * l.N4 * sizeof(float));
-    if (b.grad_x && M) {
-        l.x = cut_of(K, M, N, !act && bfloat(*b.grad, *b.weight));
-        parts = l.x.bytes;
-    }
-    if (b.grad_weight) {
-        l.w = cut_of(K, N, M, !act && bfloat(*b.grad, *b.x));
-        parts = parts > l.w.bytes ? parts : l.w.bytes;
-    }
-    l.parts = at;
-    l.bytes = at + parts;
+    if (b.grad_x && M)
+        l.x = cut_of(K, M, N, !act && bfloat(*b.grad, *b.weight), false);
+    if (b.grad_weight)
+        l.w = cut_of(K, N, M, !act && bfloat(*b.grad, *b.x), false);
+    // (tiles of 64 x 64 have little to do; 331 x 1091 x 203, float32: 40 us a call in six launches, 26 in three)
+    l.pair = b.grad_x && M && b.grad_weight && l.x.shape == MEDIUM && l.w.shape == MEDIUM;
+    l.parts_x = l.parts_w = at;
+    if (l.pair)
+        l.parts_w += l.x.bytes;
+    l.bytes = l.pair ? l.parts_w + l.w.bytes : at + (l.x.bytes > l.w.bytes ? l.x.bytes : l.w.bytes);
     return l;
 }
 
@@ -280,24 +308,38 @@ hipError_t backward(const Backward &b, void *ws, hipStream_t st)
         grad.flat = grad.f32 = true;
         grad.near = grad.rs < (1 << 21);
     }
-    if (b.grad_bias) {
-        hipLaunchKernelGGL(k_bias_join, dim3(up(N, NT)), dim3(NT), 0, st, reinterpret_cast<float *>(base + l.sums),
-                           l.sum_blocks, static_cast<int>(N), l.N4, mat_of(*b.grad_bias), b.accumulate);
-        if ((e = hipGetLastError()) != hipSuccess)
-            return e;
-    }
+    Bias bias = {};
+    if (b.grad_bias)
+        bias = Bias{reinterpret_cast<float *>(base + l.sums), l.sum_blocks, static_cast<int>(N), l.N4,
+                    mat_of(*b.grad_bias), b.accumulate};
+    const unsigned bias_blocks = b.grad_bias ? up(N, NT) : 0;
+    Gemm x = {}, w = {};
     if (b.grad_x && M) {
-        Gemm g = gemm_of(l.x, mat_of(*b.weight), grad, K, M, N, base + l.parts);
-        g.e.out = mat_of(*b.grad_x);
-        if ((e = run(g, l.x, product_dx, st)) != hipSuccess)
-            return e;
+        x = gemm_of(l.x, mat_of(*b.weight), grad, K, M, N, base + l.parts_x);
+        x.e.out = mat_of(*b.grad_x);
+        stream_of(x);
     }
     if (b.grad_weight) {
-        Gemm g = gemm_of(l.w, mat_of(*b.x), grad, K, N, M, base + l.parts);
-        g.e.out = mat_of(*b.grad_weight);
+        w = gemm_of(l.w, mat_of(*b.x), grad, K, N, M, base + l.parts_w);
+        w.e.out = mat_of(*b.grad_weight);
         if (b.accumulate)
-            g.e.residual = g.e.out;
-        e = run(g, l.w, product_dw, st);
+            w.e.residual = w.e.out;
+        stream_of(w);
+    }
+    if (l.pair) {
+        if ((e = product_pair(x, w, st)) != hipSuccess)
+            return e;
+    } else {
+        if (b.grad_x && M && (e = run(x, l.x, product_dx, st)) != hipSuccess)
+            return e;
+        if (b.grad_weight && (e = run(w, l.w, product_dw, st)) != hipSuccess)
+            return e;
+    }
+    const unsigned nx = l.pair && l.x.joined ? join_blocks(x) : 0, nw = l.pair && l.w.joined ? join_blocks(w) : 0;
+    if (nx + nw + bias_blocks) {
+        hipLaunchKernelGGL(k_join, dim3(nx + nw + bias_blocks), dim3(NT), 0, st, x, nx ? join_divisor(x) : Divisor{}, nx,
+                           w, nw ? join_divisor(w) : Divisor{}, nw, bias);
+        e = hipGetLastError();
     }
     return e;
 }
