@@ -14,9 +14,9 @@
 //   512 x 256 -> 151936 logits with a residual, bfloat16 to float32 (700 MB): 148 us, 4.7 TB/s: HBM, in tiles of 128 x 128
 //     whose epilogue goes through LDS, so that rows are read and written in whole lines.
 //   16 x 256 -> 151936 (97 MB): 20 us, 4.8 TB/s: HBM.  512 x 5120 -> 256: 9 us in 10 parts, then a join: latency.
-//   Gradients of the 512 x 256 x 151936 layer: x's 75 us, 532 TFLOP/s, with 286 MB from HBM (3.8 TB/s), in 64
-//     parts of 8 tiles, and 8.5 for their join; w's 96 us, 414 TFLOP/s for 512 of k, 317 MB.  Both are short of the bytes' time by the steps
-//     in which a tile's operands cross from L2 to LDS: a step of 64 takes as long for them as for its matrix instructions.
+//   Gradients of the 512 x 256 x 151936 layer: x's 75 us, 532 TFLOP/s, 320 MB read and written (4.3 TB/s), in 64 parts of
+//     8 tiles, and 8.5 for their join; w's 96 us, 414 TFLOP/s, 317 MB (3.3 TB/s).  Both are short of the bytes' time: a
+//     step of 64 takes about as long to bring a tile's operands from L2 to LDS as its matrix instructions take.
 //   4096 x 4096 x 4096, bfloat16: 124 to 130 us, 1.06 to 1.1 PFLOP/s in tiles of 256 x 256, 183 us in those of 128 x 128;
 //     gradients 135 and 150 us.
 // Tried and left: rows of LDS that change places by their chunk instead of lying LDS_PAD apart (x's gradient 3% less, that
