@@ -9,6 +9,9 @@
 #define DH_NS dhl
 #include "dh_gemm.h"
 
+#include <algorithm>
+#include <cmath>
+
 namespace DH_NS {
 
 hipError_t product_y(const Gemm &g, int shape, hipStream_t st);
@@ -34,7 +37,7 @@ __device__ inline void join_block(const Gemm &g, const Divisor &per, uint32_t bl
 }
 __global__ __launch_bounds__(NT) void k_gemm_join(Gemm g, Divisor per) { join_block(g, per, blockIdx.x); }
 
-// The sums of k_dpre's blocks of rows, in order.
+// The sums of k_dpre's blocks of rows: a wave takes every 4th of them, a lane a column.
 struct Bias {
     const float *sums;  // NULL: not wanted
     int blocks, N, N4;
@@ -43,13 +46,18 @@ struct Bias {
 };
 __device__ inline void bias_block(const Bias &b, int block)
 {
-    const int c = block * NT + static_cast<int>(threadIdx.x);
-    if (c >= b.N)
-        return;
+    __shared__ float part[NWAVE][64];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, c = block * 64 + lane;
     float sum = 0.f;
+    if (c < b.N)
 #pragma unroll 8
-    for (int r = 0; r < b.blocks; ++r)
-        sum += b.sums[static_cast<int64_t>(r) * b.N4 + c];
+        for (int r = wave; r < b.blocks; r += NWAVE)
+            sum += b.sums[static_cast<int64_t>(r) * b.N4 + c];
+    part[wave][lane] = sum;
+    __syncthreads();
+    if (wave || c >= b.N)
+        return;
+    sum = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
     if (b.out.f32) {
         float *p = static_cast<float *>(const_cast<void *>(b.out.data)) + c;
         *p = b.accumulate ? *p + sum : sum;
@@ -253,8 +261,10 @@ Layout layout_of(const Backward &b)
     l.dpre = at;
     if (act)
         at += static_cast<size_t>(M) * l.pitch * sizeof(float);
-    // 64 blocks of rows at most (331 rows of 203, gelu: 8 rows a block 5.6 us, 16 7.7)
-    l.sum_rows = M > 64 * SUM_ROWS ? up(M, 64 * SUM_ROWS) * SUM_ROWS : M > 64 * NWAVE ? up(M, 64 * NWAVE) * NWAVE : NWAVE;
+    // about 512 blocks: 64 to 256 of rows, of 4 rows or of multiples of 16 (331 rows of 203, gelu: 4 rows a block 4.7 us, 16
+    // 7.7; 16384 rows of 256, silu and bias, a call: 256 blocks of rows 28 us, 64 83)
+    const int most = std::min(256, std::max(64, up(512, up(N, SUM_COLS))));
+    l.sum_rows = M > most * NWAVE ? up(M, most * SUM_ROWS) * SUM_ROWS : NWAVE;
     l.sum_blocks = up(M, l.sum_rows);
     l.sums = at;
     if (b.grad_bias)
@@ -312,7 +322,7 @@ hipError_t backward(const Backward &b, void *ws, hipStream_t st)
     if (b.grad_bias)
         bias = Bias{reinterpret_cast<float *>(base + l.sums), l.sum_blocks, static_cast<int>(N), l.N4,
                     mat_of(*b.grad_bias), b.accumulate};
-    const unsigned bias_blocks = b.grad_bias ? up(N, NT) : 0;
+    const unsigned bias_blocks = b.grad_bias ? up(N, 64) : 0;
     Gemm x = {}, w = {};
     if (b.grad_x && M) {
         x = gemm_of(l.x, mat_of(*b.weight), grad, K, M, N, base + l.parts_x);
