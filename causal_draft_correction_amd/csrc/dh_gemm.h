@@ -343,21 +343,29 @@ struct Stage {
     const char *base;  // of the tile's first row and k = 0
     int64_t step;      // bytes from a k to the next
     int x0, X;
+    int end;  // across k: the tile's column where the operand's last whole unit begins (negative in a tile of a few columns)
     bool fast;
 
     __device__ static int unit(int u) { return u * NTB + static_cast<int>(threadIdx.x); }
     __device__ static bool any(int u) { return UNITS % NTB == 0 || unit(u) < UNITS; }
-    __device__ static int column(int u) { return unit(u) % (BX / COLS) * COLS; }
+    // The first column of a unit.  Those that reach past the operand's last column take its last whole unit, once more.
+    __device__ int column(int u) const
+    {
+        const int i = unit(u) % (BX / COLS) * COLS;
+        return i < end ? i : end;
+    }
     __device__ static int place(int i) { return ACROSS ? i ^ ((i >> 4) & 3) : i; }  // (4 columns a lane: all banks again)
 
     __device__ void begin(const Mat &m, int at, int n)
     {
         x0 = at, X = n;
         const char *data = static_cast<const char *>(m.data);
-        // (rows past the last are that one again, columns the last whole unit's: their products go nowhere)
-        fast = m.near && !(ACROSS && x0 + BX > X && X % COLS);
+        // (rows past the last are that one again, columns past it whatever LDS holds: their products go nowhere)
+        end = X - COLS - x0;
+        fast = m.near && !(ACROSS && X < COLS);
+        const int before = end < 0 ? -end : 0;
         if constexpr (ACROSS) {
-            base = data + static_cast<int64_t>(x0) * SIZE;
+            base = data + (static_cast<int64_t>(x0) - before) * SIZE;
             step = m.rs * SIZE;
         } else {
             base = data + static_cast<int64_t>(x0) * m.rs * SIZE;
@@ -366,8 +374,8 @@ struct Stage {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if constexpr (ACROSS) {
-                const int i = x0 + column(u) + COLS <= X ? column(u) : X - COLS - x0;
-                off[u] = static_cast<uint32_t>(unit(u) / (BX / COLS) * 8 * static_cast<uint32_t>(step) + i * SIZE);
+                off[u] = static_cast<uint32_t>(unit(u) / (BX / COLS) * 8 * static_cast<uint32_t>(step) +
+                                               (column(u) + before) * SIZE);
             } else {
                 const int i = unit(u) / CH, last = X - 1 - x0;
                 off[u] = static_cast<uint32_t>(static_cast<uint32_t>(i < last ? i : last) *
@@ -475,12 +483,13 @@ struct Stage {
                 const int i = column(u), chunk = unit(u) / (BX / COLS);
 #pragma unroll
                 for (int c = 0; c < COLS; ++c) {
+                    const int at = (i + c) & (BX - 1);  // (those before the tile go behind its last column)
                     if constexpr (SIZE == 4) {
                         float f[8];
 #pragma unroll
                         for (int r = 0; r < 8; ++r)
                             f[r] = __uint_as_float(y[S][u][r][c]);
-                        put(lds, chunk, i + c, f);
+                        put(lds, chunk, at, f);
                     } else {
                         uint4 w;
                         uint32_t *pw = reinterpret_cast<uint32_t *>(&w);
@@ -488,7 +497,7 @@ struct Stage {
                         for (int r = 0; r < 4; ++r)
                             pw[r] = __builtin_amdgcn_perm(y[S][u][2 * r + 1][c >> 1], y[S][u][2 * r][c >> 1],
                                                           c & 1 ? 0x07060302u : 0x05040100u);
-                        lds[chunk * PITCH + place(i + c)] = w;
+                        lds[chunk * PITCH + place(at)] = w;
                     }
                 }
             } else {
