@@ -57,7 +57,9 @@ inline Mat mat_of(const domino_rows &m)
     t.by = divisor(static_cast<uint32_t>(m.R));
     t.flat = m.R == 1 || m.B <= 1 || m.batch_stride == m.R * m.row_stride;
     t.f32 = m.dtype == DOMINO_F32;
-    t.near = t.flat && t.rs < (1 << 21);  // (a tile's 128 rows within 31 bits)
+    // (the rows of a tile within 31 bits, or all of them)
+    const int64_t span = (m.B - 1) * m.batch_stride + (m.R - 1) * m.row_stride + m.V;
+    t.near = t.flat ? t.rs < (1 << 21) : span < (1 << 29);
     return t;
 }
 
@@ -362,13 +364,13 @@ struct Stage {
         const char *data = static_cast<const char *>(m.data);
         // (rows past the last are that one again, columns past it whatever LDS holds: their products go nowhere)
         end = X - COLS - x0;
-        fast = m.near && !(ACROSS && X < COLS);
+        fast = m.near && !(ACROSS && (X < COLS || !m.flat));
         const int before = end < 0 ? -end : 0;
         if constexpr (ACROSS) {
             base = data + (static_cast<int64_t>(x0) - before) * SIZE;
             step = m.rs * SIZE;
         } else {
-            base = data + static_cast<int64_t>(x0) * m.rs * SIZE;
+            base = m.flat ? data + static_cast<int64_t>(x0) * m.rs * SIZE : data;
             step = SIZE;
         }
 #pragma unroll
@@ -377,9 +379,9 @@ struct Stage {
                 off[u] = static_cast<uint32_t>(unit(u) / (BX / COLS) * 8 * static_cast<uint32_t>(step) +
                                                (column(u) + before) * SIZE);
             } else {
-                const int i = unit(u) / CH, last = X - 1 - x0;
-                off[u] = static_cast<uint32_t>(static_cast<uint32_t>(i < last ? i : last) *
-                                                   static_cast<uint32_t>(m.rs * SIZE) + unit(u) % CH * 8 * SIZE);
+                const int last = X - 1 - x0, i = unit(u) / CH < last ? unit(u) / CH : last;
+                off[u] = (m.flat ? static_cast<uint32_t>(i) * static_cast<uint32_t>(m.rs * SIZE)
+                                 : static_cast<uint32_t>(m.row(x0 + i) * SIZE)) + unit(u) % CH * 8 * SIZE;
             }
         }
     }

@@ -386,3 +386,13 @@ def test_refusals_on_the_device():
     wide = matrix(4, 5000, F32, 1), matrix(6, 5000, F32, 2)
     with pytest.raises(dca.DominoError, match="EWORKSPACE"):
         dca.linear(*wide, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_long_rows_of_blocks_that_lie_apart(dtype):
+    wide, w = matrix(40 * 5, 230, dtype, 1).view(40, 5, 230), matrix(130, 200, dtype, 2)
+    for x in (wide[:, 1:4, 9:209], wide[:, 1:4, 9:209].transpose(0, 1), wide[:, :1, 3:203].expand(40, 3, 200)):
+        g = wide[:, 1:4, 50:180] if x.shape[0] == 40 else wide[:, 1:4, 50:180].transpose(0, 1)
+        assert same_bits(dca.linear(x, w)["y"], dca.linear(x.contiguous(), w)["y"])
+        got, want = dca.linear_backward(g, x, w), dca.linear_backward(g.contiguous(), x.contiguous(), w)
+        assert same_bits(got["x"], want["x"]) and same_bits(got["weight"], want["weight"])
