@@ -296,8 +296,8 @@ struct EmitTile {
 
 // ---- operands ----
 
-// Eight floats as three planes of bfloat16; what is infinite or NaN lies in the first alone (as does what bfloat16
-// rounds to infinity, from 3.39e38 on).
+// Eight floats as three planes of bfloat16.  The first is cut off at bfloat16's largest value, past which finite floats
+// would round to infinity; of an infinity or NaN the planes are such, or NaN, so that their products are not finite.
 __device__ inline void cut(const float (&f)[8], uint4 (&plane)[3])
 {
     typedef __bf16 pair __attribute__((ext_vector_type(2)));
@@ -308,15 +308,24 @@ __device__ inline void cut(const float (&f)[8], uint4 (&plane)[3])
     };
     auto low = [](uint32_t w) { return __uint_as_float(w << 16); };
     auto high = [](uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); };
-    const float inf = __builtin_huge_valf();
+    const float most = __uint_as_float(0x7F7F0000u);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        h[i] = both(f[2 * i], f[2 * i + 1]);
-        float a = fabsf(low(h[i])) < inf ? f[2 * i] - low(h[i]) : 0.f;
-        float b = fabsf(high(h[i])) < inf ? f[2 * i + 1] - high(h[i]) : 0.f;
+        h[i] = both(__builtin_amdgcn_fmed3f(f[2 * i], -most, most), __builtin_amdgcn_fmed3f(f[2 * i + 1], -most, most));
+        const float a = f[2 * i] - low(h[i]), b = f[2 * i + 1] - high(h[i]);
         m[i] = both(a, b);
         l[i] = both(a - low(m[i]), b - high(m[i]));
     }
+}
+// Two floats as what they make of a product with an infinity: infinities and NaN as they are, any other cut off to
+// bfloat16, but none to 0 (nor to a number that counts as one) that is not 0.
+__device__ inline uint32_t kinds(float a, float b)
+{
+    const auto one = [](float f) {
+        const uint32_t w = __float_as_uint(f), size = w & 0x7FFFFFFFu;
+        return size > 0x7F800000u ? 0x7FC0u : size && size < 0x00800000u ? (w >> 16 & 0x8000u) | 0x80u : w >> 16;
+    };
+    return one(a) | one(b) << 16;
 }
 
 template <typename T>
@@ -427,10 +436,11 @@ struct Stage {
                 y[0][u][r] = k + r <= left ? y[0][u][r] : two{0, 0};
         }
     }
-    // Any strides, edges and ends: k from k0 on, past k1 zeros, to LDS.
+    // Any strides, edges and ends: k from k0 on, past k1 zeros, to LDS.  KIND: the elements' kinds(), as one plane.
+    template <bool KIND = false>
     __device__ void slow(const Mat &m, int k0, int k1, uint4 *lds)
     {
-        if constexpr (ACROSS)
+        if constexpr (ACROSS && !KIND)
             if (fast) {
                 load_last(k0, k1);
                 store<0>(lds);
@@ -453,14 +463,15 @@ struct Stage {
 #pragma unroll
             for (int r = 0; r < 8; ++r)
                 f[r] = r <= last ? f[r] : 0.f;
-            if constexpr (SIZE == 4) {
+            if constexpr (SIZE == 4 && !KIND) {
                 put(lds, chunk, row, f);
             } else {
                 uint4 w;
                 uint32_t *pw = reinterpret_cast<uint32_t *>(&w);
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    pw[r] = (__float_as_uint(f[2 * r]) >> 16) | (__float_as_uint(f[2 * r + 1]) & 0xFFFF0000u);
+                    pw[r] = KIND ? kinds(f[2 * r], f[2 * r + 1])
+                                 : (__float_as_uint(f[2 * r]) >> 16) | (__float_as_uint(f[2 * r + 1]) & 0xFFFF0000u);
                 lds[chunk * PITCH + place(row)] = w;
             }
         }
@@ -656,6 +667,54 @@ __device__ __forceinline__ void Tile<TA, TB, A_ACROSS, B_ACROSS, BI, BJ, WI, WJ,
         sb.slow(g.b, t * BK, g.K, at + SA::LDS);
         __syncthreads();
         multiply();
+    }
+    // Planes of 0 make NaN of an infinity's other products, and parts of an overflowing product can have both signs.  Where
+    // a sum of planes is not finite, the operands' kinds say whether, and with what sign, the product's is: a tile that
+    // has one (0 for each finite sum: one more barrier) takes its sum once more in one plane (512 x 256 -> 151936 in
+    // float32: 263 us, with a NaN in every row 766).
+    if constexpr (PA + PB > 2) {
+        const int i = i0 + wi + 4 * (lane >> 4), j = j0 + wj + (lane & 15);
+        float odd = 0.f;
+#pragma unroll
+        for (int a = 0; a < FI; ++a)
+#pragma unroll
+            for (int b = 0; b < FJ; ++b)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)  // (columns past an operand's last are whatever LDS held)
+                    if ((!A_ACROSS || i + 16 * a + e < g.I) && (!B_ACROSS || j + 16 * b < g.J))
+                        odd = fmaf(acc[a][b][e], 0.f, odd);
+        if (__syncthreads_or(odd != odd)) {
+            f32x4 kind[FI][FJ];
+#pragma unroll
+            for (int a = 0; a < FI; ++a)
+#pragma unroll
+                for (int b = 0; b < FJ; ++b)
+                    kind[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+            for (int s = split; s < every; s += g.splits) {
+                __syncthreads();
+                sa.template slow<true>(g.a, s * BK, g.K, lds);
+                sb.template slow<true>(g.b, s * BK, g.K, lds + SA::LDS);
+                __syncthreads();
+#pragma unroll
+                for (int kk = 0; kk < BK / 32; ++kk)
+#pragma unroll
+                    for (int a = 0; a < FI; ++a)
+#pragma unroll
+                        for (int b = 0; b < FJ; ++b)
+                            kind[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                SA::fragment(lds, 0, kk, wi + 16 * a), SB::fragment(lds + SA::LDS, 0, kk, wj + 16 * b),
+                                kind[a][b], 0, 0, 0);
+            }
+            const float inf = __builtin_huge_valf();
+#pragma unroll
+            for (int a = 0; a < FI; ++a)
+#pragma unroll
+                for (int b = 0; b < FJ; ++b)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        acc[a][b][e] = fabsf(acc[a][b][e]) < inf || fabsf(kind[a][b][e]) < inf ? acc[a][b][e] : kind[a][b][e];
+        }
     }
     // a lane has four neighbouring i of one j
     if (!g.partial) {

@@ -439,8 +439,10 @@ int domino_embed_backward(const domino_rows *grad, const int32_t *ids, double sc
  *   are added to what is there (grad_x is not).  relu's slope at 0 is 0.  The residual's gradient is grad itself.
  * Operands are multiplied as they are: products of bfloat16 are exact, float32 operands go in three parts of 8 bits, so
  * that two of them multiply to 2^-24 of the product (below 2^-100 a part may fall under the type's range); sums are
- * float32, and each output is rounded once.  An infinity or NaN of an operand (float32 from 3.39e38 on among them)
- * makes the elements that it takes part in infinite or NaN.  silu and gelu of -inf are NaN, as their formulas give.
+ * float32, and each output is rounded once.  Infinities and NaN of the operands, and sums past float32, give what these
+ * products and sums give: infinity times a number that is not 0 is infinite, times 0 NaN, infinities of both signs add up
+ * to NaN (a float32 operand beside them makes such a tile take about three times as long).  silu and gelu of -inf are NaN,
+ * as their formulas give.
  * Results do not change from call to call; the last places of an element may depend on the other sizes of the call.
  * workspace >= domino_linear_workspace_size (x and weight: sizes and types alone) or domino_linear_backward_workspace_size (grad,
  * x, weight, and which gradients are wanted: likewise) bytes, 16-byte aligned (where that is 0, NULL will do).
