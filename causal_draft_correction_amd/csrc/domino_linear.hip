@@ -32,8 +32,8 @@ __device__ inline void join_block(const Gemm &g, const Divisor &per, uint32_t bl
 #pragma unroll 8
     for (int s = 1; s < g.splits; ++s)
         sum += *reinterpret_cast<const f32x4 *>(p + s * step);
-    emit(g.e, i, g.I, g.e.out.row(j), g.e.pre.data ? g.e.pre.row(j) : 0, g.e.residual.data ? g.e.residual.row(j) : 0,
-         sum);
+    emit<true>(g.e, i, g.I, g.e.out.row(j), g.e.pre.data ? g.e.pre.row(j) : 0,
+               g.e.residual.data ? g.e.residual.row(j) : 0, sum);
 }
 __global__ __launch_bounds__(NT) void k_gemm_join(Gemm g, Divisor per) { join_block(g, per, blockIdx.x); }
 
