@@ -156,6 +156,15 @@ struct Cut {
 
 // Tiles.  bf: both operands are bfloat16; few: there are tiles for up to 16 rows (forward: 16 float32 rows of 256 by
 // 151936 x 256 bfloat16 weights 21 us, in tiles of 64 rows 31; backward, 25 us either way).
+// HUGE: where both sides of the result fill more than one tile of 128, else most of the tile is padding.  bfloat16, in tiles
+// of 64, 128 and 256 squared: rows of 4096 by 151936 weights, 17 rows 221, 245, 390 us, 64 rows 266, 260, 396, 128 rows
+// 361, 286, 404, 129 rows -, 424, 395, 512 rows 1168, 791, 677; gradient of w from 512 rows, 151936 x 16 53, 52, 85, x 128
+// 83, 55, 84, x 192 114, 90, 84, x 256 145, 91, 84.  The shortest sum is 512: below, the two lie closer (gradient of w,
+// 151936 x 256 from 496, 384, 256 rows: tiles of 128 94, 76, 56, of 256 87, 71, 54; 512 x 384 -> 151936 with a float32
+// residual 182 and 181, x 256 152 and 157).
+// LARGE: from 2048 steps of 64 on, about where they cross: in tiles of 64 and 128, bfloat16, 2048 x 512 -> 2048 13.4 and 12.7
+// us, 1024 x 2048 -> 1024 18.5 and 21.8, 2048 x 1024 -> 1024 13.4 and 18.3 (float32 36 and 42); below it, 512 x 4096 -> 512
+// 15.7 and 18.5, 1024 x 1024 -> 1024 9.7 and 18.
 Cut cut_of(int64_t I, int64_t J, int64_t K, bool bf, bool few, int act = DOMINO_NO_ACT)
 {
     static const int BI[] = {128, 64, 64, 256}, BJ[] = {128, 64, 16, 256};
@@ -163,7 +172,7 @@ Cut cut_of(int64_t I, int64_t J, int64_t K, bool bf, bool few, int act = DOMINO_
     const auto tiles = [&](int shape) { return static_cast<int64_t>(up(I, BI[shape])) * up(J, BJ[shape]); };
     const int64_t steps = up(K, 64);
     c.shape = few && J <= 16 ? FEW
-              : bf && tiles(HUGE) >= 256 && K >= 512 ? HUGE
+              : bf && I > 128 && J > 128 && tiles(HUGE) >= 256 && K >= 512 ? HUGE
               : I >= 128 && J >= 128 && tiles(LARGE) * steps >= 2048 ? LARGE : MEDIUM;
     c.ti = up(I, BI[c.shape]), c.tj = up(J, BJ[c.shape]);
     // Few tiles share out their sums.  A part costs the join as I J does and saves steps as K does: 50 sqrt(K / (I J))
