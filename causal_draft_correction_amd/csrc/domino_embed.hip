@@ -492,7 +492,8 @@ __device__ inline int ordered_places(bool hit, uint32_t *count, int &place)
     return all;
 }
 
-// At most NT tokens, one a thread: a block writes `per` rows of the table, those of its tokens and zeros for the others.
+// At most NT tokens, one a thread: a block writes `per` rows of the table, those of its tokens and zeros for the others;
+// with `accumulate` (per = 1) a block for each place, of which a token's first has its row, and for every 4 NT columns.
 template <typename TG, typename TT>
 __global__ __launch_bounds__(NT) void k_embed_few(const int32_t *ids, int n, float scale, bool accumulate, int per,
                                                   Rows grad, Rows table)
@@ -500,7 +501,10 @@ __global__ __launch_bounds__(NT) void k_embed_few(const int32_t *ids, int n, flo
     __shared__ int token[NT], at[NT], mine[NT];
     __shared__ uint32_t count[NWAVE];
     __shared__ uint8_t named[NT];
-    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * per, row1 = row0 + per < table.R ? row0 + per : table.R;
+    const int64_t row0 = accumulate ? ids[blockIdx.x] : static_cast<int64_t>(blockIdx.x) * per;
+    const int64_t row1 = row0 + per < table.R ? row0 + per : table.R;
+    if (row0 < 0 || row0 >= table.R)
+        return;
     const int t = threadIdx.x, id = t < n ? ids[t] : -1;
     const bool hit = id >= row0 && id < row1;
     int place;
@@ -512,6 +516,8 @@ __global__ __launch_bounds__(NT) void k_embed_few(const int32_t *ids, int n, flo
         named[id - row0] = 1;
     }
     __syncthreads();
+    if (accumulate && at[0] != static_cast<int>(blockIdx.x))
+        return;
     const int d = table.V, quads = (d + 3) / 4, rows = static_cast<int>(row1 - row0);
     TT *out = static_cast<TT *>(const_cast<void *>(table.data)) + row0 * table.rs;
     if (!accumulate)
@@ -532,7 +538,7 @@ __global__ __launch_bounds__(NT) void k_embed_few(const int32_t *ids, int n, flo
         if (t == 0)
             named[now - row0] = 0;
         __syncthreads();
-        for (int c = 4 * t; c < d; c += 4 * NT) {
+        for (int c = 4 * (t + NT * static_cast<int>(blockIdx.y)); c < d; c += 4 * NT * static_cast<int>(gridDim.y)) {
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
             constexpr int AHEAD = 8;
             for (int i = 0; i < all; i += AHEAD) {
@@ -613,7 +619,8 @@ hipError_t forward(const domino_rows &table, const int32_t *ids, float scale, co
 }
 
 // Tokens that one launch takes, each block with its own rows of the table: no more than that many gradients are added in
-// turn, and every block reads them all.
+// turn, and every block reads them all.  (A token repeated takes its block longer: of 1024 float32 columns and 151936 rows,
+// 256 tokens 108 us, all of them the same 156, and 257, sorted, 100 either way; added to what is there, 7, 63 and 15.)
 constexpr int FEW = NT;
 
 size_t workspace_bytes(const domino_rows &grad)
@@ -625,16 +632,20 @@ hipError_t backward(const domino_rows &grad, const int32_t *ids, float scale, bo
                     const domino_rows &table, hipStream_t st)
 {
     if (static_cast<int64_t>(grad.B) * grad.R <= FEW) {
-        // 16 KiB of the table a block, and no more than makes 512 blocks: a block takes its tokens one after the other
+        // 16 KiB of the table a block, and no more than makes 512 blocks: a block takes its tokens one after the other.  Added
+        // to what is there, other rows are of no account: a block a place (32 tokens of 4096 float32 columns, a table of
+        // 151936 rows: 40 us with blocks for all rows, 7 so).
+        const int n = grad.B * grad.R;
         const int64_t row = static_cast<int64_t>(table.V) * (table.dtype == DOMINO_F32 ? 4 : 2);
         int64_t per = 16384 / row < table.R / 512 ? 16384 / row : table.R / 512;
-        per = per < 1 ? 1 : per > NT ? NT : per;
+        per = per < 1 || accumulate ? 1 : per > NT ? NT : per;
+        const dim3 grid = accumulate ? dim3(n, static_cast<unsigned>((table.V + 4 * NT - 1) / (4 * NT)))
+                                     : dim3(static_cast<unsigned>((table.R + per - 1) / per));
         const Rows g = rows_of(grad, nullptr, false), t = rows_of(table, nullptr, false);
         by_type(table.dtype, [&](auto to) {
             by_type(grad.dtype, [&](auto from) {
-                hipLaunchKernelGGL((k_embed_few<decltype(from), decltype(to)>),
-                                   dim3(static_cast<unsigned>((table.R + per - 1) / per)), dim3(NT), 0, st, ids,
-                                   grad.B * grad.R, scale, accumulate, static_cast<int>(per), g, t);
+                hipLaunchKernelGGL((k_embed_few<decltype(from), decltype(to)>), grid, dim3(NT), 0, st, ids, n, scale,
+                                   accumulate, static_cast<int>(per), g, t);
             });
         });
         return hipGetLastError();
