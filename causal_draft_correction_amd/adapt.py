@@ -100,17 +100,23 @@ def markov_table(weights: dict) -> torch.Tensor:
 @torch.no_grad()
 def token_step(W1: torch.Tensor, W2: torch.Tensor, table: torch.Tensor, H: torch.Tensor, L_base: torch.Tensor,
                last_tok: torch.Tensor, tokens: torch.Tensor, n_rows: Optional[torch.Tensor] = None,
-               entropy: float = 0.0) -> dict:
+               entropy: float = 0.0, previous: Optional[torch.Tensor] = None) -> dict:
     """Loss of a Markov head on given tokens, and its gradient in W1.grad, W2.grad and table.grad.
 
     W1 [r, d + h], W2 [V, r] and table [V, h] float32; H [B, K, d], L_base [B, K, V] and last_tok [B] as
     `DominoHead.draft` takes them; tokens [B, K] int32 (-1: a position that does not count), n_rows [B] int32 the
     positions of each row that do.  The loss is the mean of -log p over these, less `entropy` times their mean
     entropy.  Returns loss, logprob and entropy [B, K] (0 where a position does not count).
+
+    A position's state is the row of `table` of the token before it: last_tok, then those of `tokens`.  Where `tokens`
+    has -1 for a token that is there but does not count, the position after it has no such row, and a state of zeros,
+    which no draft has: `previous` [B, K] int32 then gives the tokens that the positions follow, the first one's too.
     """
     B, K, V = L_base.shape
     d = H.shape[2]
-    prev = torch.cat([last_tok[:, None], tokens[:, :-1]], 1).contiguous()
+    prev = torch.cat([last_tok[:, None], tokens[:, :-1]], 1).contiguous() if previous is None else previous
+    if prev.shape != tokens.shape:
+        raise ValueError("previous: expected shape %s, got %s" % (tuple(tokens.shape), tuple(prev.shape)))
     x = torch.cat([H.float(), embed(table, prev)], -1)
     low = linear(x, W1, activation="silu", want_pre=True)
     logits = linear(low["y"], W2, residual=L_base, dtype=torch.float32)["y"]
