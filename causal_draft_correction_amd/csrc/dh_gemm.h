@@ -6,9 +6,10 @@
 // bfloat16, transposed where the operand lies across k, -> v_mfma_f32_16x16x32_bf16, summed in float32.
 //
 // float32 operands are cut into three bfloat16 planes, x = h + m + l, each the rounded remainder of those before: that
-// is all of x's 24 bits, and every product of two planes is exact in float32.  A float32 and a bfloat16 operand take 3
-// products, two float32 operands the 6 that weigh at least 2^-18 of the first (the three left out weigh at most 2^-26 of
-// it): 0.8 and 0.4 PFLOP/s at the bfloat16 rate, where the float32 instruction reaches 0.16.
+// is all of x's 24 bits (|m| <= 2^-8 |x|, |l| <= 2^-17 |x|), and every product of two planes is exact in float32.  A
+// float32 and a bfloat16 operand take 3 products, two float32 operands the 6 without m l, l m and l l, which are at most
+// 2^-25, 2^-25 and 2^-34 of the whole product, 2^-24 together.  4096 x 4096 x 4096: 401 us (0.34 PFLOP/s) and 667 us (0.21);
+// the library's float32 product takes 920.
 //
 // What bounds it, on one MI355X.
 //   512 x 256 -> 151936 logits with a residual, bfloat16 to float32 (700 MB): 148 us, 4.7 TB/s: HBM, in tiles of 128 x 128
@@ -17,6 +18,8 @@
 //   Gradients of the 512 x 256 x 151936 layer: x's 75 us, 532 TFLOP/s, 320 MB read and written (4.3 TB/s), in 64 parts of
 //     8 tiles, and 8.5 for their join; w's 96 us, 414 TFLOP/s, 317 MB (3.3 TB/s).  Both are short of the bytes' time: a
 //     step of 64 takes about as long to bring a tile's operands from L2 to LDS as its matrix instructions take.
+//   The same layer in float32 (6 products): 264 us, gradients 237 and 254, in tiles of 128 x 128 with one LDS buffer, 0.15 to
+//     0.17 PFLOP/s: loads and the cut into planes, which every tile that shares an operand does again.
 //   4096 x 4096 x 4096, bfloat16: 124 to 130 us, 1.06 to 1.1 PFLOP/s in tiles of 256 x 256, 183 us in those of 128 x 128;
 //     gradients 135 and 150 us.
 // Tried and left: rows of LDS that change places by their chunk instead of lying LDS_PAD apart (x's gradient 3% less, that

@@ -406,7 +406,7 @@ int domino_token_logprobs_backward(const domino_logits *logits, const int32_t *t
  * ---- layers: embedding, linear, and their gradients ----
  *
  * Operands are rows of V elements, [B, R, V] as for logits: any element alignment and strides, float32 or bfloat16 each
- * for itself.  A table or a weight matrix has B = 1.  An output that shares memory with an input, another output or
+ * for itself, B R (V / 1024 + 1) < 2^24 for each of them (a table or weights among them).  A table or a weight matrix has B = 1.  An output that shares memory with an input, another output or
  * the workspace is refused (DOMINO_EINVAL) but where it says otherwise, as are outputs whose rows overlap.
  *
  * Embedding: out_i = scale * table[ids_i], 0 where ids_i is outside [0, rows of the table).  ids [B, R] int32.
@@ -418,7 +418,7 @@ int domino_token_logprobs_backward(const domino_logits *logits, const int32_t *t
  * token's are added in that order within tiles of up to 64, whose sums are added in theirs.  The result does not change
  * from call to call.  `table` is the gradient, of type and shape of its own ([1, rows, V]).  workspace >=
  * domino_embed_backward_workspace_size bytes, 16-byte aligned (where that is 0, NULL will do).  One launch for up to 256
- * tokens, three for up to 8192, above that three for each 6 bits of the table's rows besides.
+ * tokens, three for up to 8192, above that two and three more for each 6 bits of the table's number of rows.
  * V <= 2^20, scale finite in float32.  B = 0: nothing to look up; the gradient is 0 (without accumulate).
  * Asynchronous on `stream`; no allocation, no synchronization.
  */
@@ -441,13 +441,13 @@ int domino_embed_backward(const domino_rows *grad, const int32_t *ids, double sc
  * that two of them multiply to 2^-24 of the product (below 2^-100 a part may fall under the type's range); sums are
  * float32, and each output is rounded once.  Infinities and NaN of the operands, and sums past float32, give what these
  * products and sums give: infinity times a number that is not 0 is infinite, times 0 NaN, infinities of both signs add up
- * to NaN (a float32 operand beside them makes such a tile take about three times as long).  silu and gelu of -inf are NaN,
- * as their formulas give.
+ * to NaN (a float32 operand beside them makes such a tile take about three times as long).  silu and gelu of -inf, and their
+ * slopes at infinities, are NaN, as their formulas give.
  * Results do not change from call to call; the last places of an element may depend on the other sizes of the call.
  * workspace >= domino_linear_workspace_size (x and weight: sizes and types alone) or domino_linear_backward_workspace_size (grad,
  * x, weight, and which gradients are wanted: likewise) bytes, 16-byte aligned (where that is 0, NULL will do).
  * y may be the residual (same data, and strides where a dimension is longer than 1).
- * B R, N and K below 2^24 each, with gelu B R N below 2^33.  B = 0: y has no rows; grad_weight and grad_bias are 0 (without accumulate).
+ * B R, N and K below 2^24 each besides, with gelu B R N below 2^33.  B = 0: y has no rows; grad_weight and grad_bias are 0 (without accumulate).
  * At most two launches forward and six backward, asynchronous on `stream`; no allocation, no synchronization.
  */
 #define DOMINO_NO_ACT 0
