@@ -11,12 +11,12 @@
 //
 // Up to SORT_MAX tokens are sorted by one block, in LDS (6 bits a pass, ranks by ballots); the launch's other blocks
 // meanwhile clear the table, which takes longer wherever the vocabulary is large.  Up to 256 tokens take one launch, whose
-// blocks each look all tokens through for those of their rows.
+// blocks each look all tokens through for those of their rows; added to what is there, for the rows that are named alone.
 //
 // Measured on one MI355X.  Rows of 4096 bfloat16, 4096 tokens of 4096 rows (34 MB written, 23 read past the dies' caches):
 // 8.6 to 11 us, 5 to 6.5 TB/s.  Gradient of 4096 tokens, 1024 float32, a table of 151936 rows: 95 us for sorting and 622 MB
 // of zeros (6.6 TB/s, what a fill reaches), 8.5 us for the sums (16.8 MB, latency: 256 tiles, each with 8 rows in flight), 4.7
-// for the join.  32 tokens of 64 over 1024 rows: 4.2 us, a call 8 us, sorted and joined 16.
+// for the join.  32 tokens of 64 over 1024 rows: 4.4 us, a call 8 us, sorted and joined 16.
 #define DH_NT 256
 #define DH_NS dhe
 #include "dh_rows.h"
